@@ -1,7 +1,7 @@
 /*
  * rope_gb300.h -- C ABI of the GB300 (sm_103a) rotary position embedding library.
  *
- * Three operators, each an asynchronous call on a caller-given CUDA stream:
+ * Six operators, each an asynchronous call on a caller-given CUDA stream:
  *
  *   rope_inplace_partial          in-place partial-slice RoPE on a BSND tensor
  *                                 (interleave or half mode), and its backward
@@ -9,6 +9,12 @@
  *                                 mrope, GPT-NeoX or GPT-J style; V2: interleaved mrope
  *                                 splice, strided inputs, separate outputs)
  *   rope_qkv_rmsnorm_rope_cache   fused QKV split + RMSNorm + RoPE + paged KV-cache write
+ *   rope_scaled_cos_sin(_cache)   the cos/sin tables these operators read, from frequencies
+ *                                 scaled for long contexts (rope_scaled_frequencies)
+ *   rope_append_paged_kv          RoPE of query and key on the way to the output and to
+ *                                 their slots of a paged KV cache (no norm)
+ *   rope_paged_attention          attention over the paged KV cache, with a prefix shared by
+ *                                 the whole batch read once for all
  *
  * Sources (web pages, cited by title and section):
  *  [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace
@@ -22,7 +28,8 @@
  * borrowed for the duration of the call and of the work it enqueues.  All
  * tensors of a call live on the current device (cudaSetDevice), and `stream`
  * belongs to it: the launch goes to the current device.  The
- * library allocates nothing, needs no workspace, and never synchronises the
+ * library allocates nothing, needs no workspace (except rope_paged_attention,
+ * whose caller gives it one), and never synchronises the
  * stream (except rope_get_device_error, which says so).  The two-phase
  * "GetWorkspaceSize, then execute" interface of the pages collapses to one call
  * because the workspace is always zero bytes.  (The fused op's kernel uses up to
@@ -90,9 +97,12 @@ enum {
 enum {
   ROPE_DEVICE_OK = 0,
   ROPE_DEVICE_POSITION_OUT_OF_RANGE = 1, /* some position was < 0 or >= maxSeqLen */
-  ROPE_DEVICE_SLOT_OUT_OF_RANGE = 2,     /* some KV-cache slot was >= blocks * block size */
-  ROPE_DEVICE_INDEX_OUT_OF_BOUNDS = 4    /* bounds-checking builds only: a kernel formed an address
+  ROPE_DEVICE_SLOT_OUT_OF_RANGE = 2,     /* some KV-cache slot was >= blocks * block size, some page of a block
+                                            table was outside the cache, or a sequence longer than its pages */
+  ROPE_DEVICE_INDEX_OUT_OF_BOUNDS = 4,   /* bounds-checking builds only: a kernel formed an address
                                             outside the tensor it addresses (the access was skipped) */
+  ROPE_DEVICE_WAIT_EXPIRED = 8           /* a wait inside a kernel ran out (results are not valid); a defect of
+                                            the library, never caused by the values of a tensor */
 };
 
 /*
@@ -264,6 +274,176 @@ int rope_qkv_rmsnorm_rope_cache(const rope_tensor_t* qkv, int64_t num_q_heads, i
                                 const rope_tensor_t* query_start_loc, const rope_tensor_t* slot_mapping,
                                 const rope_tensor_t* q_out, const rope_tensor_t* k_cache,
                                 const rope_tensor_t* v_cache, void* stream);
+
+/*
+ * Rotary frequencies scaled for long contexts (host arithmetic in binary64; no GPU).
+ *
+ * inv_freq[i] = base^(-2i/R) for i < F = R/2, changed by `scaling` (NULL: not at all):
+ *   ROPE_SCALING_LINEAR      inv_freq[i] / factor
+ *   ROPE_SCALING_BASE        base * factor^(R/(R-2)) in the place of base (R > 2)
+ *   ROPE_SCALING_YARN        mixed between inv_freq[i] and inv_freq[i] / factor along a ramp in i: with
+ *                            i(n) = R/2 * ln(original_length / (2 pi n)) / ln(base), the index whose wave
+ *                            makes n turns over the original length, the ramp goes from 0 (kept) at
+ *                            max(0, floor(i(high))) to 1 (divided) at min(R - 1, ceil(i(low))); a ramp of no
+ *                            width is 0.001 wide.  low and high are turns (0: 1 and 32).  base > 1.
+ *   ROPE_SCALING_WAVELENGTH  with t = original_length * inv_freq[i] / (2 pi) turns over the original length:
+ *                            kept where t >= high, divided by factor where t <= low, in between
+ *                            inv_freq[i] * s + inv_freq[i] / factor * (1 - s), s = (t - low) / (high - low).
+ *                            low < high.
+ *   ROPE_SCALING_FACTORS     inv_freq[i] / factors[i]
+ * *scale receives the factor of cos and sin: scaling->attention where that is > 0, else
+ * 1 + 0.1 * ln(factor) for ROPE_SCALING_YARN with factor > 1, else 1.
+ *
+ *   rotary_dim  R: even, 2 to 2048.        base > 0, finite.
+ *   factor > 0, original_length > 0 and factors (F values > 0) where the kind uses them.
+ * Returns ROPE_OK, ROPE_ERR_PARAM_NULLPTR or ROPE_ERR_PARAM_INVALID.
+ */
+enum {
+  ROPE_SCALING_NONE = 0,
+  ROPE_SCALING_LINEAR = 1,
+  ROPE_SCALING_BASE = 2,
+  ROPE_SCALING_YARN = 3,
+  ROPE_SCALING_WAVELENGTH = 4,
+  ROPE_SCALING_FACTORS = 5
+};
+
+typedef struct {
+  int32_t kind;           /* a ROPE_SCALING_* value */
+  double factor;          /* how far the context is stretched */
+  double original_length; /* positions the unscaled frequencies were made for */
+  double low, high;       /* turns over the original length at the ends of the mixed range */
+  double attention;       /* factor of cos and sin; 0: the kind's own */
+  const double* factors;  /* ROPE_SCALING_FACTORS: R/2 HOST values */
+} rope_scaling_t;
+
+int rope_scaled_frequencies(int64_t rotary_dim, double base, const rope_scaling_t* scaling, double* inv_freq,
+                            double* scale);
+
+/*
+ * cos/sin rows for given frequencies, in the layout of the cache-indexed operators
+ * (rope_scaled_cos_sin_cache) or of the in-place one (rope_scaled_cos_sin).
+ *
+ * Row r stands for position p = first_position + (positions ? positions[r] : r), and
+ * i < F = num_freq:
+ *   cache:                     cache[r, i] = scale * cos(p * inv_freq[i]);  cache[r, F + i] = scale * sin(...)
+ *   rotary_mode 0 (half):      cos[r, i] = cos[r, F + i] = scale * cos(p * inv_freq[i]);       sin likewise
+ *   rotary_mode 1 (interleave) cos[r, 2i] = cos[r, 2i + 1] = scale * cos(p * inv_freq[i]);     sin likewise
+ *
+ *   inv_freq   HOST pointer to F binary64 frequencies (radians per position), |value| <= 1e6.  Read
+ *              before the call returns.       1 <= F <= 1024.  scale: finite, rounded to binary32.
+ *   positions  I64 device tensor of as many elements as there are rows, or NULL.
+ *   cache      [rows, 2F] (or more leading dims); cos, sin: one shape, last dim 2F, e.g. [1, S, 1, 2F]
+ *              for the in-place operator.  F32, F16 or BF16.  Element alignment; 16-byte-aligned
+ *              tensors with F a multiple of 8 (F32: 4) are written in 16-byte pieces.
+ *
+ * The angle is kept as a 64-bit fraction of a turn: p * (inv_freq / 2 pi mod 1) mod 1 is exact in
+ * integers for every int64 position but for the one rounding of inv_freq / 2 pi to 2^-64 turns (an
+ * angle error of 2 pi p * 2^-65, 2e-13 at a million), so far positions are as exact as near ones.
+ * sin and cos of the remainder are within 2 units in the last place in binary32, then scaled and rounded.
+ * An empty output is ROPE_OK and enqueues nothing.  Outputs and positions must not share memory.
+ * Returns ROPE_OK, ROPE_ERR_PARAM_NULLPTR, ROPE_ERR_PARAM_INVALID or ROPE_ERR_CUDA.
+ */
+int rope_scaled_cos_sin_cache(const double* inv_freq, int64_t num_freq, double scale, const rope_tensor_t* positions,
+                              int64_t first_position, const rope_tensor_t* cache, void* stream);
+int rope_scaled_cos_sin(const double* inv_freq, int64_t num_freq, double scale, const rope_tensor_t* positions,
+                        int64_t first_position, int64_t rotary_mode, const rope_tensor_t* cos,
+                        const rope_tensor_t* sin, void* stream);
+
+/*
+ * RoPE of query and key on the way to the query output and to a paged KV cache.
+ *
+ * The rotation of rope_with_sin_cos_cache_v2, and per token t with slot = slot_mapping[t] >= 0, BS the block size:
+ *   query_out[t, h] = rotated query head
+ *   k_cache[slot/BS, h, slot%BS, :] = rotated key head;  v_cache[slot/BS, h, slot%BS, :] = value head (copied)
+ * The layout of the caches and the meaning of slots are those of rope_qkv_rmsnorm_rope_cache.
+ *
+ *   positions, cos_sin_cache, head_size, rotary_dim, is_neox, mrope_section, cache_mode: as in
+ *                  rope_with_sin_cos_cache_v2, except that cos_sin_cache may also be F32 with F16/BF16
+ *                  data (computed in binary32), and at most 1024 (F32) or 2048 for head_size.
+ *   query          [T, numQHeads*head_size] or NULL (keys and values only).
+ *   key, value     [T, numKHeads*head_size], [T, numVHeads*head_size]: same dtype as query.  Never written.
+ *   *_row_stride   elements between the starts of consecutive rows (0: contiguous), at least the row
+ *                  width, a multiple of 16 bytes: query, key and value may be column ranges of one buffer.
+ *   slot_mapping   I64 [T]; a negative slot writes no cache (padding).  The slots of one call that are >= 0
+ *                  are distinct: where two tokens name one slot, each 16-byte piece of it is one token's.
+ *   query_out      contiguous [T, numQHeads*head_size]; NULL (or equal to a contiguous query): query is
+ *                  rotated in place.  NULL without a query.
+ *   k_cache, v_cache  [NB, numKHeads, BS, head_size], [NB, numVHeads, BS, head_size]: written at the slots
+ *                  of this call only.
+ * Float tensors 16-byte aligned, int64 tensors 8-byte aligned.  T == 0 is ROPE_OK and enqueues nothing.
+ * A tensor the call writes shares no memory with any other of the call.
+ * Each rotated element is rounded once: one FMA after an exact product where data and table are both
+ * 16-bit, else the compensated difference of products.  A token with a position outside the table writes
+ * nothing and records ROPE_DEVICE_POSITION_OUT_OF_RANGE; a slot at or past NB * BS writes no cache and
+ * records ROPE_DEVICE_SLOT_OUT_OF_RANGE (query_out is still written).
+ * Returns ROPE_OK, ROPE_ERR_PARAM_NULLPTR, ROPE_ERR_PARAM_INVALID or ROPE_ERR_CUDA.
+ */
+int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* query, const rope_tensor_t* key,
+                         const rope_tensor_t* value, const rope_tensor_t* cos_sin_cache,
+                         const rope_tensor_t* slot_mapping, const rope_tensor_t* query_out,
+                         const rope_tensor_t* k_cache, const rope_tensor_t* v_cache, int64_t head_size,
+                         int64_t rotary_dim, int32_t is_neox, const int64_t* mrope_section,
+                         int64_t mrope_section_len, int32_t cache_mode, int64_t query_row_stride,
+                         int64_t key_row_stride, int64_t value_row_stride, void* stream);
+
+/*
+ * Causal attention of a batch's new tokens over the paged KV cache, with an optional prefix that every
+ * sequence shares.
+ *
+ * Token t of sequence b (query_start_loc[b] <= t < query_start_loc[b+1]) has position
+ *   p = seq_lens[b] - (query_start_loc[b+1] - query_start_loc[b]) + (t - query_start_loc[b])
+ * and sees the keys j <= p.  Key j sits in row j % BS of page prefix_blocks[j / BS] when j < prefix_len, else
+ * in row (j - prefix_len) % BS of page block_table[b, (j - prefix_len) / BS].  Per query head h, with key head
+ * g = h / (Nq / Nk):
+ *   s_j = scale * <query[t, h], k_j[g]>;  out[t, h] = sum_j e^(s_j - lse) v_j[g];  lse[t, h] = ln(sum_j e^(s_j))
+ * A row that sees no key gives out 0 and lse -infinity.  Keys and values that a row does not see have no
+ * influence on it, NaN and infinities among them, nor have the rows of a page past a sequence's end.
+ * Rows at or past query_start_loc[B] are left as they were.
+ *
+ * The keys and values of this call's own tokens are in the cache before the call
+ * (rope_append_paged_kv, rope_qkv_rmsnorm_rope_cache).
+ *
+ *   query            [T, Nq*D], rows query_row_stride elements apart (0: contiguous; a multiple of 16 bytes);
+ *                    F32, F16 or BF16; D a multiple of 32 (F16/BF16) or 16 (F32), at most 512.
+ *   k_cache, v_cache [NB, Nk, BS, D], same dtype; Nq a multiple of Nk.
+ *   block_table      I64 [B, W]: pages of each sequence's own tokens; B >= 1, W >= 1, W * BS <= 2^30.
+ *   seq_lens         I64 [B]: tokens of each sequence, prefix and this call's included.
+ *   query_start_loc  I64 [B + 1], non-decreasing from 0 to at most T (a sequence may be empty).  Other values
+ *                    cannot make the kernels access memory outside the tensors; which sequence a token
+ *                    belongs to, and whether it is written, is then unspecified.
+ *   prefix_blocks    I64, at least ceil(prefix_len / BS) pages, or NULL with prefix_len 0.
+ *   prefix_len       0 to 2^30.
+ *   scale            > 0 and finite.
+ *   out              contiguous [T, Nq*D], query's dtype.      lse  F32 [T, Nq], or NULL.
+ *   workspace        DEVICE pointer to workspace_bytes bytes, 256-byte aligned, at least what
+ *                    rope_paged_attention_workspace says.  Used by this call only until its work is done;
+ *                    its contents before and after mean nothing, and calls whose work may run at the same
+ *                    time need workspaces of their own.
+ *   stream           a cudaStream_t (NULL: the legacy default stream).
+ * Float tensors 16-byte aligned (lse 4), int64 tensors 8-byte aligned.  T == 0 is ROPE_OK and enqueues nothing.
+ * out, lse and the workspace share no memory with any other tensor of the call.
+ *
+ * Arithmetic: scores, softmax statistics and sums are binary32 (one running maximum and sum per row; partial
+ * results over key ranges are joined in a fixed order, so results are deterministic).  With F16/BF16 data the
+ * products run on the tensor cores, and the softmax weights e^(s_j - m) are rounded to the data's type before
+ * the product with V (at most half a unit in the last place each); out is rounded once.
+ * A page outside [0, NB), and tokens of a sequence past the W pages it has, are keys that no row sees; both
+ * record ROPE_DEVICE_SLOT_OUT_OF_RANGE.
+ * Returns ROPE_OK, ROPE_ERR_PARAM_NULLPTR, ROPE_ERR_PARAM_INVALID or ROPE_ERR_CUDA.
+ */
+int rope_paged_attention(const rope_tensor_t* query, int64_t query_row_stride, const rope_tensor_t* k_cache,
+                         const rope_tensor_t* v_cache, const rope_tensor_t* block_table,
+                         const rope_tensor_t* seq_lens, const rope_tensor_t* query_start_loc,
+                         const rope_tensor_t* prefix_blocks, int64_t prefix_len, float scale,
+                         const rope_tensor_t* out, const rope_tensor_t* lse, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace that rope_paged_attention needs on the current device for num_tokens query rows of
+ * num_q_heads heads of head_size (a rope_dtype_t type).  *bytes >= 256.
+ */
+int rope_paged_attention_workspace(int64_t num_tokens, int64_t num_q_heads, int64_t num_k_heads, int64_t head_size,
+                                   int32_t dtype, int64_t prefix_len, int64_t* bytes);
 
 /*
  * Takes the device-side error word of the current device (an atomic exchange

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -28,9 +29,12 @@ ROPE_ERR_CUDA = 561000
 ROPE_DEVICE_POSITION_OUT_OF_RANGE = 1
 ROPE_DEVICE_SLOT_OUT_OF_RANGE = 2
 ROPE_DEVICE_INDEX_OUT_OF_BOUNDS = 4
+ROPE_DEVICE_WAIT_EXPIRED = 8
 
 EXPORTED = ("rope_inplace_partial", "rope_inplace_partial_backward", "rope_with_sin_cos_cache",
-            "rope_with_sin_cos_cache_v2", "rope_qkv_rmsnorm_rope_cache", "rope_get_device_error",
+            "rope_with_sin_cos_cache_v2", "rope_qkv_rmsnorm_rope_cache", "rope_scaled_frequencies",
+            "rope_scaled_cos_sin_cache", "rope_scaled_cos_sin", "rope_append_paged_kv", "rope_paged_attention",
+            "rope_paged_attention_workspace", "rope_get_device_error",
             "rope_status_string", "rope_launch_count", "rope_abi_version")
 
 
@@ -38,6 +42,13 @@ class RopeTensor(ctypes.Structure):
     """Mirror of ``rope_tensor_t``."""
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4)]
+
+
+class RopeScaling(ctypes.Structure):
+    """Mirror of ``rope_scaling_t``."""
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_length", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("attention", ctypes.c_double),
+                ("factors", ctypes.POINTER(ctypes.c_double))]
 
 
 class RopeError(RuntimeError):
@@ -74,6 +85,21 @@ def load() -> ctypes.CDLL:
     lib.rope_qkv_rmsnorm_rope_cache.argtypes = [P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P,
                                                 ctypes.c_float, P, P, P, P, P, P, P, ctypes.c_void_p]
     lib.rope_qkv_rmsnorm_rope_cache.restype = ctypes.c_int
+    D, B, V = ctypes.c_int64, ctypes.c_char_p, ctypes.c_void_p  # B: a packed rope_tensor_t (see _pack)
+    DP = ctypes.POINTER(ctypes.c_double)
+    lib.rope_scaled_frequencies.argtypes = [D, ctypes.c_double, ctypes.POINTER(RopeScaling), DP, DP]
+    lib.rope_scaled_frequencies.restype = ctypes.c_int
+    lib.rope_scaled_cos_sin_cache.argtypes = [V, D, ctypes.c_double, B, D, B, V]
+    lib.rope_scaled_cos_sin_cache.restype = ctypes.c_int
+    lib.rope_scaled_cos_sin.argtypes = [V, D, ctypes.c_double, B, D, D, B, B, V]
+    lib.rope_scaled_cos_sin.restype = ctypes.c_int
+    lib.rope_append_paged_kv.argtypes = [B] * 9 + [D, D, ctypes.c_int32, ctypes.POINTER(D), D, ctypes.c_int32, D, D,
+                                                   D, V]
+    lib.rope_append_paged_kv.restype = ctypes.c_int
+    lib.rope_paged_attention.argtypes = [B, D, B, B, B, B, B, B, D, ctypes.c_float, B, B, V, D, V]
+    lib.rope_paged_attention.restype = ctypes.c_int
+    lib.rope_paged_attention_workspace.argtypes = [D, D, D, D, ctypes.c_int32, D, ctypes.POINTER(D)]
+    lib.rope_paged_attention_workspace.restype = ctypes.c_int
     lib.rope_get_device_error.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]
     lib.rope_get_device_error.restype = ctypes.c_int
     lib.rope_status_string.argtypes = [ctypes.c_int]
@@ -310,6 +336,237 @@ def prepare_qkv_rmsnorm_rope_cache(qkv: torch.Tensor, num_q_heads: int, num_k_he
     args, descs = _qkv_args(qkv, num_q_heads, num_k_heads, num_v_heads, q_gamma, k_gamma, eps, cos_sin_cache,
                             seq_lens, query_start_loc, slot_mapping, q_out, k_cache, v_cache, stream)
     return PreparedCall(lib.rope_qkv_rmsnorm_rope_cache, args, (tensors, descs), "rope_qkv_rmsnorm_rope_cache")
+
+
+# ---------------------------------------------------------------------------
+# Scaled rotary tables, append to a paged cache, attention over it.  Their
+# descriptors are packed as bytes (a rope_tensor_t is 48 of them), which costs
+# about a third of building ctypes structures.
+# ---------------------------------------------------------------------------
+_PACK = {n: struct.Struct("Pii%dq%dx" % (n, 8 * (4 - n))).pack for n in (1, 2, 3, 4)}
+
+
+def _pack(t: torch.Tensor, dev: int) -> bytes:
+    """The bytes of a ``rope_tensor_t`` of a contiguous tensor on device ``dev``."""
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return _pack_any(t, dev)
+
+
+def _pack_any(t: torch.Tensor, dev: int) -> bytes:
+    code = DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s" % t.dtype)
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor, got one on %s" % t.device)
+    if t.get_device() != dev:
+        raise ValueError("tensors on different devices (cuda:%d and cuda:%d)" % (dev, t.get_device()))
+    shape = t.shape
+    n = len(shape)
+    if not 1 <= n <= 4:
+        raise ValueError("expected 1 to 4 dimensions, got %d" % n)
+    return _PACK[n](t.data_ptr(), code, n, *shape)
+
+
+def _pack_rows(t: torch.Tensor, dev: int):
+    """(bytes, row stride) of a 2-D tensor whose rows may be strided (see rows_desc)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a 2-D tensor with contiguous rows")
+    width = t.shape[1]
+    stride = t.stride(0) if t.shape[0] > 1 else width
+    if stride < width:
+        raise ValueError("rows overlap: row stride %d is below the row width %d" % (stride, width))
+    return _pack_any(t, dev), stride
+
+
+SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "wavelength": 4, "factors": 5}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[dict] = None):
+    """``(inv_freq, scale)``: the rotary_dim / 2 frequencies (a float64 CPU
+    tensor, radians per position) and the factor of cos and sin, changed for
+    long contexts as ``scaling`` says.
+
+    ``scaling`` is None or a dict with ``kind`` one of "none", "linear", "base",
+    "yarn", "wavelength", "factors" and that kind's ``factor``,
+    ``original_length``, ``low``, ``high``, ``attention`` and ``factors``; the
+    formulas are those of ``rope_scaled_frequencies`` in the C header."""
+    lib = load()
+    what = "rope_scaled_frequencies"
+    s = keep = None
+    if scaling is not None:
+        unknown = set(scaling) - {"kind", "factor", "original_length", "low", "high", "attention", "factors"}
+        if unknown or scaling.get("kind") not in SCALINGS:
+            raise RopeError(ROPE_ERR_PARAM_INVALID, "%s: scaling %r" % (what, scaling))
+        s = RopeScaling(SCALINGS[scaling["kind"]], *[float(scaling.get(k, 0.0)) for k in (
+            "factor", "original_length", "low", "high", "attention")])
+        if scaling.get("factors") is not None:
+            if len(scaling["factors"]) != rotary_dim // 2:
+                raise RopeError(ROPE_ERR_PARAM_INVALID, "%s: %d factors for %d frequencies"
+                                % (what, len(scaling["factors"]), rotary_dim // 2))
+            keep = (ctypes.c_double * len(scaling["factors"]))(*[float(v) for v in scaling["factors"]])
+            s.factors = ctypes.cast(keep, ctypes.POINTER(ctypes.c_double))
+    inv = torch.empty(max(1, int(rotary_dim) // 2), dtype=torch.float64)
+    scale = ctypes.c_double(0.0)
+    st = lib.rope_scaled_frequencies(int(rotary_dim), float(base), ctypes.byref(s) if s is not None else None,
+                                     ctypes.cast(inv.data_ptr(), ctypes.POINTER(ctypes.c_double)),
+                                     ctypes.byref(scale))
+    if st != ROPE_OK:
+        raise RopeError(st, what)
+    return inv, scale.value
+
+
+def _host_frequencies(inv_freq) -> torch.Tensor:
+    if not isinstance(inv_freq, torch.Tensor):
+        return torch.tensor(list(inv_freq), dtype=torch.float64)
+    if inv_freq.is_cuda:
+        raise ValueError("expected frequencies on the host, got a tensor on %s" % inv_freq.device)
+    return inv_freq.to(torch.float64).contiguous()
+
+
+def scaled_cos_sin_cache(cache: torch.Tensor, inv_freq, scale: float = 1.0, *,
+                         positions: Optional[torch.Tensor] = None, first_position: int = 0, stream=None) -> None:
+    """Writes ``cache`` [rows, 2F], the cos/sin table of the cache-indexed
+    operators: row r is position ``first_position + (positions[r] or r)``, cos in
+    the first half and sin in the second, times ``scale``.  ``inv_freq`` holds the
+    F frequencies on the host (see :func:`rope_frequencies`)."""
+    lib = load()
+    f = _host_frequencies(inv_freq)
+    dev = cache.get_device()
+    args = (f.data_ptr() or None, f.numel(), float(scale), None if positions is None else _pack(positions, dev),
+            int(first_position), _pack(cache, dev), _stream_handle(cache, stream))
+    _run(lib.rope_scaled_cos_sin_cache, args, (cache, f, positions), "rope_scaled_cos_sin_cache")
+
+
+def scaled_cos_sin(cos: torch.Tensor, sin: torch.Tensor, inv_freq, scale: float = 1.0, rotary_mode=1, *,
+                   positions: Optional[torch.Tensor] = None, first_position: int = 0, stream=None) -> None:
+    """Writes ``cos`` and ``sin`` [..., 2F] as the in-place operator reads them
+    (e.g. [1, S, 1, 2F]), in the element order of ``rotary_mode``; rows and
+    positions as in :func:`scaled_cos_sin_cache`."""
+    lib = load()
+    f = _host_frequencies(inv_freq)
+    dev = cos.get_device()
+    args = (f.data_ptr() or None, f.numel(), float(scale), None if positions is None else _pack(positions, dev),
+            int(first_position), _mode(rotary_mode), _pack(cos, dev), _pack(sin, dev), _stream_handle(cos, stream))
+    _run(lib.rope_scaled_cos_sin, args, (cos, f, positions), "rope_scaled_cos_sin")
+
+
+def _append_args(positions, query, key, value, cos_sin_cache, slot_mapping, k_cache, v_cache, head_size, rotary_dim,
+                 is_neox, mrope_section, stream, cache_mode, query_out):
+    lib = load()
+    dev = key.get_device()
+    dq, qs = (None, 0) if query is None else _pack_rows(query, dev)
+    dk, ks = _pack_rows(key, dev)
+    dv, vs = _pack_rows(value, dev)
+    sec, n_sec = None, 0
+    if mrope_section is not None:
+        n_sec = len(mrope_section)
+        sec = (ctypes.c_int64 * max(1, n_sec))(*[int(v) for v in mrope_section])
+    args = (_pack(positions, dev), dq, dk, dv, _pack(cos_sin_cache, dev), _pack(slot_mapping, dev),
+            None if query_out is None else _pack(query_out, dev), _pack(k_cache, dev), _pack(v_cache, dev),
+            int(head_size), int(cos_sin_cache.shape[1]) if rotary_dim is None else int(rotary_dim),
+            1 if is_neox else 0, sec, n_sec, int(cache_mode), qs, ks, vs, _stream_handle(key, stream))
+    return (lib.rope_append_paged_kv, args, (key, query, value, positions, cos_sin_cache, slot_mapping, query_out,
+                                             k_cache, v_cache, sec), "rope_append_paged_kv")
+
+
+def append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tensor], key: torch.Tensor, value: torch.Tensor,
+                    cos_sin_cache: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, head_size: int, rotary_dim: Optional[int] = None, is_neox: bool = True,
+                    mrope_section: Optional[Sequence[int]] = None, stream=None, *, cache_mode: int = 0,
+                    query_out: Optional[torch.Tensor] = None) -> None:
+    """RoPE of ``query`` and ``key``; query to ``query_out`` (None: in place),
+    key and value to their slots of the paged caches [blocks, heads, block
+    size, head_size] (see the C header).  ``query``, ``key`` and ``value`` may be
+    column ranges of one fused buffer; the slots >= 0 of a call are distinct."""
+    _run(*_append_args(positions, query, key, value, cos_sin_cache, slot_mapping, k_cache, v_cache, head_size,
+                       rotary_dim, is_neox, mrope_section, stream, cache_mode, query_out))
+
+
+def prepare_append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tensor], key: torch.Tensor,
+                            value: torch.Tensor, cos_sin_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                            k_cache: torch.Tensor, v_cache: torch.Tensor, head_size: int,
+                            rotary_dim: Optional[int] = None, is_neox: bool = True,
+                            mrope_section: Optional[Sequence[int]] = None, stream=None, *, cache_mode: int = 0,
+                            query_out: Optional[torch.Tensor] = None) -> "PreparedCall":
+    """:func:`append_paged_kv` with its arguments marshalled once."""
+    return PreparedCall(*_append_args(positions, query, key, value, cos_sin_cache, slot_mapping, k_cache, v_cache,
+                                      head_size, rotary_dim, is_neox, mrope_section, stream, cache_mode, query_out))
+
+
+def paged_attention_workspace(query: torch.Tensor, k_cache: torch.Tensor, prefix_len: int = 0) -> int:
+    """Bytes of workspace that :func:`paged_attention` needs for these tensors."""
+    code = DTYPE_CODE.get(query.dtype)
+    if code is None or k_cache.dim() != 4 or query.dim() != 2:
+        raise RopeError(ROPE_ERR_PARAM_INVALID, "rope_paged_attention_workspace")
+    _, nk, _, d = k_cache.shape
+    n = ctypes.c_int64(0)
+    st = _on_device(query.get_device(), load().rope_paged_attention_workspace,
+                    (query.shape[0], query.shape[1] // max(1, d), nk, d, code, int(prefix_len), ctypes.byref(n)))
+    if st != ROPE_OK:
+        raise RopeError(st, "rope_paged_attention_workspace")
+    return n.value
+
+
+def _new_workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+    """A workspace whose memory belongs to the stream that the call runs on, so
+    that it is not handed out again while the call still uses it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def _attend_args(query, k_cache, v_cache, block_table, seq_lens, query_start_loc, out, scale, prefix_blocks,
+                 prefix_len, lse, workspace, stream):
+    lib = load()
+    dev = query.get_device()
+    dq, qs = _pack_rows(query, dev)
+    dk, dv = _pack(k_cache, dev), _pack(v_cache, dev)
+    handle = _stream_handle(query, stream)
+    if workspace is None:
+        workspace = _new_workspace(paged_attention_workspace(query, k_cache, prefix_len), query, stream)
+    elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("expected a contiguous workspace on cuda:%d" % dev)
+    args = (dq, qs, dk, dv, _pack(block_table, dev), _pack(seq_lens, dev), _pack(query_start_loc, dev),
+            None if prefix_blocks is None else _pack(prefix_blocks, dev), int(prefix_len),
+            float(k_cache.shape[3]) ** -0.5 if scale is None else float(scale), _pack(out, dev),
+            None if lse is None else _pack(lse, dev), workspace.data_ptr() or None,
+            workspace.numel() * workspace.element_size(), handle)
+    return (lib.rope_paged_attention, args, (query, k_cache, v_cache, block_table, seq_lens, query_start_loc,
+                                             prefix_blocks, out, lse, workspace), "rope_paged_attention")
+
+
+def paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    seq_lens: torch.Tensor, query_start_loc: torch.Tensor, out: torch.Tensor, *,
+                    scale: Optional[float] = None, prefix_blocks: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Causal attention of the batch's new tokens ``query`` [T, Nq*D] over the
+    paged caches [blocks, Nk, block size, D] into ``out`` (see the C header).
+
+    ``seq_lens`` counts each sequence's tokens with the shared prefix and this
+    call's; ``block_table`` [B, W] holds the pages after the prefix,
+    ``prefix_blocks`` those of the ``prefix_len`` tokens that all sequences
+    share.  ``scale`` defaults to D ** -0.5; ``lse`` [T, Nq] (float32) receives
+    each row's log-sum-exp.  Without ``workspace`` one is allocated for the call
+    on its stream."""
+    _run(*_attend_args(query, k_cache, v_cache, block_table, seq_lens, query_start_loc, out, scale, prefix_blocks,
+                       prefix_len, lse, workspace, stream))
+
+
+def prepare_paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                            block_table: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                            out: torch.Tensor, *, scale: Optional[float] = None,
+                            prefix_blocks: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                            lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None) -> "PreparedCall":
+    """:func:`paged_attention` with its arguments marshalled once (and its
+    workspace, given or allocated here, kept with them)."""
+    return PreparedCall(*_attend_args(query, k_cache, v_cache, block_table, seq_lens, query_start_loc, out, scale,
+                                      prefix_blocks, prefix_len, lse, workspace, stream))
 
 
 def get_device_error(stream=None, device=None) -> int:

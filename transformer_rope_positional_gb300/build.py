@@ -31,10 +31,11 @@ LIB_PATH = os.path.join(LIB_DIR, "librope_gb300.so")
 DEBUG_LIB_PATH = os.path.join(LIB_DIR, "librope_gb300_debug.so")
 
 SOURCES = ["rope_api.cu", "rope_launch.cu", "rope_inplace_fwd.cu", "rope_inplace_bwd.cu", "rope_cache.cu",
-           "rope_qkv.cu"]
-HEADERS = ["rope_device.cuh", "rope_launch.h", "rope_inplace.cuh"]
+           "rope_qkv.cu", "serving/rope_table.cu", "serving/rope_append.cu", "serving/rope_attend.cu"]
+HEADERS = ["rope_device.cuh", "rope_launch.h", "rope_inplace.cuh", "serving/serving.h",
+           "serving/rope_attend.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
+NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
 def nvcc() -> str:
@@ -83,7 +84,7 @@ def _build_locked(lib_path: str, verbose: bool, debug: bool) -> str:
     extra = (["-Xptxas", "-v"] if verbose else []) + (["-DROPE_DEBUG_BOUNDS"] if debug else [])
 
     def compile_one(src):
-        obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(build_dir, os.path.splitext(os.path.basename(src))[0] + ".o")
         cmd = [cc, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
