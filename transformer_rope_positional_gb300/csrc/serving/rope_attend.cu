@@ -4,11 +4,21 @@
 //   s_j = scale <q, k_j>,  m = max s_j,  l = sum e^(s_j - m),  o = sum e^(s_j - m) v_j / l,
 // in one pass over the keys with a running m, l and o (o and l are multiplied by
 // e^(m_old - m_new) when the maximum grows).  Base-2 exponentials of scale * log2(e) * <q, k>.
+// Partial results over key ranges are joined by
+//   m = max m_s,  l = sum l_s e^(m_s - m),  o = sum o_s e^(m_s - m) / l.
+//
+// 16-bit data takes the unit kernels (rope_attend_mma.cuh), then a kernel that joins partial
+// results; other calls a kernel with one warp per query row.
+//
+// A shared prefix has a launch of its own when a sequence's rows fill less than a unit: the
+// rows of all sequences together fill the units of that launch, so the prefix is read once
+// for the batch instead of once a sequence.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
 
 #include "rope_attend.cuh"
+#include "rope_attend_mma.cuh"
 
 namespace rope {
 namespace {
@@ -17,91 +27,135 @@ using namespace attend;
 
 constexpr int kWarps = 4;
 
-// One warp per query row: lane i holds the row's elements i, i + 32, ..., and the warp walks
-// the keys in groups of four.
+// One warp per query row.
 template <typename T, int E>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_rows_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
                        float* __restrict__ lse, Pointers g, AttendArgs a) {
-  constexpr int KU = 4;
-  const int lane = threadIdx.x & 31;
   wait_for_prior_grid();
   const int64_t rows = a.T * a.nq;
   const int64_t tokens = ldg(g.qsl + a.B, a.qsl_span, g.err);
   for (int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * kWarps) {
     const int64_t t = row / a.nq;
     if (t >= tokens) break;
+    attend_row<T, E>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
+  }
+}
+
+// Joins the partial results of a row's units (own keys, and the prefix's where it had its own
+// launch), one warp per row; a row whose result is not finite is computed again key by key:
+// a key that a row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of
+// its value would leave NaN.  A warp takes per_warp consecutive rows and looks at their
+// records first, so that rows already finished cost one load for 32 of them.
+template <typename T, int E>
+__global__ void __launch_bounds__(kWarps * 32)
+    attend_join_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
+                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut own, Cut pre, int own_grid, int pre_grid,
+                       int per_warp) {
+  wait_for_prior_grid();
+  const int lane = threadIdx.x & 31;
+  const int64_t tokens = min(ldg(g.qsl + a.B, a.qsl_span, g.err), a.T);
+  const int64_t rows = tokens * a.nq;
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
+  const bool shared = own.shared != 0;
+  int2 mine = make_int2(0, 0), mine_pre = make_int2(0, 0);
+  if (lane < per_warp && first + lane < rows) {
+    mine = own.rec[first + lane];
+    if (shared) mine_pre = pre.rec[first + lane];
+  }
+  const bool todo = lane < per_warp && first + lane < rows && (shared || mine.x < 0 || mine.x != mine.y);
+  uint32_t left = __ballot_sync(0xffffffffu, todo);
+  while (left) {
+    const int i = __ffs(left) - 1;
+    left &= left - 1;
+    const int64_t row = first + i;
+    const int64_t t = row / a.nq;
     const int h = (int)(row - t * a.nq);
-    const int kh = h / a.G;
-    const int64_t b = batch_of(t, g, a);
-    const int64_t end = ldg(g.qsl + b + 1, a.qsl_span, g.err);
-    const int64_t len = ldg(g.seq_lens + b, a.sl_span, g.err);
-    const int64_t most = (int64_t)a.P + a.W * a.block_size;
-    if (len > most && lane == 0) atomicOr(g.err, kSlotOutOfRange);
-    const int64_t seen64 = len - (end - t) + 1;  // keys the row sees
-    const int seen = (int)(seen64 < 0 ? 0 : seen64 > most ? most : seen64);
-    const int64_t* table = g.block_table + b * a.W;
-    float qv[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = lane + 32 * e;
-      o[e] = 0.f;
-      qv[e] = d < a.D ? widen(ldg(q + t * a.q_stride + (int64_t)h * a.D + d, a.q_span, g.err)) * a.scale_log2 : 0.f;
-    }
+    const int c0 = __shfl_sync(0xffffffffu, mine.x, i), c1 = __shfl_sync(0xffffffffu, mine.y, i);
+    const int p0 = __shfl_sync(0xffffffffu, mine_pre.x, i), p1 = __shfl_sync(0xffffffffu, mine_pre.y, i);
+    bool known = c0 >= 0 && c1 >= c0 && c1 < own_grid && p0 >= 0 && p1 >= p0 && (!shared || p1 < pre_grid);
     float m = -INFINITY, l = 0.f;
-    for (int j0 = 0; j0 < seen; j0 += KU) {
-      int64_t at[KU];
-      float s[KU];
+    float2 o[E];
 #pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        const int64_t r = j0 + u < seen ? key_row(j0 + u, table, g, a) : -1;
-        if (r < 0 && j0 + u < seen && lane == 0) atomicOr(g.err, kSlotOutOfRange);
-        at[u] = r < 0 ? -1 : (r + (int64_t)kh * a.block_size) * a.D;
-        s[u] = 0.f;
-      }
+    for (int e = 0; e < E; ++e) o[e] = make_float2(0.f, 0.f);
+    if (known) {
+      // sources 0 .. n_pre - 1: the prefix's parts, then the own keys' parts
+      const int n_pre = shared ? p1 - p0 + 1 : 0, n = n_pre + c1 - c0 + 1;
+      const int64_t b = batch_of(t, g, a);
+      const int gh = h % a.G;
+      const int at_own = (int)(((t - ldg(g.qsl + b, a.qsl_span, g.err)) * a.G + gh) % own.M);
+      const int at_pre = shared ? (int)((t * a.G + gh) % pre.M) : 0;
+      auto source = [&](int s, const float*& so, const float*& sml) {
+        const bool is_pre = s < n_pre;
+        const Cut& c = is_pre ? pre : own;
+        const int first_cta = is_pre ? p0 : c0, last_cta = is_pre ? p1 : c1, at = is_pre ? at_pre : at_own;
+        if (first_cta == last_cta) {
+          so = c.dense + row * a.D;
+          sml = c.dense + a.T * a.nq * a.D + row * 2;
+        } else {
+          const int cta = first_cta + (is_pre ? s : s - n_pre);
+          const int slot = cta == first_cta ? 1 : 0;
+          so = slot_o(c, a, cta, slot) + (int64_t)at * a.D;
+          sml = slot_ml(c, a, is_pre ? pre_grid : own_grid, cta, slot) + at * 2;
+        }
+      };
+      for (int s0 = 0; s0 < n; s0 += 32) {
+        float ms = -INFINITY, ls = 0.f;
+        if (s0 + lane < n) {
+          const float *so, *sml;
+          source(s0 + lane, so, sml);
+          const float2 v = *reinterpret_cast<const float2*>(sml);
+          ms = v.x;
+          ls = v.y;
+        }
+        float top = fmaxf(m, ms);
 #pragma unroll
-      for (int u = 0; u < KU; ++u)
-        if (at[u] >= 0) {
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float base = top == -INFINITY ? 0.f : top;
+        const float keep = fast_exp2(m - base);
+        const float ws = s0 + lane < n ? fast_exp2(ms - base) : 0.f;
+        float add = ls * ws;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) add += __shfl_xor_sync(0xffffffffu, add, d);
+        l = l * keep + add;
+        m = top;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = make_float2(o[e].x * keep, o[e].y * keep);
+        const int k = min(32, n - s0);
+#pragma unroll 4
+        for (int s = 0; s < k; ++s) {
+          const float f = __shfl_sync(0xffffffffu, ws, s);
+          const float *so, *sml;
+          source(s0 + s, so, sml);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const int d = lane + 32 * e;
-            if (d < a.D) s[u] = fmaf(qv[e], widen(ldg(kc + at[u] + d, a.k_span, g.err)), s[u]);
+            const int d = lane * 2 + 64 * e;
+            if (d < a.D) {
+              const float2 v = *reinterpret_cast<const float2*>(so + d);
+              o[e].x = fmaf(f, v.x, o[e].x);
+              o[e].y = fmaf(f, v.y, o[e].y);
+            }
           }
         }
-#pragma unroll
-      for (int sh = 16; sh > 0; sh /= 2)
-#pragma unroll
-        for (int u = 0; u < KU; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], sh);
-      float top = m;
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        if (at[u] < 0) s[u] = -INFINITY;
-        top = s[u] != s[u] ? s[u] : fmaxf(top, s[u]);
       }
-      const float base = top == -INFINITY ? 0.f : top;  // no key seen yet: every weight is e^(-inf - 0) = 0
-      const float keep = exp2f(m - base);
-      l *= keep;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool fine = l <= FLT_MAX;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= keep;
-#pragma unroll
-      for (int u = 0; u < KU; ++u) {
-        if (at[u] < 0) continue;
-        const float w = exp2f(s[u] - base);
-        l += w;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int d = lane + 32 * e;
-          if (d < a.D) o[e] = fmaf(w, widen(ldg(vc + at[u] + d, a.v_span, g.err)), o[e]);
-        }
+      for (int e = 0; e < E; ++e) {
+        o[e] = l == 0.f ? make_float2(0.f, 0.f) : make_float2(o[e].x * inv, o[e].y * inv);
+        fine = fine && fabsf(o[e].x) <= FLT_MAX && fabsf(o[e].y) <= FLT_MAX;
       }
-      m = top;
+      known = __all_sync(0xffffffffu, fine);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (!known) {
+      attend_row<T, 2 * E>(t, h, q, kc, vc, out, lse, g, a);
+      continue;
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int d = lane + 32 * e;
+      const int d = lane * 2 + 64 * e;
       T* p = out + row * a.D + d;
-      if (d < a.D && access_ok(p, sizeof(T), a.out_span, g.err)) *p = narrow<T>(l == 0.f ? 0.f : o[e] * inv);
+      if (d < a.D && access_ok(p, 2 * sizeof(T), a.out_span, g.err)) narrow2(p, o[e]);
     }
     if (lse && lane == 0 && access_ok(lse + row, 4, a.lse_span, g.err))
       lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
@@ -116,6 +170,110 @@ cudaError_t launch_rows(const AttendProblem& p, const Pointers& g, const AttendA
   return launch_overlapped(kernel, (unsigned)grid, kWarps * 32, stream, static_cast<const T*>(p.query),
                            static_cast<const T*>(p.k_cache), static_cast<const T*>(p.v_cache),
                            static_cast<T*>(p.out), p.lse, g, a);
+}
+
+// ---------------------------------------------------------------------------
+// The 16-bit path: sizes of its workspace, and its launches.
+// ---------------------------------------------------------------------------
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+int padded_columns(int64_t D) { return (int)round_up(D, 64); }
+
+// One launch's part of the workspace.
+struct Part {
+  int64_t rec, slots, dense, bytes;  // offsets, and all of it
+  int64_t slot_rows;
+};
+
+Part part_of(int64_t T, int64_t nq, int64_t nk, int64_t D, int64_t M, int64_t grid, bool shared) {
+  Part s;
+  s.slot_rows = std::min(M, round_up(T * (nq / nk), 16));
+  s.rec = 0;
+  s.slots = round_up(T * nq * 8, 256);
+  s.dense = s.slots + round_up(grid * 2 * s.slot_rows * (D + 2) * 4, 256);
+  s.bytes = s.dense + (shared ? round_up(T * nq * (D + 2) * 4, 256) : 0);
+  return s;
+}
+
+int64_t mma_grid(int64_t D) { return (int64_t)sm_count() * (padded_columns(D) <= 192 ? 2 : 1); }
+
+bool tensor_path(int32_t dtype, int64_t D) { return dtype != kF32 && D <= 256; }
+
+Cut cut_of(const Part& s, char* at, int64_t M, int64_t KT) {
+  Cut c;
+  c.M = (int32_t)M;
+  c.KT = (int32_t)KT;
+  c.lo = 0;
+  c.prefix = 0;
+  c.shared = 0;
+  c.min_share = 2;
+  c.slot_rows = (int32_t)s.slot_rows;
+  c.rec = reinterpret_cast<int2*>(at + s.rec);
+  c.slots = reinterpret_cast<float*>(at + s.slots);
+  c.dense = reinterpret_cast<float*>(at + s.dense);
+  return c;
+}
+
+template <typename T, int DP>
+cudaError_t launch_mma(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
+                       cudaStream_t stream) {
+  auto kernel = attend_mma_kernel<T, DP>;
+  const size_t smem = sizeof(MmaShared<DP>);
+  const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped_smem(kernel, (unsigned)grid, kMmaThreads, smem, stream, static_cast<const T*>(p.query),
+                                static_cast<const T*>(p.k_cache), static_cast<const T*>(p.v_cache),
+                                static_cast<T*>(p.out), p.lse, g, a, c);
+}
+
+template <typename T>
+cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
+                         cudaStream_t stream) {
+  switch (padded_columns(p.D)) {
+    case 64:
+      return launch_mma<T, 64>(p, g, a, c, grid, stream);
+    case 128:
+      return launch_mma<T, 128>(p, g, a, c, grid, stream);
+    case 192:
+      return launch_mma<T, 192>(p, g, a, c, grid, stream);
+    default:
+      return launch_mma<T, 256>(p, g, a, c, grid, stream);
+  }
+}
+
+template <typename T, int E>
+cudaError_t launch_join(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& own, const Cut& pre,
+                        int64_t own_grid, int64_t pre_grid, cudaStream_t stream) {
+  const int64_t rows = p.T * p.nq;
+  const int64_t warps = (int64_t)sm_count() * 16;
+  const int per_warp = (int)std::min<int64_t>(32, (rows + warps - 1) / warps);
+  const int64_t grid = (rows + (int64_t)per_warp * kWarps - 1) / ((int64_t)per_warp * kWarps);
+  return launch_overlapped(attend_join_kernel<T, E>, (unsigned)grid, kWarps * 32, stream,
+                           static_cast<const T*>(p.query), static_cast<const T*>(p.k_cache),
+                           static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, own, pre,
+                           (int)own_grid, (int)pre_grid, per_warp);
+}
+
+template <typename T>
+cudaError_t launch_tensor(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
+  const bool shared = p.prefix_len > 0;
+  const int64_t grid = mma_grid(p.D);
+  const Part s = part_of(p.T, p.nq, p.nk, p.D, kMmaRows, grid, shared);
+  char* const ws = static_cast<char*>(p.workspace);
+  Cut own = cut_of(s, ws, kMmaRows, kMmaKeys), pre = own;
+  if (shared) {
+    own.shared = 1;
+    own.lo = a.P;
+    pre = cut_of(s, ws + s.bytes, kMmaRows, kMmaKeys);
+    pre.shared = pre.prefix = 1;
+    const cudaError_t e = launch_units<T>(p, g, a, pre, grid, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = launch_units<T>(p, g, a, own, grid, stream);
+  if (e != cudaSuccess) return e;
+  if (p.D <= 64) return launch_join<T, 1>(p, g, a, own, pre, grid, grid, stream);
+  if (p.D <= 128) return launch_join<T, 2>(p, g, a, own, pre, grid, grid, stream);
+  return launch_join<T, 4>(p, g, a, own, pre, grid, grid, stream);
 }
 
 template <typename T>
@@ -153,6 +311,9 @@ cudaError_t launch_typed(const AttendProblem& p, cudaStream_t stream) {
   g.prefix_blocks = p.prefix_blocks;
   const cudaError_t er = device_error_address(&g.err);
   if (er != cudaSuccess) return er;
+  if constexpr (sizeof(T) == 2) {
+    if (tensor_path(p.dtype, p.D)) return launch_tensor<T>(p, g, a, stream);
+  }
   if (p.D <= 64) return launch_rows<T, 2>(p, g, a, stream);
   if (p.D <= 128) return launch_rows<T, 4>(p, g, a, stream);
   if (p.D <= 256) return launch_rows<T, 8>(p, g, a, stream);
@@ -162,8 +323,10 @@ cudaError_t launch_typed(const AttendProblem& p, cudaStream_t stream) {
 }  // namespace
 
 int64_t attend_workspace(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, int64_t prefix_len) {
-  (void)T, (void)nq, (void)nk, (void)D, (void)dtype, (void)prefix_len;
-  return 256;
+  if (!tensor_path(dtype, D)) return 256;
+  const bool shared = prefix_len > 0;
+  const Part s = part_of(T, nq, nk, D, kMmaRows, mma_grid(D), shared);
+  return std::max<int64_t>(256, s.bytes * (shared ? 2 : 1));
 }
 
 cudaError_t launch_attend(const AttendProblem& p, cudaStream_t stream) {

@@ -2,6 +2,8 @@
 // key of a sequence sits in the paged cache.
 #pragma once
 
+#include <cmath>
+
 #include "rope_device.cuh"
 #include "serving.h"
 
@@ -64,6 +66,313 @@ __device__ __forceinline__ int64_t key_row(int j, const int64_t* table, const Po
   }
   if (page < 0 || page >= a.num_blocks) return -1;
   return page * a.nk * a.block_size + j;
+}
+
+// ---------------------------------------------------------------------------
+// How the work is cut.  A unit is a tile of M query rows of one sequence and key head (row r
+// of a sequence is token r / G, head r % G of the key head's group) with the keys they see;
+// or, in the launch over a shared prefix, a tile of M rows of the whole batch with the
+// prefix's keys.  A unit's work is its number of key tiles.  All units' tiles, one after the
+// other, are cut into equal shares, one per CTA of the grid, so a unit may be finished by
+// several CTAs; each leaves its rows' partial (m, l, O) in one of its two slots (slot 1: the
+// unit begins in this CTA, slot 0: it began in an earlier one), and the joining kernel adds
+// them up in order.  Every CTA finds its share by itself from the lengths on the device:
+// the cut needs no host copy of them and no extra launch.
+// ---------------------------------------------------------------------------
+struct Cut {
+  int32_t M, KT;      // rows of a unit, keys of a tile
+  int32_t lo;         // first key of the launch: P when the prefix has its own launch, else 0
+  int32_t prefix;     // this launch is over the shared prefix: units of the whole batch, keys [0, P)
+  int32_t shared;     // another launch covers the other keys: nothing is final here
+  int32_t min_share;  // fewest tiles a CTA takes
+  int32_t slot_rows;  // rows of a partial slot
+  int2* rec;          // [T * nq]: first and last CTA of the row's unit, or (-1, -1): recompute
+  float* slots;       // [grid][2][slot_rows][D] O, then [grid][2][slot_rows][2] m, l
+  float* dense;       // shared: [T * nq][D] O, then [T * nq][2] m, l, of units that one CTA finished
+};
+
+// Rows and keys of one sequence (or of the whole batch).
+struct SeqWork {
+  int64_t t0;       // first token
+  int64_t rows;     // n * G
+  int64_t pos0;     // position of token t0 (may be negative)
+  int32_t hi;       // keys end here (clamped to the pages)
+};
+
+__device__ __forceinline__ SeqWork seq_work(int64_t b, const Pointers& g, const AttendArgs& a, const Cut& c) {
+  SeqWork s;
+  if (c.prefix) {
+    s.t0 = 0;
+    const int64_t n = ldg(g.qsl + a.B, a.qsl_span, g.err);
+    s.rows = (n < 0 ? 0 : n > a.T ? a.T : n) * a.G;
+    s.pos0 = a.P;
+    s.hi = a.P;
+    return s;
+  }
+  int64_t t0 = ldg(g.qsl + b, a.qsl_span, g.err), t1 = ldg(g.qsl + b + 1, a.qsl_span, g.err);
+  const int64_t len = ldg(g.seq_lens + b, a.sl_span, g.err);
+  t0 = t0 < 0 ? 0 : t0;
+  t1 = t1 > a.T ? a.T : t1;
+  const int64_t n = t1 > t0 ? t1 - t0 : 0;
+  const int64_t most = (int64_t)a.P + a.W * a.block_size;
+  if (len > most && n > 0) atomicOr(g.err, kSlotOutOfRange);  // more tokens than pages
+  s.t0 = t0;
+  s.rows = n * a.G;
+  s.pos0 = len - n;
+  s.hi = (int)(len < 0 ? 0 : len > most ? most : len);
+  return s;
+}
+
+// Keys [lo, end) that the rows of tile i of a sequence see between them.
+__device__ __forceinline__ int tile_end(const SeqWork& s, int64_t i, const AttendArgs& a, const Cut& c) {
+  if (c.prefix) return s.hi;
+  const int64_t last = (min((i + 1) * c.M, s.rows) - 1) / a.G;  // last token of the tile
+  const int64_t e = s.pos0 + last + 1;
+  return (int)(e < c.lo ? c.lo : e > s.hi ? max(s.hi, c.lo) : e);
+}
+
+__device__ __forceinline__ int tile_work(const SeqWork& s, int64_t i, const AttendArgs& a, const Cut& c) {
+  const int keys = tile_end(s, i, a, c) - c.lo;
+  return keys <= c.KT ? 1 : (keys + c.KT - 1) / c.KT;  // a unit without keys is one (empty) tile
+}
+
+__device__ __forceinline__ int64_t row_tiles(const SeqWork& s, const Cut& c) { return (s.rows + c.M - 1) / c.M; }
+
+__device__ __forceinline__ int64_t seq_total(const SeqWork& s, const AttendArgs& a, const Cut& c) {
+  const int64_t tiles = row_tiles(s, c);
+  if (c.prefix) return tiles * tile_work(s, 0, a, c) * a.nk;
+  int64_t sum = 0;
+  for (int64_t i = 0; i < tiles; ++i) sum += tile_work(s, i, a, c);
+  return sum * a.nk;
+}
+
+// Walk over the units of this CTA's share.
+struct Walk {
+  int64_t b;       // sequence
+  SeqWork s;
+  int64_t tiles;   // row tiles of the sequence
+  int64_t i;       // row tile
+  int32_t h;       // key head
+  int32_t work;    // key tiles of the unit
+  int32_t k0;      // first key tile of the unit in this CTA
+  int64_t at;      // global tile index of (this unit, tile k0)
+  int64_t end;     // end of this CTA's share
+  int64_t share;
+  bool done;
+};
+
+// Sum over the CTA's NT threads and the exclusive prefix of each, through shared memory
+// (`tmp`: NT / 32 + 1 values).  Ends with a barrier.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* before) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) tmp[w] = x;
+  __syncthreads();
+  int64_t off = 0, total = 0;
+#pragma unroll
+  for (int j = 0; j < NT / 32; ++j) {
+    if (j < w) off += tmp[j];
+    total += tmp[j];
+  }
+  __syncthreads();
+  *before = off + x - v;
+  return total;
+}
+
+// Finds this CTA's share.  All NT threads call it; `tmp` holds NT / 32 + 2 values.
+template <int NT>
+__device__ __forceinline__ Walk find_share(const Pointers& g, const AttendArgs& a, const Cut& c, int64_t* tmp) {
+  Walk w;
+  const int64_t nb = c.prefix ? 1 : a.B;
+  int64_t total = 0, before = 0, mine = 0;
+  for (int64_t base = 0; base < nb; base += NT) {
+    const int64_t b = base + threadIdx.x;
+    mine = b < nb ? seq_total(seq_work(b, g, a, c), a, c) : 0;
+    total += block_scan<NT>(mine, tmp, &before);
+  }
+  w.share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)c.min_share);
+  w.at = w.share * blockIdx.x;
+  w.end = min(w.at + w.share, total);
+  w.done = w.at >= total;
+  if (w.done) return w;
+  int64_t run = 0;
+  for (int64_t base = 0; base < nb; base += NT) {
+    const int64_t b = base + threadIdx.x;
+    if (nb > NT) mine = b < nb ? seq_total(seq_work(b, g, a, c), a, c) : 0;
+    const int64_t sum = nb > NT ? block_scan<NT>(mine, tmp, &before) : total;
+    if (run + before <= w.at && w.at < run + before + mine) {
+      tmp[0] = b;
+      tmp[1] = w.at - run - before;
+    }
+    run += sum;
+    if (run > w.at) break;
+  }
+  __syncthreads();
+  w.b = tmp[0];
+  int64_t rest = tmp[1];
+  __syncthreads();
+  w.s = seq_work(w.b, g, a, c);
+  w.tiles = row_tiles(w.s, c);
+  if (c.prefix) {
+    w.work = tile_work(w.s, 0, a, c);
+    w.i = rest / ((int64_t)w.work * a.nk);
+    rest -= w.i * w.work * a.nk;
+  } else {
+    w.i = 0;
+    for (;;) {
+      w.work = tile_work(w.s, w.i, a, c);
+      const int64_t row = (int64_t)w.work * a.nk;
+      if (rest < row) break;
+      rest -= row;
+      ++w.i;
+    }
+  }
+  w.h = (int)(rest / w.work);
+  w.k0 = (int)(rest - (int64_t)w.h * w.work);
+  return w;
+}
+
+// Key tiles of the current unit in this CTA end here.
+__device__ __forceinline__ int walk_k1(const Walk& w) { return (int)min((int64_t)w.work, w.k0 + (w.end - w.at)); }
+
+// The next unit of the share; w.done at its end.
+__device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const AttendArgs& a, const Cut& c) {
+  w.at += walk_k1(w) - w.k0;
+  if (w.at >= w.end) {
+    w.done = true;
+    return;
+  }
+  w.k0 = 0;
+  if (++w.h < a.nk) return;
+  w.h = 0;
+  ++w.i;
+  while (w.i >= w.tiles) {
+    w.i = 0;
+    if (++w.b >= (c.prefix ? 1 : a.B)) {  // a share ends before the last sequence does: never, unless the lengths change under way
+      w.done = true;
+      return;
+    }
+    w.s = seq_work(w.b, g, a, c);
+    w.tiles = row_tiles(w.s, c);
+  }
+  w.work = tile_work(w.s, w.i, a, c);
+}
+
+// First and last CTA of the current unit.
+__device__ __forceinline__ int2 walk_ctas(const Walk& w) {
+  const int64_t first = w.at - w.k0;
+  return make_int2((int)(first / w.share), (int)((first + w.work - 1) / w.share));
+}
+
+__device__ __forceinline__ float* slot_o(const Cut& c, const AttendArgs& a, int64_t cta, int slot) {
+  return c.slots + (cta * 2 + slot) * c.slot_rows * a.D;
+}
+
+__device__ __forceinline__ float* slot_ml(const Cut& c, const AttendArgs& a, int64_t grid, int64_t cta, int slot) {
+  return c.slots + grid * 2 * c.slot_rows * a.D + (cta * 2 + slot) * c.slot_rows * 2;
+}
+
+// Keys j < limit are what row r of the current unit's sequence sees (0 past the last row).
+__device__ __forceinline__ int row_limit(const Walk& w, int64_t r, const Pointers& g, const AttendArgs& a, const Cut& c) {
+  if (r >= w.s.rows) return 0;
+  int64_t p;
+  if (c.prefix) {
+    const int64_t t = r / a.G;
+    const int64_t b = batch_of(t, g, a);
+    p = ldg(g.seq_lens + b, a.sl_span, g.err) - (ldg(g.qsl + b + 1, a.qsl_span, g.err) - t) + 1;
+  } else {
+    p = w.s.pos0 + r / a.G + 1;
+  }
+  return (int)(p < 0 ? 0 : p > w.s.hi ? w.s.hi : p);
+}
+
+// One query row by one warp, a key at a time: keys the row does not see are not read at all.
+template <typename T, int E>
+__device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict__ q, const T* __restrict__ kc,
+                                           const T* __restrict__ vc, T* __restrict__ out, float* __restrict__ lse,
+                                           const Pointers& g, const AttendArgs& a) {
+  constexpr int KU = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = t * a.nq + h;
+  const int kh = h / a.G;
+  const int64_t b = batch_of(t, g, a);
+  const int64_t end = ldg(g.qsl + b + 1, a.qsl_span, g.err);
+  const int64_t len = ldg(g.seq_lens + b, a.sl_span, g.err);
+  const int64_t most = (int64_t)a.P + a.W * a.block_size;
+  if (len > most && lane == 0) atomicOr(g.err, kSlotOutOfRange);
+  const int64_t seen64 = len - (end - t) + 1;  // keys the row sees
+  const int seen = (int)(seen64 < 0 ? 0 : seen64 > most ? most : seen64);
+  const int64_t* table = g.block_table + b * a.W;
+  float qv[E], o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = lane + 32 * e;
+    o[e] = 0.f;
+    qv[e] = d < a.D ? widen(ldg(q + t * a.q_stride + (int64_t)h * a.D + d, a.q_span, g.err)) * a.scale_log2 : 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  for (int j0 = 0; j0 < seen; j0 += KU) {
+    int64_t at[KU];
+    float s[KU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const int64_t r = j0 + u < seen ? key_row(j0 + u, table, g, a) : -1;
+      if (r < 0 && j0 + u < seen && lane == 0) atomicOr(g.err, kSlotOutOfRange);
+      at[u] = r < 0 ? -1 : (r + (int64_t)kh * a.block_size) * a.D;
+      s[u] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < KU; ++u)
+      if (at[u] >= 0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int d = lane + 32 * e;
+          if (d < a.D) s[u] = fmaf(qv[e], widen(ldg(kc + at[u] + d, a.k_span, g.err)), s[u]);
+        }
+      }
+#pragma unroll
+    for (int sh = 16; sh > 0; sh /= 2)
+#pragma unroll
+      for (int u = 0; u < KU; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], sh);
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      if (at[u] < 0) s[u] = -INFINITY;
+      top = s[u] != s[u] ? s[u] : fmaxf(top, s[u]);
+    }
+    const float base = top == -INFINITY ? 0.f : top;  // no key seen yet: every weight is e^(-inf - 0) = 0
+    const float keep = exp2f(m - base);
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= keep;
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      if (at[u] < 0) continue;
+      const float w = exp2f(s[u] - base);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int d = lane + 32 * e;
+        if (d < a.D) o[e] = fmaf(w, widen(ldg(vc + at[u] + d, a.v_span, g.err)), o[e]);
+      }
+    }
+    m = top;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = lane + 32 * e;
+    T* p = out + row * a.D + d;
+    if (d < a.D && access_ok(p, sizeof(T), a.out_span, g.err)) *p = narrow<T>(l == 0.f ? 0.f : o[e] * inv);
+  }
+  if (lse && lane == 0 && access_ok(lse + row, 4, a.lse_span, g.err))
+    lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
 }  // namespace attend

@@ -1,0 +1,384 @@
+// Attention units of up to 16 query rows: decoding steps, short drafts.
+//
+// Bound by the cache's bytes: a unit of 16 rows does 32 operations per byte of K and V, far
+// below the matrix units' 280, so the kernel is built to keep loads in flight.
+//  * A CTA's four warps each take 16 keys of every 64-key tile and run on their own: each
+//    copies its keys' K and V rows into its own ring of stages with cp.async (16-byte pieces,
+//    any page size, pages looked up one tile ahead), waits for its own copies only, and keeps
+//    its own running m, l and O; there is no barrier until the unit ends, and the copies of
+//    the next unit are already on their way then.
+//  * Scores and outputs by mma.sync m16n8k16 (the rows pad to 16): the tensor core's newer
+//    instruction wants 64 or 128 rows a tile, and these units have 1 to 16.
+//  * The weights of a score tile are, register for register, the A operand of the product
+//    with V.  They are rounded to the data's type there (half a step relative each, the
+//    sums l taken before); m, l and O stay in binary32.
+#pragma once
+
+#include <type_traits>
+
+#include "rope_attend.cuh"
+
+namespace rope {
+namespace attend {
+
+constexpr int kMmaThreads = 128;
+constexpr int kMmaRows = 16;
+constexpr int kMmaKeys = 64;
+
+template <int DP>
+__host__ __device__ constexpr int mma_stages() {
+  return DP <= 64 ? 5 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
+}
+
+// CTAs per SM: the stages of two fit up to 192 columns.
+template <int DP>
+__host__ __device__ constexpr int mma_ctas() {
+  return DP <= 192 ? 2 : 1;
+}
+
+template <int DP>
+struct MmaShared {
+  static constexpr int kStage = 2 * 16 * DP * 2;  // bytes of K and V of one warp's 16 keys
+  alignas(1024) unsigned char ring[4][mma_stages<DP>()][kStage];
+  alignas(16) unsigned char q[16 * DP * 2];
+  float o[16][DP + 8];
+  float ml[4][16][2];
+  int bad[16];
+  int64_t tmp[kMmaThreads / 32 + 2];
+};
+
+__device__ __forceinline__ unsigned smem_u32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+// 16 bytes, or zeros where !ok.
+__device__ __forceinline__ void cp_async16_or_zero(unsigned dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], unsigned at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], unsigned at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __half>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack2(const __half*, float x, float y) {
+  const __half2 v = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float x, float y) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 2^x, relative error 2^-22 (0 for -infinity).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// DP: D rounded up to a multiple of 64; columns past D are zeros in shared memory.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
+    attend_mma_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
+                      float* __restrict__ lse, Pointers g, AttendArgs a, Cut c) {
+  constexpr int S = mma_stages<DP>();
+  constexpr int CH = DP / 8;   // 16-byte chunks of a row
+  constexpr int KS = DP / 16;  // k steps of the score product
+  constexpr bool kHoldQ = DP <= 128;  // the row tile's A operands stay in registers
+  extern __shared__ __align__(1024) unsigned char raw[];
+  MmaShared<DP>& sm = *reinterpret_cast<MmaShared<DP>*>(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  wait_for_prior_grid();
+  Walk w = find_share<kMmaThreads>(g, a, c, sm.tmp);
+  if (w.done) return;
+
+  // ---- copies: the tiles of the share, in order, into the warp's ring
+  Walk pw = w;
+  int pk = pw.k0;
+  int pend = tile_end(pw.s, pw.i, a, c);
+  int slot = 0;                   // stage of the next copy
+  unsigned char* const ring = sm.ring[warp][0];
+  // cache row of this lane's key (lane & 15) of the next tile, looked up ahead of its copy
+  auto look_up = [&]() -> int64_t {
+    if (pw.done) return -1;
+    const int j = c.lo + pk * kMmaKeys + warp * 16 + (lane & 15);
+    if (j >= pend) return -1;
+    const int64_t r = key_row(j, g.block_table + pw.b * a.W, g, a);
+    if (r < 0) atomicOr(g.err, kSlotOutOfRange);
+    return r < 0 ? -1 : (r + (int64_t)pw.h * a.block_size) * a.D;
+  };
+  int64_t next = look_up();
+  uint32_t valid = 0;  // 16 bits a stage: which keys are there (S * 16 <= 96 bits in valid, valid2, valid3)
+  uint32_t valid_hi = 0, valid_top = 0;
+  auto copy_tile = [&]() {
+    if (!pw.done) {
+      const unsigned dst = smem_u32(ring + slot * MmaShared<DP>::kStage);
+#pragma unroll
+      for (int i = 0; i < 16 * CH / 32; ++i) {
+        const int idx = lane + 32 * i;
+        const int key = idx / CH, ch = idx - key * CH;
+        const int64_t at = __shfl_sync(0xffffffffu, next, key);
+        const bool ok = at >= 0 && ch * 8 < a.D;
+        const T* ks = kc + (ok ? at + ch * 8 : 0);
+        const T* vs = vc + (ok ? at + ch * 8 : 0);
+        const unsigned to = dst + key * (DP * 2) + ((ch ^ (key & 7)) << 4);
+        cp_async16_or_zero(to, ks, ok && access_ok(ks, 16, a.k_span, g.err));
+        cp_async16_or_zero(to + 16 * DP * 2, vs, ok && access_ok(vs, 16, a.v_span, g.err));
+      }
+      const uint32_t there = __ballot_sync(0xffffffffu, next >= 0) & 0xffffu;
+      uint32_t& word = slot < 2 ? valid : slot < 4 ? valid_hi : valid_top;
+      word = slot & 1 ? (word & 0x0000ffffu) | (there << 16) : (word & 0xffff0000u) | there;
+      if (++pk == walk_k1(pw)) {
+        walk_next(pw, g, a, c);
+        pk = pw.k0;
+        if (!pw.done) pend = tile_end(pw.s, pw.i, a, c);
+      }
+      next = look_up();
+    }
+    cp_async_commit();
+    slot = slot + 1 == S ? 0 : slot + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) copy_tile();
+
+  int cur = 0;  // stage of the current tile
+  const int r0 = lane >> 2, cq = (lane & 3) * 2;
+  const unsigned q_at = smem_u32(sm.q);
+  // ldmatrix rows: K (and Q) by (key, chunk), V transposed
+  const int k_row = ((lane >> 4) << 3) + (lane & 7), k_ch = (lane >> 3) & 1;
+  const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_ch = lane >> 4;
+
+  while (!w.done) {
+    // ---- the unit's query rows, as A operands
+    for (int idx = threadIdx.x; idx < 16 * CH; idx += kMmaThreads) {
+      const int r = idx / CH, ch = idx - r * CH;
+      const int64_t rr = w.i * kMmaRows + r;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (rr < w.s.rows && ch * 8 < a.D) {
+        const int64_t t = w.s.t0 + rr / a.G;
+        const T* p = q + t * a.q_stride + ((int64_t)w.h * a.G + rr % a.G) * a.D + ch * 8;
+        if (access_ok(p, 16, a.q_span, g.err)) v = __ldg(reinterpret_cast<const uint4*>(p));
+      }
+      *reinterpret_cast<uint4*>(sm.q + r * (DP * 2) + ((ch ^ (r & 7)) << 4)) = v;
+    }
+    if (threadIdx.x < 16) sm.bad[threadIdx.x] = 0;
+    __syncthreads();
+    uint32_t qa[kHoldQ ? KS : 1][4];
+    auto load_q = [&](uint32_t (&f)[4], int ks) {
+      const int r = (lane & 7) + (((lane >> 3) & 1) << 3), ch = ks * 2 + (lane >> 4);
+      ldmatrix4(f, q_at + r * (DP * 2) + ((ch ^ (r & 7)) << 4));
+    };
+    if constexpr (kHoldQ) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) load_q(qa[ks], ks);
+    }
+    int lim0 = lane < 16 ? row_limit(w, w.i * kMmaRows + lane, g, a, c) : 0;
+    const int lim1 = __shfl_sync(0xffffffffu, lim0, r0 + 8);
+    lim0 = __shfl_sync(0xffffffffu, lim0, r0);
+    const int k1 = walk_k1(w);
+
+    float o[DP / 8][4];
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (int k = w.k0; k < k1; ++k) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      const uint32_t word = cur < 2 ? valid : cur < 4 ? valid_hi : valid_top;
+      const uint32_t there = (cur & 1 ? word >> 16 : word) & 0xffffu;
+      copy_tile();  // into the stage that the last tile left
+      const unsigned kt = smem_u32(ring + cur * MmaShared<DP>::kStage), vt = kt + 16 * DP * 2;
+      cur = cur + 1 == S ? 0 : cur + 1;
+      const int j0 = c.lo + k * kMmaKeys + warp * 16;
+      // ---- scores
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t b[4], f[4];
+        ldmatrix4(b, kt + k_row * (DP * 2) + (((ks * 2 + k_ch) ^ (k_row & 7)) << 4));
+        if constexpr (!kHoldQ) load_q(f, ks);
+        mma16816<T>(s[0], kHoldQ ? qa[kHoldQ ? ks : 0] : f, b[0], b[1]);
+        mma16816<T>(s[1], kHoldQ ? qa[kHoldQ ? ks : 0] : f, b[2], b[3]);
+      }
+      // ---- unseen keys, maximum, weights
+      float t0 = m0, t1 = m1;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = n * 8 + cq + e;
+          const bool in = (there >> i) & 1;
+          s[n][e] = in && j0 + i < lim0 ? s[n][e] * a.scale_log2 : -INFINITY;
+          s[n][2 + e] = in && j0 + i < lim1 ? s[n][2 + e] * a.scale_log2 : -INFINITY;
+          t0 = fmaxf(t0, s[n][e]);
+          t1 = fmaxf(t1, s[n][2 + e]);
+        }
+#pragma unroll
+      for (int d = 1; d < 4; d *= 2) {
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+      }
+      const float b0 = t0 == -INFINITY ? 0.f : t0, b1 = t1 == -INFINITY ? 0.f : t1;
+      if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {  // some row's maximum grew
+        const float f0 = fast_exp2(m0 - b0), f1 = fast_exp2(m1 - b1);
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int n = 0; n < DP / 8; ++n) {
+          o[n][0] *= f0;
+          o[n][1] *= f0;
+          o[n][2] *= f1;
+          o[n][3] *= f1;
+        }
+        m0 = t0;
+        m1 = t1;
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][e] = fast_exp2(s[n][e] - b0);
+          s[n][2 + e] = fast_exp2(s[n][2 + e] - b1);
+          l0 += s[n][e];
+          l1 += s[n][2 + e];
+        }
+      const uint32_t p[4] = {pack2((const T*)nullptr, s[0][0], s[0][1]), pack2((const T*)nullptr, s[0][2], s[0][3]),
+                             pack2((const T*)nullptr, s[1][0], s[1][1]), pack2((const T*)nullptr, s[1][2], s[1][3])};
+      // ---- outputs
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) {
+        uint32_t b[4];
+        ldmatrix4_trans(b, vt + v_row * (DP * 2) + (((n * 2 + v_ch) ^ (v_row & 7)) << 4));
+        mma16816<T>(o[2 * n], p, b[0], b[1]);
+        mma16816<T>(o[2 * n + 1], p, b[2], b[3]);
+      }
+      __syncwarp();
+    }
+
+    // ---- the four warps' rows together
+#pragma unroll
+    for (int d = 1; d < 4; d *= 2) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    if ((lane & 3) == 0) {
+      sm.ml[warp][r0][0] = m0;
+      sm.ml[warp][r0][1] = l0;
+      sm.ml[warp][r0 + 8][0] = m1;
+      sm.ml[warp][r0 + 8][1] = l1;
+    }
+    __syncthreads();
+    auto joined = [&](int r, float& m, float& l) {
+      m = fmaxf(fmaxf(sm.ml[0][r][0], sm.ml[1][r][0]), fmaxf(sm.ml[2][r][0], sm.ml[3][r][0]));
+      const float b = m == -INFINITY ? 0.f : m;
+      l = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l += sm.ml[j][r][1] * fast_exp2(sm.ml[j][r][0] - b);
+    };
+    {
+      const float a0 = fmaxf(fmaxf(sm.ml[0][r0][0], sm.ml[1][r0][0]), fmaxf(sm.ml[2][r0][0], sm.ml[3][r0][0]));
+      const float a1 =
+          fmaxf(fmaxf(sm.ml[0][r0 + 8][0], sm.ml[1][r0 + 8][0]), fmaxf(sm.ml[2][r0 + 8][0], sm.ml[3][r0 + 8][0]));
+      const float f0 = fast_exp2(m0 - (a0 == -INFINITY ? 0.f : a0)), f1 = fast_exp2(m1 - (a1 == -INFINITY ? 0.f : a1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // in the warps' order
+        if (warp == j) {
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n) {
+            float2* p0 = reinterpret_cast<float2*>(&sm.o[r0][n * 8 + cq]);
+            float2* p1 = reinterpret_cast<float2*>(&sm.o[r0 + 8][n * 8 + cq]);
+            const float2 x0 = make_float2(o[n][0] * f0, o[n][1] * f0), x1 = make_float2(o[n][2] * f1, o[n][3] * f1);
+            if (j == 0) {
+              *p0 = x0;
+              *p1 = x1;
+            } else {
+              const float2 y0 = *p0, y1 = *p1;
+              *p0 = make_float2(y0.x + x0.x, y0.y + x0.y);
+              *p1 = make_float2(y1.x + x1.x, y1.y + x1.y);
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+    // ---- to the output, or to a partial result
+    const bool begins = w.k0 == 0, ends = k1 == w.work;
+    const bool whole = begins && ends;
+    float* const po = slot_o(c, a, blockIdx.x, begins ? 1 : 0);
+    float* const pml = slot_ml(c, a, gridDim.x, blockIdx.x, begins ? 1 : 0);
+    const int DC = a.D / 8;
+    for (int idx = threadIdx.x; idx < 16 * DC; idx += kMmaThreads) {
+      const int r = idx / DC, d = (idx - r * DC) * 8;
+      const int64_t rr = w.i * kMmaRows + r;
+      if (rr >= w.s.rows) break;
+      const int64_t t = w.s.t0 + rr / a.G;
+      const int64_t row = t * a.nq + (int64_t)w.h * a.G + rr % a.G;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = sm.o[r][d + e];
+      if (whole && !c.shared) {
+        float m, l;
+        joined(r, m, l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        Vec<T, 8> y;
+        bool fine = true;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] *= inv;
+          fine = fine && fabsf(v[e]) <= FLT_MAX;
+          y.e[e] = narrow<T>(v[e]);
+        }
+        if (!fine || !(l <= FLT_MAX)) sm.bad[r] = 1;
+        store_vec(out + row * a.D + d, y, a.out_span, g.err);
+        if (d == 0 && lse && access_ok(lse + row, 4, a.lse_span, g.err))
+          lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+      } else {
+        float* to = whole ? c.dense + row * a.D + d : po + r * a.D + d;
+        *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        if (d == 0) {
+          float m, l;
+          joined(r, m, l);
+          float* ml = whole ? c.dense + a.T * a.nq * a.D + row * 2 : pml + r * 2;
+          *reinterpret_cast<float2*>(ml) = make_float2(m, l);
+        }
+      }
+    }
+    __syncthreads();
+    if (begins && threadIdx.x < 16) {
+      const int64_t rr = w.i * kMmaRows + threadIdx.x;
+      if (rr < w.s.rows) {
+        const int64_t row = (w.s.t0 + rr / a.G) * a.nq + (int64_t)w.h * a.G + rr % a.G;
+        c.rec[row] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : walk_ctas(w);
+      }
+    }
+    walk_next(w, g, a, c);
+  }
+  cp_async_wait<0>();
+}
+
+}  // namespace attend
+}  // namespace rope
