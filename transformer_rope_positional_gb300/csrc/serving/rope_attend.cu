@@ -7,8 +7,9 @@
 // Partial results over key ranges are joined by
 //   m = max m_s,  l = sum l_s e^(m_s - m),  o = sum o_s e^(m_s - m) / l.
 //
-// 16-bit data takes the unit kernels (rope_attend_mma.cuh), then a kernel that joins partial
-// results; other calls a kernel with one warp per query row.
+// 16-bit data takes the unit kernels (rope_attend_mma.cuh for up to 16 rows a sequence and key
+// head, rope_attend_tc.cuh beyond), then a kernel that joins partial results; other calls a
+// kernel with one warp per query row.
 //
 // A shared prefix has a launch of its own when a sequence's rows fill less than a unit: the
 // rows of all sequences together fill the units of that launch, so the prefix is read once
@@ -19,6 +20,7 @@
 
 #include "rope_attend.cuh"
 #include "rope_attend_mma.cuh"
+#include "rope_attend_tc.cuh"
 
 namespace rope {
 namespace {
@@ -179,30 +181,51 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 int padded_columns(int64_t D) { return (int)round_up(D, 64); }
 
-// One launch's part of the workspace.
+// A launch of units: its kernel, cut and grid.
+struct Units {
+  bool tc;  // units of many rows (rope_attend_tc.cuh), else of 16 (rope_attend_mma.cuh)
+  int64_t M, KT, grid;
+};
+
+Units units_of(bool tc, int64_t D) {
+  const int cols = padded_columns(D);
+  Units u;
+  u.tc = tc;
+  u.M = !tc ? kMmaRows : cols <= 128 ? 256 : 128;
+  u.KT = !tc ? kMmaKeys : cols <= 128 ? 128 : 64;
+  u.grid = (int64_t)sm_count() * (!tc && cols <= 192 ? 2 : 1);
+  return u;
+}
+
+// One launch's part of the workspace: records, partial slots, and with `dense` the rows that
+// one CTA finished.
 struct Part {
   int64_t rec, slots, dense, bytes;  // offsets, and all of it
   int64_t slot_rows;
 };
 
-Part part_of(int64_t T, int64_t nq, int64_t nk, int64_t D, int64_t M, int64_t grid, bool shared) {
+Part part_of(int64_t T, int64_t nq, int64_t nk, int64_t D, const Units& u, bool dense) {
   Part s;
-  s.slot_rows = std::min(M, round_up(T * (nq / nk), 16));
+  s.slot_rows = std::min(u.M, round_up(T * (nq / nk), 16));
   s.rec = 0;
   s.slots = round_up(T * nq * 8, 256);
-  s.dense = s.slots + round_up(grid * 2 * s.slot_rows * (D + 2) * 4, 256);
-  s.bytes = s.dense + (shared ? round_up(T * nq * (D + 2) * 4, 256) : 0);
+  s.dense = s.slots + round_up(u.grid * 2 * s.slot_rows * (D + 2) * 4, 256);
+  s.bytes = s.dense + (dense ? round_up(T * nq * (D + 2) * 4, 256) : 0);
   return s;
 }
 
-int64_t mma_grid(int64_t D) { return (int64_t)sm_count() * (padded_columns(D) <= 192 ? 2 : 1); }
+// The larger of both kernels' parts: which one runs depends on the batch as well.
+int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, bool dense) {
+  return std::max(part_of(T, nq, nk, D, units_of(false, D), dense).bytes,
+                  part_of(T, nq, nk, D, units_of(true, D), dense).bytes);
+}
 
 bool tensor_path(int32_t dtype, int64_t D) { return dtype != kF32 && D <= 256; }
 
-Cut cut_of(const Part& s, char* at, int64_t M, int64_t KT) {
+Cut cut_of(const Part& s, char* at, const Units& u) {
   Cut c;
-  c.M = (int32_t)M;
-  c.KT = (int32_t)KT;
+  c.M = (int32_t)u.M;
+  c.KT = (int32_t)u.KT;
   c.lo = 0;
   c.prefix = 0;
   c.shared = 0;
@@ -226,19 +249,31 @@ cudaError_t launch_mma(const AttendProblem& p, const Pointers& g, const AttendAr
                                 static_cast<T*>(p.out), p.lse, g, a, c);
 }
 
+template <typename T, int DP>
+cudaError_t launch_tc(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
+                      cudaStream_t stream) {
+  auto kernel = attend_tc_kernel<T, DP>;
+  const size_t smem = sizeof(TcShared<DP>);
+  const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped_smem(kernel, (unsigned)grid, TcShape<DP>::kThreads, smem, stream,
+                                static_cast<const T*>(p.query), static_cast<const T*>(p.k_cache),
+                                static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, c);
+}
+
 template <typename T>
-cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
+cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, const Units& u,
                          cudaStream_t stream) {
-  switch (padded_columns(p.D)) {
-    case 64:
-      return launch_mma<T, 64>(p, g, a, c, grid, stream);
-    case 128:
-      return launch_mma<T, 128>(p, g, a, c, grid, stream);
-    case 192:
-      return launch_mma<T, 192>(p, g, a, c, grid, stream);
-    default:
-      return launch_mma<T, 256>(p, g, a, c, grid, stream);
+  const int cols = padded_columns(p.D);
+  if (u.tc) {
+    if (cols <= 64) return launch_tc<T, 64>(p, g, a, c, u.grid, stream);
+    if (cols <= 128) return launch_tc<T, 128>(p, g, a, c, u.grid, stream);
+    return launch_tc<T, 256>(p, g, a, c, u.grid, stream);
   }
+  if (cols <= 64) return launch_mma<T, 64>(p, g, a, c, u.grid, stream);
+  if (cols <= 128) return launch_mma<T, 128>(p, g, a, c, u.grid, stream);
+  if (cols <= 192) return launch_mma<T, 192>(p, g, a, c, u.grid, stream);
+  return launch_mma<T, 256>(p, g, a, c, u.grid, stream);
 }
 
 template <typename T, int E>
@@ -256,24 +291,29 @@ cudaError_t launch_join(const AttendProblem& p, const Pointers& g, const AttendA
 
 template <typename T>
 cudaError_t launch_tensor(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
-  const bool shared = p.prefix_len > 0;
-  const int64_t grid = mma_grid(p.D);
-  const Part s = part_of(p.T, p.nq, p.nk, p.D, kMmaRows, grid, shared);
+  // rows of a sequence and key head, on average: only the lengths' sum is known here
+  const double rows = (double)p.T * a.G / (double)p.B;
+  // the prefix has a launch of its own where that saves re-reads of it worth more than the launch
+  // (8 MB are 1.2 us of the copy bandwidth) and a sequence's rows do not fill a tile by themselves
+  const double saved = (double)(p.B - 1) * (double)p.prefix_len * (double)p.nk * (double)p.D * 4;
+  const bool shared = saved > 8e6 && rows < 128;
+  const Units u_own = units_of(rows > kMmaRows, p.D), u_pre = units_of(p.T * a.G > kMmaRows, p.D);
+  const Part s_own = part_of(p.T, p.nq, p.nk, p.D, u_own, shared);
   char* const ws = static_cast<char*>(p.workspace);
-  Cut own = cut_of(s, ws, kMmaRows, kMmaKeys), pre = own;
+  Cut own = cut_of(s_own, ws, u_own), pre = own;
   if (shared) {
     own.shared = 1;
     own.lo = a.P;
-    pre = cut_of(s, ws + s.bytes, kMmaRows, kMmaKeys);
+    pre = cut_of(part_of(p.T, p.nq, p.nk, p.D, u_pre, true), ws + s_own.bytes, u_pre);
     pre.shared = pre.prefix = 1;
-    const cudaError_t e = launch_units<T>(p, g, a, pre, grid, stream);
+    const cudaError_t e = launch_units<T>(p, g, a, pre, u_pre, stream);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = launch_units<T>(p, g, a, own, grid, stream);
+  const cudaError_t e = launch_units<T>(p, g, a, own, u_own, stream);
   if (e != cudaSuccess) return e;
-  if (p.D <= 64) return launch_join<T, 1>(p, g, a, own, pre, grid, grid, stream);
-  if (p.D <= 128) return launch_join<T, 2>(p, g, a, own, pre, grid, grid, stream);
-  return launch_join<T, 4>(p, g, a, own, pre, grid, grid, stream);
+  if (p.D <= 64) return launch_join<T, 1>(p, g, a, own, pre, u_own.grid, u_pre.grid, stream);
+  if (p.D <= 128) return launch_join<T, 2>(p, g, a, own, pre, u_own.grid, u_pre.grid, stream);
+  return launch_join<T, 4>(p, g, a, own, pre, u_own.grid, u_pre.grid, stream);
 }
 
 template <typename T>
@@ -325,8 +365,7 @@ cudaError_t launch_typed(const AttendProblem& p, cudaStream_t stream) {
 int64_t attend_workspace(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, int64_t prefix_len) {
   if (!tensor_path(dtype, D)) return 256;
   const bool shared = prefix_len > 0;
-  const Part s = part_of(T, nq, nk, D, kMmaRows, mma_grid(D), shared);
-  return std::max<int64_t>(256, s.bytes * (shared ? 2 : 1));
+  return part_bytes(T, nq, nk, D, shared) * (shared ? 2 : 1);
 }
 
 cudaError_t launch_attend(const AttendProblem& p, cudaStream_t stream) {
