@@ -7,9 +7,9 @@
 // Partial results over key ranges are joined by
 //   m = max m_s,  l = sum l_s e^(m_s - m),  o = sum o_s e^(m_s - m) / l.
 //
-// 16-bit data takes the unit kernels (rope_attend_mma.cuh for up to 16 rows a sequence and key
-// head, rope_attend_tc.cuh beyond), then a kernel that joins partial results; other calls a
-// kernel with one warp per query row.
+// Heads of up to 256 take the unit kernels (16-bit data: rope_attend_mma.cuh for up to 16 rows
+// a sequence and key head, rope_attend_tc.cuh beyond; binary32: rope_attend_f32.cuh), then a
+// kernel that joins partial results; larger heads a kernel with one warp per query row.
 //
 // A shared prefix has a launch of its own when a sequence's rows fill less than a unit: the
 // rows of all sequences together fill the units of that launch, so the prefix is read once
@@ -19,6 +19,7 @@
 #include <cmath>
 
 #include "rope_attend.cuh"
+#include "rope_attend_f32.cuh"
 #include "rope_attend_mma.cuh"
 #include "rope_attend_tc.cuh"
 
@@ -175,7 +176,7 @@ cudaError_t launch_rows(const AttendProblem& p, const Pointers& g, const AttendA
 }
 
 // ---------------------------------------------------------------------------
-// The 16-bit path: sizes of its workspace, and its launches.
+// The cut path: sizes of its workspace, and its launches.
 // ---------------------------------------------------------------------------
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
@@ -183,14 +184,23 @@ int padded_columns(int64_t D) { return (int)round_up(D, 64); }
 
 // A launch of units: its kernel, cut and grid.
 struct Units {
-  bool tc;  // units of many rows (rope_attend_tc.cuh), else of 16 (rope_attend_mma.cuh)
+  bool tall;  // units of many rows (rope_attend_tc.cuh), else of 16 (rope_attend_mma.cuh); binary32: 64 or 16
   int64_t M, KT, grid;
 };
 
-Units units_of(bool tc, int64_t D) {
+Units units_of(bool tc, int64_t D, int32_t dtype) {
   const int cols = padded_columns(D);
   Units u;
-  u.tc = tc;
+  u.tall = tc;
+  if (dtype == kF32) {
+    u.M = tc ? 64 : 16;
+    u.KT = kF32Keys;
+    const int ctas = cols <= 64    ? tc ? f32_ctas<64, 4>() : f32_ctas<64, 1>()
+                     : cols <= 128 ? tc ? f32_ctas<128, 4>() : f32_ctas<128, 1>()
+                                   : tc ? f32_ctas<256, 4>() : f32_ctas<256, 1>();
+    u.grid = (int64_t)sm_count() * ctas;
+    return u;
+  }
   u.M = !tc ? kMmaRows : cols <= 128 ? 256 : 128;
   u.KT = !tc ? kMmaKeys : cols <= 128 ? 128 : 64;
   u.grid = (int64_t)sm_count() * (!tc && cols <= 192 ? 2 : 1);
@@ -215,12 +225,12 @@ Part part_of(int64_t T, int64_t nq, int64_t nk, int64_t D, const Units& u, bool 
 }
 
 // The larger of both kernels' parts: which one runs depends on the batch as well.
-int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, bool dense) {
-  return std::max(part_of(T, nq, nk, D, units_of(false, D), dense).bytes,
-                  part_of(T, nq, nk, D, units_of(true, D), dense).bytes);
+int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, bool dense) {
+  return std::max(part_of(T, nq, nk, D, units_of(false, D, dtype), dense).bytes,
+                  part_of(T, nq, nk, D, units_of(true, D, dtype), dense).bytes);
 }
 
-bool tensor_path(int32_t dtype, int64_t D) { return dtype != kF32 && D <= 256; }
+bool unit_path(int64_t D) { return D <= 256; }
 
 Cut cut_of(const Part& s, char* at, const Units& u) {
   Cut c;
@@ -261,19 +271,39 @@ cudaError_t launch_tc(const AttendProblem& p, const Pointers& g, const AttendArg
                                 static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, c);
 }
 
+template <int DP, int RPT>
+cudaError_t launch_f32(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
+                       cudaStream_t stream) {
+  auto kernel = attend_f32_kernel<DP, RPT>;
+  const size_t smem = sizeof(F32Shared<DP, RPT>);
+  const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped_smem(kernel, (unsigned)grid, kF32Threads, smem, stream, static_cast<const float*>(p.query),
+                                static_cast<const float*>(p.k_cache), static_cast<const float*>(p.v_cache),
+                                static_cast<float*>(p.out), p.lse, g, a, c);
+}
+
 template <typename T>
 cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, const Units& u,
                          cudaStream_t stream) {
   const int cols = padded_columns(p.D);
-  if (u.tc) {
-    if (cols <= 64) return launch_tc<T, 64>(p, g, a, c, u.grid, stream);
-    if (cols <= 128) return launch_tc<T, 128>(p, g, a, c, u.grid, stream);
-    return launch_tc<T, 256>(p, g, a, c, u.grid, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (cols <= 64)
+      return u.tall ? launch_f32<64, 4>(p, g, a, c, u.grid, stream) : launch_f32<64, 1>(p, g, a, c, u.grid, stream);
+    if (cols <= 128)
+      return u.tall ? launch_f32<128, 4>(p, g, a, c, u.grid, stream) : launch_f32<128, 1>(p, g, a, c, u.grid, stream);
+    return u.tall ? launch_f32<256, 4>(p, g, a, c, u.grid, stream) : launch_f32<256, 1>(p, g, a, c, u.grid, stream);
+  } else {
+    if (u.tall) {
+      if (cols <= 64) return launch_tc<T, 64>(p, g, a, c, u.grid, stream);
+      if (cols <= 128) return launch_tc<T, 128>(p, g, a, c, u.grid, stream);
+      return launch_tc<T, 256>(p, g, a, c, u.grid, stream);
+    }
+    if (cols <= 64) return launch_mma<T, 64>(p, g, a, c, u.grid, stream);
+    if (cols <= 128) return launch_mma<T, 128>(p, g, a, c, u.grid, stream);
+    if (cols <= 192) return launch_mma<T, 192>(p, g, a, c, u.grid, stream);
+    return launch_mma<T, 256>(p, g, a, c, u.grid, stream);
   }
-  if (cols <= 64) return launch_mma<T, 64>(p, g, a, c, u.grid, stream);
-  if (cols <= 128) return launch_mma<T, 128>(p, g, a, c, u.grid, stream);
-  if (cols <= 192) return launch_mma<T, 192>(p, g, a, c, u.grid, stream);
-  return launch_mma<T, 256>(p, g, a, c, u.grid, stream);
 }
 
 template <typename T, int E>
@@ -290,14 +320,14 @@ cudaError_t launch_join(const AttendProblem& p, const Pointers& g, const AttendA
 }
 
 template <typename T>
-cudaError_t launch_tensor(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
+cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
   // rows of a sequence and key head, on average: only the lengths' sum is known here
   const double rows = (double)p.T * a.G / (double)p.B;
   // the prefix has a launch of its own where that saves re-reads of it worth more than the launch
   // (8 MB are 1.2 us of the copy bandwidth) and a sequence's rows do not fill a tile by themselves
   const double saved = (double)(p.B - 1) * (double)p.prefix_len * (double)p.nk * (double)p.D * 4;
   const bool shared = saved > 8e6 && rows < 128;
-  const Units u_own = units_of(rows > kMmaRows, p.D), u_pre = units_of(p.T * a.G > kMmaRows, p.D);
+  const Units u_own = units_of(rows > 16, p.D, p.dtype), u_pre = units_of(p.T * a.G > 16, p.D, p.dtype);
   const Part s_own = part_of(p.T, p.nq, p.nk, p.D, u_own, shared);
   char* const ws = static_cast<char*>(p.workspace);
   Cut own = cut_of(s_own, ws, u_own), pre = own;
@@ -351,21 +381,16 @@ cudaError_t launch_typed(const AttendProblem& p, cudaStream_t stream) {
   g.prefix_blocks = p.prefix_blocks;
   const cudaError_t er = device_error_address(&g.err);
   if (er != cudaSuccess) return er;
-  if constexpr (sizeof(T) == 2) {
-    if (tensor_path(p.dtype, p.D)) return launch_tensor<T>(p, g, a, stream);
-  }
-  if (p.D <= 64) return launch_rows<T, 2>(p, g, a, stream);
-  if (p.D <= 128) return launch_rows<T, 4>(p, g, a, stream);
-  if (p.D <= 256) return launch_rows<T, 8>(p, g, a, stream);
+  if (unit_path(p.D)) return launch_cut<T>(p, g, a, stream);
   return launch_rows<T, 16>(p, g, a, stream);
 }
 
 }  // namespace
 
 int64_t attend_workspace(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, int64_t prefix_len) {
-  if (!tensor_path(dtype, D)) return 256;
+  if (!unit_path(D)) return 256;
   const bool shared = prefix_len > 0;
-  return part_bytes(T, nq, nk, D, shared) * (shared ? 2 : 1);
+  return std::max<int64_t>(256, part_bytes(T, nq, nk, D, dtype, shared) * (shared ? 2 : 1));
 }
 
 cudaError_t launch_attend(const AttendProblem& p, cudaStream_t stream) {
