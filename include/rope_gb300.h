@@ -404,7 +404,8 @@ int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* qu
  * (rope_append_paged_kv, rope_qkv_rmsnorm_rope_cache).
  *
  *   query            [T, Nq*D], rows query_row_stride elements apart (0: contiguous; a multiple of 16 bytes);
- *                    F32, F16 or BF16; D a multiple of 32 (F16/BF16) or 16 (F32), at most 512.
+ *                    F32, F16 or BF16; D a multiple of 32 (F16/BF16) or 16 (F32), at most 512;
+ *                    Nq at most 65536, T * Nq below 2^31 - 512.
  *   k_cache, v_cache [NB, Nk, BS, D], same dtype; Nq a multiple of Nk.
  *   block_table      I64 [B, W]: pages of each sequence's own tokens; B >= 1, W >= 1, W * BS <= 2^30.
  *   seq_lens         I64 [B]: tokens of each sequence, prefix and this call's included.

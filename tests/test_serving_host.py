@@ -295,11 +295,12 @@ def test_workspace_sizes(lib):
         return st, n.value
 
     for a in ((1, 1, 1, 64, C.F16, 0), (4096, 32, 8, 128, C.BF16, 4096), (7, 4, 2, 64, C.F32, 5), (0, 4, 2, 64, C.F32, 0),
-              (1 << 31, 1 << 16, 1, 512, C.BF16, 1)):
+              (1 << 20, 1 << 10, 1, 512, C.BF16, 1), (1 << 20, 1 << 10, 1, 128, C.BF16, 1)):
         st, n = size(*a)
         assert st == OK and n >= 256, a
     for a in ((-1, 1, 1, 64, C.F16, 0), (1, 3, 2, 64, C.F16, 0), (1, 2, 2, 48, C.F16, 0), (1, 2, 2, 64, C.I64, 0),
-              (1, 2, 2, 64, C.F16, -1), ((1 << 31) + 1, 2, 2, 64, C.F16, 0), (1, 0, 1, 64, C.F16, 0), (1, 2, 2, 544, C.F16, 0)):
+              (1, 2, 2, 64, C.F16, -1), ((1 << 31) + 1, 2, 2, 64, C.F16, 0), (1 << 30, 2, 2, 64, C.F16, 0),
+              (1, 1 << 17, 1, 64, C.F16, 0), (1, 0, 1, 64, C.F16, 0), (1, 2, 2, 544, C.F16, 0)):
         assert size(*a)[0] == BAD, a
     assert lib.rope_paged_attention_workspace(1, 1, 1, 64, C.F16, 0, None) == NULL
 

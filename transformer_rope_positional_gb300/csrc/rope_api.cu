@@ -584,8 +584,8 @@ int append_call(const rope_tensor_t* positions, const rope_tensor_t* query, cons
 // workspace's size stays in int64).
 bool attend_sizes_ok(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dt) {
   const int64_t mult = dt == kF32 ? 16 : 32;
-  return is_float(dt) && T >= 0 && T <= (int64_t(1) << 31) && nq >= 1 && nk >= 1 && nq % nk == 0 && nq <= (int64_t(1) << 16) && D >= mult &&
-         D % mult == 0 && D <= 512;
+  return is_float(dt) && nq >= 1 && nk >= 1 && nq <= (int64_t(1) << 16) && nq % nk == 0 && T >= 0 &&
+         T <= (int64_t(1) << 31) && T * nq < (int64_t(1) << 31) - 512 && D >= mult && D % mult == 0 && D <= 512;
 }
 
 // Checks of the attention call, then the launch.

@@ -49,34 +49,35 @@ __global__ void __launch_bounds__(kWarps * 32)
 // launch), one warp per row; a row whose result is not finite is computed again key by key:
 // a key that a row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of
 // its value would leave NaN.  A warp takes per_warp consecutive rows and looks at their
-// records first, so that rows already finished cost one load for 32 of them.
+// records first, so that rows already finished cost one load for all of them.  The partial
+// results of a row are read eight at a time, all loads before any arithmetic.
 template <typename T, int E>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_join_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
-                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut own, Cut pre, int own_grid, int pre_grid,
-                       int per_warp) {
+                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut own, Cut pre, int per_warp) {
+  constexpr int NS = 8;
   wait_for_prior_grid();
   const int lane = threadIdx.x & 31;
-  const int64_t tokens = min(ldg(g.qsl + a.B, a.qsl_span, g.err), a.T);
-  const int64_t rows = tokens * a.nq;
   const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
+  const int64_t rows = min(ldg(g.qsl + a.B, a.qsl_span, g.err), a.T) * a.nq;
   const bool shared = own.shared != 0;
   int2 mine = make_int2(0, 0), mine_pre = make_int2(0, 0);
-  if (lane < per_warp && first + lane < rows) {
+  bool todo = lane < per_warp && first + lane < a.T * a.nq;
+  if (todo) {
     mine = own.rec[first + lane];
     if (shared) mine_pre = pre.rec[first + lane];
   }
-  const bool todo = lane < per_warp && first + lane < rows && (shared || mine.x < 0 || mine.x != mine.y);
+  todo = todo && first + lane < rows && (shared || mine.x < 0 || (mine.x & 0xffff) != mine.x >> 16);
   uint32_t left = __ballot_sync(0xffffffffu, todo);
   while (left) {
     const int i = __ffs(left) - 1;
     left &= left - 1;
     const int64_t row = first + i;
-    const int64_t t = row / a.nq;
-    const int h = (int)(row - t * a.nq);
-    const int c0 = __shfl_sync(0xffffffffu, mine.x, i), c1 = __shfl_sync(0xffffffffu, mine.y, i);
-    const int p0 = __shfl_sync(0xffffffffu, mine_pre.x, i), p1 = __shfl_sync(0xffffffffu, mine_pre.y, i);
-    bool known = c0 >= 0 && c1 >= c0 && c1 < own_grid && p0 >= 0 && p1 >= p0 && (!shared || p1 < pre_grid);
+    const int x = __shfl_sync(0xffffffffu, mine.x, i), x_at = __shfl_sync(0xffffffffu, mine.y, i);
+    const int y = __shfl_sync(0xffffffffu, mine_pre.x, i), y_at = __shfl_sync(0xffffffffu, mine_pre.y, i);
+    const int c0 = x & 0xffff, c1 = x >> 16, p0 = y & 0xffff, p1 = y >> 16;
+    bool known = c1 >= c0 && c1 < own.grid && (unsigned)x_at < (unsigned)own.slot_rows;
+    if (shared) known = known && p1 >= p0 && p1 < pre.grid && (unsigned)y_at < (unsigned)pre.slot_rows;
     float m = -INFINITY, l = 0.f;
     float2 o[E];
 #pragma unroll
@@ -84,74 +85,63 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (known) {
       // sources 0 .. n_pre - 1: the prefix's parts, then the own keys' parts
       const int n_pre = shared ? p1 - p0 + 1 : 0, n = n_pre + c1 - c0 + 1;
-      const int64_t b = batch_of(t, g, a);
-      const int gh = h % a.G;
-      const int at_own = (int)(((t - ldg(g.qsl + b, a.qsl_span, g.err)) * a.G + gh) % own.M);
-      const int at_pre = shared ? (int)((t * a.G + gh) % pre.M) : 0;
-      auto source = [&](int s, const float*& so, const float*& sml) {
-        const bool is_pre = s < n_pre;
-        const Cut& c = is_pre ? pre : own;
-        const int first_cta = is_pre ? p0 : c0, last_cta = is_pre ? p1 : c1, at = is_pre ? at_pre : at_own;
-        if (first_cta == last_cta) {
-          so = c.dense + row * a.D;
-          sml = c.dense + a.T * a.nq * a.D + row * 2;
-        } else {
-          const int cta = first_cta + (is_pre ? s : s - n_pre);
-          const int slot = cta == first_cta ? 1 : 0;
-          so = slot_o(c, a, cta, slot) + (int64_t)at * a.D;
-          sml = slot_ml(c, a, is_pre ? pre_grid : own_grid, cta, slot) + at * 2;
-        }
-      };
-      for (int s0 = 0; s0 < n; s0 += 32) {
-        float ms = -INFINITY, ls = 0.f;
-        if (s0 + lane < n) {
-          const float *so, *sml;
-          source(s0 + lane, so, sml);
-          const float2 v = *reinterpret_cast<const float2*>(sml);
-          ms = v.x;
-          ls = v.y;
-        }
-        float top = fmaxf(m, ms);
+      for (int s0 = 0; s0 < n; s0 += NS) {
+        float2 v[NS][E], ml[NS];
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float base = top == -INFINITY ? 0.f : top;
-        const float keep = fast_exp2(m - base);
-        const float ws = s0 + lane < n ? fast_exp2(ms - base) : 0.f;
-        float add = ls * ws;
+        for (int s = 0; s < NS; ++s) {
+          if (s0 + s < n) {
+            const bool is_pre = s0 + s < n_pre;
+            const int c_first = is_pre ? p0 : c0, c_last = is_pre ? p1 : c1;
+            const int cta = c_first + (is_pre ? s0 + s : s0 + s - n_pre), slot = cta == c_first ? 1 : 0;
+            const int at = is_pre ? y_at : x_at;
+            const Cut& c = is_pre ? pre : own;
+            const bool whole = c_first == c_last;
+            const float* so = whole ? c.dense + row * a.D : slot_o(c, a, cta, slot) + (int64_t)at * a.D;
+            const float* sml = whole ? c.dense + a.T * a.nq * a.D + row * 2 : slot_ml(c, a, cta, slot) + at * 2;
+            ml[s] = *reinterpret_cast<const float2*>(sml);
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) add += __shfl_xor_sync(0xffffffffu, add, d);
-        l = l * keep + add;
-        m = top;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = make_float2(o[e].x * keep, o[e].y * keep);
-        const int k = min(32, n - s0);
-#pragma unroll 4
-        for (int s = 0; s < k; ++s) {
-          const float f = __shfl_sync(0xffffffffu, ws, s);
-          const float *so, *sml;
-          source(s0 + s, so, sml);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const int d = lane * 2 + 64 * e;
-            if (d < a.D) {
-              const float2 v = *reinterpret_cast<const float2*>(so + d);
-              o[e].x = fmaf(f, v.x, o[e].x);
-              o[e].y = fmaf(f, v.y, o[e].y);
+            for (int e = 0; e < E; ++e) {
+              const int d = lane * 2 + 64 * e;
+              v[s][e] = d < a.D ? *reinterpret_cast<const float2*>(so + d) : make_float2(0.f, 0.f);
             }
+          } else {
+            ml[s] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[s][e] = make_float2(0.f, 0.f);
           }
         }
+        float top = m;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) top = fmaxf(top, ml[s].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float keep = fast_exp2(m - base);
+        l *= keep;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = make_float2(o[e].x * keep, o[e].y * keep);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const float f = fast_exp2(ml[s].x - base);
+          l = fmaf(ml[s].y, f, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            o[e].x = fmaf(f, v[s][e].x, o[e].x);
+            o[e].y = fmaf(f, v[s][e].y, o[e].y);
+          }
+        }
+        m = top;
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       bool fine = l <= FLT_MAX;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        o[e] = l == 0.f ? make_float2(0.f, 0.f) : make_float2(o[e].x * inv, o[e].y * inv);
+        o[e] = make_float2(o[e].x * inv, o[e].y * inv);
         fine = fine && fabsf(o[e].x) <= FLT_MAX && fabsf(o[e].y) <= FLT_MAX;
       }
       known = __all_sync(0xffffffffu, fine);
     }
     if (!known) {
-      attend_row<T, 2 * E>(t, h, q, kc, vc, out, lse, g, a);
+      const int64_t t = row / a.nq;
+      attend_row<T, 2 * E>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
       continue;
     }
 #pragma unroll
@@ -185,7 +175,7 @@ int padded_columns(int64_t D) { return (int)round_up(D, 64); }
 // A launch of units: its kernel, cut and grid.
 struct Units {
   bool tall;  // units of many rows (rope_attend_tc.cuh), else of 16 (rope_attend_mma.cuh); binary32: 64 or 16
-  int64_t M, KT, grid;
+  int64_t M, grid;
 };
 
 Units units_of(bool tc, int64_t D, int32_t dtype) {
@@ -194,7 +184,6 @@ Units units_of(bool tc, int64_t D, int32_t dtype) {
   u.tall = tc;
   if (dtype == kF32) {
     u.M = tc ? 64 : 16;
-    u.KT = kF32Keys;
     const int ctas = cols <= 64    ? tc ? f32_ctas<64, 4>() : f32_ctas<64, 1>()
                      : cols <= 128 ? tc ? f32_ctas<128, 4>() : f32_ctas<128, 1>()
                                    : tc ? f32_ctas<256, 4>() : f32_ctas<256, 1>();
@@ -202,7 +191,6 @@ Units units_of(bool tc, int64_t D, int32_t dtype) {
     return u;
   }
   u.M = !tc ? kMmaRows : cols <= 128 ? 256 : 128;
-  u.KT = !tc ? kMmaKeys : cols <= 128 ? 128 : 64;
   u.grid = (int64_t)sm_count() * (!tc && cols <= 192 ? 2 : 1);
   return u;
 }
@@ -230,12 +218,13 @@ int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, 
                   part_of(T, nq, nk, D, units_of(true, D, dtype), dense).bytes);
 }
 
-bool unit_path(int64_t D) { return D <= 256; }
+// The unit kernels keep cache rows in 32 bits: fewer than 2^31 rows of one head (137 GB a cache
+// at the smallest 64-byte rows).
+bool unit_path(int64_t D, int64_t cache_rows) { return D <= 256 && cache_rows < (int64_t(1) << 31); }
 
 Cut cut_of(const Part& s, char* at, const Units& u) {
   Cut c;
-  c.M = (int32_t)u.M;
-  c.KT = (int32_t)u.KT;
+  c.grid = (int32_t)u.grid;
   c.lo = 0;
   c.prefix = 0;
   c.shared = 0;
@@ -308,15 +297,16 @@ cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const Attend
 
 template <typename T, int E>
 cudaError_t launch_join(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& own, const Cut& pre,
-                        int64_t own_grid, int64_t pre_grid, cudaStream_t stream) {
+                        cudaStream_t stream) {
   const int64_t rows = p.T * p.nq;
-  const int64_t warps = (int64_t)sm_count() * 16;
-  const int per_warp = (int)std::min<int64_t>(32, (rows + warps - 1) / warps);
+  // one row a warp while that leaves few warps to an SM, up to 8 where most rows are finished
+  const int64_t warps = (int64_t)sm_count() * 32;
+  const int per_warp = (int)std::min<int64_t>(8, (rows + warps - 1) / warps);
   const int64_t grid = (rows + (int64_t)per_warp * kWarps - 1) / ((int64_t)per_warp * kWarps);
   return launch_overlapped(attend_join_kernel<T, E>, (unsigned)grid, kWarps * 32, stream,
                            static_cast<const T*>(p.query), static_cast<const T*>(p.k_cache),
                            static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, own, pre,
-                           (int)own_grid, (int)pre_grid, per_warp);
+                           per_warp);
 }
 
 template <typename T>
@@ -341,9 +331,9 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
   }
   const cudaError_t e = launch_units<T>(p, g, a, own, u_own, stream);
   if (e != cudaSuccess) return e;
-  if (p.D <= 64) return launch_join<T, 1>(p, g, a, own, pre, u_own.grid, u_pre.grid, stream);
-  if (p.D <= 128) return launch_join<T, 2>(p, g, a, own, pre, u_own.grid, u_pre.grid, stream);
-  return launch_join<T, 4>(p, g, a, own, pre, u_own.grid, u_pre.grid, stream);
+  if (p.D <= 64) return launch_join<T, 1>(p, g, a, own, pre, stream);
+  if (p.D <= 128) return launch_join<T, 2>(p, g, a, own, pre, stream);
+  return launch_join<T, 4>(p, g, a, own, pre, stream);
 }
 
 template <typename T>
@@ -381,14 +371,15 @@ cudaError_t launch_typed(const AttendProblem& p, cudaStream_t stream) {
   g.prefix_blocks = p.prefix_blocks;
   const cudaError_t er = device_error_address(&g.err);
   if (er != cudaSuccess) return er;
-  if (unit_path(p.D)) return launch_cut<T>(p, g, a, stream);
+  if (unit_path(p.D, p.num_blocks * p.nk * p.block_size)) return launch_cut<T>(p, g, a, stream);
+  if (p.D <= 64) return launch_rows<T, 2>(p, g, a, stream);
   return launch_rows<T, 16>(p, g, a, stream);
 }
 
 }  // namespace
 
 int64_t attend_workspace(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, int64_t prefix_len) {
-  if (!unit_path(D)) return 256;
+  if (!unit_path(D, 0)) return 256;
   const bool shared = prefix_len > 0;
   return std::max<int64_t>(256, part_bytes(T, nq, nk, D, dtype, shared) * (shared ? 2 : 1));
 }

@@ -68,6 +68,23 @@ __device__ __forceinline__ int64_t key_row(int j, const int64_t* table, const Po
   return page * a.nk * a.block_size + j;
 }
 
+// The page that holds key j, or -1 (see key_row), and the key's row within it.
+struct PageRow {
+  int64_t page;
+  int32_t row;
+};
+
+__device__ __forceinline__ PageRow page_row(int j, const int64_t* table, const Pointers& g, const AttendArgs& a) {
+  if (j < a.P) {
+    const int i = page_of(j, a);
+    return {ldg(g.prefix_blocks + i, a.pb_span, g.err), j - i * a.block_size};
+  }
+  j -= a.P;
+  const int i = page_of(j, a);
+  if (i >= a.W) return {-1, 0};
+  return {ldg(table + i, a.bt_span, g.err), j - i * a.block_size};
+}
+
 // ---------------------------------------------------------------------------
 // How the work is cut.  A unit is a tile of M query rows of one sequence and key head (row r
 // of a sequence is token r / G, head r % G of the key head's group) with the keys they see;
@@ -80,21 +97,22 @@ __device__ __forceinline__ int64_t key_row(int j, const int64_t* table, const Po
 // the cut needs no host copy of them and no extra launch.
 // ---------------------------------------------------------------------------
 struct Cut {
-  int32_t M, KT;      // rows of a unit, keys of a tile
   int32_t lo;         // first key of the launch: P when the prefix has its own launch, else 0
   int32_t prefix;     // this launch is over the shared prefix: units of the whole batch, keys [0, P)
   int32_t shared;     // another launch covers the other keys: nothing is final here
   int32_t min_share;  // fewest tiles a CTA takes
   int32_t slot_rows;  // rows of a partial slot
-  int2* rec;          // [T * nq]: first and last CTA of the row's unit, or (-1, -1): recompute
+  int32_t grid;       // CTAs of the launch
+  int2* rec;          // [T * nq]: first and last CTA of the row's unit (16 bits each) and the row's
+                      // place in the unit; -1: recompute
   float* slots;       // [grid][2][slot_rows][D] O, then [grid][2][slot_rows][2] m, l
   float* dense;       // shared: [T * nq][D] O, then [T * nq][2] m, l, of units that one CTA finished
 };
 
-// Rows and keys of one sequence (or of the whole batch).
+// Rows and keys of one sequence (or of the whole batch).  T * nq is below 2^31 - 512.
 struct SeqWork {
-  int64_t t0;       // first token
-  int64_t rows;     // n * G
+  int32_t t0;       // first token
+  int32_t rows;     // n * G
   int64_t pos0;     // position of token t0 (may be negative)
   int32_t hi;       // keys end here (clamped to the pages)
 };
@@ -102,21 +120,21 @@ struct SeqWork {
 __device__ __forceinline__ SeqWork seq_work(int64_t b, const Pointers& g, const AttendArgs& a, const Cut& c) {
   SeqWork s;
   if (c.prefix) {
-    s.t0 = 0;
     const int64_t n = ldg(g.qsl + a.B, a.qsl_span, g.err);
-    s.rows = (n < 0 ? 0 : n > a.T ? a.T : n) * a.G;
+    s.t0 = 0;
+    s.rows = (int)(n < 0 ? 0 : n > a.T ? a.T : n) * a.G;
     s.pos0 = a.P;
     s.hi = a.P;
     return s;
   }
   int64_t t0 = ldg(g.qsl + b, a.qsl_span, g.err), t1 = ldg(g.qsl + b + 1, a.qsl_span, g.err);
   const int64_t len = ldg(g.seq_lens + b, a.sl_span, g.err);
-  t0 = t0 < 0 ? 0 : t0;
+  t0 = t0 < 0 ? 0 : t0 > a.T ? a.T : t0;
   t1 = t1 > a.T ? a.T : t1;
-  const int64_t n = t1 > t0 ? t1 - t0 : 0;
+  const int n = t1 > t0 ? (int)(t1 - t0) : 0;
   const int64_t most = (int64_t)a.P + a.W * a.block_size;
   if (len > most && n > 0) atomicOr(g.err, kSlotOutOfRange);  // more tokens than pages
-  s.t0 = t0;
+  s.t0 = (int)t0;
   s.rows = n * a.G;
   s.pos0 = len - n;
   s.hi = (int)(len < 0 ? 0 : len > most ? most : len);
@@ -124,42 +142,51 @@ __device__ __forceinline__ SeqWork seq_work(int64_t b, const Pointers& g, const 
 }
 
 // Keys [lo, end) that the rows of tile i of a sequence see between them.
-__device__ __forceinline__ int tile_end(const SeqWork& s, int64_t i, const AttendArgs& a, const Cut& c) {
+template <int M>
+__device__ __forceinline__ int tile_end(const SeqWork& s, int i, const AttendArgs& a, const Cut& c) {
   if (c.prefix) return s.hi;
-  const int64_t last = (min((i + 1) * c.M, s.rows) - 1) / a.G;  // last token of the tile
+  const int last = (int)((unsigned)(min((i + 1) * M, s.rows) - 1) / (unsigned)a.G);  // last token of the tile
   const int64_t e = s.pos0 + last + 1;
   return (int)(e < c.lo ? c.lo : e > s.hi ? max(s.hi, c.lo) : e);
 }
 
-__device__ __forceinline__ int tile_work(const SeqWork& s, int64_t i, const AttendArgs& a, const Cut& c) {
-  const int keys = tile_end(s, i, a, c) - c.lo;
-  return keys <= c.KT ? 1 : (keys + c.KT - 1) / c.KT;  // a unit without keys is one (empty) tile
+template <int M, int KT>
+__device__ __forceinline__ int tile_work(const SeqWork& s, int i, const AttendArgs& a, const Cut& c) {
+  const int keys = tile_end<M>(s, i, a, c) - c.lo;
+  return keys <= KT ? 1 : (keys + KT - 1) / KT;  // a unit without keys is one (empty) tile
 }
 
-__device__ __forceinline__ int64_t row_tiles(const SeqWork& s, const Cut& c) { return (s.rows + c.M - 1) / c.M; }
+template <int M>
+__device__ __forceinline__ int row_tiles(const SeqWork& s) {
+  return (s.rows + M - 1) / M;
+}
 
+template <int M, int KT>
 __device__ __forceinline__ int64_t seq_total(const SeqWork& s, const AttendArgs& a, const Cut& c) {
-  const int64_t tiles = row_tiles(s, c);
-  if (c.prefix) return tiles * tile_work(s, 0, a, c) * a.nk;
+  const int tiles = row_tiles<M>(s);
+  if (c.prefix) return (int64_t)tiles * tile_work<M, KT>(s, 0, a, c) * a.nk;
   int64_t sum = 0;
-  for (int64_t i = 0; i < tiles; ++i) sum += tile_work(s, i, a, c);
+  for (int i = 0; i < tiles; ++i) sum += tile_work<M, KT>(s, i, a, c);
   return sum * a.nk;
 }
 
 // Walk over the units of this CTA's share.
 struct Walk {
-  int64_t b;       // sequence
+  int32_t b;       // sequence
   SeqWork s;
-  int64_t tiles;   // row tiles of the sequence
-  int64_t i;       // row tile
+  int32_t tiles;   // row tiles of the sequence
+  int32_t i;       // row tile
   int32_t h;       // key head
   int32_t work;    // key tiles of the unit
   int32_t k0;      // first key tile of the unit in this CTA
-  int64_t at;      // global tile index of (this unit, tile k0)
-  int64_t end;     // end of this CTA's share
+  int64_t left;    // tiles of this CTA's share from (this unit, tile k0) on
   int64_t share;
   bool done;
 };
+
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  return (n | d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
 
 // Sum over the CTA's NT threads and the exclusive prefix of each, through shared memory
 // (`tmp`: NT / 32 + 1 values).  Ends with a barrier.
@@ -186,65 +213,67 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* 
 }
 
 // Finds this CTA's share.  All NT threads call it; `tmp` holds NT / 32 + 2 values.
-template <int NT>
+template <int M, int KT, int NT>
 __device__ __forceinline__ Walk find_share(const Pointers& g, const AttendArgs& a, const Cut& c, int64_t* tmp) {
   Walk w;
-  const int64_t nb = c.prefix ? 1 : a.B;
+  const int nb = c.prefix ? 1 : (int)a.B;
   int64_t total = 0, before = 0, mine = 0;
-  for (int64_t base = 0; base < nb; base += NT) {
-    const int64_t b = base + threadIdx.x;
-    mine = b < nb ? seq_total(seq_work(b, g, a, c), a, c) : 0;
+  for (int base = 0; base < nb; base += NT) {
+    const int b = base + threadIdx.x;
+    mine = b < nb ? seq_total<M, KT>(seq_work(b, g, a, c), a, c) : 0;
     total += block_scan<NT>(mine, tmp, &before);
   }
-  w.share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)c.min_share);
-  w.at = w.share * blockIdx.x;
-  w.end = min(w.at + w.share, total);
-  w.done = w.at >= total;
+  w.share = max(quotient(total + gridDim.x - 1, gridDim.x), (int64_t)c.min_share);
+  const int64_t at = w.share * blockIdx.x;
+  w.left = min(w.share, total - at);
+  w.done = at >= total;
   if (w.done) return w;
   int64_t run = 0;
-  for (int64_t base = 0; base < nb; base += NT) {
-    const int64_t b = base + threadIdx.x;
-    if (nb > NT) mine = b < nb ? seq_total(seq_work(b, g, a, c), a, c) : 0;
+  for (int base = 0; base < nb; base += NT) {
+    const int b = base + threadIdx.x;
+    if (nb > NT) mine = b < nb ? seq_total<M, KT>(seq_work(b, g, a, c), a, c) : 0;
     const int64_t sum = nb > NT ? block_scan<NT>(mine, tmp, &before) : total;
-    if (run + before <= w.at && w.at < run + before + mine) {
+    if (run + before <= at && at < run + before + mine) {
       tmp[0] = b;
-      tmp[1] = w.at - run - before;
+      tmp[1] = at - run - before;
     }
     run += sum;
-    if (run > w.at) break;
+    if (run > at) break;
   }
   __syncthreads();
-  w.b = tmp[0];
+  w.b = (int)tmp[0];
   int64_t rest = tmp[1];
   __syncthreads();
   w.s = seq_work(w.b, g, a, c);
-  w.tiles = row_tiles(w.s, c);
+  w.tiles = row_tiles<M>(w.s);
   if (c.prefix) {
-    w.work = tile_work(w.s, 0, a, c);
-    w.i = rest / ((int64_t)w.work * a.nk);
-    rest -= w.i * w.work * a.nk;
+    w.work = tile_work<M, KT>(w.s, 0, a, c);
+    const int64_t row = (int64_t)w.work * a.nk;
+    w.i = (int)quotient(rest, row);
+    rest -= w.i * row;
   } else {
     w.i = 0;
     for (;;) {
-      w.work = tile_work(w.s, w.i, a, c);
+      w.work = tile_work<M, KT>(w.s, w.i, a, c);
       const int64_t row = (int64_t)w.work * a.nk;
       if (rest < row) break;
       rest -= row;
       ++w.i;
     }
   }
-  w.h = (int)(rest / w.work);
+  w.h = (int)quotient(rest, w.work);
   w.k0 = (int)(rest - (int64_t)w.h * w.work);
   return w;
 }
 
 // Key tiles of the current unit in this CTA end here.
-__device__ __forceinline__ int walk_k1(const Walk& w) { return (int)min((int64_t)w.work, w.k0 + (w.end - w.at)); }
+__device__ __forceinline__ int walk_k1(const Walk& w) { return (int)min((int64_t)w.work, w.k0 + w.left); }
 
 // The next unit of the share; w.done at its end.
+template <int M, int KT>
 __device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const AttendArgs& a, const Cut& c) {
-  w.at += walk_k1(w) - w.k0;
-  if (w.at >= w.end) {
+  w.left -= walk_k1(w) - w.k0;
+  if (w.left <= 0) {
     w.done = true;
     return;
   }
@@ -254,40 +283,70 @@ __device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const Atte
   ++w.i;
   while (w.i >= w.tiles) {
     w.i = 0;
-    if (++w.b >= (c.prefix ? 1 : a.B)) {  // a share ends before the last sequence does: never, unless the lengths change under way
+    if (++w.b >= (c.prefix ? 1 : (int)a.B)) {  // a share ends before the last sequence does: never, unless the lengths change under way
       w.done = true;
       return;
     }
     w.s = seq_work(w.b, g, a, c);
-    w.tiles = row_tiles(w.s, c);
+    w.tiles = row_tiles<M>(w.s);
   }
-  w.work = tile_work(w.s, w.i, a, c);
+  w.work = tile_work<M, KT>(w.s, w.i, a, c);
 }
 
-// First and last CTA of the current unit.
-__device__ __forceinline__ int2 walk_ctas(const Walk& w) {
-  const int64_t first = w.at - w.k0;
-  return make_int2((int)(first / w.share), (int)((first + w.work - 1) / w.share));
+// The record of row r of a unit that begins in this CTA: its CTAs and the row's place.
+__device__ __forceinline__ int2 unit_record(const Walk& w, int r) {
+  int last = blockIdx.x;
+  if (w.work > w.left) {  // the rest of the unit, in shares below its size
+    const uint32_t rest = (uint32_t)(w.work - w.left);
+    last += (int)((rest + (uint32_t)w.share - 1) / (uint32_t)w.share);
+  }
+  return make_int2(blockIdx.x | last << 16, r);
+}
+
+// Row r of a unit as (token, head of the group), by 32-bit arithmetic.
+struct UnitRows {
+  int32_t t0;   // token of the unit's first row
+  int32_t rem;  // its head within the group
+  int32_t rows;
+};
+
+template <int M>
+__device__ __forceinline__ UnitRows unit_rows(const Walk& w, const AttendArgs& a) {
+  const unsigned first = (unsigned)w.i * M;
+  UnitRows u;
+  const unsigned t = first / (unsigned)a.G;
+  u.t0 = w.s.t0 + (int)t;
+  u.rem = (int)(first - t * a.G);
+  u.rows = min(M, w.s.rows - (int)first);
+  return u;
+}
+
+struct RowAt {
+  int64_t t;
+  int32_t h;  // query head
+};
+
+__device__ __forceinline__ RowAt row_at(const UnitRows& u, int r, int key_head, const AttendArgs& a) {
+  const unsigned x = (unsigned)(u.rem + r), tt = x / (unsigned)a.G;
+  return {(int64_t)u.t0 + tt, key_head * a.G + (int)(x - tt * a.G)};
 }
 
 __device__ __forceinline__ float* slot_o(const Cut& c, const AttendArgs& a, int64_t cta, int slot) {
   return c.slots + (cta * 2 + slot) * c.slot_rows * a.D;
 }
 
-__device__ __forceinline__ float* slot_ml(const Cut& c, const AttendArgs& a, int64_t grid, int64_t cta, int slot) {
-  return c.slots + grid * 2 * c.slot_rows * a.D + (cta * 2 + slot) * c.slot_rows * 2;
+__device__ __forceinline__ float* slot_ml(const Cut& c, const AttendArgs& a, int64_t cta, int slot) {
+  return c.slots + (int64_t)c.grid * 2 * c.slot_rows * a.D + (cta * 2 + slot) * c.slot_rows * 2;
 }
 
-// Keys j < limit are what row r of the current unit's sequence sees (0 past the last row).
-__device__ __forceinline__ int row_limit(const Walk& w, int64_t r, const Pointers& g, const AttendArgs& a, const Cut& c) {
-  if (r >= w.s.rows) return 0;
+// Keys j < limit are what the row of token t of the current unit's sequence sees.
+__device__ __forceinline__ int row_limit(const Walk& w, int64_t t, const Pointers& g, const AttendArgs& a, const Cut& c) {
   int64_t p;
   if (c.prefix) {
-    const int64_t t = r / a.G;
     const int64_t b = batch_of(t, g, a);
     p = ldg(g.seq_lens + b, a.sl_span, g.err) - (ldg(g.qsl + b + 1, a.qsl_span, g.err) - t) + 1;
   } else {
-    p = w.s.pos0 + r / a.G + 1;
+    p = w.s.pos0 + (t - w.s.t0) + 1;
   }
   return (int)(p < 0 ? 0 : p > w.s.hi ? w.s.hi : p);
 }

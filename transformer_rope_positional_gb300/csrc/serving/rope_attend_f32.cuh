@@ -47,14 +47,11 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP, RPT>())
   F32Shared<DP, RPT>& sm = *reinterpret_cast<F32Shared<DP, RPT>*>(raw);
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   wait_for_prior_grid();
-  Walk w = find_share<kF32Threads>(g, a, c, reinterpret_cast<int64_t*>(sm.p));
+  Walk w = find_share<M, kF32Keys, kF32Threads>(g, a, c, reinterpret_cast<int64_t*>(sm.p));
   while (!w.done) {
     const int k1 = walk_k1(w);
-    const int end = tile_end(w.s, w.i, a, c);
-    const int64_t first = w.i * M;
-    const int u_rows = (int)min((int64_t)M, w.s.rows - first);
-    const int64_t ut = w.s.t0 + first / a.G;
-    const int rem = (int)(first % a.G);
+    const int end = tile_end<M>(w.s, w.i, a, c);
+    const UnitRows u = unit_rows<M>(w, a);
     const int64_t* table = g.block_table + w.b * a.W;
     // cache row of key tid (< 64) of tile k, into rows[k & 1]
     auto look_up = [&](int k) {
@@ -83,9 +80,9 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP, RPT>())
     look_up(w.k0);
     for (int idx = tid; idx < M * CH; idx += kF32Threads) {
       const int r = idx / CH, ch = idx - r * CH;
-      const int x = rem + r, tt = x / a.G;
-      const bool there = r < u_rows && ch * 4 < a.D;
-      const float* p = q + (there ? (ut + tt) * a.q_stride + ((int64_t)w.h * a.G + (x - tt * a.G)) * a.D + ch * 4 : 0);
+      const bool there = r < u.rows && ch * 4 < a.D;
+      const RowAt at = row_at(u, r, w.h, a);
+      const float* p = q + (there ? at.t * a.q_stride + (int64_t)at.h * a.D + ch * 4 : 0);
       cp_async16_or_zero(smem_u32(sm.q + r * DP + ((ch ^ (r & 7)) << 2)), p,
                          there && access_ok(p, 16, a.q_span, g.err));
     }
@@ -94,7 +91,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP, RPT>())
     int limit[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i)
-      limit[i] = ty * RPT + i < u_rows ? row_limit(w, first + ty * RPT + i, g, a, c) : 0;
+      limit[i] = ty * RPT + i < u.rows ? row_limit(w, row_at(u, ty * RPT + i, w.h, a).t, g, a, c) : 0;
     float m[RPT], l[RPT];
     float2 o[RPT][NC * 2];
 #pragma unroll
@@ -209,9 +206,9 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP, RPT>())
 #pragma unroll
       for (int d = 1; d < 16; d *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
       const int r = ty * RPT + i;
-      const bool mine = r < u_rows;
-      const int x = rem + (mine ? r : 0), tt = x / a.G;
-      const int64_t row = (ut + tt) * a.nq + (int64_t)w.h * a.G + (x - tt * a.G);
+      const bool mine = r < u.rows;
+      const RowAt at = row_at(u, mine ? r : 0, w.h, a);
+      const int64_t row = at.t * a.nq + at.h;
       const float f = !final ? 1.f : l[i] == 0.f ? 0.f : 1.f / l[i];
       float* const to = final ? out + row * a.D
                         : whole ? c.dense + row * a.D
@@ -233,14 +230,14 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP, RPT>())
             lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.693147180559945309f;
         } else {
           float* ml = whole ? c.dense + a.T * a.nq * a.D + row * 2
-                            : slot_ml(c, a, gridDim.x, blockIdx.x, begins ? 1 : 0) + r * 2;
+                            : slot_ml(c, a, blockIdx.x, begins ? 1 : 0) + r * 2;
           *reinterpret_cast<float2*>(ml) = make_float2(m[i], l[i]);
         }
-        if (begins) c.rec[row] = final && !all_fine ? make_int2(-1, -1) : walk_ctas(w);
+        if (begins) c.rec[row] = final && !all_fine ? make_int2(-1, -1) : unit_record(w, r);
       }
     }
     __syncthreads();  // the buffers are free
-    walk_next(w, g, a, c);
+    walk_next<M, kF32Keys>(w, g, a, c);
   }
 }
 

@@ -41,7 +41,7 @@ struct MmaShared {
   static constexpr int kStage = 2 * 16 * DP * 2;  // bytes of K and V of one warp's 16 keys
   alignas(1024) unsigned char ring[4][mma_stages<DP>()][kStage];
   alignas(16) unsigned char q[16 * DP * 2];
-  float o[16][DP + 8];
+  float o[4][4][DP + 8];  // four rows of the four warps
   float ml[4][16][2];
   int bad[16];
   int64_t tmp[kMmaThreads / 32 + 2];
@@ -111,13 +111,13 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
   MmaShared<DP>& sm = *reinterpret_cast<MmaShared<DP>*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_prior_grid();
-  Walk w = find_share<kMmaThreads>(g, a, c, sm.tmp);
+  Walk w = find_share<kMmaRows, kMmaKeys, kMmaThreads>(g, a, c, sm.tmp);
   if (w.done) return;
 
   // ---- copies: the tiles of the share, in order, into the warp's ring
   Walk pw = w;
   int pk = pw.k0;
-  int pend = tile_end(pw.s, pw.i, a, c);
+  int pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
   int slot = 0;                   // stage of the next copy
   unsigned char* const ring = sm.ring[warp][0];
   // cache row of this lane's key (lane & 15) of the next tile, looked up ahead of its copy
@@ -151,9 +151,9 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
       uint32_t& word = slot < 2 ? valid : slot < 4 ? valid_hi : valid_top;
       word = slot & 1 ? (word & 0x0000ffffu) | (there << 16) : (word & 0xffff0000u) | there;
       if (++pk == walk_k1(pw)) {
-        walk_next(pw, g, a, c);
+        walk_next<kMmaRows, kMmaKeys>(pw, g, a, c);
         pk = pw.k0;
-        if (!pw.done) pend = tile_end(pw.s, pw.i, a, c);
+        if (!pw.done) pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
       }
       next = look_up();
     }
@@ -170,18 +170,33 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
   const int k_row = ((lane >> 4) << 3) + (lane & 7), k_ch = (lane >> 3) & 1;
   const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_ch = lane >> 4;
 
-  while (!w.done) {
-    // ---- the unit's query rows, as A operands
-    for (int idx = threadIdx.x; idx < 16 * CH; idx += kMmaThreads) {
+  // a unit's query rows, in 16-byte pieces of this thread: read while the unit before ends
+  constexpr int NQ = 16 * CH / kMmaThreads;
+  uint4 qv[NQ];
+  auto read_q = [&](const Walk& x) {
+    const UnitRows u = unit_rows<kMmaRows>(x, a);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int idx = threadIdx.x + kMmaThreads * i;
       const int r = idx / CH, ch = idx - r * CH;
-      const int64_t rr = w.i * kMmaRows + r;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (rr < w.s.rows && ch * 8 < a.D) {
-        const int64_t t = w.s.t0 + rr / a.G;
-        const T* p = q + t * a.q_stride + ((int64_t)w.h * a.G + rr % a.G) * a.D + ch * 8;
-        if (access_ok(p, 16, a.q_span, g.err)) v = __ldg(reinterpret_cast<const uint4*>(p));
+      qv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < u.rows && ch * 8 < a.D) {
+        const RowAt at = row_at(u, r, x.h, a);
+        const T* p = q + at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8;
+        if (access_ok(p, 16, a.q_span, g.err)) qv[i] = __ldg(reinterpret_cast<const uint4*>(p));
       }
-      *reinterpret_cast<uint4*>(sm.q + r * (DP * 2) + ((ch ^ (r & 7)) << 4)) = v;
+    }
+  };
+  read_q(w);
+
+  while (!w.done) {
+    const UnitRows u = unit_rows<kMmaRows>(w, a);
+    // ---- the unit's query rows, as A operands
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int idx = threadIdx.x + kMmaThreads * i;
+      const int r = idx / CH, ch = idx - r * CH;
+      *reinterpret_cast<uint4*>(sm.q + r * (DP * 2) + ((ch ^ (r & 7)) << 4)) = qv[i];
     }
     if (threadIdx.x < 16) sm.bad[threadIdx.x] = 0;
     __syncthreads();
@@ -194,7 +209,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) load_q(qa[ks], ks);
     }
-    int lim0 = lane < 16 ? row_limit(w, w.i * kMmaRows + lane, g, a, c) : 0;
+    int lim0 = lane < u.rows ? row_limit(w, row_at(u, lane, w.h, a).t, g, a, c) : 0;
     const int lim1 = __shfl_sync(0xffffffffu, lim0, r0 + 8);
     lim0 = __shfl_sync(0xffffffffu, lim0, r0);
     const int k1 = walk_k1(w);
@@ -278,7 +293,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
       __syncwarp();
     }
 
-    // ---- the four warps' rows together
+    // ---- the four warps' rows together, four rows at a time, to the output or a partial result
 #pragma unroll
     for (int d = 1; d < 4; d *= 2) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -290,92 +305,67 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
       sm.ml[warp][r0 + 8][0] = m1;
       sm.ml[warp][r0 + 8][1] = l1;
     }
-    __syncthreads();
-    auto joined = [&](int r, float& m, float& l) {
-      m = fmaxf(fmaxf(sm.ml[0][r][0], sm.ml[1][r][0]), fmaxf(sm.ml[2][r][0], sm.ml[3][r][0]));
-      const float b = m == -INFINITY ? 0.f : m;
-      l = 0.f;
+    Walk nw = w;
+    walk_next<kMmaRows, kMmaKeys>(nw, g, a, c);
+    if (!nw.done) read_q(nw);
+    const bool begins = w.k0 == 0, whole = begins && k1 == w.work, final = whole && !c.shared;
+    float* const po = slot_o(c, a, blockIdx.x, begins ? 1 : 0);
+    float* const pml = slot_ml(c, a, blockIdx.x, begins ? 1 : 0);
+    for (int p4 = 0; p4 < u.rows; p4 += 4) {
+      if ((r0 & 4) == (p4 & 4)) {  // this lane has row r0 & 3 of the four: r0, or r0 + 8
+        float* to = &sm.o[warp][r0 & 3][cq];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) l += sm.ml[j][r][1] * fast_exp2(sm.ml[j][r][0] - b);
-    };
-    {
-      const float a0 = fmaxf(fmaxf(sm.ml[0][r0][0], sm.ml[1][r0][0]), fmaxf(sm.ml[2][r0][0], sm.ml[3][r0][0]));
-      const float a1 =
-          fmaxf(fmaxf(sm.ml[0][r0 + 8][0], sm.ml[1][r0 + 8][0]), fmaxf(sm.ml[2][r0 + 8][0], sm.ml[3][r0 + 8][0]));
-      const float f0 = fast_exp2(m0 - (a0 == -INFINITY ? 0.f : a0)), f1 = fast_exp2(m1 - (a1 == -INFINITY ? 0.f : a1));
+        for (int n = 0; n < DP / 8; ++n)
+          *reinterpret_cast<float2*>(to + n * 8) = p4 < 8 ? make_float2(o[n][0], o[n][1]) : make_float2(o[n][2], o[n][3]);
+      }
+      __syncthreads();
+      for (int idx = threadIdx.x; idx < DP; idx += kMmaThreads) {  // 4 rows x DP / 4 pieces
+        const int r = idx / (DP / 4), d = (idx - r * (DP / 4)) * 4;
+        const int rr = p4 + r;
+        if (rr >= u.rows || d >= a.D) continue;
+        const float m = fmaxf(fmaxf(sm.ml[0][rr][0], sm.ml[1][rr][0]), fmaxf(sm.ml[2][rr][0], sm.ml[3][rr][0]));
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // in the warps' order
-        if (warp == j) {
-#pragma unroll
-          for (int n = 0; n < DP / 8; ++n) {
-            float2* p0 = reinterpret_cast<float2*>(&sm.o[r0][n * 8 + cq]);
-            float2* p1 = reinterpret_cast<float2*>(&sm.o[r0 + 8][n * 8 + cq]);
-            const float2 x0 = make_float2(o[n][0] * f0, o[n][1] * f0), x1 = make_float2(o[n][2] * f1, o[n][3] * f1);
-            if (j == 0) {
-              *p0 = x0;
-              *p1 = x1;
-            } else {
-              const float2 y0 = *p0, y1 = *p1;
-              *p0 = make_float2(y0.x + x0.x, y0.y + x0.y);
-              *p1 = make_float2(y1.x + x1.x, y1.y + x1.y);
-            }
+        for (int j = 0; j < 4; ++j) {
+          const float f = fast_exp2(sm.ml[j][rr][0] - base);
+          const float4 x = *reinterpret_cast<const float4*>(&sm.o[j][r][d]);
+          l = fmaf(sm.ml[j][rr][1], f, l);
+          v.x = fmaf(x.x, f, v.x);
+          v.y = fmaf(x.y, f, v.y);
+          v.z = fmaf(x.z, f, v.z);
+          v.w = fmaf(x.w, f, v.w);
+        }
+        const RowAt at = row_at(u, rr, w.h, a);
+        const int64_t row = at.t * a.nq + at.h;
+        if (final) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+          if (!(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX &&
+                l <= FLT_MAX))
+            sm.bad[rr] = 1;
+          Vec<T, 4> y;
+          narrow2(&y.e[0], make_float2(v.x, v.y));
+          narrow2(&y.e[2], make_float2(v.z, v.w));
+          store_vec(out + row * a.D + d, y, a.out_span, g.err);
+          if (d == 0 && lse && access_ok(lse + row, 4, a.lse_span, g.err))
+            lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+        } else {
+          *reinterpret_cast<float4*>(whole ? c.dense + row * a.D + d : po + rr * a.D + d) = v;
+          if (d == 0) {
+            float* ml = whole ? c.dense + a.T * a.nq * a.D + row * 2 : pml + rr * 2;
+            *reinterpret_cast<float2*>(ml) = make_float2(m, l);
           }
         }
-        __syncthreads();
       }
+      __syncthreads();
     }
-    // ---- to the output, or to a partial result
-    const bool begins = w.k0 == 0, ends = k1 == w.work;
-    const bool whole = begins && ends;
-    float* const po = slot_o(c, a, blockIdx.x, begins ? 1 : 0);
-    float* const pml = slot_ml(c, a, gridDim.x, blockIdx.x, begins ? 1 : 0);
-    const int DC = a.D / 8;
-    for (int idx = threadIdx.x; idx < 16 * DC; idx += kMmaThreads) {
-      const int r = idx / DC, d = (idx - r * DC) * 8;
-      const int64_t rr = w.i * kMmaRows + r;
-      if (rr >= w.s.rows) break;
-      const int64_t t = w.s.t0 + rr / a.G;
-      const int64_t row = t * a.nq + (int64_t)w.h * a.G + rr % a.G;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = sm.o[r][d + e];
-      if (whole && !c.shared) {
-        float m, l;
-        joined(r, m, l);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        Vec<T, 8> y;
-        bool fine = true;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] *= inv;
-          fine = fine && fabsf(v[e]) <= FLT_MAX;
-          y.e[e] = narrow<T>(v[e]);
-        }
-        if (!fine || !(l <= FLT_MAX)) sm.bad[r] = 1;
-        store_vec(out + row * a.D + d, y, a.out_span, g.err);
-        if (d == 0 && lse && access_ok(lse + row, 4, a.lse_span, g.err))
-          lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
-      } else {
-        float* to = whole ? c.dense + row * a.D + d : po + r * a.D + d;
-        *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        if (d == 0) {
-          float m, l;
-          joined(r, m, l);
-          float* ml = whole ? c.dense + a.T * a.nq * a.D + row * 2 : pml + r * 2;
-          *reinterpret_cast<float2*>(ml) = make_float2(m, l);
-        }
-      }
+    if (begins && threadIdx.x < u.rows) {
+      const RowAt at = row_at(u, threadIdx.x, w.h, a);
+      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record(w, threadIdx.x);
     }
-    __syncthreads();
-    if (begins && threadIdx.x < 16) {
-      const int64_t rr = w.i * kMmaRows + threadIdx.x;
-      if (rr < w.s.rows) {
-        const int64_t row = (w.s.t0 + rr / a.G) * a.nq + (int64_t)w.h * a.G + rr % a.G;
-        c.rec[row] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : walk_ctas(w);
-      }
-    }
-    walk_next(w, g, a, c);
+    w = nw;
   }
   cp_async_wait<0>();
 }

@@ -3,10 +3,12 @@
 //
 // Bound by the matrix units (two products of M x KT x D per key tile) once the rows of a unit
 // outnumber about 280 operations per byte of K and V, so the kernel keeps tcgen05.mma fed:
-//  * one CTA per SM, its warps in roles.  Four warps copy Q, K and V tiles into shared memory
+//  * one CTA per SM, its warps in roles.  Two warps copy Q, K and V tiles into shared memory
 //    with cp.async (any page size and row order: a page's rows are found key by key), one
 //    thread issues the products, and one or two groups of four warps do the softmax, one
-//    thread a row.  Everything between them is barriers in shared memory.
+//    thread a row.  Everything between them is barriers in shared memory.  (11 warps leave a
+//    thread 168 registers, so that a row's 128 scores are read once; four copying warps left
+//    128 and two passes over the scores.)
 //  * scores S = Q K^T (128 rows x KT keys) land in tensor memory; the softmax threads read
 //    their row, write the weights over it in 16 bits, and O += P V takes them from there as
 //    its A operand: scores and weights never touch shared memory.
@@ -40,11 +42,12 @@ struct TcShape {
   static constexpr int M = 128 * NW;                // rows of a unit
   static constexpr int kStage = KT * DP * 2;        // bytes of a K or V tile
   static constexpr int NS = DP <= 64 ? 8 : 5;       // tiles in the ring
-  static constexpr int kLag = NS - 2;               // copies in flight beyond the oldest
   static constexpr int kQ = 128 * DP * 2;           // bytes of a row tile
   static constexpr int kSoftmax = 128 * NW;         // softmax threads
-  static constexpr int kThreads = kSoftmax + 128 + 32;
-  static constexpr int KW = KT / 4;                 // keys a copying warp takes
+  static constexpr int kCopy = 64;                  // copying threads
+  static constexpr int kThreads = kSoftmax + kCopy + 32;
+  static constexpr int KW = KT / 2;                 // keys a copying warp takes
+  static constexpr int KL = KW / 32;                // of them, keys a lane looks up
   static constexpr int kS = KT;                     // columns between the score buffers
   static constexpr int kO = 256;                    // first column of O; the second O follows
 };
@@ -66,24 +69,6 @@ struct TcShared {
   uint32_t tmem;
   int dead;
 };
-
-// Row r of the unit's tile as (token, head of the group), by 32-bit arithmetic.
-struct UnitRows {
-  int64_t t0;   // token of the unit's first row
-  int32_t rem;  // its head within the group
-  int32_t rows;
-};
-
-template <int M>
-__device__ __forceinline__ UnitRows unit_rows(const Walk& w, const AttendArgs& a) {
-  const int64_t first = w.i * M;
-  UnitRows u;
-  const int64_t t = first / a.G;
-  u.t0 = w.s.t0 + t;
-  u.rem = (int32_t)(first - t * a.G);
-  u.rows = (int32_t)min((int64_t)M, w.s.rows - first);
-  return u;
-}
 
 // Tile of the n-th copy of a unit of kt key tiles, `lead` of whose K tiles come first: the
 // order in which the products take them, K_0 .. K_(lead-1), V_0, K_lead, V_1, ...
@@ -116,7 +101,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char raw[];
   TcShared<DP>& sm = *reinterpret_cast<TcShared<DP>*>(raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + 4;
+  constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + S::kCopy / 32;
 
   if (tc::smem_at(raw) & 1023) {  // the operands' swizzle counts on it
     if (tid == 0) atomicOr(g.err, kWaitExpired);
@@ -125,10 +110,10 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   if (tid == 0) {
     sm.dead = 0;
     for (int i = 0; i < NS; ++i) {
-      tc::bar_init(&sm.full[i], 128);
+      tc::bar_init(&sm.full[i], S::kCopy);
       tc::bar_init(&sm.empty[i], 1);
     }
-    tc::bar_init(&sm.q_full, 128);
+    tc::bar_init(&sm.q_full, S::kCopy);
     tc::bar_init(&sm.q_free, 1);
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&sm.s_full[i], 1);
@@ -136,13 +121,13 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       tc::bar_init(&sm.pv_done[i], 1);
       tc::bar_init(&sm.o_free[i], 128);
     }
-    for (int i = 0; i < 16; ++i) tc::bar_init(&sm.seen_full[i], 4);
+    for (int i = 0; i < 16; ++i) tc::bar_init(&sm.seen_full[i], S::kCopy / 32);
     tc::bar_init(&sm.ml_full, 128);
     tc::bar_init(&sm.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   wait_for_prior_grid();
-  Walk w = find_share<S::kThreads>(g, a, c, sm.tmp);
+  Walk w = find_share<S::M, KT, S::kThreads>(g, a, c, sm.tmp);
   if (w.done) return;
   if (warp == kMmaWarp) {
     tc::tmem_alloc(&sm.tmem, 512);
@@ -155,132 +140,131 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
 
   if (warp >= kCopyWarp && warp < kMmaWarp) {
     // ------------------------------------------------------------------ copies
+    // Copies never wait for their data: the barrier of a tile gets an arrival of each copying
+    // thread when its part is there.  Pages are looked up one K tile ahead; the rows of a tile
+    // are kept until its V follows.
     const int cw = warp - kCopyWarp, ct = tid - S::kSoftmax;
-    int64_t issued = 0;   // ring tiles so far
-    int64_t arrived = 0;  // of them, handed over
-    int64_t k_count = 0;  // K tiles so far
+    int stage = 0;
+    unsigned round = 0;   // of the ring
+    int k_count = 0;      // K tiles so far
     unsigned unit = 0;
     bool ok = true;
-    auto hand_over = [&]() {  // the oldest tile not handed over is complete for this thread
-      tc::fence_to_tensor();
-      tc::bar_arrive(&sm.full[arrived % NS]);
-      ++arrived;
-    };
-    auto flush = [&]() {
-      cp_async_wait<0>();
-      while (arrived < issued) hand_over();
-    };
     while (!w.done) {
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
       const int lead = nt == 2 ? 1 : 2;
       const int k1 = walk_k1(w), kt = k1 - w.k0;
-      const int end = tile_end(w.s, w.i, a, c);
+      const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
-      // cache row of this lane's key of the n-th copy
-      auto look_up = [&](int n) -> int64_t {
-        if (n >= 2 * kt) return -1;
-        const int j = c.lo + (w.k0 + copy_item(n, kt, lead).tile) * KT + cw * S::KW + (lane & (S::KW - 1));
-        if (j >= end) return -1;
-        const int64_t r = key_row(j, table, g, a);
-        if (r < 0) atomicOr(g.err, kSlotOutOfRange);
-        return r < 0 ? -1 : (r + (int64_t)w.h * a.block_size) * a.D;
+      PageRow pages[S::KL];  // of this lane's keys (lane, lane + 32) of the next K tile
+      int rows[2][S::KL];    // cache rows of its keys of the last two K tiles, -1 where there is none
+      auto look_up = [&](int tile) {
+#pragma unroll
+        for (int i = 0; i < S::KL; ++i) {
+          const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + i * 32 + lane;
+          pages[i] = {-2, 0};  // no such key
+          if (tile < kt && j < end) pages[i] = page_row(j, table, g, a);
+        }
       };
-      int64_t next = look_up(0);
+      look_up(0);
       // ---- Q, once the last unit's scores are done
-      if (unit > 0 && !tc::bar_try(&sm.q_free, (unit - 1) & 1)) {
-        flush();
-        ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
-      }
+      if (unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
       ++unit;
       if (!__all_sync(0xffffffffu, ok)) break;
-      for (int idx = ct; idx < 128 * nt * CH; idx += 128) {
+#pragma unroll 4
+      for (int idx = ct; idx < 128 * nt * CH; idx += S::kCopy) {
         const int r = idx / CH, ch = idx - r * CH;
-        const int x = u.rem + r, tt = x / a.G;
         const bool there = r < u.rows && ch * 8 < a.D;
-        const T* p = q + (there ? (u.t0 + tt) * a.q_stride + ((int64_t)w.h * a.G + (x - tt * a.G)) * a.D + ch * 8 : 0);
+        const RowAt at = row_at(u, r, w.h, a);
+        const T* p = q + (there ? at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8 : 0);
         const int rr = r & 127;
         cp_async16_or_zero(tc::smem_at(sm.q[NW == 2 ? r >> 7 : 0]) + (ch >> 3) * (128 * 128) + rr * 128 +
                                (((ch & 7) ^ (rr & 7)) << 4),
                            p, there && access_ok(p, 16, a.q_span, g.err));
       }
-      cp_async_commit();
-      flush();
-      tc::fence_to_tensor();
-      tc::bar_arrive(&sm.q_full);
+      tc::bar_arrive_after_copies(&sm.q_full);
       // ---- K and V
       for (int n = 0; n < 2 * kt; ++n) {
         const CopyItem it = copy_item(n, kt, lead);
-        const int st = (int)(issued % NS);
-        const unsigned round = (unsigned)(issued / NS);
-        if (round > 0 && !tc::bar_try(&sm.empty[st], (round - 1) & 1)) {
-          flush();
-          ok = tc::bar_wait(&sm.empty[st], (round - 1) & 1, &sm.dead);
-        }
+        if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const unsigned dst = tc::smem_at(sm.ring[st]) + cw * S::KW * 128;
+        int now[S::KL];
+        if (!it.is_v) {
+#pragma unroll
+          for (int i = 0; i < S::KL; ++i) {
+            int r = -1;
+            if (pages[i].page >= 0 && pages[i].page < a.num_blocks)
+              r = ((int)pages[i].page * a.nk + w.h) * a.block_size + pages[i].row;
+            else if (pages[i].page != -2)
+              atomicOr(g.err, kSlotOutOfRange);
+            now[i] = r;
+            if (it.tile & 1) rows[1][i] = r;
+            else rows[0][i] = r;
+            const uint32_t there = __ballot_sync(0xffffffffu, r >= 0);
+            if (lane == 0) sm.seen[k_count & 15][cw * S::KL + i] = there;
+          }
+          if (lane == 0) tc::bar_arrive(&sm.seen_full[k_count & 15]);
+          ++k_count;
+          look_up(it.tile + 1);
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::KL; ++i) now[i] = it.tile & 1 ? rows[1][i] : rows[0][i];
+        }
+        const unsigned dst = tc::smem_at(sm.ring[stage]) + cw * S::KW * 128;
         const T* const src = it.is_v ? vc : kc;
         const Span& span = it.is_v ? a.v_span : a.k_span;
 #pragma unroll
         for (int i = 0; i < S::KW * CH / 32; ++i) {
           const int idx = lane + 32 * i;
           const int key = idx / CH, ch = idx - key * CH;
-          const int64_t at = __shfl_sync(0xffffffffu, next, key);
-          const bool there = at >= 0 && ch * 8 < a.D;
-          const T* p = src + (there ? at + ch * 8 : 0);
+          const int r = __shfl_sync(0xffffffffu, now[i * 32 / CH / 32], key & 31);
+          const bool there = r >= 0 && ch * 8 < a.D;
+          const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 8 : 0));
           cp_async16_or_zero(dst + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), p,
                              there && access_ok(p, 16, span, g.err));
         }
-        cp_async_commit();
-        if (!it.is_v) {
-          const uint32_t there = __ballot_sync(0xffffffffu, next >= 0);
-          if (lane == 0) {
-            sm.seen[k_count & 15][cw] = there;
-            tc::bar_arrive(&sm.seen_full[k_count & 15]);
-          }
-          ++k_count;
-        }
-        ++issued;
-        next = look_up(n + 1);
-        if (issued - arrived > S::kLag) {
-          cp_async_wait<S::kLag>();
-          hand_over();
-        }
+        tc::bar_arrive_after_copies(&sm.full[stage]);
+        if (++stage == NS) stage = 0, ++round;
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      walk_next(w, g, a, c);
+      walk_next<S::M, KT>(w, g, a, c);
     }
-    flush();
+    cp_async_commit();
+    cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ products
     if (lane == 0) {
       constexpr uint32_t kScores = tc::instruction<T>(128, KT, false), kOutput = tc::instruction<T>(128, DP, true);
-      int64_t taken = 0;  // ring tiles so far
+      int next_stage = 0;
+      unsigned round = 0;  // of the ring
       unsigned unit = 0;
       unsigned p_seen[2] = {0, 0}, o_units[2] = {0, 0};
       bool ok = true;
       while (!w.done && ok) {
-        const int nt = min((int64_t)S::M, w.s.rows - w.i * S::M) > 128 ? 2 : 1;
+        const int nt = w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1;
         const int kt = walk_k1(w) - w.k0, jobs = kt * nt;
         ok = tc::bar_wait(&sm.q_full, unit & 1, &sm.dead);
+        tc::fence_to_tensor();
         ++unit;
         if (!ok) break;
         int k_stage = 0, v_stage = 0;
         auto take = [&](int& stage) {
-          stage = (int)(taken % NS);
-          ok = ok && tc::bar_wait(&sm.full[stage], (unsigned)(taken / NS) & 1, &sm.dead);
-          ++taken;
+          stage = next_stage;
+          ok = ok && tc::bar_wait(&sm.full[stage], round & 1, &sm.dead);
+          tc::fence_to_tensor();
+          if (++next_stage == NS) next_stage = 0, ++round;
         };
         auto scores = [&](int x) {
           const int tile = nt == 2 ? x & 1 : 0;
           if (nt == 1 || tile == 0) take(k_stage);
           if (!ok) return;
           tc::fence_after();
-          const unsigned qa = tc::smem_at(sm.q[NW == 2 ? tile : 0]), ka = tc::smem_at(sm.ring[k_stage]);
+          const uint64_t qa = tc::k_major(tc::smem_at(sm.q[NW == 2 ? tile : 0]));
+          const uint64_t ka = tc::k_major(tc::smem_at(sm.ring[k_stage]));
 #pragma unroll
-          for (int ks = 0; ks < DP / 16; ++ks)
-            tc::mma_ss(tm + (x & 1) * S::kS, tc::k_major(qa + (ks >> 2) * (128 * 128) + (ks & 3) * 32),
-                       tc::k_major(ka + (ks >> 2) * (KT * 128) + (ks & 3) * 32), kScores, ks > 0);
+          for (int ks = 0; ks < DP / 16; ++ks)  // descriptors count in 16 bytes
+            tc::mma_ss(tm + (x & 1) * S::kS, qa + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16,
+                       ka + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16, kScores, ks > 0);
           tc::commit(&sm.s_full[x & 1]);
           if (nt == 1 || tile == 1) tc::commit(&sm.empty[k_stage]);
           if (x == jobs - 1) tc::commit(&sm.q_free);
@@ -297,16 +281,16 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           ++p_seen[buf];
           if (!ok) break;
           tc::fence_after();
-          const unsigned va = tc::smem_at(sm.ring[v_stage]);
+          const uint64_t va = tc::mn_major(tc::smem_at(sm.ring[v_stage]), KT * 128);
 #pragma unroll
           for (int ks = 0; ks < KT / 16; ++ks)
-            tc::mma_ts(tm + S::kO + o * DP, tm + buf * S::kS + ks * 8, tc::mn_major(va + ks * 2048, KT * 128), kOutput,
+            tc::mma_ts(tm + S::kO + o * DP, tm + buf * S::kS + ks * 8, va + ks * 2048 / 16, kOutput,
                        !first || ks > 0);
           tc::commit(&sm.pv_done[o]);
           if (nt == 1 || buf == 1) tc::commit(&sm.empty[v_stage]);
           if (x + 2 < jobs) scores(x + 2);
         }
-        if (ok) walk_next(w, g, a, c);
+        if (ok) walk_next<S::M, KT>(w, g, a, c);
       }
       // everything issued is done before the tensor memory is given back
       tc::commit(&sm.drained);
@@ -321,7 +305,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     unsigned s_seen[2] = {0, 0};
     unsigned pv = 0;          // products into this group's O so far
-    int64_t k_base = 0;       // K tiles before this unit
+    int k_base = 0;           // K tiles before this unit
     unsigned ml_seen = 0;
     bool ok = true;
     while (!w.done) {
@@ -329,7 +313,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const int nt = u.rows > 128 ? 2 : 1;
       const int k1 = walk_k1(w), kt = k1 - w.k0, jobs = kt * nt;
       const int r = nt == 2 ? group * 128 + r_tile : r_tile;
-      const int limit = r < u.rows ? row_limit(w, w.i * S::M + r, g, a, c) : 0;
+      const bool mine = r < u.rows;
+      const RowAt at = row_at(u, mine ? r : 0, w.h, a);
+      const int limit = mine ? row_limit(w, at.t, g, a, c) : 0;
       const uint32_t t_o = tm + lanes + S::kO + (NW == 2 ? group : 0) * DP;
       float m = -INFINITY, l = 0.f;
       bool any = false;  // O holds something of this unit
@@ -339,38 +325,38 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const int j0 = c.lo + (w.k0 + kk) * KT;
         const uint32_t t_s = tm + lanes + buf * S::kS;
         ok = tc::bar_wait(&sm.seen_full[(k_base + kk) & 15], (unsigned)((k_base + kk) >> 4) & 1, &sm.dead);
-        uint32_t there[4];
+        uint32_t there[KT / 32];
         bool all_there = true;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < KT / 32; ++i) {
           there[i] = sm.seen[(k_base + kk) & 15][i];
           all_there = all_there && there[i] == 0xffffffffu;
-        }
-        if constexpr (KT == 64) {  // 16 keys a word (the upper lanes repeat them)
-          there[0] = (there[0] & 0xffffu) | (there[1] << 16);
-          there[1] = (there[2] & 0xffffu) | (there[3] << 16);
         }
         ok = ok && tc::bar_wait(&sm.s_full[buf], s_seen[buf] & 1, &sm.dead);
         ++s_seen[buf];
         if (!__all_sync(0xffffffffu, ok)) break;
         tc::fence_after();
         const bool open = __all_sync(0xffffffffu, all_there && j0 + KT <= limit);
-        auto hide = [&](uint32_t (&v)[32], int ch) {  // scores of unseen keys of columns ch * 32 ..
-          const uint32_t word = there[ch];
+        uint32_t v[KT / 32][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((word >> i) & 1) || j0 + ch * 32 + i >= limit) v[i] = 0xff800000u;
-        };
-        float top = -INFINITY;
+        for (int ch = 0; ch < KT / 32; ++ch) tc::tmem_load32(v[ch], t_s + ch * 32);
+        tc::wait_loads();
+        if (!open) {  // scores of unseen keys
 #pragma unroll
-        for (int ch = 0; ch < KT / 32; ++ch) {
-          uint32_t v[32];
-          tc::tmem_load32(v, t_s + ch * 32);
-          tc::wait_loads();
-          if (!open) hide(v, ch);
+          for (int ch = 0; ch < KT / 32; ++ch) {
+            const uint32_t word = there[ch];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) top = max3(top, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            for (int i = 0; i < 32; ++i)
+              if (!((word >> i) & 1) || j0 + ch * 32 + i >= limit) v[ch][i] = 0xff800000u;
+          }
         }
+        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int ch = 0; ch < KT / 32; ++ch)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
+        const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
         const float mt = top * a.scale_log2;  // -infinity stays (scale > 0)
         if (!any) {
           m = mt;
@@ -383,14 +369,14 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           const float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
           l *= f;
           m = up;
-#pragma unroll
-          for (int ch = 0; ch < DP / 32; ++ch) {
-            uint32_t v[32];
-            tc::tmem_load32(v, t_o + ch * 32);
+#pragma unroll 1
+          for (int ch = 0; ch < DP / 16; ++ch) {  // rare: few registers rather than few waits
+            uint32_t x[16];
+            tc::tmem_load16(x, t_o + ch * 16);
             tc::wait_loads();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-            tc::tmem_store32(t_o + ch * 32, v);
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            tc::tmem_store16(t_o + ch * 16, x);
           }
         }
         any = true;
@@ -399,19 +385,17 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int ch = 0; ch < KT / 32; ++ch) {
-          uint32_t v[32], p[16];
-          tc::tmem_load32(v, t_s + ch * 32);
-          tc::wait_loads();
-          if (!open) hide(v, ch);
+          uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            float2 e = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, minus2);
+            float2 e =
+                __ffma2_rn(make_float2(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])), scale2, minus2);
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
             sum = __fadd2_rn(sum, e);
             p[i / 2] = pack2((const T*)nullptr, e.x, e.y);
           }
-          tc::tmem_store16(t_s + ch * 16, p);  // over scores that this thread has read
+          tc::tmem_store16(t_s + ch * 16, p);  // over the scores
         }
         l += sum.x + sum.y;
         // pv_done is waited for by parity, so it may be one product behind at most.  With two groups
@@ -453,9 +437,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       if (!(NW == 2 && nt == 1 && group == 1)) {
         const bool begins = w.k0 == 0, whole = begins && k1 == w.work;
         const bool final = whole && !c.shared;
-        const bool mine = r < u.rows;
-        const int xr = u.rem + (mine ? r : 0), tt = xr / a.G;
-        const int64_t row = (u.t0 + tt) * a.nq + (int64_t)w.h * a.G + (xr - tt * a.G);
+        const int64_t row = at.t * a.nq + at.h;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (final) {
           f0 *= inv;
@@ -502,10 +484,10 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
               lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
           } else {
             float* ml = whole ? c.dense + a.T * a.nq * a.D + row * 2
-                              : slot_ml(c, a, gridDim.x, blockIdx.x, begins ? 1 : 0) + r * 2;
+                              : slot_ml(c, a, blockIdx.x, begins ? 1 : 0) + r * 2;
             *reinterpret_cast<float2*>(ml) = make_float2(m, l);
           }
-          if (begins) c.rec[row] = final && !fine ? make_int2(-1, -1) : walk_ctas(w);
+          if (begins) c.rec[row] = final && !fine ? make_int2(-1, -1) : unit_record(w, r);
         }
       }
       // O may be written again: by the group that read it (both, when it read both)
@@ -516,7 +498,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         tc::bar_arrive(&sm.o_free[0]);
         if (halves) tc::bar_arrive(&sm.o_free[1]);
       }
-      walk_next(w, g, a, c);
+      walk_next<S::M, KT>(w, g, a, c);
     }
   }
   __syncthreads();

@@ -60,8 +60,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity, int* de
   }
 }
 
-// Shared memory written by this thread's ordinary stores (or finished cp.async copies) becomes
-// visible to the tensor core.
+// The barrier gets one arrival when all cp.async copies of this thread so far are there.
+__device__ __forceinline__ void bar_arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_at(bar)) : "memory");
+}
+
+// Shared memory written by ordinary stores or cp.async copies, this thread's or others' that it
+// has waited for, is visible to the products that this thread issues from here on.
 __device__ __forceinline__ void fence_to_tensor() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
@@ -92,6 +97,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&v)[32], uint32_t at) {
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : ROPE_R8(v, 0), ROPE_R8(v, 8), ROPE_R8(v, 16), ROPE_R8(v, 24)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&v)[16], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : ROPE_R8(v, 0), ROPE_R8(v, 8)
       : "r"(at)
       : "memory");
 }
