@@ -233,34 +233,34 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      constexpr uint32_t kScores = tc::instruction<T>(128, KT, false), kOutput = tc::instruction<T>(128, DP, true);
-      int next_stage = 0;
-      unsigned round = 0;  // of the ring
-      unsigned unit = 0;
-      unsigned p_seen[2] = {0, 0}, o_units[2] = {0, 0};
-      bool ok = true;
-      while (!w.done && ok) {
-        const int nt = w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1;
-        const int kt = walk_k1(w) - w.k0, jobs = kt * nt;
-        ok = tc::bar_wait(&sm.q_full, unit & 1, &sm.dead);
+    constexpr uint32_t kScores = tc::instruction<T>(128, KT, false), kOutput = tc::instruction<T>(128, DP, true);
+    int next_stage = 0;
+    unsigned round = 0;  // of the ring
+    unsigned unit = 0;
+    unsigned p_seen[2] = {0, 0}, o_units[2] = {0, 0};
+    bool ok = true;
+    while (!w.done && ok) {
+      const int nt = w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1;
+      const int kt = walk_k1(w) - w.k0, jobs = kt * nt;
+      ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.q_full, unit & 1, &sm.dead));
+      tc::fence_to_tensor();
+      ++unit;
+      if (!ok) break;
+      int k_stage = 0, v_stage = 0;
+      auto take = [&](int& stage) {
+        stage = next_stage;
+        ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.full[stage], round & 1, &sm.dead));
         tc::fence_to_tensor();
-        ++unit;
-        if (!ok) break;
-        int k_stage = 0, v_stage = 0;
-        auto take = [&](int& stage) {
-          stage = next_stage;
-          ok = ok && tc::bar_wait(&sm.full[stage], round & 1, &sm.dead);
-          tc::fence_to_tensor();
-          if (++next_stage == NS) next_stage = 0, ++round;
-        };
-        auto scores = [&](int x) {
-          const int tile = nt == 2 ? x & 1 : 0;
-          if (nt == 1 || tile == 0) take(k_stage);
-          if (!ok) return;
-          tc::fence_after();
-          const uint64_t qa = tc::k_major(tc::smem_at(sm.q[NW == 2 ? tile : 0]));
-          const uint64_t ka = tc::k_major(tc::smem_at(sm.ring[k_stage]));
+        if (++next_stage == NS) next_stage = 0, ++round;
+      };
+      auto scores = [&](int x) {
+        const int tile = nt == 2 ? x & 1 : 0;
+        if (nt == 1 || tile == 0) take(k_stage);
+        if (!ok) return;
+        tc::fence_after();
+        const uint64_t qa = tc::k_major(tc::smem_at(sm.q[NW == 2 ? tile : 0]));
+        const uint64_t ka = tc::k_major(tc::smem_at(sm.ring[k_stage]));
+        if (tc::elect()) {
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks)  // descriptors count in 16 bytes
             tc::mma_ss(tm + (x & 1) * S::kS, qa + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16,
@@ -268,35 +268,40 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           tc::commit(&sm.s_full[x & 1]);
           if (nt == 1 || tile == 1) tc::commit(&sm.empty[k_stage]);
           if (x == jobs - 1) tc::commit(&sm.q_free);
-        };
-        scores(0);
-        if (ok && jobs > 1) scores(1);
-        for (int x = 0; x < jobs && ok; ++x) {
-          const int buf = x & 1, o = NW == 2 ? buf : 0;
-          const bool first = x < NW;  // of this O in this unit
-          if (nt == 1 || buf == 0) take(v_stage);
-          if (ok && first && o_units[o] > 0) ok = tc::bar_wait(&sm.o_free[o], (o_units[o] - 1) & 1, &sm.dead);
-          if (first) ++o_units[o];
-          ok = ok && tc::bar_wait(&sm.p_full[buf], p_seen[buf] & 1, &sm.dead);
-          ++p_seen[buf];
-          if (!ok) break;
-          tc::fence_after();
-          const uint64_t va = tc::mn_major(tc::smem_at(sm.ring[v_stage]), KT * 128);
+        }
+        __syncwarp();
+      };
+      scores(0);
+      if (ok && jobs > 1) scores(1);
+      for (int x = 0; x < jobs && ok; ++x) {
+        const int buf = x & 1, o = NW == 2 ? buf : 0;
+        const bool first = x < NW;  // of this O in this unit
+        if (nt == 1 || buf == 0) take(v_stage);
+        if (ok && first && o_units[o] > 0)
+          ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.o_free[o], (o_units[o] - 1) & 1, &sm.dead));
+        if (first) ++o_units[o];
+        ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.p_full[buf], p_seen[buf] & 1, &sm.dead));
+        ++p_seen[buf];
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t va = tc::mn_major(tc::smem_at(sm.ring[v_stage]), KT * 128);
+        if (tc::elect()) {
 #pragma unroll
           for (int ks = 0; ks < KT / 16; ++ks)
-            tc::mma_ts(tm + S::kO + o * DP, tm + buf * S::kS + ks * 8, va + ks * 2048 / 16, kOutput,
-                       !first || ks > 0);
+            tc::mma_ts(tm + S::kO + o * DP, tm + buf * S::kS + ks * 8, va + ks * 2048 / 16, kOutput, !first || ks > 0);
           tc::commit(&sm.pv_done[o]);
           if (nt == 1 || buf == 1) tc::commit(&sm.empty[v_stage]);
-          if (x + 2 < jobs) scores(x + 2);
         }
-        if (ok) walk_next<S::M, KT>(w, g, a, c);
+        __syncwarp();
+        if (x + 2 < jobs) scores(x + 2);
       }
-      // everything issued is done before the tensor memory is given back
-      tc::commit(&sm.drained);
-      int never = 0;
-      if (!tc::bar_wait(&sm.drained, 0, &never)) sm.dead = 1;
+      if (ok) walk_next<S::M, KT>(w, g, a, c);
     }
+    // everything issued is done before the tensor memory is given back
+    if (tc::elect()) tc::commit(&sm.drained);
+    __syncwarp();
+    int never = 0;
+    if (!tc::bar_wait(&sm.drained, 0, &never)) sm.dead = 1;
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax, one thread a row

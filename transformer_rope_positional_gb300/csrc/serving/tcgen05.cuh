@@ -124,7 +124,10 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16
 #undef ROPE_I8
 
 // ---------------------------------------------------------------------------
-// Products.  16-bit operands of one type, binary32 accumulators; issued by one thread.
+// Products.  16-bit operands of one type, binary32 accumulators; issued by one thread, the one
+// that elect() picks of a whole converged warp (under it the compiler keeps the descriptors in
+// the warp's uniform registers; issued from a branch on the lane, each product first moved its
+// operands there, which took longer than the product).
 //
 // Operands in shared memory are panels of 64 columns: row r of a panel is 128 bytes at
 // r * 128, its 16-byte piece i at place i ^ (r & 7) (the 128-byte swizzle; panels start on
@@ -145,6 +148,16 @@ __device__ __forceinline__ uint64_t k_major(unsigned at) {
 // groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t mn_major(unsigned at, unsigned panel) {
   return (uint64_t)((at & 0x3ffff) >> 4) | ((uint64_t)(panel >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ bool elect() {
+  uint32_t leader;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(leader)::"memory");
+  return leader != 0;
 }
 
 // d (+)= a b, a and b in shared memory.
