@@ -3,7 +3,7 @@
 //
 // Bound by the matrix units (two products of M x KT x D per key tile) once the rows of a unit
 // outnumber about 280 operations per byte of K and V, so the kernel keeps tcgen05.mma fed:
-//  * one CTA per SM, its warps in roles.  Two warps copy Q, K and V tiles into shared memory
+//  * one CTA per SM, its 12 warps in roles.  Two warps copy Q, K and V tiles into shared memory
 //    with cp.async (any page size and row order: a page's rows are found key by key), one
 //    thread issues the products, and one or two groups of four warps do the softmax, one
 //    thread a row.  Everything between them is barriers in shared memory.  (11 warps leave a
@@ -12,11 +12,12 @@
 //  * scores S = Q K^T (128 rows x KT keys) land in tensor memory; the softmax threads read
 //    their row, write the weights over it in 16 bits, and O += P V takes them from there as
 //    its A operand: scores and weights never touch shared memory.
-//  * two score buffers.  With more than 128 rows they belong to two row tiles that share each
-//    K and V tile; with fewer, both softmax groups take alternate key tiles of the one row
-//    tile, each with its own m, l and O, joined when the unit ends.  Either way the products
-//    of one run while the exponentials of the other do.  Heads of 256 have room for one O:
-//    one softmax group with alternating score buffers.
+//  * a softmax group has two score buffers of 64 keys, so that the products of its next scores
+//    run while it works.  With more than 128 rows the two groups have a row tile each and share
+//    every K and V tile; with fewer, they take alternate key tiles of the one row tile, each
+//    with its own m, l and O, joined when the unit ends.  Heads of 256 have room for one O, and
+//    one group.  (One buffer of 128 keys a group left the tensor core idle for half the time:
+//    4 chunks of 1984 tokens behind 4096 took 708 us.)
 //  * O is multiplied by e^(m_old - m_new) only when a row's maximum grew by more than 2^8
 //    (the weights then stay below 2^8, far inside both 16-bit types), which is rare after the
 //    first tiles.  The result is the same: l and O always refer to the same m.
@@ -37,18 +38,17 @@ constexpr unsigned kWaitExpired = 8u;
 
 template <int DP>
 struct TcShape {
-  static constexpr int KT = DP <= 128 ? 128 : 64;   // keys of a tile
+  static constexpr int KT = 64;                     // keys of a tile
   static constexpr int NW = DP <= 128 ? 2 : 1;      // softmax groups
   static constexpr int M = 128 * NW;                // rows of a unit
   static constexpr int kStage = KT * DP * 2;        // bytes of a K or V tile
-  static constexpr int NS = DP <= 64 ? 8 : 5;       // tiles in the ring
+  static constexpr int NS = DP <= 64 ? 16 : DP <= 128 ? 10 : 5;  // tiles in the ring
   static constexpr int kQ = 128 * DP * 2;           // bytes of a row tile
   static constexpr int kSoftmax = 128 * NW;         // softmax threads
   static constexpr int kCopy = 64;                  // copying threads
-  static constexpr int kThreads = kSoftmax + kCopy + 32;
+  static constexpr int kThreads = kSoftmax + kCopy + 64;
   static constexpr int KW = KT / 2;                 // keys a copying warp takes
-  static constexpr int KL = KW / 32;                // of them, keys a lane looks up
-  static constexpr int kS = KT;                     // columns between the score buffers
+  static constexpr int kAhead = 2 * NW;             // scores ahead of the outputs
   static constexpr int kO = 256;                    // first column of O; the second O follows
 };
 
@@ -57,13 +57,14 @@ struct TcShared {
   using S = TcShape<DP>;
   alignas(1024) unsigned char ring[S::NS][S::kStage];
   alignas(1024) unsigned char q[S::NW][S::kQ];
-  uint64_t full[S::NS], empty[S::NS];
-  uint64_t q_full, q_free;
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t copied[S::NS], full[S::NS], empty[S::NS];  // a tile is there, visible to the tensor core, read
+  uint64_t q_copied, q_full, q_free;
+  uint64_t s_full[4], p_full[4];  // [2 * group + buffer]
+  uint64_t pv_done[2], o_free[2];
   uint64_t seen_full[16];   // the words below are there
   uint64_t ml_full;         // the second group's m and l are there
   uint64_t drained;
-  uint32_t seen[16][4];     // which keys of the last 16 K tiles are there
+  uint32_t seen[16][2];     // which keys of the last 16 K tiles are there
   float ml[128][2];
   int64_t tmp[S::kThreads / 32 + 2];
   uint32_t tmem;
@@ -100,8 +101,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   constexpr int CH = DP / 8;
   extern __shared__ __align__(1024) unsigned char raw[];
   TcShared<DP>& sm = *reinterpret_cast<TcShared<DP>*>(raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + S::kCopy / 32;
+  const int tid = threadIdx.x, warp = (int)tc::uniform(tid >> 5), lane = tid & 31;
+  constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + S::kCopy / 32,
+                kRelayWarp = kMmaWarp + 1;
 
   if (tc::smem_at(raw) & 1023) {  // the operands' swizzle counts on it
     if (tid == 0) atomicOr(g.err, kWaitExpired);
@@ -110,14 +112,18 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   if (tid == 0) {
     sm.dead = 0;
     for (int i = 0; i < NS; ++i) {
-      tc::bar_init(&sm.full[i], S::kCopy);
+      tc::bar_init(&sm.copied[i], S::kCopy);
+      tc::bar_init(&sm.full[i], 1);
       tc::bar_init(&sm.empty[i], 1);
     }
-    tc::bar_init(&sm.q_full, S::kCopy);
+    tc::bar_init(&sm.q_copied, S::kCopy);
+    tc::bar_init(&sm.q_full, 1);
     tc::bar_init(&sm.q_free, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       tc::bar_init(&sm.s_full[i], 1);
       tc::bar_init(&sm.p_full[i], 128);
+    }
+    for (int i = 0; i < 2; ++i) {
       tc::bar_init(&sm.pv_done[i], 1);
       tc::bar_init(&sm.o_free[i], 128);
     }
@@ -136,13 +142,14 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tm = sm.tmem;
+  const uint32_t tm = tc::uniform(sm.tmem);
 
   if (warp >= kCopyWarp && warp < kMmaWarp) {
     // ------------------------------------------------------------------ copies
     // Copies never wait for their data: the barrier of a tile gets an arrival of each copying
     // thread when its part is there.  Pages are looked up one K tile ahead; the rows of a tile
     // are kept until its V follows.
+    static_assert(S::KW == 32, "a lane looks up one key");
     const int cw = warp - kCopyWarp, ct = tid - S::kSoftmax;
     int stage = 0;
     unsigned round = 0;   // of the ring
@@ -152,63 +159,68 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     while (!w.done) {
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
-      const int lead = nt == 2 ? 1 : 2;
+      const int lead = S::kAhead / nt;
       const int k1 = walk_k1(w), kt = k1 - w.k0;
       const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
-      PageRow pages[S::KL];  // of this lane's keys (lane, lane + 32) of the next K tile
-      int rows[2][S::KL];    // cache rows of its keys of the last two K tiles, -1 where there is none
+      PageRow page;                    // of this lane's key of the next K tile
+      int rows[S::kAhead];             // cache rows of its keys of the K tiles whose V has not followed
+      int waiting = 0;                 // so many
       auto look_up = [&](int tile) {
-#pragma unroll
-        for (int i = 0; i < S::KL; ++i) {
-          const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + i * 32 + lane;
-          pages[i] = {-2, 0};  // no such key
-          if (tile < kt && j < end) pages[i] = page_row(j, table, g, a);
-        }
+        const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + lane;
+        page = {-2, 0};  // no such key
+        if (tile < kt && j < end) page = page_row(j, table, g, a);
       };
       look_up(0);
-      // ---- Q, once the last unit's scores are done
-      if (unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
-      ++unit;
-      if (!__all_sync(0xffffffffu, ok)) break;
-#pragma unroll 4
-      for (int idx = ct; idx < 128 * nt * CH; idx += S::kCopy) {
-        const int r = idx / CH, ch = idx - r * CH;
-        const bool there = r < u.rows && ch * 8 < a.D;
-        const RowAt at = row_at(u, r, w.h, a);
-        const T* p = q + (there ? at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8 : 0);
-        const int rr = r & 127;
-        cp_async16_or_zero(tc::smem_at(sm.q[NW == 2 ? r >> 7 : 0]) + (ch >> 3) * (128 * 128) + rr * 128 +
-                               (((ch & 7) ^ (rr & 7)) << 4),
-                           p, there && access_ok(p, 16, a.q_span, g.err));
-      }
-      tc::bar_arrive_after_copies(&sm.q_full);
-      // ---- K and V
       for (int n = 0; n < 2 * kt; ++n) {
+        if (n == min(lead, kt)) {
+          // ---- Q, once the last unit's scores are done: after the first K tiles, which need not wait
+          if (unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          // this thread's piece of rows ct / CH, + kCopy / CH, ...: (token, head) stepped without division
+          constexpr int kStep = S::kCopy / (CH < S::kCopy ? CH : S::kCopy);
+          const int ch = ct % CH;
+          int r = ct / CH;
+          RowAt at = row_at(u, r, w.h, a);
+          int head = at.h - w.h * a.G;
+          for (; r < 128 * nt; r += kStep) {
+            const bool there = r < u.rows && ch * 8 < a.D;
+            const T* p = q + (there ? at.t * a.q_stride + (int64_t)(w.h * a.G + head) * a.D + ch * 8 : 0);
+            const int rr = r & 127;
+            cp_async16_or_zero(tc::smem_at(sm.q[NW == 2 ? r >> 7 : 0]) + (ch >> 3) * (128 * 128) + rr * 128 +
+                                   (((ch & 7) ^ (rr & 7)) << 4),
+                               p, there && access_ok(p, 16, a.q_span, g.err));
+            head += kStep;
+            while (head >= a.G) head -= a.G, ++at.t;
+          }
+          tc::bar_arrive_after_copies(&sm.q_copied);
+        }
+        // ---- K and V
         const CopyItem it = copy_item(n, kt, lead);
         if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
-        int now[S::KL];
+        int now = rows[0];
         if (!it.is_v) {
+          now = -1;
+          if (page.page >= 0 && page.page < a.num_blocks)
+            now = ((int)page.page * a.nk + w.h) * a.block_size + page.row;
+          else if (page.page != -2)
+            atomicOr(g.err, kSlotOutOfRange);
 #pragma unroll
-          for (int i = 0; i < S::KL; ++i) {
-            int r = -1;
-            if (pages[i].page >= 0 && pages[i].page < a.num_blocks)
-              r = ((int)pages[i].page * a.nk + w.h) * a.block_size + pages[i].row;
-            else if (pages[i].page != -2)
-              atomicOr(g.err, kSlotOutOfRange);
-            now[i] = r;
-            if (it.tile & 1) rows[1][i] = r;
-            else rows[0][i] = r;
-            const uint32_t there = __ballot_sync(0xffffffffu, r >= 0);
-            if (lane == 0) sm.seen[k_count & 15][cw * S::KL + i] = there;
+          for (int i = 0; i < S::kAhead; ++i)
+            if (i == waiting) rows[i] = now;
+          ++waiting;
+          const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
+          if (lane == 0) {
+            sm.seen[k_count & 15][cw] = there;
+            tc::bar_arrive(&sm.seen_full[k_count & 15]);
           }
-          if (lane == 0) tc::bar_arrive(&sm.seen_full[k_count & 15]);
           ++k_count;
           look_up(it.tile + 1);
         } else {
 #pragma unroll
-          for (int i = 0; i < S::KL; ++i) now[i] = it.tile & 1 ? rows[1][i] : rows[0][i];
+          for (int i = 0; i + 1 < S::kAhead; ++i) rows[i] = rows[i + 1];
+          --waiting;
         }
         const unsigned dst = tc::smem_at(sm.ring[stage]) + cw * S::KW * 128;
         const T* const src = it.is_v ? vc : kc;
@@ -217,83 +229,126 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         for (int i = 0; i < S::KW * CH / 32; ++i) {
           const int idx = lane + 32 * i;
           const int key = idx / CH, ch = idx - key * CH;
-          const int r = __shfl_sync(0xffffffffu, now[i * 32 / CH / 32], key & 31);
+          const int r = __shfl_sync(0xffffffffu, now, key);
           const bool there = r >= 0 && ch * 8 < a.D;
           const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 8 : 0));
           cp_async16_or_zero(dst + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), p,
                              there && access_ok(p, 16, span, g.err));
         }
-        tc::bar_arrive_after_copies(&sm.full[stage]);
+        tc::bar_arrive_after_copies(&sm.copied[stage]);
         if (++stage == NS) stage = 0, ++round;
       }
+      ++unit;
       if (!__all_sync(0xffffffffu, ok)) break;
       walk_next<S::M, KT>(w, g, a, c);
     }
     cp_async_commit();
     cp_async_wait<0>();
+  } else if (warp == kRelayWarp) {
+    // ------------------------------------------------------------------ relay
+    // What cp.async wrote becomes visible to the tensor core by a fence that takes about 600
+    // cycles: one thread does nothing else, ahead of the products.
+    if (lane == 0) {
+      int stage = 0;
+      unsigned round = 0, unit = 0;
+      bool ok = true;
+      while (!w.done && ok) {
+        const int nt = w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1;
+        const int kt = walk_k1(w) - w.k0, first = min(S::kAhead / nt, kt);
+        for (int n = 0; n < 2 * kt && ok; ++n) {
+          if (n == first) {
+            ok = tc::bar_wait(&sm.q_copied, unit & 1, &sm.dead);
+            tc::fence_to_tensor();
+            if (ok) tc::bar_arrive(&sm.q_full);
+          }
+          ok = ok && tc::bar_wait(&sm.copied[stage], round & 1, &sm.dead);
+          tc::fence_to_tensor();
+          if (ok) tc::bar_arrive(&sm.full[stage]);
+          if (++stage == NS) stage = 0, ++round;
+        }
+        ++unit;
+        if (ok) walk_next<S::M, KT>(w, g, a, c);
+      }
+    }
+    __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ products
     constexpr uint32_t kScores = tc::instruction<T>(128, KT, false), kOutput = tc::instruction<T>(128, DP, true);
+    const uint32_t q0 = tc::uniform(tc::k_major(tc::smem_at(sm.q[0])));
+    const uint32_t k0 = tc::uniform(tc::k_major(tc::smem_at(sm.ring[0])));
+    const uint32_t v0 = tc::uniform(tc::mn_major(tc::smem_at(sm.ring[0]), KT * 128));
     int next_stage = 0;
     unsigned round = 0;  // of the ring
     unsigned unit = 0;
-    unsigned p_seen[2] = {0, 0}, o_units[2] = {0, 0};
+    // a bit a group: which of its score buffers is next, for scores and for outputs, and whether
+    // its O was used; a bit a buffer: parity of its weights; a bit a group: parity of its O
+    unsigned s_next = 0, o_next = 0, o_used = 0, p_parity = 0, o_parity = 0;
     bool ok = true;
-    while (!w.done && ok) {
-      const int nt = w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1;
-      const int kt = walk_k1(w) - w.k0, jobs = kt * nt;
+    while (__any_sync(0xffffffffu, !w.done && ok)) {
+      const int nt = (int)tc::uniform(w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1);
+      const int jobs = (int)tc::uniform((walk_k1(w) - w.k0) * nt);  // job x is of group x % NW
       ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.q_full, unit & 1, &sm.dead));
-      tc::fence_to_tensor();
       ++unit;
       if (!ok) break;
       int k_stage = 0, v_stage = 0;
-      auto take = [&](int& stage) {
-        stage = next_stage;
-        ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.full[stage], round & 1, &sm.dead));
-        tc::fence_to_tensor();
+      auto take = [&]() {
+        const int stage = next_stage;
+        ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.full[stage], round & 1, &sm.dead));
         if (++next_stage == NS) next_stage = 0, ++round;
+        return stage;
       };
       auto scores = [&](int x) {
-        const int tile = nt == 2 ? x & 1 : 0;
-        if (nt == 1 || tile == 0) take(k_stage);
+        const int group = NW == 2 ? x & 1 : 0;
+        const bool second = nt == 2 && group == 1;  // the other row tile, on the K tile of the first
+        if (!second) k_stage = take();
         if (!ok) return;
         tc::fence_after();
-        const uint64_t qa = tc::k_major(tc::smem_at(sm.q[NW == 2 ? tile : 0]));
-        const uint64_t ka = tc::k_major(tc::smem_at(sm.ring[k_stage]));
+        const int buf = group * 2 + ((s_next >> group) & 1);
+        s_next ^= 1u << group;
+        const uint32_t qa = tc::uniform(q0 + (second ? S::kQ / 16 : 0));
+        const uint32_t ka = tc::uniform(k0 + k_stage * (S::kStage / 16));
+        const uint32_t to = tc::uniform(tm + buf * KT);
         if (tc::elect()) {
 #pragma unroll
-          for (int ks = 0; ks < DP / 16; ++ks)  // descriptors count in 16 bytes
-            tc::mma_ss(tm + (x & 1) * S::kS, qa + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16,
-                       ka + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16, kScores, ks > 0);
-          tc::commit(&sm.s_full[x & 1]);
-          if (nt == 1 || tile == 1) tc::commit(&sm.empty[k_stage]);
+          for (int ks = 0; ks < DP / 16; ++ks)
+            tc::mma_ss(to, tc::operand(qa + ((ks >> 2) * (128 * 128) + (ks & 3) * 32) / 16),
+                       tc::operand(ka + ((ks >> 2) * (KT * 128) + (ks & 3) * 32) / 16), kScores, ks > 0);
+          tc::commit(&sm.s_full[buf]);
+          if (nt == 1 || second) tc::commit(&sm.empty[k_stage]);
           if (x == jobs - 1) tc::commit(&sm.q_free);
         }
         __syncwarp();
       };
-      scores(0);
-      if (ok && jobs > 1) scores(1);
+      for (int x = 0; x < S::kAhead && x < jobs && ok; ++x) scores(x);
       for (int x = 0; x < jobs && ok; ++x) {
-        const int buf = x & 1, o = NW == 2 ? buf : 0;
+        const int group = NW == 2 ? x & 1 : 0;
         const bool first = x < NW;  // of this O in this unit
-        if (nt == 1 || buf == 0) take(v_stage);
-        if (ok && first && o_units[o] > 0)
-          ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.o_free[o], (o_units[o] - 1) & 1, &sm.dead));
-        if (first) ++o_units[o];
-        ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.p_full[buf], p_seen[buf] & 1, &sm.dead));
-        ++p_seen[buf];
+        const bool second = nt == 2 && group == 1;
+        if (!second) v_stage = take();
+        if (first) {
+          if (ok && ((o_used >> group) & 1)) {
+            ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.o_free[group], (o_parity >> group) & 1, &sm.dead));
+            o_parity ^= 1u << group;
+          }
+          o_used |= 1u << group;
+        }
+        const int buf = group * 2 + ((o_next >> group) & 1);
+        o_next ^= 1u << group;
+        ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.p_full[buf], (p_parity >> buf) & 1, &sm.dead));
+        p_parity ^= 1u << buf;
         if (!ok) break;
         tc::fence_after();
-        const uint64_t va = tc::mn_major(tc::smem_at(sm.ring[v_stage]), KT * 128);
+        const uint32_t va = tc::uniform(v0 + v_stage * (S::kStage / 16));
+        const uint32_t to = tc::uniform(tm + S::kO + group * DP), from = tc::uniform(tm + buf * KT);
         if (tc::elect()) {
 #pragma unroll
           for (int ks = 0; ks < KT / 16; ++ks)
-            tc::mma_ts(tm + S::kO + o * DP, tm + buf * S::kS + ks * 8, va + ks * 2048 / 16, kOutput, !first || ks > 0);
-          tc::commit(&sm.pv_done[o]);
-          if (nt == 1 || buf == 1) tc::commit(&sm.empty[v_stage]);
+            tc::mma_ts(to, from + ks * 8, tc::operand(va + ks * 2048 / 16), kOutput, !first || ks > 0);
+          tc::commit(&sm.pv_done[group]);
+          if (nt == 1 || second) tc::commit(&sm.empty[v_stage]);
         }
         __syncwarp();
-        if (x + 2 < jobs) scores(x + 2);
+        if (x + S::kAhead < jobs) scores(x + S::kAhead);
       }
       if (ok) walk_next<S::M, KT>(w, g, a, c);
     }
@@ -308,8 +363,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     const int group = warp >> 2;
     const int r_tile = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    unsigned s_seen[2] = {0, 0};
-    unsigned pv = 0;          // products into this group's O so far
+    unsigned pv = 0;          // score tiles, and products into this group's O, so far
     int k_base = 0;           // K tiles before this unit
     unsigned ml_seen = 0;
     bool ok = true;
@@ -325,10 +379,10 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       float m = -INFINITY, l = 0.f;
       bool any = false;  // O holds something of this unit
       for (int x = NW == 2 ? group : 0; x < jobs; x += NW) {
-        const int buf = x & 1;
+        const int buf = (NW == 2 ? group * 2 : 0) + (pv & 1);
         const int kk = nt == 2 ? x >> 1 : x;
         const int j0 = c.lo + (w.k0 + kk) * KT;
-        const uint32_t t_s = tm + lanes + buf * S::kS;
+        const uint32_t t_s = tm + lanes + buf * KT;
         ok = tc::bar_wait(&sm.seen_full[(k_base + kk) & 15], (unsigned)((k_base + kk) >> 4) & 1, &sm.dead);
         uint32_t there[KT / 32];
         bool all_there = true;
@@ -337,8 +391,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           there[i] = sm.seen[(k_base + kk) & 15][i];
           all_there = all_there && there[i] == 0xffffffffu;
         }
-        ok = ok && tc::bar_wait(&sm.s_full[buf], s_seen[buf] & 1, &sm.dead);
-        ++s_seen[buf];
+        ok = ok && tc::bar_wait(&sm.s_full[buf], (pv >> 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc::fence_after();
         const bool open = __all_sync(0xffffffffu, all_there && j0 + KT <= limit);
@@ -403,9 +456,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           tc::tmem_store16(t_s + ch * 16, p);  // over the scores
         }
         l += sum.x + sum.y;
-        // pv_done is waited for by parity, so it may be one product behind at most.  With two groups
-        // these scores came after the group's last product; with one, they came before it.
-        if (NW == 1 && pv > 0) ok = tc::bar_wait(&sm.pv_done[0], (pv - 1) & 1, &sm.dead);
+        // pv_done is waited for by parity, so it may be one product behind at most
+        if (pv > 0) ok = tc::bar_wait(&sm.pv_done[NW == 2 ? group : 0], (pv - 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc::wait_stores();
         tc::fence_before();

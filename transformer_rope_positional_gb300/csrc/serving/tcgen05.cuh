@@ -125,9 +125,9 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16
 
 // ---------------------------------------------------------------------------
 // Products.  16-bit operands of one type, binary32 accumulators; issued by one thread, the one
-// that elect() picks of a whole converged warp (under it the compiler keeps the descriptors in
-// the warp's uniform registers; issued from a branch on the lane, each product first moved its
-// operands there, which took longer than the product).
+// that elect() picks of a whole converged warp.  The instruction takes its operands from the
+// warp's uniform registers: the values it is given pass through uniform() once, so that no
+// product waits for moves of its own.
 //
 // Operands in shared memory are panels of 64 columns: row r of a panel is 128 bytes at
 // r * 128, its 16-byte piece i at place i ^ (r & 7) (the 128-byte swizzle; panels start on
@@ -140,14 +140,18 @@ __host__ __device__ constexpr uint32_t instruction(int m, int n, bool b_transpos
          ((uint32_t)(m >> 4) << 24);
 }
 
-// K along the panel's rows of 128 bytes: 8-row groups are 1024 bytes apart.
-__device__ __forceinline__ uint64_t k_major(unsigned at) {
-  return (uint64_t)((at & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-// K down the rows (the operand is transposed): 64-column panels `panel` bytes apart, 8-row
-// groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t mn_major(unsigned at, unsigned panel) {
-  return (uint64_t)((at & 0x3ffff) >> 4) | ((uint64_t)(panel >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// A value that is the same in all lanes of a converged warp, as the compiler's to know.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Descriptors of operands in shared memory: the upper half says how 8-row groups follow each
+// other (1024 bytes) and the swizzle, the lower half holds the address in 16 bytes (an offset
+// may be added to it) and, where K runs down the rows (a transposed operand), how 64-column
+// panels follow each other.
+constexpr uint32_t kLayout = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t operand(uint32_t low) { return (uint64_t)kLayout << 32 | low; }
+__device__ __forceinline__ uint32_t k_major(unsigned at) { return ((at & 0x3ffff) >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t mn_major(unsigned at, unsigned panel) {
+  return ((at & 0x3ffff) >> 4) | (panel >> 4) << 16;
 }
 
 __device__ __forceinline__ bool elect() {
