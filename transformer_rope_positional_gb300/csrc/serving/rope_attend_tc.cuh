@@ -172,29 +172,32 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         if (tile < kt && j < end) page = page_row(j, table, g, a);
       };
       look_up(0);
-      for (int n = 0; n < 2 * kt; ++n) {
-        if (n == min(lead, kt)) {
-          // ---- Q, once the last unit's scores are done: after the first K tiles, which need not wait
-          if (unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          // this thread's piece of rows ct / CH, + kCopy / CH, ...: (token, head) stepped without division
-          constexpr int kStep = S::kCopy / (CH < S::kCopy ? CH : S::kCopy);
-          const int ch = ct % CH;
-          int r = ct / CH;
-          RowAt at = row_at(u, r, w.h, a);
-          int head = at.h - w.h * a.G;
-          for (; r < 128 * nt; r += kStep) {
-            const bool there = r < u.rows && ch * 8 < a.D;
-            const T* p = q + (there ? at.t * a.q_stride + (int64_t)(w.h * a.G + head) * a.D + ch * 8 : 0);
-            const int rr = r & 127;
-            cp_async16_or_zero(tc::smem_at(sm.q[NW == 2 ? r >> 7 : 0]) + (ch >> 3) * (128 * 128) + rr * 128 +
-                                   (((ch & 7) ^ (rr & 7)) << 4),
-                               p, there && access_ok(p, 16, a.q_span, g.err));
-            head += kStep;
-            while (head >= a.G) head -= a.G, ++at.t;
-          }
-          tc::bar_arrive_after_copies(&sm.q_copied);
+      // ---- Q, once the last unit's scores are done
+      if (unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
+      ++unit;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      {
+        // this thread's piece of rows ct / CH, + kStep, ...: (token, head) stepped without division
+        constexpr int kStep = S::kCopy / (CH < S::kCopy ? CH : S::kCopy);
+        const int ch = ct % CH;
+        const RowAt at = row_at(u, ct / CH, w.h, a);
+        int head = at.h - w.h * a.G;
+        const T* p = q + at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8;
+        const int64_t next_token = a.q_stride - (int64_t)a.G * a.D;
+        unsigned dst = tc::smem_at(sm.q[0]) + (ch >> 3) * (128 * 128);
+#pragma unroll 4
+        for (int r = ct / CH; r < 128 * nt; r += kStep) {
+          const bool there = r < u.rows && ch * 8 < a.D;
+          const int rr = r & 127;
+          cp_async16_or_zero(dst + (NW == 2 ? r >> 7 : 0) * S::kQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                             there ? p : q, there && access_ok(p, 16, a.q_span, g.err));
+          p += kStep * a.D;
+          head += kStep;
+          while (head >= a.G) head -= a.G, p += next_token;
         }
+        tc::bar_arrive_after_copies(&sm.q_copied);
+      }
+      for (int n = 0; n < 2 * kt; ++n) {
         // ---- K and V
         const CopyItem it = copy_item(n, kt, lead);
         if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
@@ -238,7 +241,6 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         tc::bar_arrive_after_copies(&sm.copied[stage]);
         if (++stage == NS) stage = 0, ++round;
       }
-      ++unit;
       if (!__all_sync(0xffffffffu, ok)) break;
       walk_next<S::M, KT>(w, g, a, c);
     }
@@ -253,14 +255,11 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       unsigned round = 0, unit = 0;
       bool ok = true;
       while (!w.done && ok) {
-        const int nt = w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1;
-        const int kt = walk_k1(w) - w.k0, first = min(S::kAhead / nt, kt);
+        const int kt = walk_k1(w) - w.k0;
+        ok = tc::bar_wait(&sm.q_copied, unit & 1, &sm.dead);
+        tc::fence_to_tensor();
+        if (ok) tc::bar_arrive(&sm.q_full);
         for (int n = 0; n < 2 * kt && ok; ++n) {
-          if (n == first) {
-            ok = tc::bar_wait(&sm.q_copied, unit & 1, &sm.dead);
-            tc::fence_to_tensor();
-            if (ok) tc::bar_arrive(&sm.q_full);
-          }
           ok = ok && tc::bar_wait(&sm.copied[stage], round & 1, &sm.dead);
           tc::fence_to_tensor();
           if (ok) tc::bar_arrive(&sm.full[stage]);
@@ -305,9 +304,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         tc::fence_after();
         const int buf = group * 2 + ((s_next >> group) & 1);
         s_next ^= 1u << group;
-        const uint32_t qa = tc::uniform(q0 + (second ? S::kQ / 16 : 0));
-        const uint32_t ka = tc::uniform(k0 + k_stage * (S::kStage / 16));
-        const uint32_t to = tc::uniform(tm + buf * KT);
+        const uint32_t qa = q0 + (second ? S::kQ / 16 : 0), ka = k0 + k_stage * (S::kStage / 16);
+        const uint32_t to = tm + buf * KT;
         if (tc::elect()) {
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks)
@@ -338,8 +336,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         p_parity ^= 1u << buf;
         if (!ok) break;
         tc::fence_after();
-        const uint32_t va = tc::uniform(v0 + v_stage * (S::kStage / 16));
-        const uint32_t to = tc::uniform(tm + S::kO + group * DP), from = tc::uniform(tm + buf * KT);
+        const uint32_t va = v0 + v_stage * (S::kStage / 16);
+        const uint32_t to = tm + S::kO + group * DP, from = tm + buf * KT;
         if (tc::elect()) {
 #pragma unroll
           for (int ks = 0; ks < KT / 16; ++ks)
