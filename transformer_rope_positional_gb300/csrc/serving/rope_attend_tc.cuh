@@ -12,12 +12,14 @@
 //  * scores S = Q K^T (128 rows x KT keys) land in tensor memory; the softmax threads read
 //    their row, write the weights over it in 16 bits, and O += P V takes them from there as
 //    its A operand: scores and weights never touch shared memory.
-//  * a softmax group has two score buffers of 64 keys, so that the products of its next scores
-//    run while it works.  With more than 128 rows the two groups have a row tile each and share
-//    every K and V tile; with fewer, they take alternate key tiles of the one row tile, each
-//    with its own m, l and O, joined when the unit ends.  Heads of 256 have room for one O, and
-//    one group.  (One buffer of 128 keys a group left the tensor core idle for half the time:
-//    4 chunks of 1984 tokens behind 4096 took 708 us.)
+//  * heads of up to 128: two softmax groups.  With more than 128 rows they have a row tile each
+//    and share every K and V tile; with fewer, they take alternate key tiles of the one row
+//    tile, each with its own m, l and O, joined when the unit ends.  The products of one run
+//    while the other works.  A group hands the weights over 64 keys at a time, so that the
+//    first half's product runs while it works on the second.  (Scores of 128 keys are one
+//    product of full rate; products of 64 keys read the queries from shared memory twice as
+//    often and run at two thirds of it.)
+//  * heads of 256 have room for one O: one softmax group with two score buffers of 64 keys.
 //  * O is multiplied by e^(m_old - m_new) only when a row's maximum grew by more than 2^8
 //    (the weights then stay below 2^8, far inside both 16-bit types), which is rare after the
 //    first tiles.  The result is the same: l and O always refer to the same m.
@@ -38,17 +40,19 @@ constexpr unsigned kWaitExpired = 8u;
 
 template <int DP>
 struct TcShape {
-  static constexpr int KT = 64;                     // keys of a tile
+  static constexpr int KT = DP <= 128 ? 128 : 64;   // keys of a tile
   static constexpr int NW = DP <= 128 ? 2 : 1;      // softmax groups
+  static constexpr int kParts = KT / 64;            // parts of 64 keys in which its weights are handed over
   static constexpr int M = 128 * NW;                // rows of a unit
   static constexpr int kStage = KT * DP * 2;        // bytes of a K or V tile
-  static constexpr int NS = DP <= 64 ? 16 : DP <= 128 ? 10 : 5;  // tiles in the ring
+  static constexpr int NS = DP <= 64 ? 8 : 5;       // tiles in the ring
   static constexpr int kQ = 128 * DP * 2;           // bytes of a row tile
   static constexpr int kSoftmax = 128 * NW;         // softmax threads
   static constexpr int kCopy = 64;                  // copying threads
   static constexpr int kThreads = kSoftmax + kCopy + 64;
   static constexpr int KW = KT / 2;                 // keys a copying warp takes
-  static constexpr int kAhead = 2 * NW;             // scores ahead of the outputs
+  static constexpr int KL = KW / 32;                // of them, keys a lane looks up
+  static constexpr int kAhead = 2;                  // scores ahead of the outputs
   static constexpr int kO = 256;                    // first column of O; the second O follows
 };
 
@@ -59,12 +63,13 @@ struct TcShared {
   alignas(1024) unsigned char q[S::NW][S::kQ];
   uint64_t copied[S::NS], full[S::NS], empty[S::NS];  // a tile is there, visible to the tensor core, read
   uint64_t q_copied, q_full, q_free;
-  uint64_t s_full[4], p_full[4];  // [2 * group + buffer]
+  uint64_t s_full[2];             // of a score buffer (of a group, or alternate ones of the one group)
+  uint64_t p_full[4];             // [2 * group + part or buffer]
   uint64_t pv_done[2], o_free[2];
   uint64_t seen_full[16];   // the words below are there
   uint64_t ml_full;         // the second group's m and l are there
   uint64_t drained;
-  uint32_t seen[16][2];     // which keys of the last 16 K tiles are there
+  uint32_t seen[16][4];     // which keys of the last 16 K tiles are there
   float ml[128][2];
   int64_t tmp[S::kThreads / 32 + 2];
   uint32_t tmem;
@@ -119,11 +124,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     tc::bar_init(&sm.q_copied, S::kCopy);
     tc::bar_init(&sm.q_full, 1);
     tc::bar_init(&sm.q_free, 1);
-    for (int i = 0; i < 4; ++i) {
-      tc::bar_init(&sm.s_full[i], 1);
-      tc::bar_init(&sm.p_full[i], 128);
-    }
+    for (int i = 0; i < 4; ++i) tc::bar_init(&sm.p_full[i], 128);
     for (int i = 0; i < 2; ++i) {
+      tc::bar_init(&sm.s_full[i], 1);
       tc::bar_init(&sm.pv_done[i], 1);
       tc::bar_init(&sm.o_free[i], 128);
     }
@@ -149,7 +152,6 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     // Copies never wait for their data: the barrier of a tile gets an arrival of each copying
     // thread when its part is there.  Pages are looked up one K tile ahead; the rows of a tile
     // are kept until its V follows.
-    static_assert(S::KW == 32, "a lane looks up one key");
     const int cw = warp - kCopyWarp, ct = tid - S::kSoftmax;
     int stage = 0;
     unsigned round = 0;   // of the ring
@@ -163,13 +165,16 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const int k1 = walk_k1(w), kt = k1 - w.k0;
       const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
-      PageRow page;                    // of this lane's key of the next K tile
-      int rows[S::kAhead];             // cache rows of its keys of the K tiles whose V has not followed
+      PageRow page[S::KL];             // of this lane's keys (lane, lane + 32) of the next K tile
+      int rows[S::kAhead][S::KL];      // cache rows of its keys of the K tiles whose V has not followed
       int waiting = 0;                 // so many
       auto look_up = [&](int tile) {
-        const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + lane;
-        page = {-2, 0};  // no such key
-        if (tile < kt && j < end) page = page_row(j, table, g, a);
+#pragma unroll
+        for (int i = 0; i < S::KL; ++i) {
+          const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + i * 32 + lane;
+          page[i] = {-2, 0};  // no such key
+          if (tile < kt && j < end) page[i] = page_row(j, table, g, a);
+        }
       };
       look_up(0);
       // ---- Q, once the last unit's scores are done
@@ -202,27 +207,32 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const CopyItem it = copy_item(n, kt, lead);
         if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
-        int now = rows[0];
-        if (!it.is_v) {
-          now = -1;
-          if (page.page >= 0 && page.page < a.num_blocks)
-            now = ((int)page.page * a.nk + w.h) * a.block_size + page.row;
-          else if (page.page != -2)
-            atomicOr(g.err, kSlotOutOfRange);
+        int now[S::KL];
 #pragma unroll
-          for (int i = 0; i < S::kAhead; ++i)
-            if (i == waiting) rows[i] = now;
-          ++waiting;
-          const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
-          if (lane == 0) {
-            sm.seen[k_count & 15][cw] = there;
-            tc::bar_arrive(&sm.seen_full[k_count & 15]);
+        for (int i = 0; i < S::KL; ++i) {
+          now[i] = rows[0][i];
+          if (!it.is_v) {
+            now[i] = -1;
+            if (page[i].page >= 0 && page[i].page < a.num_blocks)
+              now[i] = ((int)page[i].page * a.nk + w.h) * a.block_size + page[i].row;
+            else if (page[i].page != -2)
+              atomicOr(g.err, kSlotOutOfRange);
+            const uint32_t there = __ballot_sync(0xffffffffu, now[i] >= 0);
+            if (lane == 0) sm.seen[k_count & 15][cw * S::KL + i] = there;
+#pragma unroll
+            for (int n_ = 0; n_ < S::kAhead; ++n_)
+              if (n_ == waiting) rows[n_][i] = now[i];
+          } else {
+#pragma unroll
+            for (int n_ = 0; n_ + 1 < S::kAhead; ++n_) rows[n_][i] = rows[n_ + 1][i];
           }
+        }
+        if (!it.is_v) {
+          if (lane == 0) tc::bar_arrive(&sm.seen_full[k_count & 15]);
           ++k_count;
+          ++waiting;
           look_up(it.tile + 1);
         } else {
-#pragma unroll
-          for (int i = 0; i + 1 < S::kAhead; ++i) rows[i] = rows[i + 1];
           --waiting;
         }
         const unsigned dst = tc::smem_at(sm.ring[stage]) + cw * S::KW * 128;
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         for (int i = 0; i < S::KW * CH / 32; ++i) {
           const int idx = lane + 32 * i;
           const int key = idx / CH, ch = idx - key * CH;
-          const int r = __shfl_sync(0xffffffffu, now, key);
+          const int r = __shfl_sync(0xffffffffu, now[i * 32 / CH / 32], key & 31);
           const bool there = r >= 0 && ch * 8 < a.D;
           const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 8 : 0));
           cp_async16_or_zero(dst + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), p,
@@ -279,9 +289,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     int next_stage = 0;
     unsigned round = 0;  // of the ring
     unsigned unit = 0;
-    // a bit a group: which of its score buffers is next, for scores and for outputs, and whether
-    // its O was used; a bit a buffer: parity of its weights; a bit a group: parity of its O
-    unsigned s_next = 0, o_next = 0, o_used = 0, p_parity = 0, o_parity = 0;
+    // the one group's score buffer that is next, for scores and for outputs; a bit a group: whether
+    // its O was used, and its parity; a bit a buffer: parity of its weights
+    unsigned s_next = 0, o_next = 0, o_used = 0, o_parity = 0, p_parity = 0;
     bool ok = true;
     while (__any_sync(0xffffffffu, !w.done && ok)) {
       const int nt = (int)tc::uniform(w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1);
@@ -302,8 +312,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         if (!second) k_stage = take();
         if (!ok) return;
         tc::fence_after();
-        const int buf = group * 2 + ((s_next >> group) & 1);
-        s_next ^= 1u << group;
+        const int buf = NW == 2 ? group : s_next;
+        s_next ^= 1u;
         const uint32_t qa = q0 + (second ? S::kQ / 16 : 0), ka = k0 + k_stage * (S::kStage / 16);
         const uint32_t to = tm + buf * KT;
         if (tc::elect()) {
@@ -330,22 +340,27 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           }
           o_used |= 1u << group;
         }
-        const int buf = group * 2 + ((o_next >> group) & 1);
-        o_next ^= 1u << group;
-        ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.p_full[buf], (p_parity >> buf) & 1, &sm.dead));
-        p_parity ^= 1u << buf;
-        if (!ok) break;
-        tc::fence_after();
         const uint32_t va = v0 + v_stage * (S::kStage / 16);
-        const uint32_t to = tm + S::kO + group * DP, from = tm + buf * KT;
-        if (tc::elect()) {
+        const uint32_t to = tm + S::kO + group * DP, from = tm + (NW == 2 ? group : o_next) * KT;
 #pragma unroll
-          for (int ks = 0; ks < KT / 16; ++ks)
-            tc::mma_ts(to, from + ks * 8, tc::operand(va + ks * 2048 / 16), kOutput, !first || ks > 0);
-          tc::commit(&sm.pv_done[group]);
-          if (nt == 1 || second) tc::commit(&sm.empty[v_stage]);
+        for (int part = 0; part < S::kParts; ++part) {
+          const int bar = NW == 2 ? group * 2 + part : o_next;
+          ok = __all_sync(0xffffffffu, ok && tc::bar_wait(&sm.p_full[bar], (p_parity >> bar) & 1, &sm.dead));
+          p_parity ^= 1u << bar;
+          if (!ok) break;
+          tc::fence_after();
+          if (tc::elect()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              tc::mma_ts(to, from + part * 64 + ks * 8, tc::operand(va + (part * 4 + ks) * 2048 / 16), kOutput,
+                         !first || part > 0 || ks > 0);
+            tc::commit(&sm.pv_done[group]);
+            if (part == S::kParts - 1 && (nt == 1 || second)) tc::commit(&sm.empty[v_stage]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        o_next ^= 1u;
+        if (!ok) break;
         if (x + S::kAhead < jobs) scores(x + S::kAhead);
       }
       if (ok) walk_next<S::M, KT>(w, g, a, c);
@@ -361,7 +376,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     const int group = warp >> 2;
     const int r_tile = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    unsigned pv = 0;          // score tiles, and products into this group's O, so far
+    unsigned pv = 0;          // parts of scores, and products into this group's O, so far
     int k_base = 0;           // K tiles before this unit
     unsigned ml_seen = 0;
     bool ok = true;
@@ -376,30 +391,34 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const uint32_t t_o = tm + lanes + S::kO + (NW == 2 ? group : 0) * DP;
       float m = -INFINITY, l = 0.f;
       bool any = false;  // O holds something of this unit
-      for (int x = NW == 2 ? group : 0; x < jobs; x += NW) {
-        const int buf = (NW == 2 ? group * 2 : 0) + (pv & 1);
+      // parts of 64 keys: part y & 1 of job x, or one a job
+      const int parts = NW == 2 ? nt == 2 ? 2 * kt : ((jobs + 1 - group) >> 1) * 2 : jobs;
+      for (int y = 0; y < parts; ++y) {
+        const int x = NW == 2 ? (y >> 1) * 2 + group : y;
+        const int part = NW == 2 ? y & 1 : 0;
+        const int buf = (NW == 2 ? group * 2 : 0) + (pv & 1);  // of the weights
         const int kk = nt == 2 ? x >> 1 : x;
-        const int j0 = c.lo + (w.k0 + kk) * KT;
-        const uint32_t t_s = tm + lanes + buf * KT;
+        const int j0 = c.lo + (w.k0 + kk) * KT + part * 64;
+        const uint32_t t_s = tm + lanes + buf * 64;  // scores of 128 keys are two parts side by side
         ok = tc::bar_wait(&sm.seen_full[(k_base + kk) & 15], (unsigned)((k_base + kk) >> 4) & 1, &sm.dead);
-        uint32_t there[KT / 32];
+        uint32_t there[2];
         bool all_there = true;
 #pragma unroll
-        for (int i = 0; i < KT / 32; ++i) {
-          there[i] = sm.seen[(k_base + kk) & 15][i];
+        for (int i = 0; i < 2; ++i) {
+          there[i] = sm.seen[(k_base + kk) & 15][part * 2 + i];
           all_there = all_there && there[i] == 0xffffffffu;
         }
-        ok = ok && tc::bar_wait(&sm.s_full[buf], (pv >> 1) & 1, &sm.dead);
+        ok = ok && tc::bar_wait(&sm.s_full[NW == 2 ? group : buf], (pv >> 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc::fence_after();
-        const bool open = __all_sync(0xffffffffu, all_there && j0 + KT <= limit);
-        uint32_t v[KT / 32][32];
+        const bool open = __all_sync(0xffffffffu, all_there && j0 + 64 <= limit);
+        uint32_t v[2][32];
 #pragma unroll
-        for (int ch = 0; ch < KT / 32; ++ch) tc::tmem_load32(v[ch], t_s + ch * 32);
+        for (int ch = 0; ch < 2; ++ch) tc::tmem_load32(v[ch], t_s + ch * 32);
         tc::wait_loads();
         if (!open) {  // scores of unseen keys
 #pragma unroll
-          for (int ch = 0; ch < KT / 32; ++ch) {
+          for (int ch = 0; ch < 2; ++ch) {
             const uint32_t word = there[ch];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -408,7 +427,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         }
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int ch = 0; ch < KT / 32; ++ch)
+        for (int ch = 0; ch < 2; ++ch)
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
             top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), minus2 = make_float2(-base, -base);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int ch = 0; ch < KT / 32; ++ch) {
+        for (int ch = 0; ch < 2; ++ch) {
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
