@@ -65,7 +65,8 @@ struct TcShared {
   uint64_t q_copied, q_full, q_free;
   uint64_t s_full[2];             // of a score buffer (of a group, or alternate ones of the one group)
   uint64_t p_full[4];             // [2 * group + part or buffer]
-  uint64_t pv_done[2], o_free[2];
+  uint64_t pv_done[4];            // [2 * group + parity of the product]
+  uint64_t o_free[2];
   uint64_t seen_full[16];   // the words below are there
   uint64_t ml_full;         // the second group's m and l are there
   uint64_t drained;
@@ -124,10 +125,12 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     tc::bar_init(&sm.q_copied, S::kCopy);
     tc::bar_init(&sm.q_full, 1);
     tc::bar_init(&sm.q_free, 1);
-    for (int i = 0; i < 4; ++i) tc::bar_init(&sm.p_full[i], 128);
+    for (int i = 0; i < 4; ++i) {
+      tc::bar_init(&sm.p_full[i], 128);
+      tc::bar_init(&sm.pv_done[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       tc::bar_init(&sm.s_full[i], 1);
-      tc::bar_init(&sm.pv_done[i], 1);
       tc::bar_init(&sm.o_free[i], 128);
     }
     for (int i = 0; i < 16; ++i) tc::bar_init(&sm.seen_full[i], S::kCopy / 32);
@@ -220,11 +223,11 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
             const uint32_t there = __ballot_sync(0xffffffffu, now[i] >= 0);
             if (lane == 0) sm.seen[k_count & 15][cw * S::KL + i] = there;
 #pragma unroll
-            for (int n_ = 0; n_ < S::kAhead; ++n_)
-              if (n_ == waiting) rows[n_][i] = now[i];
+            for (int e = 0; e < S::kAhead; ++e)
+              if (e == waiting) rows[e][i] = now[i];
           } else {
 #pragma unroll
-            for (int n_ = 0; n_ + 1 < S::kAhead; ++n_) rows[n_][i] = rows[n_ + 1][i];
+            for (int e = 0; e + 1 < S::kAhead; ++e) rows[e][i] = rows[e + 1][i];
           }
         }
         if (!it.is_v) {
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
             for (int ks = 0; ks < 4; ++ks)
               tc::mma_ts(to, from + part * 64 + ks * 8, tc::operand(va + (part * 4 + ks) * 2048 / 16), kOutput,
                          !first || part > 0 || ks > 0);
-            tc::commit(&sm.pv_done[group]);
+            tc::commit(&sm.pv_done[bar]);
             if (part == S::kParts - 1 && (nt == 1 || second)) tc::commit(&sm.empty[v_stage]);
           }
           __syncwarp();
@@ -380,6 +383,13 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     int k_base = 0;           // K tiles before this unit
     unsigned ml_seen = 0;
     bool ok = true;
+    // The last product into this group's O.  Even and odd ones have a barrier each: by the time
+    // that one is waited for, the one before it on the same barrier was done (two groups: before
+    // these scores; one group: before the last but one), so its parity is not taken for it.
+    auto product_done = [&]() -> bool {
+      return __all_sync(0xffffffffu, tc::bar_wait(&sm.pv_done[(NW == 2 ? group * 2 : 0) + ((pv - 1) & 1)],
+                                                  ((pv - 1) >> 1) & 1, &sm.dead));
+    };
     while (!w.done) {
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
@@ -393,6 +403,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       bool any = false;  // O holds something of this unit
       // parts of 64 keys: part y & 1 of job x, or one a job
       const int parts = NW == 2 ? nt == 2 ? 2 * kt : ((jobs + 1 - group) >> 1) * 2 : jobs;
+      uint32_t there[2 * S::kParts];  // which keys of the job are there
       for (int y = 0; y < parts; ++y) {
         const int x = NW == 2 ? (y >> 1) * 2 + group : y;
         const int part = NW == 2 ? y & 1 : 0;
@@ -400,18 +411,18 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const int kk = nt == 2 ? x >> 1 : x;
         const int j0 = c.lo + (w.k0 + kk) * KT + part * 64;
         const uint32_t t_s = tm + lanes + buf * 64;  // scores of 128 keys are two parts side by side
-        ok = tc::bar_wait(&sm.seen_full[(k_base + kk) & 15], (unsigned)((k_base + kk) >> 4) & 1, &sm.dead);
-        uint32_t there[2];
-        bool all_there = true;
+        if (part == 0) {
+          ok = tc::bar_wait(&sm.seen_full[(k_base + kk) & 15], (unsigned)((k_base + kk) >> 4) & 1, &sm.dead);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          there[i] = sm.seen[(k_base + kk) & 15][part * 2 + i];
-          all_there = all_there && there[i] == 0xffffffffu;
+          for (int i = 0; i < 2 * S::kParts; ++i) there[i] = sm.seen[(k_base + kk) & 15][i];
+          ok = ok && tc::bar_wait(&sm.s_full[NW == 2 ? group : buf], (pv >> 1) & 1, &sm.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc::fence_after();
+        } else {
+          there[0] = there[2 * S::kParts - 2];
+          there[1] = there[2 * S::kParts - 1];
         }
-        ok = ok && tc::bar_wait(&sm.s_full[NW == 2 ? group : buf], (pv >> 1) & 1, &sm.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc::fence_after();
-        const bool open = __all_sync(0xffffffffu, all_there && j0 + 64 <= limit);
+        const bool open = __all_sync(0xffffffffu, (there[0] & there[1]) == 0xffffffffu && j0 + 64 <= limit);
         uint32_t v[2][32];
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) tc::tmem_load32(v[ch], t_s + ch * 32);
@@ -437,8 +448,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           m = mt;
         } else if (__any_sync(0xffffffffu, mt > m + 8.f)) {
           // the last product into O is done before O is changed
-          ok = tc::bar_wait(&sm.pv_done[NW == 2 ? group : 0], (pv - 1) & 1, &sm.dead);
-          if (!__all_sync(0xffffffffu, ok)) break;
+          ok = product_done();
+          if (!ok) break;
           tc::fence_after();
           const float up = fmaxf(m, mt);
           const float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
@@ -473,9 +484,6 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           tc::tmem_store16(t_s + ch * 16, p);  // over the scores
         }
         l += sum.x + sum.y;
-        // pv_done is waited for by parity, so it may be one product behind at most
-        if (pv > 0) ok = tc::bar_wait(&sm.pv_done[NW == 2 ? group : 0], (pv - 1) & 1, &sm.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
         tc::wait_stores();
         tc::fence_before();
         tc::bar_arrive(&sm.p_full[buf]);
@@ -485,8 +493,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
 
       // ---- the unit's rows: wait for the last product, then out
-      if (any) ok = tc::bar_wait(&sm.pv_done[NW == 2 ? group : 0], (pv - 1) & 1, &sm.dead);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (any) ok = product_done();
+      if (!ok) break;
       tc::fence_after();
       const bool halves = NW == 2 && nt == 1 && jobs > 1;  // the second group has keys of the same rows
       float f0 = 1.f, f1 = 0.f;
