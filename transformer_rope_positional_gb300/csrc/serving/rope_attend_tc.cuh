@@ -48,10 +48,9 @@ struct TcShape {
   static constexpr int NS = DP <= 64 ? 8 : 5;       // tiles in the ring
   static constexpr int kQ = 128 * DP * 2;           // bytes of a row tile
   static constexpr int kSoftmax = 128 * NW;         // softmax threads
-  static constexpr int kCopy = 64;                  // copying threads
+  static constexpr int kCopy = DP <= 128 ? 128 : 64;  // copying threads
   static constexpr int kThreads = kSoftmax + kCopy + 64;
-  static constexpr int KW = KT / 2;                 // keys a copying warp takes
-  static constexpr int KL = KW / 32;                // of them, keys a lane looks up
+  static constexpr int KW = KT / (kCopy / 32);      // keys a copying warp takes, one a lane
   static constexpr int kAhead = 2;                  // scores ahead of the outputs
   static constexpr int kO = 256;                    // first column of O; the second O follows
 };
@@ -155,6 +154,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     // Copies never wait for their data: the barrier of a tile gets an arrival of each copying
     // thread when its part is there.  Pages are looked up one K tile ahead; the rows of a tile
     // are kept until its V follows.
+    static_assert(S::KW == 32, "a lane looks up one key");
     const int cw = warp - kCopyWarp, ct = tid - S::kSoftmax;
     int stage = 0;
     unsigned round = 0;   // of the ring
@@ -168,16 +168,13 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const int k1 = walk_k1(w), kt = k1 - w.k0;
       const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
-      PageRow page[S::KL];             // of this lane's keys (lane, lane + 32) of the next K tile
-      int rows[S::kAhead][S::KL];      // cache rows of its keys of the K tiles whose V has not followed
+      PageRow page;                    // of this lane's key of the next K tile
+      int rows[S::kAhead];             // cache rows of its keys of the K tiles whose V has not followed
       int waiting = 0;                 // so many
       auto look_up = [&](int tile) {
-#pragma unroll
-        for (int i = 0; i < S::KL; ++i) {
-          const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + i * 32 + lane;
-          page[i] = {-2, 0};  // no such key
-          if (tile < kt && j < end) page[i] = page_row(j, table, g, a);
-        }
+        const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + lane;
+        page = {-2, 0};  // no such key
+        if (tile < kt && j < end) page = page_row(j, table, g, a);
       };
       look_up(0);
       // ---- Q, once the last unit's scores are done
@@ -210,32 +207,27 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const CopyItem it = copy_item(n, kt, lead);
         if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
         if (!__all_sync(0xffffffffu, ok)) break;
-        int now[S::KL];
-#pragma unroll
-        for (int i = 0; i < S::KL; ++i) {
-          now[i] = rows[0][i];
-          if (!it.is_v) {
-            now[i] = -1;
-            if (page[i].page >= 0 && page[i].page < a.num_blocks)
-              now[i] = ((int)page[i].page * a.nk + w.h) * a.block_size + page[i].row;
-            else if (page[i].page != -2)
-              atomicOr(g.err, kSlotOutOfRange);
-            const uint32_t there = __ballot_sync(0xffffffffu, now[i] >= 0);
-            if (lane == 0) sm.seen[k_count & 15][cw * S::KL + i] = there;
-#pragma unroll
-            for (int e = 0; e < S::kAhead; ++e)
-              if (e == waiting) rows[e][i] = now[i];
-          } else {
-#pragma unroll
-            for (int e = 0; e + 1 < S::kAhead; ++e) rows[e][i] = rows[e + 1][i];
-          }
-        }
+        int now = rows[0];
         if (!it.is_v) {
-          if (lane == 0) tc::bar_arrive(&sm.seen_full[k_count & 15]);
-          ++k_count;
+          now = -1;
+          if (page.page >= 0 && page.page < a.num_blocks)
+            now = ((int)page.page * a.nk + w.h) * a.block_size + page.row;
+          else if (page.page != -2)
+            atomicOr(g.err, kSlotOutOfRange);
+#pragma unroll
+          for (int e = 0; e < S::kAhead; ++e)
+            if (e == waiting) rows[e] = now;
           ++waiting;
+          const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
+          if (lane == 0) {
+            sm.seen[k_count & 15][cw] = there;
+            tc::bar_arrive(&sm.seen_full[k_count & 15]);
+          }
+          ++k_count;
           look_up(it.tile + 1);
         } else {
+#pragma unroll
+          for (int e = 0; e + 1 < S::kAhead; ++e) rows[e] = rows[e + 1];
           --waiting;
         }
         const unsigned dst = tc::smem_at(sm.ring[stage]) + cw * S::KW * 128;
@@ -245,7 +237,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         for (int i = 0; i < S::KW * CH / 32; ++i) {
           const int idx = lane + 32 * i;
           const int key = idx / CH, ch = idx - key * CH;
-          const int r = __shfl_sync(0xffffffffu, now[i * 32 / CH / 32], key & 31);
+          const int r = __shfl_sync(0xffffffffu, now, key);
           const bool there = r >= 0 && ch * 8 < a.D;
           const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 8 : 0));
           cp_async16_or_zero(dst + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), p,
