@@ -191,7 +191,7 @@ Units units_of(bool tc, int64_t D, int32_t dtype) {
     return u;
   }
   u.M = !tc ? kMmaRows : cols <= 128 ? 256 : 128;
-  u.grid = (int64_t)sm_count() * (!tc && cols <= 192 ? 2 : 1);
+  u.grid = (int64_t)sm_count() * (tc ? 1 : 2);
   return u;
 }
 

@@ -25,23 +25,21 @@ constexpr int kMmaThreads = 128;
 constexpr int kMmaRows = 16;
 constexpr int kMmaKeys = 64;
 
+// Stages of 16 rows of K or of V in a warp's ring, and rows of the four warps that are put
+// together at a time: as many as let two CTAs share an SM.
 template <int DP>
-__host__ __device__ constexpr int mma_stages() {
-  return DP <= 64 ? 5 : DP <= 128 ? 3 : DP <= 192 ? 2 : 3;
-}
-
-// CTAs per SM: the stages of two fit up to 192 columns.
-template <int DP>
-__host__ __device__ constexpr int mma_ctas() {
-  return DP <= 192 ? 2 : 1;
-}
+struct MmaShape {
+  static constexpr int kStages = DP <= 64 ? 11 : DP <= 128 ? 6 : DP <= 192 ? 4 : 3;
+  static constexpr int kJoin = DP <= 128 ? 4 : 2;
+  static constexpr int kStage = 16 * DP * 2;  // bytes
+};
 
 template <int DP>
 struct MmaShared {
-  static constexpr int kStage = 2 * 16 * DP * 2;  // bytes of K and V of one warp's 16 keys
-  alignas(1024) unsigned char ring[4][mma_stages<DP>()][kStage];
+  using S = MmaShape<DP>;
+  alignas(1024) unsigned char ring[4][S::kStages][S::kStage];
   alignas(16) unsigned char q[16 * DP * 2];
-  float o[4][4][DP + 8];  // four rows of the four warps
+  float o[4][S::kJoin][DP + 8];
   float ml[4][16][2];
   int bad[16];
   int64_t tmp[kMmaThreads / 32 + 2];
@@ -100,10 +98,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
 
 // DP: D rounded up to a multiple of 64; columns past D are zeros in shared memory.
 template <typename T, int DP>
-__global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
+__global__ void __launch_bounds__(kMmaThreads, 2)
     attend_mma_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut c) {
-  constexpr int S = mma_stages<DP>();
+  using Shape = MmaShape<DP>;
+  constexpr int S = Shape::kStages;
   constexpr int CH = DP / 8;   // 16-byte chunks of a row
   constexpr int KS = DP / 16;  // k steps of the score product
   constexpr bool kHoldQ = DP <= 128;  // the row tile's A operands stay in registers
@@ -114,56 +113,73 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
   Walk w = find_share<kMmaRows, kMmaKeys, kMmaThreads>(g, a, c, sm.tmp);
   if (w.done) return;
 
-  // ---- copies: the tiles of the share, in order, into the warp's ring
+  // ---- copies: K then V of the tiles of the share, in order, into the warp's ring
   Walk pw = w;
   int pk = pw.k0;
   int pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
-  int slot = 0;                   // stage of the next copy
+  int slot = 0;         // stage of the next copy
+  int p_tile = 0;       // tile of the next copy, modulo 6
+  bool p_v = false;     // its V is next
   unsigned char* const ring = sm.ring[warp][0];
-  // cache row of this lane's key (lane & 15) of the next tile, looked up ahead of its copy
-  auto look_up = [&]() -> int64_t {
-    if (pw.done) return -1;
+  // page of this lane's key (lane & 15) of the next tile: looked up ahead, used when it is copied
+  PageRow page;
+  auto look_up = [&]() {
+    page = {-2, 0};  // no such key
+    if (pw.done) return;
     const int j = c.lo + pk * kMmaKeys + warp * 16 + (lane & 15);
-    if (j >= pend) return -1;
-    const int64_t r = key_row(j, g.block_table + pw.b * a.W, g, a);
-    if (r < 0) atomicOr(g.err, kSlotOutOfRange);
-    return r < 0 ? -1 : (r + (int64_t)pw.h * a.block_size) * a.D;
+    if (j < pend) page = page_row(j, g.block_table + (int64_t)pw.b * a.W, g, a);
   };
-  int64_t next = look_up();
-  uint32_t valid = 0;  // 16 bits a stage: which keys are there (S * 16 <= 96 bits in valid, valid2, valid3)
-  uint32_t valid_hi = 0, valid_top = 0;
-  auto copy_tile = [&]() {
-    if (!pw.done) {
-      const unsigned dst = smem_u32(ring + slot * MmaShared<DP>::kStage);
+  look_up();
+  int row = -1;  // cache row of the key of the tile whose K was copied last
+  // 16 bits a tile: which of its keys are there, for the last 6 tiles
+  uint32_t valid0 = 0, valid1 = 0, valid2 = 0;
+  auto copy_stage = [&]() {
+    if (!p_v) {
+      row = -1;
+      if (page.page >= 0 && page.page < a.num_blocks)
+        row = ((int)page.page * a.nk + pw.h) * a.block_size + page.row;
+      else if (page.page != -2)
+        atomicOr(g.err, kSlotOutOfRange);
+      const uint32_t there = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+      uint32_t& word = p_tile < 2 ? valid0 : p_tile < 4 ? valid1 : valid2;
+      word = p_tile & 1 ? (word & 0x0000ffffu) | (there << 16) : (word & 0xffff0000u) | there;
+      p_tile = p_tile == 5 ? 0 : p_tile + 1;
+      if (!pw.done) {
+        if (++pk == walk_k1(pw)) {
+          walk_next<kMmaRows, kMmaKeys>(pw, g, a, c);
+          pk = pw.k0;
+          if (!pw.done) pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
+        }
+      }
+      look_up();
+    }
+    const T* const src = p_v ? vc : kc;
+    const Span& span = p_v ? a.v_span : a.k_span;
+    const unsigned dst = smem_u32(ring + slot * Shape::kStage);
+    if (__any_sync(0xffffffffu, row >= 0)) {
 #pragma unroll
       for (int i = 0; i < 16 * CH / 32; ++i) {
         const int idx = lane + 32 * i;
         const int key = idx / CH, ch = idx - key * CH;
-        const int64_t at = __shfl_sync(0xffffffffu, next, key);
-        const bool ok = at >= 0 && ch * 8 < a.D;
-        const T* ks = kc + (ok ? at + ch * 8 : 0);
-        const T* vs = vc + (ok ? at + ch * 8 : 0);
-        const unsigned to = dst + key * (DP * 2) + ((ch ^ (key & 7)) << 4);
-        cp_async16_or_zero(to, ks, ok && access_ok(ks, 16, a.k_span, g.err));
-        cp_async16_or_zero(to + 16 * DP * 2, vs, ok && access_ok(vs, 16, a.v_span, g.err));
+        const int r = __shfl_sync(0xffffffffu, row, key);
+        const bool ok = r >= 0 && ch * 8 < a.D;
+        const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (ok ? ch * 8 : 0));
+        cp_async16_or_zero(dst + key * (DP * 2) + ((ch ^ (key & 7)) << 4), p, ok && access_ok(p, 16, span, g.err));
       }
-      const uint32_t there = __ballot_sync(0xffffffffu, next >= 0) & 0xffffu;
-      uint32_t& word = slot < 2 ? valid : slot < 4 ? valid_hi : valid_top;
-      word = slot & 1 ? (word & 0x0000ffffu) | (there << 16) : (word & 0xffff0000u) | there;
-      if (++pk == walk_k1(pw)) {
-        walk_next<kMmaRows, kMmaKeys>(pw, g, a, c);
-        pk = pw.k0;
-        if (!pw.done) pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
-      }
-      next = look_up();
+    } else if (p_v) {  // no key of the tile: its weights are 0, and V must not be NaN
+#pragma unroll
+      for (int i = 0; i < 16 * CH / 32; ++i)
+        *reinterpret_cast<uint4*>(ring + slot * Shape::kStage + (lane + 32 * i) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
+    p_v = !p_v;
     cp_async_commit();
     slot = slot + 1 == S ? 0 : slot + 1;
   };
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) copy_tile();
+#pragma unroll 1
+  for (int i = 0; i < S - 1; ++i) copy_stage();
 
-  int cur = 0;  // stage of the current tile
+  int cur = 0;     // stage of the next product
+  int tile = 0;    // current tile, modulo 6
   const int r0 = lane >> 2, cq = (lane & 3) * 2;
   const unsigned q_at = smem_u32(sm.q);
   // ldmatrix rows: K (and Q) by (key, chunk), V transposed
@@ -222,10 +238,11 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
     for (int k = w.k0; k < k1; ++k) {
       cp_async_wait<S - 2>();
       __syncwarp();
-      const uint32_t word = cur < 2 ? valid : cur < 4 ? valid_hi : valid_top;
-      const uint32_t there = (cur & 1 ? word >> 16 : word) & 0xffffu;
-      copy_tile();  // into the stage that the last tile left
-      const unsigned kt = smem_u32(ring + cur * MmaShared<DP>::kStage), vt = kt + 16 * DP * 2;
+      const uint32_t word = tile < 2 ? valid0 : tile < 4 ? valid1 : valid2;
+      const uint32_t there = (tile & 1 ? word >> 16 : word) & 0xffffu;
+      tile = tile == 5 ? 0 : tile + 1;
+      copy_stage();  // into the stage that the last product left
+      const unsigned kt = smem_u32(ring + cur * Shape::kStage);
       cur = cur + 1 == S ? 0 : cur + 1;
       const int j0 = c.lo + k * kMmaKeys + warp * 16;
       // ---- scores
@@ -283,6 +300,11 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
       const uint32_t p[4] = {pack2((const T*)nullptr, s[0][0], s[0][1]), pack2((const T*)nullptr, s[0][2], s[0][3]),
                              pack2((const T*)nullptr, s[1][0], s[1][1]), pack2((const T*)nullptr, s[1][2], s[1][3])};
       // ---- outputs
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      copy_stage();
+      const unsigned vt = smem_u32(ring + cur * Shape::kStage);
+      cur = cur + 1 == S ? 0 : cur + 1;
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         uint32_t b[4];
@@ -293,7 +315,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
       __syncwarp();
     }
 
-    // ---- the four warps' rows together, four rows at a time, to the output or a partial result
+    // ---- the four warps' rows together, a few rows at a time, to the output or a partial result
 #pragma unroll
     for (int d = 1; d < 4; d *= 2) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -311,17 +333,19 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas<DP>())
     const bool begins = w.k0 == 0, whole = begins && k1 == w.work, final = whole && !c.shared;
     float* const po = slot_o(c, a, blockIdx.x, begins ? 1 : 0);
     float* const pml = slot_ml(c, a, blockIdx.x, begins ? 1 : 0);
-    for (int p4 = 0; p4 < u.rows; p4 += 4) {
-      if ((r0 & 4) == (p4 & 4)) {  // this lane has row r0 & 3 of the four: r0, or r0 + 8
-        float* to = &sm.o[warp][r0 & 3][cq];
+    constexpr int RJ = Shape::kJoin;
+    for (int p0 = 0; p0 < u.rows; p0 += RJ) {
+      if ((r0 & (8 - RJ)) == (p0 & (8 - RJ))) {  // this lane has row r0 % RJ of them: r0, or r0 + 8
+        float* to = &sm.o[warp][r0 & (RJ - 1)][cq];
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n)
-          *reinterpret_cast<float2*>(to + n * 8) = p4 < 8 ? make_float2(o[n][0], o[n][1]) : make_float2(o[n][2], o[n][3]);
+          *reinterpret_cast<float2*>(to + n * 8) = p0 < 8 ? make_float2(o[n][0], o[n][1]) : make_float2(o[n][2], o[n][3]);
       }
       __syncthreads();
-      for (int idx = threadIdx.x; idx < DP; idx += kMmaThreads) {  // 4 rows x DP / 4 pieces
+#pragma unroll
+      for (int idx = threadIdx.x; idx < RJ * (DP / 4); idx += kMmaThreads) {  // RJ rows x DP / 4 pieces
         const int r = idx / (DP / 4), d = (idx - r * (DP / 4)) * 4;
-        const int rr = p4 + r;
+        const int rr = p0 + r;
         if (rr >= u.rows || d >= a.D) continue;
         const float m = fmaxf(fmaxf(sm.ml[0][rr][0], sm.ml[1][rr][0]), fmaxf(sm.ml[2][rr][0], sm.ml[3][rr][0]));
         const float base = m == -INFINITY ? 0.f : m;
