@@ -21,7 +21,7 @@ def lib():
 
 
 def d(dtype, shape, ptr):
-    return C._PACK[len(shape)](ptr, dtype, len(shape), *shape)
+    return ctypes.byref(C.describe(ptr, dtype, shape))
 
 
 # ---------------------------------------------------------------------------
@@ -320,11 +320,3 @@ def test_binding_takes_cuda_tensors_only(lib):
         R.append_paged_kv(i, x, x, x, x, i, kv, kv, 64)
     with pytest.raises(ValueError):
         R.paged_attention(x, kv, kv, i.view(4, 1), i, torch.zeros(5, dtype=torch.int64), x)
-
-
-def test_packed_descriptor_is_the_structure(lib):
-    for shape in ((5,), (5, 6), (5, 6, 7), (5, 6, 7, 8)):
-        raw = d(C.BF16, shape, 0x123456789ABC)
-        assert len(raw) == ctypes.sizeof(C.RopeTensor) == 48
-        s = C.RopeTensor.from_buffer_copy(raw)
-        assert (s.data, s.dtype, s.ndim) == (0x123456789ABC, C.BF16, len(shape)) and tuple(s.shape)[:len(shape)] == shape

@@ -1,15 +1,17 @@
 """ctypes binding of ``librope_gb300.so`` (see ``include/rope_gb300.h``).
 
-Argument marshalling only: every step of both operators runs in the CUDA
-library.  The library must have been built (``python -m
+Argument marshalling only: every step of the operators runs in the CUDA
+library.  The serving operators (scaled tables, paged append, paged attention)
+are marshalled by ``lib/rope_binding.so``, built with it.  The library must have been built (``python -m
 transformer_rope_positional_gb300.build``); there is no fallback, and calling
 an operator without it raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 from typing import Optional, Sequence
 
 import torch
@@ -85,7 +87,7 @@ def load() -> ctypes.CDLL:
     lib.rope_qkv_rmsnorm_rope_cache.argtypes = [P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, P, P,
                                                 ctypes.c_float, P, P, P, P, P, P, P, ctypes.c_void_p]
     lib.rope_qkv_rmsnorm_rope_cache.restype = ctypes.c_int
-    D, B, V = ctypes.c_int64, ctypes.c_char_p, ctypes.c_void_p  # B: a packed rope_tensor_t (see _pack)
+    D, B, V = ctypes.c_int64, P, ctypes.c_void_p
     DP = ctypes.POINTER(ctypes.c_double)
     lib.rope_scaled_frequencies.argtypes = [D, ctypes.c_double, ctypes.POINTER(RopeScaling), DP, DP]
     lib.rope_scaled_frequencies.restype = ctypes.c_int
@@ -339,44 +341,37 @@ def prepare_qkv_rmsnorm_rope_cache(qkv: torch.Tensor, num_q_heads: int, num_k_he
 
 
 # ---------------------------------------------------------------------------
-# Scaled rotary tables, append to a paged cache, attention over it.  Their
-# descriptors are packed as bytes (a rope_tensor_t is 48 of them), which costs
-# about a third of building ctypes structures.
+# Scaled rotary tables, append to a paged cache, attention over it: marshalled
+# by the compiled binding.
 # ---------------------------------------------------------------------------
-_PACK = {n: struct.Struct("Pii%dq%dx" % (n, 8 * (4 - n))).pack for n in (1, 2, 3, 4)}
+_binding = None
 
 
-def _pack(t: torch.Tensor, dev: int) -> bytes:
-    """The bytes of a ``rope_tensor_t`` of a contiguous tensor on device ``dev``."""
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return _pack_any(t, dev)
+def _load_binding():
+    global _binding
+    if _binding is None:
+        load()  # the library first: it says how to build both
+        path = os.path.join(_HERE, "lib", "rope_binding.so")
+        loader = importlib.machinery.ExtensionFileLoader("rope_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("rope_binding", loader))
+        loader.exec_module(module)
+        module.init(LIB_PATH)
+        _binding = module
+    return _binding
 
 
-def _pack_any(t: torch.Tensor, dev: int) -> bytes:
-    code = DTYPE_CODE.get(t.dtype)
-    if code is None:
-        raise ValueError("unsupported dtype %s" % t.dtype)
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor, got one on %s" % t.device)
-    if t.get_device() != dev:
-        raise ValueError("tensors on different devices (cuda:%d and cuda:%d)" % (dev, t.get_device()))
-    shape = t.shape
-    n = len(shape)
-    if not 1 <= n <= 4:
-        raise ValueError("expected 1 to 4 dimensions, got %d" % n)
-    return _PACK[n](t.data_ptr(), code, n, *shape)
-
-
-def _pack_rows(t: torch.Tensor, dev: int):
-    """(bytes, row stride) of a 2-D tensor whose rows may be strided (see rows_desc)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("expected a 2-D tensor with contiguous rows")
-    width = t.shape[1]
-    stride = t.stride(0) if t.shape[0] > 1 else width
-    if stride < width:
-        raise ValueError("rows overlap: row stride %d is below the row width %d" % (stride, width))
-    return _pack_any(t, dev), stride
+def _issue(name, args, like, stream, what) -> None:
+    """Call the binding's function on ``args`` and the stream, with the device of ``like`` current."""
+    dev = like.get_device()
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor, got one on %s" % like.device)
+    fn = getattr(_binding or _load_binding(), name)
+    if stream is None and _raw_current_stream is not None and _current_device() == dev:
+        st = fn(*args, _raw_current_stream(dev))
+    else:
+        st = _on_device(dev, fn, args + (_stream_handle(like, stream),))
+    if st != ROPE_OK:
+        raise RopeError(st, what)
 
 
 SCALINGS = {"none": 0, "linear": 1, "base": 2, "yarn": 3, "wavelength": 4, "factors": 5}
@@ -391,34 +386,33 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[d
     "yarn", "wavelength", "factors" and that kind's ``factor``,
     ``original_length``, ``low``, ``high``, ``attention`` and ``factors``; the
     formulas are those of ``rope_scaled_frequencies`` in the C header."""
-    lib = load()
     what = "rope_scaled_frequencies"
-    s = keep = None
-    if scaling is not None:
-        unknown = set(scaling) - {"kind", "factor", "original_length", "low", "high", "attention", "factors"}
-        if unknown or scaling.get("kind") not in SCALINGS:
-            raise RopeError(ROPE_ERR_PARAM_INVALID, "%s: scaling %r" % (what, scaling))
-        s = RopeScaling(SCALINGS[scaling["kind"]], *[float(scaling.get(k, 0.0)) for k in (
-            "factor", "original_length", "low", "high", "attention")])
-        if scaling.get("factors") is not None:
-            if len(scaling["factors"]) != rotary_dim // 2:
-                raise RopeError(ROPE_ERR_PARAM_INVALID, "%s: %d factors for %d frequencies"
-                                % (what, len(scaling["factors"]), rotary_dim // 2))
-            keep = (ctypes.c_double * len(scaling["factors"]))(*[float(v) for v in scaling["factors"]])
-            s.factors = ctypes.cast(keep, ctypes.POINTER(ctypes.c_double))
+    fn = (_binding or _load_binding()).frequencies
     inv = torch.empty(max(1, int(rotary_dim) // 2), dtype=torch.float64)
-    scale = ctypes.c_double(0.0)
-    st = lib.rope_scaled_frequencies(int(rotary_dim), float(base), ctypes.byref(s) if s is not None else None,
-                                     ctypes.cast(inv.data_ptr(), ctypes.POINTER(ctypes.c_double)),
-                                     ctypes.byref(scale))
+    if scaling is None:
+        st, scale = fn(rotary_dim, base, -1, 0.0, 0.0, 0.0, 0.0, 0.0, None, inv)
+    else:
+        get = scaling.get
+        if get("kind") not in SCALINGS or not _SCALING_KEYS.issuperset(scaling):
+            raise RopeError(ROPE_ERR_PARAM_INVALID, "%s: scaling %r" % (what, scaling))
+        factors = get("factors")
+        if factors is not None:
+            factors = torch.as_tensor(factors, dtype=torch.float64, device="cpu").contiguous()
+        st, scale = fn(rotary_dim, base, SCALINGS[scaling["kind"]], get("factor", 0.0), get("original_length", 0.0),
+                       get("low", 0.0), get("high", 0.0), get("attention", 0.0), factors, inv)
     if st != ROPE_OK:
         raise RopeError(st, what)
-    return inv, scale.value
+    return inv, scale
+
+
+_SCALING_KEYS = frozenset(("kind", "factor", "original_length", "low", "high", "attention", "factors"))
 
 
 def _host_frequencies(inv_freq) -> torch.Tensor:
     if not isinstance(inv_freq, torch.Tensor):
         return torch.tensor(list(inv_freq), dtype=torch.float64)
+    if inv_freq.dtype == torch.float64:
+        return inv_freq.contiguous()
     if inv_freq.is_cuda:
         raise ValueError("expected frequencies on the host, got a tensor on %s" % inv_freq.device)
     return inv_freq.to(torch.float64).contiguous()
@@ -430,12 +424,8 @@ def scaled_cos_sin_cache(cache: torch.Tensor, inv_freq, scale: float = 1.0, *,
     operators: row r is position ``first_position + (positions[r] or r)``, cos in
     the first half and sin in the second, times ``scale``.  ``inv_freq`` holds the
     F frequencies on the host (see :func:`rope_frequencies`)."""
-    lib = load()
-    f = _host_frequencies(inv_freq)
-    dev = cache.get_device()
-    args = (f.data_ptr() or None, f.numel(), float(scale), None if positions is None else _pack(positions, dev),
-            int(first_position), _pack(cache, dev), _stream_handle(cache, stream))
-    _run(lib.rope_scaled_cos_sin_cache, args, (cache, f, positions), "rope_scaled_cos_sin_cache")
+    _issue("scaled_cos_sin_cache", (_host_frequencies(inv_freq), scale, positions, first_position, cache), cache,
+           stream, "rope_scaled_cos_sin_cache")
 
 
 def scaled_cos_sin(cos: torch.Tensor, sin: torch.Tensor, inv_freq, scale: float = 1.0, rotary_mode=1, *,
@@ -443,31 +433,8 @@ def scaled_cos_sin(cos: torch.Tensor, sin: torch.Tensor, inv_freq, scale: float 
     """Writes ``cos`` and ``sin`` [..., 2F] as the in-place operator reads them
     (e.g. [1, S, 1, 2F]), in the element order of ``rotary_mode``; rows and
     positions as in :func:`scaled_cos_sin_cache`."""
-    lib = load()
-    f = _host_frequencies(inv_freq)
-    dev = cos.get_device()
-    args = (f.data_ptr() or None, f.numel(), float(scale), None if positions is None else _pack(positions, dev),
-            int(first_position), _mode(rotary_mode), _pack(cos, dev), _pack(sin, dev), _stream_handle(cos, stream))
-    _run(lib.rope_scaled_cos_sin, args, (cos, f, positions), "rope_scaled_cos_sin")
-
-
-def _append_args(positions, query, key, value, cos_sin_cache, slot_mapping, k_cache, v_cache, head_size, rotary_dim,
-                 is_neox, mrope_section, stream, cache_mode, query_out):
-    lib = load()
-    dev = key.get_device()
-    dq, qs = (None, 0) if query is None else _pack_rows(query, dev)
-    dk, ks = _pack_rows(key, dev)
-    dv, vs = _pack_rows(value, dev)
-    sec, n_sec = None, 0
-    if mrope_section is not None:
-        n_sec = len(mrope_section)
-        sec = (ctypes.c_int64 * max(1, n_sec))(*[int(v) for v in mrope_section])
-    args = (_pack(positions, dev), dq, dk, dv, _pack(cos_sin_cache, dev), _pack(slot_mapping, dev),
-            None if query_out is None else _pack(query_out, dev), _pack(k_cache, dev), _pack(v_cache, dev),
-            int(head_size), int(cos_sin_cache.shape[1]) if rotary_dim is None else int(rotary_dim),
-            1 if is_neox else 0, sec, n_sec, int(cache_mode), qs, ks, vs, _stream_handle(key, stream))
-    return (lib.rope_append_paged_kv, args, (key, query, value, positions, cos_sin_cache, slot_mapping, query_out,
-                                             k_cache, v_cache, sec), "rope_append_paged_kv")
+    _issue("scaled_cos_sin", (_host_frequencies(inv_freq), scale, positions, first_position, _mode(rotary_mode), cos,
+                              sin), cos, stream, "rope_scaled_cos_sin")
 
 
 def append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tensor], key: torch.Tensor, value: torch.Tensor,
@@ -479,8 +446,9 @@ def append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tensor], key:
     key and value to their slots of the paged caches [blocks, heads, block
     size, head_size] (see the C header).  ``query``, ``key`` and ``value`` may be
     column ranges of one fused buffer; the slots >= 0 of a call are distinct."""
-    _run(*_append_args(positions, query, key, value, cos_sin_cache, slot_mapping, k_cache, v_cache, head_size,
-                       rotary_dim, is_neox, mrope_section, stream, cache_mode, query_out))
+    _issue("append_paged_kv", (positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache,
+                               head_size, rotary_dim, is_neox, mrope_section, cache_mode), key, stream,
+           "rope_append_paged_kv")
 
 
 def prepare_append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tensor], key: torch.Tensor,
@@ -489,54 +457,31 @@ def prepare_append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tenso
                             rotary_dim: Optional[int] = None, is_neox: bool = True,
                             mrope_section: Optional[Sequence[int]] = None, stream=None, *, cache_mode: int = 0,
                             query_out: Optional[torch.Tensor] = None) -> "PreparedCall":
-    """:func:`append_paged_kv` with its arguments marshalled once."""
-    return PreparedCall(*_append_args(positions, query, key, value, cos_sin_cache, slot_mapping, k_cache, v_cache,
-                                      head_size, rotary_dim, is_neox, mrope_section, stream, cache_mode, query_out))
+    """:func:`append_paged_kv` as a call to be issued many times, on the stream of now."""
+    args = (positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache, head_size,
+            rotary_dim, is_neox, None if mrope_section is None else tuple(mrope_section), cache_mode,
+            _stream_handle(key, stream))
+    return PreparedCall(_load_binding().append_paged_kv, args, (key,), "rope_append_paged_kv")
 
 
 def paged_attention_workspace(query: torch.Tensor, k_cache: torch.Tensor, prefix_len: int = 0) -> int:
     """Bytes of workspace that :func:`paged_attention` needs for these tensors."""
-    code = DTYPE_CODE.get(query.dtype)
-    if code is None or k_cache.dim() != 4 or query.dim() != 2:
+    n = _on_device(query.get_device(), _load_binding().attention_workspace, (query, k_cache, prefix_len))
+    if n < 0:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "rope_paged_attention_workspace")
-    _, nk, _, d = k_cache.shape
-    n = ctypes.c_int64(0)
-    st = _on_device(query.get_device(), load().rope_paged_attention_workspace,
-                    (query.shape[0], query.shape[1] // max(1, d), nk, d, code, int(prefix_len), ctypes.byref(n)))
-    if st != ROPE_OK:
-        raise RopeError(st, "rope_paged_attention_workspace")
-    return n.value
+    return n
 
 
-def _new_workspace(nbytes: int, like: torch.Tensor, stream) -> torch.Tensor:
+def _workspace_for(query, k_cache, prefix_len, stream) -> torch.Tensor:
     """A workspace whose memory belongs to the stream that the call runs on, so
     that it is not handed out again while the call still uses it."""
+    nbytes = paged_attention_workspace(query, k_cache, prefix_len)
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=query.device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        stream = torch.cuda.ExternalStream(int(stream), device=query.device)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-
-
-def _attend_args(query, k_cache, v_cache, block_table, seq_lens, query_start_loc, out, scale, prefix_blocks,
-                 prefix_len, lse, workspace, stream):
-    lib = load()
-    dev = query.get_device()
-    dq, qs = _pack_rows(query, dev)
-    dk, dv = _pack(k_cache, dev), _pack(v_cache, dev)
-    handle = _stream_handle(query, stream)
-    if workspace is None:
-        workspace = _new_workspace(paged_attention_workspace(query, k_cache, prefix_len), query, stream)
-    elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("expected a contiguous workspace on cuda:%d" % dev)
-    args = (dq, qs, dk, dv, _pack(block_table, dev), _pack(seq_lens, dev), _pack(query_start_loc, dev),
-            None if prefix_blocks is None else _pack(prefix_blocks, dev), int(prefix_len),
-            float(k_cache.shape[3]) ** -0.5 if scale is None else float(scale), _pack(out, dev),
-            None if lse is None else _pack(lse, dev), workspace.data_ptr() or None,
-            workspace.numel() * workspace.element_size(), handle)
-    return (lib.rope_paged_attention, args, (query, k_cache, v_cache, block_table, seq_lens, query_start_loc,
-                                             prefix_blocks, out, lse, workspace), "rope_paged_attention")
+        return torch.empty(nbytes, dtype=torch.uint8, device=query.device)
 
 
 def paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -553,8 +498,13 @@ def paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     share.  ``scale`` defaults to D ** -0.5; ``lse`` [T, Nq] (float32) receives
     each row's log-sum-exp.  Without ``workspace`` one is allocated for the call
     on its stream."""
-    _run(*_attend_args(query, k_cache, v_cache, block_table, seq_lens, query_start_loc, out, scale, prefix_blocks,
-                       prefix_len, lse, workspace, stream))
+    if scale is None:
+        scale = k_cache.shape[-1] ** -0.5
+    if workspace is None and stream is not None:
+        _stream_handle(query, stream)  # its device is the tensors'
+        workspace = _workspace_for(query, k_cache, prefix_len, stream)
+    _issue("paged_attention", (query, k_cache, v_cache, block_table, seq_lens, query_start_loc, prefix_blocks,
+                               prefix_len, scale, out, lse, workspace), query, stream, "rope_paged_attention")
 
 
 def prepare_paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -563,10 +513,16 @@ def prepare_paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache:
                             prefix_blocks: Optional[torch.Tensor] = None, prefix_len: int = 0,
                             lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                             stream=None) -> "PreparedCall":
-    """:func:`paged_attention` with its arguments marshalled once (and its
-    workspace, given or allocated here, kept with them)."""
-    return PreparedCall(*_attend_args(query, k_cache, v_cache, block_table, seq_lens, query_start_loc, out, scale,
-                                      prefix_blocks, prefix_len, lse, workspace, stream))
+    """:func:`paged_attention` as a call to be issued many times, on the stream of
+    now, with its workspace (given or allocated here) kept."""
+    handle = _stream_handle(query, stream)
+    if scale is None:
+        scale = k_cache.shape[-1] ** -0.5
+    if workspace is None:
+        workspace = _workspace_for(query, k_cache, prefix_len, stream)
+    args = (query, k_cache, v_cache, block_table, seq_lens, query_start_loc, prefix_blocks, prefix_len, scale, out,
+            lse, workspace, handle)
+    return PreparedCall(_load_binding().paged_attention, args, (query,), "rope_paged_attention")
 
 
 def get_device_error(stream=None, device=None) -> int:

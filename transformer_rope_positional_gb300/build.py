@@ -3,7 +3,9 @@
 Usage: ``python -m transformer_rope_positional_gb300.build [--force] [--verbose] [--debug]``.
 The translation units compile in parallel; the shared library lands in
 ``transformer_rope_positional_gb300/lib/``.  The CUDA runtime is linked
-statically, so the library needs only the driver at run time.
+statically, so the library needs only the driver at run time.  Beside it lands
+``rope_binding.so``, the Python binding of the serving operators (g++ against
+the installed torch's headers).
 
 ``--debug`` builds ``librope_gb300_debug.so`` with ``-DROPE_DEBUG_BOUNDS``:
 every global access of every kernel is checked against the span of the tensor
@@ -16,10 +18,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import fcntl
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -29,6 +33,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "librope_gb300.so")
 DEBUG_LIB_PATH = os.path.join(LIB_DIR, "librope_gb300_debug.so")
+BINDING_PATH = os.path.join(LIB_DIR, "rope_binding.so")
+BINDING = "serving/binding.cpp"
 
 SOURCES = ["rope_api.cu", "rope_launch.cu", "rope_inplace_fwd.cu", "rope_inplace_bwd.cu", "rope_cache.cu",
            "rope_qkv.cu", "serving/rope_table.cu", "serving/rope_append.cu", "serving/rope_attend.cu"]
@@ -47,14 +53,14 @@ def nvcc() -> str:
 
 
 def _inputs():
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    srcs = [os.path.join(CSRC, s) for s in SOURCES + [BINDING]]
     return srcs + [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "rope_gb300.h")]
 
 
 def up_to_date(lib: str = LIB_PATH) -> bool:
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(lib), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -77,6 +83,20 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
             fcntl.flock(lock, fcntl.LOCK_UN)
 
 
+def _build_binding() -> None:
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    tmp = BINDING_PATH + ".%d.tmp" % os.getpid()
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-I", inc, "-I",
+           os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(CSRC, BINDING), "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s\n%s" % (BINDING, r.stdout, r.stderr))
+    os.replace(tmp, BINDING_PATH)
+
+
 def _build_locked(lib_path: str, verbose: bool, debug: bool) -> str:
     build_dir = BUILD_DIR + ("_debug" if debug else "")
     os.makedirs(build_dir, exist_ok=True)
@@ -92,8 +112,10 @@ def _build_locked(lib_path: str, verbose: bool, debug: bool) -> str:
             raise RuntimeError("nvcc failed on %s:\n%s\n%s" % (src, r.stdout, r.stderr))
         return obj, r.stderr
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
