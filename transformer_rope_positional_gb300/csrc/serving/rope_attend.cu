@@ -228,7 +228,6 @@ Cut cut_of(const Part& s, char* at, const Units& u) {
   c.lo = 0;
   c.prefix = 0;
   c.shared = 0;
-  c.min_share = 2;
   c.slot_rows = (int32_t)s.slot_rows;
   c.rec = reinterpret_cast<int2*>(at + s.rec);
   c.slots = reinterpret_cast<float*>(at + s.slots);

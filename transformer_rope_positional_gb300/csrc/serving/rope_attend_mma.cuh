@@ -129,7 +129,26 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     const int j = c.lo + pk * kMmaKeys + warp * 16 + (lane & 15);
     if (j < pend) page = page_row(j, g.block_table + (int64_t)pw.b * a.W, g, a);
   };
+  // a unit's query rows, in 16-byte pieces of this thread: read while the unit before ends
+  constexpr int NQ = 16 * CH / kMmaThreads;
+  uint4 qv[NQ];
+  auto read_q = [&](const Walk& x) {
+    const UnitRows u = unit_rows<kMmaRows>(x, a);
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int idx = threadIdx.x + kMmaThreads * i;
+      const int r = idx / CH, ch = idx - r * CH;
+      qv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < u.rows && ch * 8 < a.D) {
+        const RowAt at = row_at(u, r, x.h, a);
+        const T* p = q + at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8;
+        if (access_ok(p, 16, a.q_span, g.err)) qv[i] = __ldg(reinterpret_cast<const uint4*>(p));
+      }
+    }
+  };
+
   look_up();
+  read_q(w);
   int row = -1;  // cache row of the key of the tile whose K was copied last
   // 16 bits a tile: which of its keys are there, for the last 6 tiles
   uint32_t valid0 = 0, valid1 = 0, valid2 = 0;
@@ -185,25 +204,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   // ldmatrix rows: K (and Q) by (key, chunk), V transposed
   const int k_row = ((lane >> 4) << 3) + (lane & 7), k_ch = (lane >> 3) & 1;
   const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_ch = lane >> 4;
-
-  // a unit's query rows, in 16-byte pieces of this thread: read while the unit before ends
-  constexpr int NQ = 16 * CH / kMmaThreads;
-  uint4 qv[NQ];
-  auto read_q = [&](const Walk& x) {
-    const UnitRows u = unit_rows<kMmaRows>(x, a);
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      const int idx = threadIdx.x + kMmaThreads * i;
-      const int r = idx / CH, ch = idx - r * CH;
-      qv[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < u.rows && ch * 8 < a.D) {
-        const RowAt at = row_at(u, r, x.h, a);
-        const T* p = q + at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8;
-        if (access_ok(p, 16, a.q_span, g.err)) qv[i] = __ldg(reinterpret_cast<const uint4*>(p));
-      }
-    }
-  };
-  read_q(w);
 
   while (!w.done) {
     const UnitRows u = unit_rows<kMmaRows>(w, a);

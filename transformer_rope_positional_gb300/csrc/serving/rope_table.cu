@@ -6,12 +6,14 @@
 //  * The angle as a fraction of a turn.  The host turns f_i into w_i = f_i / 2pi mod 1 in
 //    units of 2^-64, so p * w_i in wrapping 64-bit integers is the angle modulo whole turns,
 //    exactly, for any p: there is no range reduction, and far positions lose nothing.  (The
-//    same product in binary32 is off by a radian beyond 2^24; binary64 products and
-//    reductions run at a sixtieth of the integer rate here.)
+//    same product in binary32 is off by a radian beyond 2^24.)  From row to row of one column
+//    the angle grows by a constant: one 64-bit addition.
 //  * sin and cos.  The two top bits (rounded) are the quadrant, the rest r in [-1/2, 1/2)
 //    quadrants; sin(pi/2 r) = r S(r^2) and cos(pi/2 r) = C(r^2) with S and C fitted here at
-//    Chebyshev nodes on [0, 1/4] (errors 6.8e-12 and 4.7e-11): 9 FMAs for both.
+//    Chebyshev nodes on [0, 1/4] (errors 6.8e-12 and 4.7e-11): 9 FMAs for both, two columns
+//    in one packed instruction.
 //  * One thread owns V consecutive frequencies (16 bytes of the output) and walks rows.
+// Bound by instruction issue, about 25 a value pair, just above the rate of the stores.
 #include <algorithm>
 #include <cmath>
 
@@ -41,31 +43,40 @@ struct TableArgs {
   Span pos_span, cos_span, sin_span;
 };
 
-// sin and cos of 2 pi * phase / 2^64, scaled.
-__device__ __forceinline__ void sin_cos_turn(uint64_t phase, float scale, float& sn, float& cs) {
-  const uint64_t q = (phase + (uint64_t(1) << 61)) >> 62;  // nearest quadrant
-  const int64_t rem = (int64_t)(phase - (q << 62));        // [-2^61, 2^61)
-  const int hi = (int)(rem >> 32);
-  float r = (float)hi;
-  r *= 9.31322574615478515625e-10f;  // 2^-30
-  // few bits left above the low word (angles near a whole quadrant): convert all 62
-  if (abs(hi) < (1 << 25)) r = __ll2float_rn(rem) * 2.16840434497100886801e-19f;  // 2^-62
-  const float z = r * r;
-  float s = fmaf(z, 1.582063036e-4f, -4.681266257e-3f);
-  s = fmaf(z, s, 7.969258273e-2f);
-  s = fmaf(z, s, -6.459640961e-1f);
+// What is left of the angle phase / 2^64 turns to the nearest quadrant, in quadrants: all 62
+// bits count, for angles near a whole quadrant (the upper word converted, the top 23 bits of
+// the lower one by an exponent put in front of them).
+__device__ __forceinline__ float rest_of(uint64_t phase, uint32_t& quadrant) {
+  const uint32_t hi = (uint32_t)(phase >> 32), lo = (uint32_t)phase;
+  quadrant = (hi + 0x20000000u) >> 30;
+  const int rest = (int)(hi - (quadrant << 30));  // [-2^29, 2^29)
+  const float low = __uint_as_float(0x4b000000u | (lo >> 9)) - 8388608.0f;  // lo / 2^9
+  return fmaf(low, 1.1102230246251565e-16f /* 2^-53 */, (float)rest * 9.31322574615478515625e-10f /* 2^-30 */);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// sin and cos of two angles, scaled.
+__device__ __forceinline__ void sin_cos_turn2(uint64_t p0, uint64_t p1, float scale, float2& sn, float2& cs) {
+  uint32_t q0, q1;
+  const float2 r = make_float2(rest_of(p0, q0), rest_of(p1, q1));
+  const float2 z = __fmul2_rn(r, r);
+  float2 s = __ffma2_rn(z, both(1.582063036e-4f), both(-4.681266257e-3f));
+  s = __ffma2_rn(z, s, both(7.969258273e-2f));
+  s = __ffma2_rn(z, s, both(-6.459640961e-1f));
   // pi/2 = 1.57079637 - 4.371139e-8: the leading term's own rounding is put back
-  s = fmaf(z, s, -4.371139e-8f);
-  s = fmaf(r, 1.57079637050628662109375f, r * s);
-  float c = fmaf(z, 9.036280664e-4f, -2.086006950e-2f);
-  c = fmaf(z, c, 2.536692037e-1f);
-  c = fmaf(z, c, -1.233700541f);
-  c = fmaf(z, c, 1.0f);
-  const bool odd = q & 1;
-  const float a = odd ? c : s, b = odd ? s : c;
+  s = __ffma2_rn(z, s, both(-4.371139e-8f));
+  s = __ffma2_rn(r, both(1.57079637050628662109375f), __fmul2_rn(r, s));
+  float2 c = __ffma2_rn(z, both(9.036280664e-4f), both(-2.086006950e-2f));
+  c = __ffma2_rn(z, c, both(2.536692037e-1f));
+  c = __ffma2_rn(z, c, both(-1.233700541f));
+  c = __ffma2_rn(z, c, both(1.0f));
+  s = __fmul2_rn(s, both(scale));
+  c = __fmul2_rn(c, both(scale));
   // quadrants 0..3: sin s, c, -s, -c; cos c, -s, -c, s
-  sn = (q & 2 ? -a : a) * scale;
-  cs = ((q + 1) & 2 ? -b : b) * scale;
+  auto sign = [](float v, uint32_t bit1) { return __uint_as_float(__float_as_uint(v) ^ ((bit1 << 30) & 0x80000000u)); };
+  sn = make_float2(sign(q0 & 1 ? c.x : s.x, q0), sign(q1 & 1 ? c.y : s.y, q1));
+  cs = make_float2(sign(q0 & 1 ? s.x : c.x, q0 + 1), sign(q1 & 1 ? s.y : c.y, q1 + 1));
 }
 
 // V frequencies per thread; VECTOR: F is a multiple of V and the outputs are 16-byte aligned.
@@ -82,15 +93,31 @@ __global__ void __launch_bounds__(kThreads)
   for (int e = 0; e < V; ++e) w[e] = i0 + e < a.F ? turns.w[i0 + e] : 0;
   wait_for_prior_grid();
   const int64_t width = 2 * (int64_t)a.F;
+  // without positions: the angle of the first row, and what a step of rows adds to it
+  uint64_t phase[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) phase[e] = (uint64_t)(a.first + row) * w[e];
+  if (!positions) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] *= (uint64_t)a.stride;
+  }
   for (; row < a.rows; row += a.stride) {
-    const int64_t p = a.first + (positions ? ldg(positions + row, a.pos_span, err) : row);
+    if (positions) {
+      const int64_t p = a.first + ldg(positions + row, a.pos_span, err);
+#pragma unroll
+      for (int e = 0; e < V; ++e) phase[e] = (uint64_t)p * w[e];
+    }
     Vec<T, V> c, s;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float sn, cs;
-      sin_cos_turn((uint64_t)p * w[e], a.scale, sn, cs);
-      c.e[e] = narrow<T>(cs);
-      s.e[e] = narrow<T>(sn);
+    for (int e = 0; e < V; e += 2) {
+      float2 sn, cs;
+      sin_cos_turn2(phase[e], phase[e + 1], a.scale, sn, cs);
+      narrow2(&c.e[e], cs);
+      narrow2(&s.e[e], sn);
+    }
+    if (!positions) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) phase[e] += w[e];
     }
     T* const c0 = cos + row * width;
     T* const s0 = (LAYOUT == kCache ? cos : sin) + row * width;
@@ -181,10 +208,12 @@ cudaError_t launch_layout(const TableProblem& p, cudaStream_t stream) {
   constexpr int V = 16 / sizeof(T);
   const bool vector = p.F % V == 0 && reinterpret_cast<uintptr_t>(p.cos) % 16 == 0 &&
                       reinterpret_cast<uintptr_t>(p.sin) % 16 == 0;
-  // up to 128 frequencies (heads of 256) the launch carries 1 KB of them, else 8 KB
+  // up to 128 frequencies (heads of 256) the launch carries 1 KB of them, else 8 KB; where the rows
+  // allow no 16-byte stores a thread takes two columns, so that a warp's stores lie side by side
+  // (85060 rows of 28 bf16 columns: 24.6 us with eight)
   if (p.F <= 128)
-    return vector ? launch_n<T, V, LAYOUT, true, 128>(p, stream) : launch_n<T, V, LAYOUT, false, 128>(p, stream);
-  return vector ? launch_n<T, V, LAYOUT, true, 1024>(p, stream) : launch_n<T, V, LAYOUT, false, 1024>(p, stream);
+    return vector ? launch_n<T, V, LAYOUT, true, 128>(p, stream) : launch_n<T, 2, LAYOUT, false, 128>(p, stream);
+  return vector ? launch_n<T, V, LAYOUT, true, 1024>(p, stream) : launch_n<T, 2, LAYOUT, false, 1024>(p, stream);
 }
 
 template <typename T>
