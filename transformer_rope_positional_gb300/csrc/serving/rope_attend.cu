@@ -172,26 +172,28 @@ int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 int padded_columns(int64_t D) { return (int)round_up(D, 64); }
 
-// A launch of units: its kernel, cut and grid.
+// A launch of units: its kernel, rows of a unit and grid.
 struct Units {
-  bool tall;  // units of many rows (rope_attend_tc.cuh), else of 16 (rope_attend_mma.cuh); binary32: 64 or 16
+  // 16-bit data: tall or not, M = 256 / 128 (rope_attend_tc.cuh) or 16 (rope_attend_mma.cuh);
+  // binary32 (rope_attend_f32.cuh): 64 or 8 / 4
+  bool tall;
   int64_t M, grid;
 };
 
-Units units_of(bool tc, int64_t D, int32_t dtype) {
+// The kernel for `rows` rows of a sequence and key head.  16-bit: units of 16 rows up to 16 rows
+// (beyond, K and V would be read again for every 16).  Binary32: 4 rows up to 4, 8 up to 8.
+Units units_for(double rows, int64_t D, int32_t dtype) {
   const int cols = padded_columns(D);
   Units u;
-  u.tall = tc;
   if (dtype == kF32) {
-    u.M = tc ? 64 : 16;
-    const int ctas = cols <= 64    ? tc ? f32_ctas<64, 4>() : f32_ctas<64, 1>()
-                     : cols <= 128 ? tc ? f32_ctas<128, 4>() : f32_ctas<128, 1>()
-                                   : tc ? f32_ctas<256, 4>() : f32_ctas<256, 1>();
-    u.grid = (int64_t)sm_count() * ctas;
-    return u;
+    u.tall = rows > 8;
+    u.M = u.tall ? 64 : rows > 4 ? 8 : 4;
+    u.grid = (int64_t)sm_count() * (u.tall && cols > 128 ? f32_ctas<256>() : 2);
+  } else {
+    u.tall = rows > 16;
+    u.M = !u.tall ? kMmaRows : cols <= 128 ? 256 : 128;
+    u.grid = (int64_t)sm_count() * (u.tall ? 1 : 2);
   }
-  u.M = !tc ? kMmaRows : cols <= 128 ? 256 : 128;
-  u.grid = (int64_t)sm_count() * (tc ? 1 : 2);
   return u;
 }
 
@@ -212,10 +214,12 @@ Part part_of(int64_t T, int64_t nq, int64_t nk, int64_t D, const Units& u, bool 
   return s;
 }
 
-// The larger of both kernels' parts: which one runs depends on the batch as well.
+// The largest part of the kernels': which one runs depends on the batch as well.
 int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, bool dense) {
-  return std::max(part_of(T, nq, nk, D, units_of(false, D, dtype), dense).bytes,
-                  part_of(T, nq, nk, D, units_of(true, D, dtype), dense).bytes);
+  int64_t most = 0;
+  for (double rows : {4.0, 8.0, 16.0, 17.0})
+    most = std::max(most, part_of(T, nq, nk, D, units_for(rows, D, dtype), dense).bytes);
+  return most;
 }
 
 // The unit kernels keep cache rows in 32 bits: fewer than 2^31 rows of one head (137 GB a cache
@@ -259,16 +263,26 @@ cudaError_t launch_tc(const AttendProblem& p, const Pointers& g, const AttendArg
                                 static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, c);
 }
 
-template <int DP, int RPT>
-cudaError_t launch_f32(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
-                       cudaStream_t stream) {
-  auto kernel = attend_f32_kernel<DP, RPT>;
-  const size_t smem = sizeof(F32Shared<DP, RPT>);
+template <typename K>
+cudaError_t launch_f32_kernel(K kernel, size_t smem, int threads, const AttendProblem& p, const Pointers& g,
+                              const AttendArgs& a, const Cut& c, int64_t grid, cudaStream_t stream) {
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped_smem(kernel, (unsigned)grid, kF32Threads, smem, stream, static_cast<const float*>(p.query),
+  return launch_overlapped_smem(kernel, (unsigned)grid, threads, smem, stream, static_cast<const float*>(p.query),
                                 static_cast<const float*>(p.k_cache), static_cast<const float*>(p.v_cache),
                                 static_cast<float*>(p.out), p.lse, g, a, c);
+}
+
+template <int DP>
+cudaError_t launch_f32(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, const Units& u,
+                       cudaStream_t stream) {
+  if (u.tall)
+    return launch_f32_kernel(attend_f32_kernel<DP>, sizeof(F32Shared<DP>), kF32Threads, p, g, a, c, u.grid, stream);
+  if (u.M == 8)
+    return launch_f32_kernel(attend_f32_few_kernel<DP, 8>, sizeof(FewShared<DP>), kFewThreads, p, g, a, c, u.grid,
+                             stream);
+  return launch_f32_kernel(attend_f32_few_kernel<DP, 4>, sizeof(FewShared<DP>), kFewThreads, p, g, a, c, u.grid,
+                           stream);
 }
 
 template <typename T>
@@ -276,11 +290,9 @@ cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const Attend
                          cudaStream_t stream) {
   const int cols = padded_columns(p.D);
   if constexpr (sizeof(T) == 4) {
-    if (cols <= 64)
-      return u.tall ? launch_f32<64, 4>(p, g, a, c, u.grid, stream) : launch_f32<64, 1>(p, g, a, c, u.grid, stream);
-    if (cols <= 128)
-      return u.tall ? launch_f32<128, 4>(p, g, a, c, u.grid, stream) : launch_f32<128, 1>(p, g, a, c, u.grid, stream);
-    return u.tall ? launch_f32<256, 4>(p, g, a, c, u.grid, stream) : launch_f32<256, 1>(p, g, a, c, u.grid, stream);
+    if (cols <= 64) return launch_f32<64>(p, g, a, c, u, stream);
+    if (cols <= 128) return launch_f32<128>(p, g, a, c, u, stream);
+    return launch_f32<256>(p, g, a, c, u, stream);
   } else {
     if (u.tall) {
       if (cols <= 64) return launch_tc<T, 64>(p, g, a, c, u.grid, stream);
@@ -316,7 +328,7 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
   // (8 MB are 1.2 us of the copy bandwidth) and a sequence's rows do not fill a tile by themselves
   const double saved = (double)(p.B - 1) * (double)p.prefix_len * (double)p.nk * (double)p.D * 4;
   const bool shared = saved > 8e6 && rows < 128;
-  const Units u_own = units_of(rows > 16, p.D, p.dtype), u_pre = units_of(p.T * a.G > 16, p.D, p.dtype);
+  const Units u_own = units_for(rows, p.D, p.dtype), u_pre = units_for((double)p.T * a.G, p.D, p.dtype);
   const Part s_own = part_of(p.T, p.nq, p.nk, p.D, u_own, shared);
   char* const ws = static_cast<char*>(p.workspace);
   Cut own = cut_of(s_own, ws, u_own), pre = own;

@@ -16,7 +16,7 @@
 
 #include <type_traits>
 
-#include "rope_attend.cuh"
+#include "rope_attend_ring.cuh"
 
 namespace rope {
 namespace attend {
@@ -44,13 +44,6 @@ struct MmaShared {
   int bad[16];
   int64_t tmp[kMmaThreads / 32 + 2];
 };
-
-__device__ __forceinline__ unsigned smem_u32(const void* p) { return (unsigned)__cvta_generic_to_shared(p); }
-
-// 16 bytes, or zeros where !ok.
-__device__ __forceinline__ void cp_async16_or_zero(unsigned dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], unsigned at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -89,13 +82,6 @@ __device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float x, float y
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 2^x, relative error 2^-22 (0 for -infinity).
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // DP: D rounded up to a multiple of 64; columns past D are zeros in shared memory.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kMmaThreads, 2)
@@ -113,22 +99,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   Walk w = find_share<kMmaRows, kMmaKeys, kMmaThreads>(g, a, c, sm.tmp);
   if (w.done) return;
 
-  // ---- copies: K then V of the tiles of the share, in order, into the warp's ring
-  Walk pw = w;
-  int pk = pw.k0;
-  int pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
-  int slot = 0;         // stage of the next copy
-  int p_tile = 0;       // tile of the next copy, modulo 6
-  bool p_v = false;     // its V is next
-  unsigned char* const ring = sm.ring[warp][0];
-  // page of this lane's key (lane & 15) of the next tile: looked up ahead, used when it is copied
-  PageRow page;
-  auto look_up = [&]() {
-    page = {-2, 0};  // no such key
-    if (pw.done) return;
-    const int j = c.lo + pk * kMmaKeys + warp * 16 + (lane & 15);
-    if (j < pend) page = page_row(j, g.block_table + (int64_t)pw.b * a.W, g, a);
-  };
+  Ring<T, 16, DP, S, kMmaRows, kMmaKeys, true> ring;
+  ring.start(w, sm.ring[warp][0], g, a, c);
   // a unit's query rows, in 16-byte pieces of this thread: read while the unit before ends
   constexpr int NQ = 16 * CH / kMmaThreads;
   uint4 qv[NQ];
@@ -147,58 +119,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     }
   };
 
-  look_up();
   read_q(w);
-  int row = -1;  // cache row of the key of the tile whose K was copied last
-  // 16 bits a tile: which of its keys are there, for the last 6 tiles
-  uint32_t valid0 = 0, valid1 = 0, valid2 = 0;
-  auto copy_stage = [&]() {
-    if (!p_v) {
-      row = -1;
-      if (page.page >= 0 && page.page < a.num_blocks)
-        row = ((int)page.page * a.nk + pw.h) * a.block_size + page.row;
-      else if (page.page != -2)
-        atomicOr(g.err, kSlotOutOfRange);
-      const uint32_t there = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-      uint32_t& word = p_tile < 2 ? valid0 : p_tile < 4 ? valid1 : valid2;
-      word = p_tile & 1 ? (word & 0x0000ffffu) | (there << 16) : (word & 0xffff0000u) | there;
-      p_tile = p_tile == 5 ? 0 : p_tile + 1;
-      if (!pw.done) {
-        if (++pk == walk_k1(pw)) {
-          walk_next<kMmaRows, kMmaKeys>(pw, g, a, c);
-          pk = pw.k0;
-          if (!pw.done) pend = tile_end<kMmaRows>(pw.s, pw.i, a, c);
-        }
-      }
-      look_up();
-    }
-    const T* const src = p_v ? vc : kc;
-    const Span& span = p_v ? a.v_span : a.k_span;
-    const unsigned dst = smem_u32(ring + slot * Shape::kStage);
-    if (__any_sync(0xffffffffu, row >= 0)) {
-#pragma unroll
-      for (int i = 0; i < 16 * CH / 32; ++i) {
-        const int idx = lane + 32 * i;
-        const int key = idx / CH, ch = idx - key * CH;
-        const int r = __shfl_sync(0xffffffffu, row, key);
-        const bool ok = r >= 0 && ch * 8 < a.D;
-        const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (ok ? ch * 8 : 0));
-        cp_async16_or_zero(dst + key * (DP * 2) + ((ch ^ (key & 7)) << 4), p, ok && access_ok(p, 16, span, g.err));
-      }
-    } else if (p_v) {  // no key of the tile: its weights are 0, and V must not be NaN
-#pragma unroll
-      for (int i = 0; i < 16 * CH / 32; ++i)
-        *reinterpret_cast<uint4*>(ring + slot * Shape::kStage + (lane + 32 * i) * 16) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    p_v = !p_v;
-    cp_async_commit();
-    slot = slot + 1 == S ? 0 : slot + 1;
-  };
 #pragma unroll 1
-  for (int i = 0; i < S - 1; ++i) copy_stage();
+  for (int i = 0; i < S - 1; ++i) ring.copy(kc, vc, g, a, c);
 
-  int cur = 0;     // stage of the next product
-  int tile = 0;    // current tile, modulo 6
   const int r0 = lane >> 2, cq = (lane & 3) * 2;
   const unsigned q_at = smem_u32(sm.q);
   // ldmatrix rows: K (and Q) by (key, chunk), V transposed
@@ -238,12 +162,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     for (int k = w.k0; k < k1; ++k) {
       cp_async_wait<S - 2>();
       __syncwarp();
-      const uint32_t word = tile < 2 ? valid0 : tile < 4 ? valid1 : valid2;
-      const uint32_t there = (tile & 1 ? word >> 16 : word) & 0xffffu;
-      tile = tile == 5 ? 0 : tile + 1;
-      copy_stage();  // into the stage that the last product left
-      const unsigned kt = smem_u32(ring + cur * Shape::kStage);
-      cur = cur + 1 == S ? 0 : cur + 1;
+      const uint32_t there = ring.seen();
+      const unsigned kt = smem_u32(ring.take(kc, vc, g, a, c));
       const int j0 = c.lo + k * kMmaKeys + warp * 16;
       // ---- scores
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -302,9 +222,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       // ---- outputs
       cp_async_wait<S - 2>();
       __syncwarp();
-      copy_stage();
-      const unsigned vt = smem_u32(ring + cur * Shape::kStage);
-      cur = cur + 1 == S ? 0 : cur + 1;
+      const unsigned vt = smem_u32(ring.take(kc, vc, g, a, c));
 #pragma unroll
       for (int n = 0; n < DP / 16; ++n) {
         uint32_t b[4];
