@@ -97,6 +97,13 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
+// 32 bytes at once: whole sectors, where each lane writes a row of its own.
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     attend_tc_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
@@ -547,8 +554,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(to + ch * 32 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+              for (int i = 0; i < 32; i += 8) store8(to + ch * 32 + i, &y[i]);
             }
           }
         }
