@@ -95,6 +95,12 @@ __device__ __forceinline__ PageRow page_row(int j, const int64_t* table, const P
 // unit begins in this CTA, slot 0: it began in an earlier one), and the joining kernel adds
 // them up in order.  Every CTA finds its share by itself from the lengths on the device:
 // the cut needs no host copy of them and no extra launch.
+//
+// A unit of up to whole_tiles() tiles is not split: the CTA in which it begins finishes it.  A
+// split costs writing and reading M rows of binary32 twice, about 3 tiles' time for 256 rows (68
+// sequences of 45 tokens on 219, 8 rows a key head: 56 us with every unit split where the shares
+// end, 43 with 4 tiles kept whole) and less than one for 16 or 64 (2 sequences of 14 tokens in
+// binary32: 25 us split, 40 us whole).
 // ---------------------------------------------------------------------------
 struct Cut {
   int32_t lo;         // first key of the launch: P when the prefix has its own launch, else 0
@@ -183,8 +189,44 @@ struct Walk {
   bool done;
 };
 
+// Units of at most so many tiles are not split.
+template <int M>
+__host__ __device__ constexpr int whole_tiles() {
+  return M > 64 ? 4 : 1;
+}
+
+// Key tiles of the current unit in this CTA end here.
+template <int M>
+__device__ __forceinline__ int walk_k1(const Walk& w) {
+  return w.work <= whole_tiles<M>() ? w.work : (int)min((int64_t)w.work, w.k0 + w.left);
+}
+
 __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
   return (n | d) >> 32 ? n / d : (int64_t)((uint32_t)n / (uint32_t)d);
+}
+
+// The next unit of the share; w.done at its end.
+template <int M, int KT>
+__device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const AttendArgs& a, const Cut& c) {
+  w.left -= walk_k1<M>(w) - w.k0;
+  if (w.left <= 0) {
+    w.done = true;
+    return;
+  }
+  w.k0 = 0;
+  if (++w.h < a.nk) return;
+  w.h = 0;
+  ++w.i;
+  while (w.i >= w.tiles) {
+    w.i = 0;
+    if (++w.b >= (c.prefix ? 1 : (int)a.B)) {  // a share ends before the last sequence does: never, unless the lengths change under way
+      w.done = true;
+      return;
+    }
+    w.s = seq_work(w.b, g, a, c);
+    w.tiles = row_tiles<M>(w.s);
+  }
+  w.work = tile_work<M, KT>(w.s, w.i, a, c);
 }
 
 // Sum over the CTA's NT threads and the exclusive prefix of each, through shared memory
@@ -296,40 +338,16 @@ __device__ __forceinline__ Walk find_share(const Pointers& g, const AttendArgs& 
   }
   w.h = (int)quotient(rest, w.work);
   w.k0 = (int)(rest - (int64_t)w.h * w.work);
+  if (w.k0 > 0 && w.work <= whole_tiles<M>()) walk_next<M, KT>(w, g, a, c);  // the CTA before finishes it
   return w;
 }
 
-// Key tiles of the current unit in this CTA end here.
-__device__ __forceinline__ int walk_k1(const Walk& w) { return (int)min((int64_t)w.work, w.k0 + w.left); }
-
-// The next unit of the share; w.done at its end.
-template <int M, int KT>
-__device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const AttendArgs& a, const Cut& c) {
-  w.left -= walk_k1(w) - w.k0;
-  if (w.left <= 0) {
-    w.done = true;
-    return;
-  }
-  w.k0 = 0;
-  if (++w.h < a.nk) return;
-  w.h = 0;
-  ++w.i;
-  while (w.i >= w.tiles) {
-    w.i = 0;
-    if (++w.b >= (c.prefix ? 1 : (int)a.B)) {  // a share ends before the last sequence does: never, unless the lengths change under way
-      w.done = true;
-      return;
-    }
-    w.s = seq_work(w.b, g, a, c);
-    w.tiles = row_tiles<M>(w.s);
-  }
-  w.work = tile_work<M, KT>(w.s, w.i, a, c);
-}
 
 // The record of row r of a unit that begins in this CTA: its CTAs and the row's place.
+template <int M>
 __device__ __forceinline__ int2 unit_record(const Walk& w, int r) {
   int last = blockIdx.x;
-  if (w.work > w.left) {  // the rest of the unit, in shares below its size
+  if (w.work > whole_tiles<M>() && w.work > w.left) {  // the rest of the unit, in shares below its size
     const uint32_t rest = (uint32_t)(w.work - w.left);
     last += (int)((rest + (uint32_t)w.share - 1) / (uint32_t)w.share);
   }

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP>())
   wait_for_prior_grid();
   Walk w = find_share<M, kF32Keys, kF32Threads>(g, a, c, reinterpret_cast<int64_t*>(sm.p));
   while (!w.done) {
-    const int k1 = walk_k1(w);
+    const int k1 = walk_k1<M>(w);
     const int end = tile_end<M>(w.s, w.i, a, c);
     const UnitRows u = unit_rows<M>(w, a);
     const int64_t* table = g.block_table + w.b * a.W;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP>())
                             : slot_ml(c, a, blockIdx.x, begins ? 1 : 0) + r * 2;
           *reinterpret_cast<float2*>(ml) = make_float2(m[i], l[i]);
         }
-        if (begins) c.rec[row] = final && !all_fine ? make_int2(-1, -1) : unit_record(w, r);
+        if (begins) c.rec[row] = final && !all_fine ? make_int2(-1, -1) : unit_record<M>(w, r);
       }
     }
     __syncthreads();  // the buffers are free
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
-    const int k1 = walk_k1(w);
+    const int k1 = walk_k1<R>(w);
     for (int k = w.k0; k < k1; ++k) {
       cp_async_wait<S - 2>();
       __syncwarp();
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     if (begins && threadIdx.x < u.rows) {
       const RowAt at = row_at(u, threadIdx.x, w.h, a);
-      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record(w, threadIdx.x);
+      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record<R>(w, threadIdx.x);
     }
     walk_next<R, kFewKeys>(w, g, a, c);
   }

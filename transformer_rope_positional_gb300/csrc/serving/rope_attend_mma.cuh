@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     int lim0 = lane < u.rows ? row_limit(w, row_at(u, lane, w.h, a).t, g, a, c) : 0;
     const int lim1 = __shfl_sync(0xffffffffu, lim0, r0 + 8);
     lim0 = __shfl_sync(0xffffffffu, lim0, r0);
-    const int k1 = walk_k1(w);
+    const int k1 = walk_k1<kMmaRows>(w);
 
     float o[DP / 8][4];
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     }
     if (begins && threadIdx.x < u.rows) {
       const RowAt at = row_at(u, threadIdx.x, w.h, a);
-      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record(w, threadIdx.x);
+      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record<kMmaRows>(w, threadIdx.x);
     }
     w = nw;
   }

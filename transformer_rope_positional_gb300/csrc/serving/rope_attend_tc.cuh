@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
       const int lead = S::kAhead / nt;
-      const int k1 = walk_k1(w), kt = k1 - w.k0;
+      const int k1 = walk_k1<S::M>(w), kt = k1 - w.k0;
       const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
       PageRow page;                    // of this lane's key of the next K tile
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       unsigned round = 0, unit = 0;
       bool ok = true;
       while (!w.done && ok) {
-        const int kt = walk_k1(w) - w.k0;
+        const int kt = walk_k1<S::M>(w) - w.k0;
         ok = tc::bar_wait(&sm.q_copied, unit & 1, &sm.dead);
         tc::fence_to_tensor();
         if (ok) tc::bar_arrive(&sm.q_full);
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     bool ok = true;
     while (__any_sync(0xffffffffu, !w.done && ok)) {
       const int nt = (int)tc::uniform(w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1);
-      const int jobs = (int)tc::uniform((walk_k1(w) - w.k0) * nt);  // job x is of group x % NW
+      const int jobs = (int)tc::uniform((walk_k1<S::M>(w) - w.k0) * nt);  // job x is of group x % NW
       ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.q_full, unit & 1, &sm.dead));
       ++unit;
       if (!ok) break;
@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     unsigned pv = 0;          // parts of scores, and products into this group's O, so far
     int k_base = 0;           // K tiles before this unit
     unsigned ml_seen = 0;
+    const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;  // a row of out is a multiple of 64 bytes
     bool ok = true;
     // The last product into this group's O.  Even and odd ones have a barrier each: by the time
     // that one is waited for, the one before it on the same barrier was done (two groups: before
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     while (!w.done) {
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
-      const int k1 = walk_k1(w), kt = k1 - w.k0, jobs = kt * nt;
+      const int k1 = walk_k1<S::M>(w), kt = k1 - w.k0, jobs = kt * nt;
       const int r = nt == 2 ? group * 128 + r_tile : r_tile;
       const bool mine = r < u.rows;
       const RowAt at = row_at(u, mine ? r : 0, w.h, a);
@@ -543,14 +544,22 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           if (mine && ch * 32 < a.D) {
             if (final) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                Vec<T, 8> o;
+              for (int i = 0; i < 32; i += 16) {
+                alignas(16) T o[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  fine = fine && fabsf(y[i + e]) <= FLT_MAX;
-                  o.e[e] = narrow<T>(y[i + e]);
+                for (int e = 0; e < 16; e += 2) {
+                  fine = fine && fabsf(y[i + e]) <= FLT_MAX && fabsf(y[i + e + 1]) <= FLT_MAX;
+                  narrow2(&o[e], make_float2(y[i + e], y[i + e + 1]));
                 }
-                store_vec(out + row * a.D + ch * 32 + i, o, a.out_span, g.err);
+                T* const p = out + row * a.D + ch * 32 + i;
+                if (access_ok(p, 32, a.out_span, g.err)) {
+                  if (wide) {
+                    store8(reinterpret_cast<float*>(p), reinterpret_cast<const float*>(o));
+                  } else {
+                    reinterpret_cast<uint4*>(p)[0] = reinterpret_cast<const uint4*>(o)[0];
+                    reinterpret_cast<uint4*>(p)[1] = reinterpret_cast<const uint4*>(o)[1];
+                  }
+                }
               }
             } else {
 #pragma unroll
@@ -567,7 +576,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
                               : slot_ml(c, a, blockIdx.x, begins ? 1 : 0) + r * 2;
             *reinterpret_cast<float2*>(ml) = make_float2(m, l);
           }
-          if (begins) c.rec[row] = final && !fine ? make_int2(-1, -1) : unit_record(w, r);
+          if (begins) c.rec[row] = final && !fine ? make_int2(-1, -1) : unit_record<S::M>(w, r);
         }
       }
       // O may be written again: by the group that read it (both, when it read both)
