@@ -2,16 +2,20 @@
 //
 // Bound by the cache's bytes: a unit of 16 rows does 32 operations per byte of K and V, far
 // below the matrix units' 280, so the kernel is built to keep loads in flight.
-//  * A CTA's four warps each take 16 keys of every 64-key tile and run on their own: each
-//    copies its keys' K and V rows into its own ring of stages with cp.async (16-byte pieces,
-//    any page size, pages looked up one tile ahead), waits for its own copies only, and keeps
-//    its own running m, l and O; there is no barrier until the unit ends, and the copies of
-//    the next unit are already on their way then.
+//  * A CTA's four warps each take 16 keys of every 64-key tile and run on their own, each with
+//    its own ring of copies (rope_attend_ring.cuh) and its own running m, l and O; there is no
+//    barrier until the unit ends, and the copies of the next unit are already on their way
+//    then.  Two CTAs an SM, so that one copies while the other ends a unit (heads of 256 with
+//    one CTA: 105 us for the own keys of 32 drafts, with two 58).
 //  * Scores and outputs by mma.sync m16n8k16 (the rows pad to 16): the tensor core's newer
 //    instruction wants 64 or 128 rows a tile, and these units have 1 to 16.
 //  * The weights of a score tile are, register for register, the A operand of the product
 //    with V.  They are rounded to the data's type there (half a step relative each, the
 //    sums l taken before); m, l and O stay in binary32.
+//
+// 64 requests of up to 8192 tokens, 32 q and 8 k heads of 128, bf16: 176 us, 6.3 TB/s, 0.93 of
+// the measured copy bandwidth.  4 requests of 300 tokens: 8.9 us with the joining kernel, all of
+// it latency (lengths, pages, rows, two launches).
 #pragma once
 
 #include <type_traits>
