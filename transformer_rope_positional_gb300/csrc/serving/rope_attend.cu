@@ -45,113 +45,180 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// Joins the partial results of a row's units (own keys, and the prefix's where it had its own
-// launch), one warp per row; a row whose result is not finite is computed again key by key:
-// a key that a row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of
-// its value would leave NaN.  A warp takes per_warp consecutive rows and looks at their
-// records first, so that rows already finished cost one load for all of them.  The partial
-// results of a row are read eight at a time, all loads before any arithmetic.
+// The joining kernels add the partial results of rows up, a warp to a row.  A row whose result
+// is not finite is computed again key by key: a key that a row does not see has weight 0 in the
+// unit kernels, and 0 * infinity or NaN of its value would leave NaN.
+
+// Where partial result s of a row lies: (m, l) and O.
+struct Source {
+  const float* ml;
+  const float* o;
+};
+
+__device__ __forceinline__ Source slot_source(const Cut& c, const AttendArgs& a, int cta, bool begins, int at) {
+  return {slot_ml(c, a, cta, begins ? 1 : 0) + at * 2, slot_o(c, a, cta, begins ? 1 : 0) + (int64_t)at * a.D};
+}
+
+// Adds up n partial results of each of R rows, NS at a time, all loads before any arithmetic:
+// m, l, and this lane's columns 2 lane + 64 e of O.  source(r, s) is called for s < n only.
+template <int E, int R, int NS, typename F>
+__device__ __forceinline__ void add_up(int n, const AttendArgs& a, F&& source, float (&m)[R], float (&l)[R],
+                                       float2 (&o)[R][E]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[r][e] = make_float2(0.f, 0.f);
+  }
+  for (int s0 = 0; s0 < n; s0 += NS) {
+    float2 v[R][NS][E], ml[R][NS];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        ml[r][s] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[r][s][e] = make_float2(0.f, 0.f);
+        if (s0 + s < n) {
+          const Source x = source(r, s0 + s);
+          ml[r][s] = *reinterpret_cast<const float2*>(x.ml);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (lane * 2 + 64 * e < a.D) v[r][s][e] = *reinterpret_cast<const float2*>(x.o + lane * 2 + 64 * e);
+        }
+      }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = m[r];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) top = fmaxf(top, ml[r][s].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float keep = fast_exp2(m[r] - base);
+      l[r] *= keep;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[r][e] = make_float2(o[r][e].x * keep, o[r][e].y * keep);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const float f = fast_exp2(ml[r][s].x - base);
+        l[r] = fmaf(ml[r][s].y, f, l[r]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          o[r][e].x = fmaf(f, v[r][s][e].x, o[r][e].x);
+          o[r][e].y = fmaf(f, v[r][s][e].y, o[r][e].y);
+        }
+      }
+      m[r] = top;
+    }
+  }
+}
+
+// The row's result from m, l and O, if it is finite.
+template <typename T, int E>
+__device__ __forceinline__ bool write_row(int64_t row, float m, float l, float2 (&o)[E], T* __restrict__ out,
+                                          float* __restrict__ lse, const Pointers& g, const AttendArgs& a) {
+  const int lane = threadIdx.x & 31;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  bool fine = l <= FLT_MAX;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    o[e] = make_float2(o[e].x * inv, o[e].y * inv);
+    fine = fine && fabsf(o[e].x) <= FLT_MAX && fabsf(o[e].y) <= FLT_MAX;
+  }
+  if (!__all_sync(0xffffffffu, fine)) return false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int d = lane * 2 + 64 * e;
+    T* p = out + row * a.D + d;
+    if (d < a.D && access_ok(p, 2 * sizeof(T), a.out_span, g.err)) narrow2(p, o[e]);
+  }
+  if (lse && lane == 0 && access_ok(lse + row, 4, a.lse_span, g.err))
+    lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+  return true;
+}
+
+// With a launch for the prefix: every row has partial results of both, the prefix's first.
+template <typename T, int E>
+__global__ void __launch_bounds__(kWarps * 32)
+    attend_join_both_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
+                            T* __restrict__ out, float* __restrict__ lse, Pointers g, AttendArgs a, Cut own, Cut pre) {
+  wait_for_prior_grid();
+  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (row >= a.T * a.nq) return;
+  const int64_t rows = min(ldg(g.qsl + a.B, a.qsl_span, g.err), a.T) * a.nq;
+  const int2 x = own.rec[row], y = pre.rec[row];
+  if (row >= rows) return;
+  const int c0 = x.x & 0xffff, c1 = x.x >> 16, p0 = y.x & 0xffff, p1 = y.x >> 16;
+  float m[1] = {-INFINITY}, l[1] = {NAN};
+  float2 o[1][E] = {};
+  // (a row that no unit covered, for starts out of order, has any record: key by key)
+  if (c1 >= c0 && c1 < own.grid && (unsigned)x.y < (unsigned)own.slot_rows && p1 >= p0 && p1 < pre.grid &&
+      (unsigned)y.y < (unsigned)pre.slot_rows) {
+    const int n_pre = p1 - p0 + 1;
+    add_up<E, 1, 8>(n_pre + c1 - c0 + 1, a, [&](int, int s) -> Source {
+      const bool is_pre = s < n_pre;
+      const Cut& c = is_pre ? pre : own;
+      const int first = is_pre ? p0 : c0, last = is_pre ? p1 : c1;
+      if (first == last) return {c.dense + a.T * a.nq * a.D + row * 2, c.dense + row * a.D};
+      const int cta = first + (is_pre ? s : s - n_pre);
+      return slot_source(c, a, cta, cta == first, is_pre ? y.y : x.y);
+    }, m, l, o);
+  }
+  if (!write_row<T, E>(row, m[0], l[0], o[0], out, lse, g, a)) {
+    const int64_t t = row / a.nq;
+    attend_row<T, 2 * E>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
+  }
+}
+
+// Without: the rows whose unit was split.  A warp looks at the records of per_warp consecutive
+// rows with one load, and takes rows of two parts (most, where there are many rows) four at a time.
 template <typename T, int E>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_join_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
-                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut own, Cut pre, int per_warp) {
-  constexpr int NS = 8;
+                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut own, int per_warp) {
   wait_for_prior_grid();
   const int lane = threadIdx.x & 31;
   const int64_t first = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * per_warp;
   const int64_t rows = min(ldg(g.qsl + a.B, a.qsl_span, g.err), a.T) * a.nq;
-  const bool shared = own.shared != 0;
-  int2 mine = make_int2(0, 0), mine_pre = make_int2(0, 0);
-  bool todo = lane < per_warp && first + lane < a.T * a.nq;
-  if (todo) {
-    mine = own.rec[first + lane];
-    if (shared) mine_pre = pre.rec[first + lane];
+  int2 mine = make_int2(0, 0);
+  if (lane < per_warp && first + lane < a.T * a.nq) mine = own.rec[first + lane];
+  const int n_mine = (mine.x >> 16) - (mine.x & 0xffff) + 1;
+  const bool todo = first + lane < rows && (mine.x < 0 || n_mine != 1);
+  // (a row that no unit covered, for starts out of order, has any record)
+  const bool known = mine.x >= 0 && n_mine > 1 && (mine.x >> 16) < own.grid && (unsigned)mine.y < (unsigned)own.slot_rows;
+  uint32_t again = __ballot_sync(0xffffffffu, todo && !known), two = __ballot_sync(0xffffffffu, todo && known && n_mine == 2),
+           more = __ballot_sync(0xffffffffu, todo && known && n_mine > 2);
+  while (two) {
+    int row[4], cta[4], at[4], count = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      row[r] = two ? __ffs(two) - 1 : row[r > 0 ? r - 1 : 0];
+      count += two != 0;
+      two &= two - 1;
+      cta[r] = __shfl_sync(0xffffffffu, mine.x, row[r]) & 0xffff;
+      at[r] = __shfl_sync(0xffffffffu, mine.y, row[r]);
+    }
+    float m[4], l[4];
+    float2 o[4][E];
+    add_up<E, 4, 2>(2, a, [&](int r, int s) { return slot_source(own, a, cta[r] + s, s == 0, at[r]); }, m, l, o);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < count && !write_row<T, E>(first + row[r], m[r], l[r], o[r], out, lse, g, a)) again |= 1u << row[r];
   }
-  todo = todo && first + lane < rows && (shared || mine.x < 0 || (mine.x & 0xffff) != mine.x >> 16);
-  uint32_t left = __ballot_sync(0xffffffffu, todo);
-  while (left) {
-    const int i = __ffs(left) - 1;
-    left &= left - 1;
-    const int64_t row = first + i;
-    const int x = __shfl_sync(0xffffffffu, mine.x, i), x_at = __shfl_sync(0xffffffffu, mine.y, i);
-    const int y = __shfl_sync(0xffffffffu, mine_pre.x, i), y_at = __shfl_sync(0xffffffffu, mine_pre.y, i);
-    const int c0 = x & 0xffff, c1 = x >> 16, p0 = y & 0xffff, p1 = y >> 16;
-    bool known = c1 >= c0 && c1 < own.grid && (unsigned)x_at < (unsigned)own.slot_rows;
-    if (shared) known = known && p1 >= p0 && p1 < pre.grid && (unsigned)y_at < (unsigned)pre.slot_rows;
-    float m = -INFINITY, l = 0.f;
-    float2 o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = make_float2(0.f, 0.f);
-    if (known) {
-      // sources 0 .. n_pre - 1: the prefix's parts, then the own keys' parts
-      const int n_pre = shared ? p1 - p0 + 1 : 0, n = n_pre + c1 - c0 + 1;
-      for (int s0 = 0; s0 < n; s0 += NS) {
-        float2 v[NS][E], ml[NS];
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          if (s0 + s < n) {
-            const bool is_pre = s0 + s < n_pre;
-            const int c_first = is_pre ? p0 : c0, c_last = is_pre ? p1 : c1;
-            const int cta = c_first + (is_pre ? s0 + s : s0 + s - n_pre), slot = cta == c_first ? 1 : 0;
-            const int at = is_pre ? y_at : x_at;
-            const Cut& c = is_pre ? pre : own;
-            const bool whole = c_first == c_last;
-            const float* so = whole ? c.dense + row * a.D : slot_o(c, a, cta, slot) + (int64_t)at * a.D;
-            const float* sml = whole ? c.dense + a.T * a.nq * a.D + row * 2 : slot_ml(c, a, cta, slot) + at * 2;
-            ml[s] = *reinterpret_cast<const float2*>(sml);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const int d = lane * 2 + 64 * e;
-              v[s][e] = d < a.D ? *reinterpret_cast<const float2*>(so + d) : make_float2(0.f, 0.f);
-            }
-          } else {
-            ml[s] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[s][e] = make_float2(0.f, 0.f);
-          }
-        }
-        float top = m;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) top = fmaxf(top, ml[s].x);
-        const float base = top == -INFINITY ? 0.f : top;
-        const float keep = fast_exp2(m - base);
-        l *= keep;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = make_float2(o[e].x * keep, o[e].y * keep);
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const float f = fast_exp2(ml[s].x - base);
-          l = fmaf(ml[s].y, f, l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            o[e].x = fmaf(f, v[s][e].x, o[e].x);
-            o[e].y = fmaf(f, v[s][e].y, o[e].y);
-          }
-        }
-        m = top;
-      }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      bool fine = l <= FLT_MAX;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        o[e] = make_float2(o[e].x * inv, o[e].y * inv);
-        fine = fine && fabsf(o[e].x) <= FLT_MAX && fabsf(o[e].y) <= FLT_MAX;
-      }
-      known = __all_sync(0xffffffffu, fine);
-    }
-    if (!known) {
-      const int64_t t = row / a.nq;
-      attend_row<T, 2 * E>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
-      continue;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int d = lane * 2 + 64 * e;
-      T* p = out + row * a.D + d;
-      if (d < a.D && access_ok(p, 2 * sizeof(T), a.out_span, g.err)) narrow2(p, o[e]);
-    }
-    if (lse && lane == 0 && access_ok(lse + row, 4, a.lse_span, g.err))
-      lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+  while (more) {
+    const int i = __ffs(more) - 1;
+    more &= more - 1;
+    const int x = __shfl_sync(0xffffffffu, mine.x, i), at = __shfl_sync(0xffffffffu, mine.y, i), cta = x & 0xffff;
+    float m[1], l[1];
+    float2 o[1][E];
+    add_up<E, 1, 8>((x >> 16) - cta + 1, a, [&](int, int s) { return slot_source(own, a, cta + s, s == 0, at); }, m, l, o);
+    if (!write_row<T, E>(first + i, m[0], l[0], o[0], out, lse, g, a)) again |= 1u << i;
+  }
+  while (again) {
+    const int64_t row = first + __ffs(again) - 1, t = row / a.nq;
+    again &= again - 1;
+    attend_row<T, 2 * E>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
   }
 }
 
@@ -310,15 +377,19 @@ cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const Attend
 template <typename T, int E>
 cudaError_t launch_join(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& own, const Cut& pre,
                         cudaStream_t stream) {
+  const T *q = static_cast<const T*>(p.query), *kc = static_cast<const T*>(p.k_cache),
+          *vc = static_cast<const T*>(p.v_cache);
+  T* const out = static_cast<T*>(p.out);
   const int64_t rows = p.T * p.nq;
-  // one row a warp while that leaves few warps to an SM, up to 8 where most rows are finished
+  if (own.shared)
+    return launch_overlapped(attend_join_both_kernel<T, E>, (unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32,
+                             stream, q, kc, vc, out, p.lse, g, a, own, pre);
+  // one row a warp while that leaves few warps to an SM, up to 32 where most rows are finished
   const int64_t warps = (int64_t)sm_count() * 32;
-  const int per_warp = (int)std::min<int64_t>(8, (rows + warps - 1) / warps);
+  const int per_warp = (int)std::min<int64_t>(32, (rows + warps - 1) / warps);
   const int64_t grid = (rows + (int64_t)per_warp * kWarps - 1) / ((int64_t)per_warp * kWarps);
-  return launch_overlapped(attend_join_kernel<T, E>, (unsigned)grid, kWarps * 32, stream,
-                           static_cast<const T*>(p.query), static_cast<const T*>(p.k_cache),
-                           static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, own, pre,
-                           per_warp);
+  return launch_overlapped(attend_join_kernel<T, E>, (unsigned)grid, kWarps * 32, stream, q, kc, vc, out, p.lse, g, a,
+                           own, per_warp);
 }
 
 template <typename T>
