@@ -280,7 +280,7 @@ int rope_qkv_rmsnorm_rope_cache(const rope_tensor_t* qkv, int64_t num_q_heads, i
  *
  * inv_freq[i] = base^(-2i/R) for i < F = R/2, changed by `scaling` (NULL: not at all):
  *   ROPE_SCALING_LINEAR      inv_freq[i] / factor
- *   ROPE_SCALING_BASE        base * factor^(R/(R-2)) in the place of base (R > 2)
+ *   ROPE_SCALING_BASE        base * factor^(R/(R-2)) in the place of base (R > 2; > 0, finite)
  *   ROPE_SCALING_YARN        mixed between inv_freq[i] and inv_freq[i] / factor along a ramp in i: with
  *                            i(n) = R/2 * ln(original_length / (2 pi n)) / ln(base), the index whose wave
  *                            makes n turns over the original length, the ramp goes from 0 (kept) at
@@ -408,12 +408,12 @@ int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* qu
  *                    Nq at most 65536, T * Nq below 2^31 - 512.
  *   k_cache, v_cache [NB, Nk, BS, D], same dtype; Nq a multiple of Nk.
  *   block_table      I64 [B, W]: pages of each sequence's own tokens; B >= 1, W >= 1, W * BS <= 2^30.
- *   seq_lens         I64 [B]: tokens of each sequence, prefix and this call's included.
+ *   seq_lens         I64 [B]: tokens of each sequence, prefix and this call's included.  Not negative.
  *   query_start_loc  I64 [B + 1], non-decreasing from 0 to at most T (a sequence may be empty).  Other values
  *                    cannot make the kernels access memory outside the tensors; which sequence a token
  *                    belongs to, and whether it is written, is then unspecified.
  *   prefix_blocks    I64, at least ceil(prefix_len / BS) pages, or NULL with prefix_len 0.
- *   prefix_len       0 to 2^30.
+ *   prefix_len       0 to 2^30; prefix_len + W * BS below 2^31 - 512.
  *   scale            > 0 and finite.
  *   out              contiguous [T, Nq*D], query's dtype.      lse  F32 [T, Nq], or NULL.
  *   workspace        DEVICE pointer to workspace_bytes bytes, 256-byte aligned, at least what

@@ -78,6 +78,19 @@ def test_far_positions_keep_their_angle(rope_gpu):
         assert float((out - near).abs().max()) <= bound
 
 
+def test_negative_frequencies_keep_their_angle(rope_gpu):
+    """cos is even and sin is odd in the frequency, at far positions as well.  An angle is off by 2^-64 turns a
+    position (half a unit in each of two tables, and what a table's piece of 9 bits leaves out): 2^-24 of a turn,
+    2 pi * 2^-24 < 2^-21, at 2^40; the values are then within 4 half steps each."""
+    f = torch.tensor([1e-4, 2.0 ** -30, 0.3, 7.0, 1e5], dtype=torch.float64)
+    a, b = torch.empty(3, 10, device="cuda"), torch.empty(3, 10, device="cuda")
+    for first in (5, 1 << 40):
+        R.scaled_cos_sin_cache(a, f, first_position=first)
+        R.scaled_cos_sin_cache(b, -f, first_position=first)
+        sign = torch.cat([torch.ones(5), -torch.ones(5)]).cuda()
+        assert float((a - b * sign).abs().max()) <= 2.0 ** -21 + 8 * 2.0 ** -24
+
+
 def test_large_table_every_row(rope_gpu):
     """More rows than one pass of the grid."""
     inv, scale = R.rope_frequencies(64, 500000.0, SCALINGS[3])

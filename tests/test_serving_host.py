@@ -98,6 +98,7 @@ def test_wavelength(lib):
     (64, 1e4, {"kind": "wavelength", "factor": 2, "original_length": 4096}),
     (64, 1e4, {"kind": "wavelength", "factor": 2, "original_length": 4096, "low": 4, "high": 4}),
     (64, 1e4, {"kind": "factors", "factors": [1.0] * 31}), (64, 1e4, {"kind": "factors", "factors": [0.0] * 32}),
+    (64, 1e300, {"kind": "base", "factor": 1e10}), (1 << 60, 1e4, None),
     (64, 1e4, {"kind": "linear", "factor": math.nan}), (64, 1e4, {"kind": "linear", "factor": 2, "attention": -1})])
 def test_frequencies_refused(lib, dim, base, scaling):
     with pytest.raises(R.RopeError) as e:
@@ -267,6 +268,8 @@ def _attend(lib, **over):
     ({"block_table": d(C.I64, (NBATCH, 1 << 29), 3 << 20)}, BAD), ({"starts": d(C.I64, (NBATCH,), 5 << 20)}, BAD),
     ({"seq_lens": d(C.I64, (0,), 4 << 20), "starts": d(C.I64, (1,), 5 << 20), "block_table": d(C.I64, (0, W), 3 << 20)}, BAD),
     ({"P": -1}, BAD), ({"P": 9}, BAD), ({"P": (1 << 30) + 1}, BAD),
+    ({"P": 1 << 30, "prefix": d(C.I64, (1 << 28,), 1 << 44),  # each in its range, but 2^31 keys together
+      "block_table": d(C.I64, (NBATCH, 1 << 28), 1 << 45)}, BAD),
     ({"scale": 0.0}, BAD), ({"scale": -1.0}, BAD), ({"scale": math.nan}, BAD), ({"scale": math.inf}, BAD),
     ({"out": d(C.BF16, (T + 1, HQ * D), 7 << 20)}, BAD), ({"lse": d(C.F32, (T, HK), 10 << 20)}, BAD),
     ({"bytes": 0}, BAD), ({"bytes": 255}, BAD), ({"workspace": (16 << 20) + 128}, BAD),
@@ -320,3 +323,12 @@ def test_binding_takes_cuda_tensors_only(lib):
         R.append_paged_kv(i, x, x, x, x, i, kv, kv, 64)
     with pytest.raises(ValueError):
         R.paged_attention(x, kv, kv, i.view(4, 1), i, torch.zeros(5, dtype=torch.int64), x)
+
+
+def test_heads_of_no_columns(lib):
+    """Without a scale: no power of zero."""
+    kv = torch.zeros(3, 1, 4, 0)
+    i = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        R.paged_attention(torch.zeros(4, 64), kv, kv, i.view(4, 1), i, torch.zeros(5, dtype=torch.int64),
+                          torch.zeros(4, 64))

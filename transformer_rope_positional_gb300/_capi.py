@@ -388,7 +388,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[d
     formulas are those of ``rope_scaled_frequencies`` in the C header."""
     what = "rope_scaled_frequencies"
     fn = (_binding or _load_binding()).frequencies
-    inv = torch.empty(max(1, int(rotary_dim) // 2), dtype=torch.float64)
+    inv = torch.empty(min(max(1, int(rotary_dim) // 2), 1024), dtype=torch.float64)
     if scaling is None:
         st, scale = fn(rotary_dim, base, -1, 0.0, 0.0, 0.0, 0.0, 0.0, None, inv)
     else:
@@ -484,6 +484,11 @@ def _workspace_for(query, k_cache, prefix_len, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=query.device)
 
 
+def _default_scale(k_cache) -> float:
+    D = k_cache.shape[-1] if k_cache.dim() else 0
+    return D ** -0.5 if D else 1.0  # (heads of no columns are refused by the call)
+
+
 def paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                     seq_lens: torch.Tensor, query_start_loc: torch.Tensor, out: torch.Tensor, *,
                     scale: Optional[float] = None, prefix_blocks: Optional[torch.Tensor] = None, prefix_len: int = 0,
@@ -499,7 +504,7 @@ def paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     each row's log-sum-exp.  Without ``workspace`` one is allocated for the call
     on its stream."""
     if scale is None:
-        scale = k_cache.shape[-1] ** -0.5
+        scale = _default_scale(k_cache)
     if workspace is None and stream is not None:
         _stream_handle(query, stream)  # its device is the tensors'
         workspace = _workspace_for(query, k_cache, prefix_len, stream)
@@ -517,7 +522,7 @@ def prepare_paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache:
     now, with its workspace (given or allocated here) kept."""
     handle = _stream_handle(query, stream)
     if scale is None:
-        scale = k_cache.shape[-1] ** -0.5
+        scale = _default_scale(k_cache)
     if workspace is None:
         workspace = _workspace_for(query, k_cache, prefix_len, stream)
     args = (query, k_cache, v_cache, block_table, seq_lens, query_start_loc, prefix_blocks, prefix_len, scale, out,

@@ -357,6 +357,7 @@ int frequencies(int64_t R, double base, const rope_scaling_t* s, double* inv_fre
   if (kind == ROPE_SCALING_BASE) {
     if (R == 2) return ROPE_ERR_PARAM_INVALID;
     base *= std::pow(s->factor, (double)R / (double)(R - 2));
+    if (!(base > 0) || !std::isfinite(base)) return ROPE_ERR_PARAM_INVALID;
   } else if (kind == ROPE_SCALING_YARN) {
     low = low == 0 ? 1 : low;
     high = high == 0 ? 32 : high;
@@ -623,7 +624,7 @@ int attend_call(const rope_tensor_t* query, int64_t q_row_stride, const rope_ten
   const int64_t most = int64_t(1) << 30;
   if (B < 1 || B > most || qsl->shape[0] != B + 1 || block_table->shape[0] != B || W < 1)
     return ROPE_ERR_PARAM_INVALID;
-  if (W > most / BS || P < 0 || P > most) return ROPE_ERR_PARAM_INVALID;
+  if (W > most / BS || P < 0 || P > most || P + W * BS >= 2 * most - 512) return ROPE_ERR_PARAM_INVALID;
   if (P > 0 && !prefix_blocks) return ROPE_ERR_PARAM_NULLPTR;
   if (P > 0 && numel(prefix_blocks) < (P + BS - 1) / BS) return ROPE_ERR_PARAM_INVALID;
   if (!(scale > 0.0f) || !std::isfinite(scale)) return ROPE_ERR_PARAM_INVALID;

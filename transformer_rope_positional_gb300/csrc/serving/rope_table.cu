@@ -166,8 +166,10 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // f / 2pi modulo whole turns, in units of 2^-64: the product with 1/2pi as the sum of two
-// doubles, hi exact by an FMA, so that the only rounding is the last one.
+// doubles, hi exact by an FMA, so that the only rounding is the last one.  (Of |f|: the fraction
+// of a small negative number is next to 1, where doubles are 2^-53 apart.)
 uint64_t turns_of(double f) {
+  if (f < 0) return -turns_of(-f);
   const double c1 = 0x1.45f306dc9c883p-3, c2 = -0x1.6b01ec5417056p-57;  // 1/2pi = c1 + c2
   const double hi = f * c1;
   const double lo = std::fma(f, c1, -hi) + f * c2;
