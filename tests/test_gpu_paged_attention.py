@@ -6,7 +6,7 @@ import torch
 
 import transformer_rope_positional_gb300 as R
 from parity import same_bits
-from serving_ref import attend_case, attend_reference, check_attend, run_attend
+from serving_ref import assert_close, attend_case, attend_reference, check_attend, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -154,3 +154,34 @@ def test_repeated_calls_are_bit_identical(rope_gpu):
         c = attend_case(16, dtype, [1, 1, 7], [900, 33, 200], P=500, hq=8, hk=2, D=128)
         a, b = run_attend(R, c), run_attend(R, c)
         assert same_bits(a[0], b[0]) and same_bits(a[1], b[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("bad", [None, float("nan")])
+def test_joins_of_many_rows(rope_gpu, dtype, bad):
+    """So many rows that a joining warp takes several; the last key of each sequence, which only its last row sees,
+    may be NaN."""
+    c = attend_case(17, dtype, [700, 0, 1900], [1300, 0, 1900], P=9, hq=8, hk=2, D=64)
+    out, lse, tol, ltol = attend_reference(c)
+    keep = torch.ones(c["T"], dtype=torch.bool)
+    if bad is not None:
+        for b, n in ((0, 1300), (2, 1900)):
+            c["k"][c["table"][b, (n - 1) // 16], :, (n - 1) % 16] = bad
+            keep[int(c["starts"][b + 1]) - 1] = False
+    got, got_lse = run_attend(R, c)
+    assert_close(got[keep], out[keep], tol[keep], "out")
+    assert_close(got_lse[keep], lse[keep], ltol[keep], "lse")
+    if bad is not None:
+        assert torch.isnan(got[~keep]).all()
+    assert R.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("hq,hk,D", [(4, 2, 64), (8, 1, 128), (16, 2, 96)])
+def test_units_of_every_length(rope_gpu, dtype, hq, hk, D):
+    """Own lengths of one key to several tiles side by side: shares that begin or end within a unit's cost."""
+    own = [1 + (i * 61) % 413 for i in range(47)]
+    for P in (0, 5):
+        check_attend(R, attend_case(18, dtype, [1] * 47, own, P=P, hq=hq, hk=hk, D=D), "lengths")
+    new = [min(n, 1 + (i * 5) % 40) for i, n in enumerate(own)]
+    check_attend(R, attend_case(19, dtype, new, own, P=0, hq=hq, hk=hk, D=D), "lengths")
