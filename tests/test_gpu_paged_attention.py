@@ -6,7 +6,7 @@ import torch
 
 import transformer_rope_positional_gb300 as R
 from parity import same_bits
-from serving_ref import assert_close, attend_case, attend_reference, check_attend, run_attend
+from serving_ref import assert_close, attend_case, attend_reference, check_attend, run_attend, widened
 
 pytestmark = pytest.mark.gpu
 
@@ -95,15 +95,15 @@ def test_unseen_tokens_of_the_call_have_no_influence(rope_gpu, dtype, bad, D):
             j = own[b] - 1  # the last token
             c["k"][c["table"][b, j // 16], :, j % 16] = bad
             c["v"][c["table"][b, j // 16], :, j % 16] = bad
-        out, lse = run_attend(R, c)
-        from serving_ref import assert_close
         last = {int(c["starts"][1]) - 1, int(c["starts"][2]) - 1}
         rows = [t for t in range(c["T"]) if t not in last]
-        assert_close(out[rows], clean[0][rows], clean[2][rows], "out")
-        assert_close(lse[rows], clean[1][rows], clean[3][rows], "lse")
-        if bad != bad:
-            assert torch.isnan(out[list(last)]).all()
-        assert R.get_device_error() == 0
+        for case in (c, widened(c)):
+            out, lse = run_attend(R, case)
+            assert_close(out[rows], clean[0][rows], clean[2][rows], "out")
+            assert_close(lse[rows], clean[1][rows], clean[3][rows], "lse")
+            if bad != bad:
+                assert torch.isnan(out[list(last)]).all()
+            assert R.get_device_error() == 0
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
@@ -121,19 +121,20 @@ def test_lowest_values(rope_gpu, dtype):
     check_attend(R, c, "tiny")
 
 
-def test_pages_outside_the_cache_are_unseen(rope_gpu):
+@pytest.mark.parametrize("new", [[1, 2], [60, 33]])
+def test_pages_outside_the_cache_are_unseen(rope_gpu, new):
     for dtype in DTYPES:
-        c = attend_case(14, dtype, [1, 2], [60, 50], P=40, hq=4, hk=2, D=64)
+        c = attend_case(14, dtype, new, [60, 50], P=40, hq=4, hk=2, D=64)
         c["table"][0, 1] = -3
         c["table"][1, 0] = c["k"].shape[0]
         c["prefix"][1] = 1 << 50
-        R.get_device_error()
-        out, lse = run_attend(R, c)
-        assert R.get_device_error() == R.ROPE_DEVICE_SLOT_OUT_OF_RANGE
         ro, rl, to, tl = attend_reference(c)
-        from serving_ref import assert_close
-        assert_close(out, ro, to, "out")
-        assert_close(lse, rl, tl, "lse")
+        R.get_device_error()
+        for case in (c, widened(c)):
+            out, lse = run_attend(R, case)
+            assert R.get_device_error() == R.ROPE_DEVICE_SLOT_OUT_OF_RANGE
+            assert_close(out, ro, to, "out")
+            assert_close(lse, rl, tl, "lse")
 
 
 def test_sequences_past_their_pages(rope_gpu):
@@ -145,15 +146,16 @@ def test_sequences_past_their_pages(rope_gpu):
         assert R.get_device_error() == R.ROPE_DEVICE_SLOT_OUT_OF_RANGE
         c["lens"][0] = 64
         ro, rl, to, tl = attend_reference(c)
-        from serving_ref import assert_close
         assert_close(out, ro, to, "out")
 
 
 def test_repeated_calls_are_bit_identical(rope_gpu):
     for dtype in DTYPES:
-        c = attend_case(16, dtype, [1, 1, 7], [900, 33, 200], P=500, hq=8, hk=2, D=128)
-        a, b = run_attend(R, c), run_attend(R, c)
-        assert same_bits(a[0], b[0]) and same_bits(a[1], b[1])
+        for new in ([1, 1, 7], [20, 33, 7]):
+            c = attend_case(16, dtype, new, [900, 33, 200], P=500, hq=8, hk=2, D=128)
+            for case in (c, widened(c)):
+                a, b = run_attend(R, case), run_attend(R, case)
+                assert same_bits(a[0], b[0]) and same_bits(a[1], b[1])
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
@@ -185,3 +187,13 @@ def test_units_of_every_length(rope_gpu, dtype, hq, hk, D):
         check_attend(R, attend_case(18, dtype, [1] * 47, own, P=P, hq=hq, hk=hk, D=D), "lengths")
     new = [min(n, 1 + (i * 5) % 40) for i, n in enumerate(own)]
     check_attend(R, attend_case(19, dtype, new, own, P=0, hq=hq, hk=hk, D=D), "lengths")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_prefix_behind_many_rows(rope_gpu, dtype, D):
+    """A prefix whose launch takes tall units, ragged own keys after it."""
+    n = 50
+    new = [1 + (i % 9 == 4) for i in range(n)]
+    own = [new[i] + (i * 29) % 70 for i in range(n)]
+    check_attend(R, attend_case(20, dtype, new, own, P=2900 if D == 64 else 1500, hq=16, hk=2, D=D, bs=32), "long prefix")

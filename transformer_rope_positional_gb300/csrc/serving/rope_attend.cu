@@ -247,22 +247,36 @@ struct Units {
   int64_t M, grid;
 };
 
-// The kernel for `rows` rows of a sequence and key head.  16-bit: units of 16 rows up to 16 rows
-// (beyond, K and V would be read again for every 16).  Binary32: 4 rows up to 4, 8 up to 16 (33
-// sequences of 16 rows: 10 us, with units of 64 rows 15 us).
-Units units_for(double rows, int64_t D, int32_t dtype) {
+// Kernels of 16-bit units of 16 rows, binary32 units of 8 and 4, and the tall ones.
+Units units_of(int64_t M, int64_t D, int32_t dtype) {
   const int cols = padded_columns(D);
   Units u;
-  if (dtype == kF32) {
-    u.tall = rows > 16;
-    u.M = u.tall ? 64 : rows > 4 ? 8 : 4;
-    u.grid = (int64_t)sm_count() * (u.tall && cols > 128 ? f32_ctas<256>() : 2);
-  } else {
-    u.tall = rows > 16;
-    u.M = !u.tall ? kMmaRows : cols <= 128 ? 256 : 128;
-    u.grid = (int64_t)sm_count() * (u.tall ? 1 : 2);
-  }
+  u.tall = M > 16;
+  u.M = M;
+  int per_sm = 2;
+  if (u.tall) per_sm = dtype != kF32 ? 1 : cols > 128 ? f32_ctas<256>() : 2;
+  u.grid = (int64_t)sm_count() * per_sm;
   return u;
+}
+
+int64_t tall_rows(int64_t D, int32_t dtype) { return dtype == kF32 ? 64 : padded_columns(D) <= 128 ? 256 : 128; }
+
+// The kernel for B sequences of `rows` rows a key head, on average, and up to `keys` keys: small
+// units up to 16 rows (binary32: 4 rows up to 4, else 8; 33 sequences of 16 rows: 10 us, with units of
+// 64 rows 15 us).  Beyond, K and V are read again for every small unit, and tall ones take them once
+// on the 5th-generation tensor cores, or in wider products; but a tall unit takes 12 us at the least,
+// so where all the work is a few small tiles a CTA they stay (107 sequences of up to 8 tokens on 63,
+// 4 heads of 64: 8.9 us, tall 12.3; 20 of up to 97 on 605: 12.3, 18.5; binary32, 5 of up to 26 on 61, 16
+// heads of 160: 16.4, 25.3).  Four tiles of 128 columns a CTA, and two of 256 (four of those: 22
+// sequences of up to 15 tokens on 188, 10 heads of 256: 19.1 us, tall 16.4); eight in binary32.
+Units units_for(double rows, int64_t B, int64_t nk, int64_t keys, int64_t D, int32_t dtype) {
+  const bool f32 = dtype == kF32;
+  const int64_t few = !f32 ? kMmaRows : rows > 4 ? 8 : 4;
+  const Units u = units_of(few, D, dtype);
+  if (rows <= 16) return u;
+  const double tiles = (rows / (double)few + 1) * (double)(B * nk) * (double)(keys / (f32 ? kFewKeys : kMmaKeys) + 1);
+  const double most = (double)u.grid * (f32 ? 8 : 512 / padded_columns(D));
+  return tiles <= most ? u : units_of(tall_rows(D, dtype), D, dtype);
 }
 
 // One launch's part of the workspace: records, partial slots, and with `dense` the rows that
@@ -285,8 +299,8 @@ Part part_of(int64_t T, int64_t nq, int64_t nk, int64_t D, const Units& u, bool 
 // The largest part of the kernels': which one runs depends on the batch as well.
 int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, bool dense) {
   int64_t most = 0;
-  for (double rows : {4.0, 8.0, 16.0, 17.0})
-    most = std::max(most, part_of(T, nq, nk, D, units_for(rows, D, dtype), dense).bytes);
+  for (int64_t M : {(int64_t)4, (int64_t)8, (int64_t)kMmaRows, tall_rows(D, dtype)})
+    most = std::max(most, part_of(T, nq, nk, D, units_of(M, D, dtype), dense).bytes);
   return most;
 }
 
@@ -400,7 +414,8 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
   // (8 MB are 1.2 us of the copy bandwidth) and a sequence's rows do not fill a tile by themselves
   const double saved = (double)(p.B - 1) * (double)p.prefix_len * (double)p.nk * (double)p.D * 4;
   const bool shared = saved > 8e6 && rows < 128;
-  const Units u_own = units_for(rows, p.D, p.dtype), u_pre = units_for((double)p.T * a.G, p.D, p.dtype);
+  const Units u_own = units_for(rows, p.B, p.nk, p.W * p.block_size + (shared ? 0 : p.prefix_len), p.D, p.dtype),
+              u_pre = units_for((double)p.T * a.G, 1, p.nk, p.prefix_len, p.D, p.dtype);
   const Part s_own = part_of(p.T, p.nq, p.nk, p.D, u_own, shared);
   char* const ws = static_cast<char*>(p.workspace);
   Cut own = cut_of(s_own, ws, u_own), pre = own;

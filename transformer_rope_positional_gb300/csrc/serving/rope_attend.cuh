@@ -89,8 +89,8 @@ __device__ __forceinline__ PageRow page_row(int j, const int64_t* table, const P
 // How the work is cut.  A unit is a tile of M query rows of one sequence and key head (row r
 // of a sequence is token r / G, head r % G of the key head's group) with the keys they see;
 // or, in the launch over a shared prefix, a tile of M rows of the whole batch with the
-// prefix's keys.  A unit's work is its number of key tiles and unit_cost().  All units' work, one after the
-// other, are cut into equal shares, one per CTA of the grid, so a unit may be finished by
+// prefix's keys.  A unit's work is its number of key tiles and unit_cost().  All units' work,
+// one after the other, is cut into equal shares, one per CTA of the grid: a unit may be finished by
 // several CTAs; each leaves its rows' partial (m, l, O) in one of its two slots (slot 1: the
 // unit begins in this CTA, slot 0: it began in an earlier one), and the joining kernel adds
 // them up in order.  Every CTA finds its share by itself from the lengths on the device:
