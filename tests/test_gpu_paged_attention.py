@@ -197,3 +197,52 @@ def test_long_prefix_behind_many_rows(rope_gpu, dtype, D):
     new = [1 + (i % 9 == 4) for i in range(n)]
     own = [new[i] + (i * 29) % 70 for i in range(n)]
     check_attend(R, attend_case(20, dtype, new, own, P=2900 if D == 64 else 1500, hq=16, hk=2, D=D, bs=32), "long prefix")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("new,own", [([1, 1, 2], [20, 1, 30]), ([9, 3, 60], [40, 3, 60])])
+def test_short_sequences_with_bad_values(rope_gpu, dtype, bad, new, own):
+    """Calls that need no joining launch: rows that a NaN or infinite key or value of another row's sight reaches in
+    the products are computed again, by the kernel that finished them."""
+    for bs, D in ((16, 64), (7, 256)):
+        c = attend_case(21, dtype, new, own, P=0, hq=8, hk=2, D=D, bs=bs)
+        clean = attend_reference(c)
+        last = torch.zeros(c["T"], dtype=torch.bool)
+        for b, n in enumerate(own):
+            if new[b] > 1:
+                c["k"][c["table"][b, (n - 1) // bs], :, (n - 1) % bs] = bad
+                c["v"][c["table"][b, (n - 1) // bs], :, (n - 1) % bs] = bad
+                last[int(c["starts"][b + 1]) - 1] = True
+        for case in (c, widened(c)):
+            n = R.launch_count()
+            out, lse = run_attend(R, case)
+            launches = R.launch_count() - n
+            assert_close(out[~last], clean[0][~last], clean[2][~last], "out")
+            assert_close(lse[~last], clean[1][~last], clean[3][~last], "lse")
+            assert launches == (1 if case is c else 2)
+            assert R.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("D", [128, 160])
+def test_short_prompts_with_bad_values(rope_gpu, dtype, D):
+    """Many short prompts: tall units, none of them split, one launch."""
+    n = 40
+    own = [14 + (i * 7) % 90 for i in range(n)]
+    new = [min(own[i], 8 + i % 13) for i in range(n)]
+    c = attend_case(22, dtype, new, own, P=0, hq=16, hk=2, D=D)
+    clean = attend_reference(c)
+    last = torch.zeros(c["T"], dtype=torch.bool)
+    for b in range(0, n, 3):
+        j = own[b] - 1
+        c["k"][c["table"][b, j // 16], :, j % 16] = float("nan")
+        c["v"][c["table"][b, j // 16], :, j % 16] = float("inf")
+        last[int(c["starts"][b + 1]) - 1] = True
+    before = R.launch_count()
+    out, lse = run_attend(R, c)
+    assert R.launch_count() - before == 1
+    assert_close(out[~last], clean[0][~last], clean[2][~last], "out")
+    assert_close(lse[~last], clean[1][~last], clean[3][~last], "lse")
+    assert torch.isnan(out[last]).all()
+    assert R.get_device_error() == 0

@@ -46,8 +46,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // The joining kernels add the partial results of rows up, a warp to a row.  A row whose result
-// is not finite is computed again key by key: a key that a row does not see has weight 0 in the
-// unit kernels, and 0 * infinity or NaN of its value would leave NaN.
+// is not finite is computed again key by key (see mend_rows).
 
 // Where partial result s of a row lies: (m, l) and O.
 struct Source {
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   int2 mine = make_int2(0, 0);
   if (lane < per_warp && first + lane < a.T * a.nq) mine = own.rec[first + lane];
   const int n_mine = (mine.x >> 16) - (mine.x & 0xffff) + 1;
-  const bool todo = first + lane < rows && (mine.x < 0 || n_mine != 1);
+  const bool todo = first + lane < rows && n_mine != 1;
   // (a row that no unit covered, for starts out of order, has any record)
   const bool known = mine.x >= 0 && n_mine > 1 && (mine.x >> 16) < own.grid && (unsigned)mine.y < (unsigned)own.slot_rows;
   uint32_t again = __ballot_sync(0xffffffffu, todo && !known), two = __ballot_sync(0xffffffffu, todo && known && n_mine == 2),
@@ -315,6 +314,8 @@ Cut cut_of(const Part& s, char* at, const Units& u) {
   c.prefix = 0;
   c.shared = 0;
   c.slot_rows = (int32_t)s.slot_rows;
+  c.whole = whole_tiles(u.M);
+  c.solo = 0;
   c.rec = reinterpret_cast<int2*>(at + s.rec);
   c.slots = reinterpret_cast<float*>(at + s.slots);
   c.dense = reinterpret_cast<float*>(at + s.dense);
@@ -406,6 +407,15 @@ cudaError_t launch_join(const AttendProblem& p, const Pointers& g, const AttendA
                            own, per_warp);
 }
 
+// Where no sequence can have more keys than this, no unit is split and the joining launch is saved:
+// 22 sequences of 1 or 2 tokens 8.2 -> 6.8 us; 12 of 14 tokens on 369, heads of 160 16.4 -> 15.6.  With more
+// keys the tiles of a unit, one after the other, take longer than the launch (4 sequences of 300, units of 16
+// rows: 8.9 -> 10.3 us; binary32, 6 of up to 40 tokens on 434: 14.4 -> 25.3).
+int64_t solo_keys(const Units& u, int32_t dtype) {
+  if (dtype == kF32) return u.tall ? kF32Keys : 4 * kFewKeys;
+  return u.tall ? 512 : 4 * kMmaKeys;
+}
+
 template <typename T>
 cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
   // rows of a sequence and key head, on average: only the lengths' sum is known here
@@ -426,9 +436,12 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
     pre.shared = pre.prefix = 1;
     const cudaError_t e = launch_units<T>(p, g, a, pre, u_pre, stream);
     if (e != cudaSuccess) return e;
+  } else if (p.prefix_len + p.W * p.block_size <= solo_keys(u_own, p.dtype)) {
+    own.whole = INT32_MAX;
+    own.solo = 1;
   }
   const cudaError_t e = launch_units<T>(p, g, a, own, u_own, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || own.solo) return e;
   if (p.D <= 64) return launch_join<T, 1>(p, g, a, own, pre, stream);
   if (p.D <= 128) return launch_join<T, 2>(p, g, a, own, pre, stream);
   return launch_join<T, 4>(p, g, a, own, pre, stream);

@@ -2,6 +2,7 @@
 // key of a sequence sits in the paged cache.
 #pragma once
 
+#include <cfloat>
 #include <cmath>
 
 #include "rope_device.cuh"
@@ -108,8 +109,10 @@ struct Cut {
   int32_t shared;     // another launch covers the other keys: nothing is final here
   int32_t slot_rows;  // rows of a partial slot
   int32_t grid;       // CTAs of the launch
+  int32_t whole;      // units of up to so many tiles are not split
+  int32_t solo;       // no unit is split and no joining kernel follows: no records
   int2* rec;          // [T * nq]: first and last CTA of the row's unit (16 bits each) and the row's
-                      // place in the unit; -1: recompute
+                      // place in the unit
   float* slots;       // [grid][2][slot_rows][D] O, then [grid][2][slot_rows][2] m, l
   float* dense;       // shared: [T * nq][D] O, then [T * nq][2] m, l, of units that one CTA finished
 };
@@ -201,15 +204,11 @@ struct Walk {
 };
 
 // Units of at most so many tiles are not split.
-template <int M>
-__host__ __device__ constexpr int whole_tiles() {
-  return M > 64 ? 4 : 1;
-}
+inline int whole_tiles(int64_t M) { return M > 64 ? 4 : 1; }
 
 // Key tiles of the current unit in this CTA end here.
-template <int M>
-__device__ __forceinline__ int walk_k1(const Walk& w) {
-  return w.work <= whole_tiles<M>() ? w.work : (int)min((int64_t)w.work, w.k0 + w.left);
+__device__ __forceinline__ int walk_k1(const Walk& w, const Cut& c) {
+  return w.work <= c.whole ? w.work : (int)min((int64_t)w.work, w.k0 + w.left);
 }
 
 __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
@@ -219,7 +218,7 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
 // The next unit of the share; w.done at its end.
 template <int M, int KT>
 __device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const AttendArgs& a, const Cut& c) {
-  w.left -= walk_k1<M>(w) - w.k0 + unit_cost<M>();
+  w.left -= walk_k1(w, c) - w.k0 + unit_cost<M>();
   if (w.left <= 0) {
     w.done = true;
     return;
@@ -354,16 +353,15 @@ __device__ __forceinline__ Walk find_share(const Pointers& g, const AttendArgs& 
     w.k0 = 0;
     w.done = w.left <= 0;
   }
-  if (w.k0 > 0 && w.work <= whole_tiles<M>()) walk_next<M, KT>(w, g, a, c);  // the CTA before finishes it
+  if (w.k0 > 0 && w.work <= c.whole) walk_next<M, KT>(w, g, a, c);  // the CTA before finishes it
   return w;
 }
 
 
 // The record of row r of a unit that begins in this CTA: its CTAs and the row's place.
-template <int M>
-__device__ __forceinline__ int2 unit_record(const Walk& w, int r) {
+__device__ __forceinline__ int2 unit_record(const Walk& w, int r, const Cut& c) {
   int last = blockIdx.x;
-  if (w.work > whole_tiles<M>() && w.work > w.left) {  // the rest of the unit, in shares below its size
+  if (w.work > c.whole && w.work > w.left) {  // the rest of the unit, in shares below its size
     const uint32_t rest = (uint32_t)(w.work - w.left);
     last += (int)((rest + (uint32_t)w.share - 1) / (uint32_t)w.share);
   }
@@ -499,6 +497,29 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
   }
   if (lse && lane == 0 && access_ok(lse + row, 4, a.lse_span, g.err))
     lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+// The rows that this CTA finished and whose result is not finite, once more key by key: a key that a
+// row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of its value leaves NaN.
+// All NT threads call it after a barrier; `tmp` as for find_share.
+template <typename T, int DP, int M, int KT, int NT>
+__device__ __forceinline__ void mend_rows(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
+                                          T* __restrict__ out, float* __restrict__ lse, const Pointers& g,
+                                          const AttendArgs& a, const Cut& c, int64_t* tmp) {
+  const int lane = threadIdx.x & 31;
+  Walk w = find_share<M, KT, NT>(g, a, c, tmp);
+  while (!w.done) {
+    const UnitRows u = unit_rows<M>(w, a);
+    if (w.k0 == 0 && walk_k1(w, c) == w.work)
+      for (int r = threadIdx.x >> 5; r < u.rows; r += NT / 32) {
+        const RowAt at = row_at(u, r, w.h, a);
+        const T* o = out + (at.t * a.nq + at.h) * a.D;
+        bool fine = true;
+        for (int d = lane; d < a.D; d += 32) fine = fine && fabsf(widen(o[d])) <= FLT_MAX;
+        if (!__all_sync(0xffffffffu, fine)) attend_row<T, DP / 32>(at.t, at.h, q, kc, vc, out, lse, g, a);
+      }
+    walk_next<M, KT>(w, g, a, c);
+  }
 }
 
 }  // namespace attend

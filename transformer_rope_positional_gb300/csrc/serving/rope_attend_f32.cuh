@@ -36,7 +36,8 @@ struct F32Shared {
   alignas(16) float k[kF32Keys * DP];
   alignas(16) float v[kF32Keys * DP];
   alignas(16) float p[kF32Keys * M];  // weights, [key][row]
-  int64_t rows[2][kF32Keys];          // cache rows of this and the next tile
+  int32_t rows[2][kF32Keys];          // cache rows of this and the next tile
+  int bad;                            // some finished row is not finite
 };
 
 template <int DP>
@@ -57,8 +58,10 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP>())
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   wait_for_prior_grid();
   Walk w = find_share<M, kF32Keys, kF32Threads>(g, a, c, reinterpret_cast<int64_t*>(sm.p));
+  if (w.done) return;
+  if (tid == 0) sm.bad = 0;
   while (!w.done) {
-    const int k1 = walk_k1<M>(w);
+    const int k1 = walk_k1(w, c);
     const int end = tile_end<M>(w.s, w.i, a, c);
     const UnitRows u = unit_rows<M>(w, a);
     const int64_t* table = g.block_table + w.b * a.W;
@@ -76,15 +79,15 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP>())
           r = ((int)page.page * a.nk + w.h) * a.block_size + page.row;
         else if (page.page != -2)
           atomicOr(g.err, kSlotOutOfRange);
-        sm.rows[k & 1][tid] = r < 0 ? -1 : (int64_t)r * a.D;
+        sm.rows[k & 1][tid] = r;
       }
     };
     auto copy = [&](int k, float* dst, const float* __restrict__ src, const Span& span, bool rotate) {
       for (int idx = tid; idx < KT * CH; idx += kF32Threads) {
         const int key = idx / CH, ch = idx - key * CH;
-        const int64_t at = sm.rows[k & 1][key];
-        const bool there = at >= 0 && ch * 4 < a.D;
-        const float* p = src + (there ? at + ch * 4 : 0);
+        const int r = sm.rows[k & 1][key];
+        const bool there = r >= 0 && ch * 4 < a.D;
+        const float* p = src + (there ? (int64_t)r * a.D + ch * 4 : 0);
         cp_async16_or_zero(smem_u32(dst + key * DP + ((rotate ? ch ^ (key & 7) : ch) << 2)), p,
                            there && access_ok(p, 16, span, g.err));
       }
@@ -237,12 +240,15 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP>())
                             : slot_ml(c, a, blockIdx.x, begins ? 1 : 0) + r * 2;
           *reinterpret_cast<float2*>(ml) = make_float2(m[i], l[i]);
         }
-        if (begins) c.rec[row] = final && !all_fine ? make_int2(-1, -1) : unit_record<M>(w, r);
+        if (final && !all_fine) sm.bad = 1;
+        if (begins && !c.solo) c.rec[row] = unit_record(w, r, c);
       }
     }
     __syncthreads();  // the buffers are free
     walk_next<M, kF32Keys>(w, g, a, c);
   }
+  if (sm.bad)
+    mend_rows<float, DP, M, kF32Keys, kF32Threads>(q, kc, vc, out, lse, g, a, c, reinterpret_cast<int64_t*>(sm.p));
 }
 
 // ---------------------------------------------------------------------------
@@ -262,7 +268,7 @@ struct FewShared {
   alignas(16) float ring[4][FewShape<DP>::kStages][8 * DP];
   alignas(16) float o[4][FewShape<DP>::kJoin][DP];
   float ml[4][8][2];
-  int bad[8];
+  int bad;  // some finished row is not finite
   int64_t tmp[kFewThreads / 32 + 2];
 };
 
@@ -317,6 +323,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   wait_for_prior_grid();
   Walk w = find_share<R, kFewKeys, kFewThreads>(g, a, c, sm.tmp);
   if (w.done) return;
+  if (threadIdx.x == 0) sm.bad = 0;
   Ring<float, 8, DP, S, R, kFewKeys, false> ring;
   ring.start(w, reinterpret_cast<unsigned char*>(sm.ring[warp][0]), g, a, c);
 #pragma unroll 1
@@ -339,7 +346,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
       }
     }
-    if (threadIdx.x < R) sm.bad[threadIdx.x] = 0;
     int limit[RG];
     float m[RG], l[RG];  // of row 4 i + my_row; l of this lane's keys
 #pragma unroll
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
-    const int k1 = walk_k1<R>(w);
+    const int k1 = walk_k1(w, c);
     for (int k = w.k0; k < k1; ++k) {
       cp_async_wait<S - 2>();
       __syncwarp();
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
           if (!(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX &&
                 sum <= FLT_MAX))
-            sm.bad[rr] = 1;
+            sm.bad = 1;
           float* to = out + row * a.D + d;
           if (access_ok(to, 16, a.out_span, g.err)) *reinterpret_cast<float4*>(to) = v;
           if (d == 0 && lse && access_ok(lse + row, 4, a.lse_span, g.err))
@@ -471,13 +477,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       }
       __syncthreads();
     }
-    if (begins && threadIdx.x < u.rows) {
+    if (begins && !c.solo && threadIdx.x < u.rows) {
       const RowAt at = row_at(u, threadIdx.x, w.h, a);
-      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record<R>(w, threadIdx.x);
+      c.rec[at.t * a.nq + at.h] = unit_record(w, threadIdx.x, c);
     }
     walk_next<R, kFewKeys>(w, g, a, c);
   }
   cp_async_wait<0>();
+  __syncthreads();
+  if (sm.bad) mend_rows<float, DP, R, kFewKeys, kFewThreads>(q, kc, vc, out, lse, g, a, c, sm.tmp);
 }
 
 }  // namespace attend

@@ -45,7 +45,7 @@ struct MmaShared {
   alignas(16) unsigned char q[16 * DP * 2];
   float o[4][S::kJoin][DP + 8];
   float ml[4][16][2];
-  int bad[16];
+  int bad;  // some finished row is not finite
   int64_t tmp[kMmaThreads / 32 + 2];
 };
 
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   wait_for_prior_grid();
   Walk w = find_share<kMmaRows, kMmaKeys, kMmaThreads>(g, a, c, sm.tmp);
   if (w.done) return;
+  if (threadIdx.x == 0) sm.bad = 0;
 
   Ring<T, 16, DP, S, kMmaRows, kMmaKeys, true> ring;
   ring.start(w, sm.ring[warp][0], g, a, c);
@@ -142,7 +143,6 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       const int r = idx / CH, ch = idx - r * CH;
       *reinterpret_cast<uint4*>(sm.q + r * (DP * 2) + ((ch ^ (r & 7)) << 4)) = qv[i];
     }
-    if (threadIdx.x < 16) sm.bad[threadIdx.x] = 0;
     __syncthreads();
     uint32_t qa[kHoldQ ? KS : 1][4];
     auto load_q = [&](uint32_t (&f)[4], int ks) {
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
     int lim0 = lane < u.rows ? row_limit(w, row_at(u, lane, w.h, a).t, g, a, c) : 0;
     const int lim1 = __shfl_sync(0xffffffffu, lim0, r0 + 8);
     lim0 = __shfl_sync(0xffffffffu, lim0, r0);
-    const int k1 = walk_k1<kMmaRows>(w);
+    const int k1 = walk_k1(w, c);
 
     float o[DP / 8][4];
 #pragma unroll
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
           if (!(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX &&
                 l <= FLT_MAX))
-            sm.bad[rr] = 1;
+            sm.bad = 1;
           Vec<T, 4> y;
           narrow2(&y.e[0], make_float2(v.x, v.y));
           narrow2(&y.e[2], make_float2(v.z, v.w));
@@ -307,13 +307,15 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       }
       __syncthreads();
     }
-    if (begins && threadIdx.x < u.rows) {
+    if (begins && !c.solo && threadIdx.x < u.rows) {
       const RowAt at = row_at(u, threadIdx.x, w.h, a);
-      c.rec[at.t * a.nq + at.h] = sm.bad[threadIdx.x] ? make_int2(-1, -1) : unit_record<kMmaRows>(w, threadIdx.x);
+      c.rec[at.t * a.nq + at.h] = unit_record(w, threadIdx.x, c);
     }
     w = nw;
   }
   cp_async_wait<0>();
+  __syncthreads();
+  if (sm.bad) mend_rows<T, DP, kMmaRows, kMmaKeys, kMmaThreads>(q, kc, vc, out, lse, g, a, c, sm.tmp);
 }
 
 }  // namespace attend

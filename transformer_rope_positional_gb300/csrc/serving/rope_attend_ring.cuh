@@ -81,7 +81,7 @@ struct Ring {
       word = next_tile & 1 ? (word & 0x0000ffffu) | (there << 16) : (word & 0xffff0000u) | there;
       next_tile = next_tile == 5 ? 0 : next_tile + 1;
       if (!pw.done) {
-        if (++pk == walk_k1<M>(pw)) {
+        if (++pk == walk_k1(pw, c)) {
           walk_next<M, KT>(pw, g, a, c);
           pk = pw.k0;
           if (!pw.done) pend = tile_end<M>(pw.s, pw.i, a, c);

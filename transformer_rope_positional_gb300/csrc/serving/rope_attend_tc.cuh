@@ -79,6 +79,7 @@ struct TcShared {
   int64_t tmp[S::kThreads / 32 + 2];
   uint32_t tmem;
   int dead;
+  int bad;  // some finished row is not finite
 };
 
 // Tile of the n-th copy of a unit of kt key tiles, `lead` of whose K tiles come first: the
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   }
   if (tid == 0) {
     sm.dead = 0;
+    sm.bad = 0;
     for (int i = 0; i < NS; ++i) {
       tc::bar_init(&sm.copied[i], S::kCopy);
       tc::bar_init(&sm.full[i], 1);
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
       const int lead = S::kAhead / nt;
-      const int k1 = walk_k1<S::M>(w), kt = k1 - w.k0;
+      const int k1 = walk_k1(w, c), kt = k1 - w.k0;
       const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
       PageRow page;                    // of this lane's key of the next K tile
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       unsigned round = 0, unit = 0;
       bool ok = true;
       while (!w.done && ok) {
-        const int kt = walk_k1<S::M>(w) - w.k0;
+        const int kt = walk_k1(w, c) - w.k0;
         ok = tc::bar_wait(&sm.q_copied, unit & 1, &sm.dead);
         tc::fence_to_tensor();
         if (ok) tc::bar_arrive(&sm.q_full);
@@ -302,7 +304,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     bool ok = true;
     while (__any_sync(0xffffffffu, !w.done && ok)) {
       const int nt = (int)tc::uniform(w.s.rows - w.i * S::M > 128 && S::M > 128 ? 2 : 1);
-      const int jobs = (int)tc::uniform((walk_k1<S::M>(w) - w.k0) * nt);  // job x is of group x % NW
+      const int jobs = (int)tc::uniform((walk_k1(w, c) - w.k0) * nt);  // job x is of group x % NW
       ok = __all_sync(0xffffffffu, tc::bar_wait(&sm.q_full, unit & 1, &sm.dead));
       ++unit;
       if (!ok) break;
@@ -398,7 +400,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     while (!w.done) {
       const UnitRows u = unit_rows<S::M>(w, a);
       const int nt = u.rows > 128 ? 2 : 1;
-      const int k1 = walk_k1<S::M>(w), kt = k1 - w.k0, jobs = kt * nt;
+      const int k1 = walk_k1(w, c), kt = k1 - w.k0, jobs = kt * nt;
       const int r = nt == 2 ? group * 128 + r_tile : r_tile;
       const bool mine = r < u.rows;
       const RowAt at = row_at(u, mine ? r : 0, w.h, a);
@@ -581,7 +583,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
                               : slot_ml(c, a, blockIdx.x, begins ? 1 : 0) + r * 2;
             *reinterpret_cast<float2*>(ml) = make_float2(m, l);
           }
-          if (begins) c.rec[row] = final && !fine ? make_int2(-1, -1) : unit_record<S::M>(w, r);
+          if (final && !fine) sm.bad = 1;
+          if (begins && !c.solo) c.rec[row] = unit_record(w, r, c);
         }
       }
       // O may be written again: by the group that read it (both, when it read both)
@@ -598,6 +601,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   __syncthreads();
   if (tid == 0 && sm.dead) atomicOr(g.err, kWaitExpired);
   if (warp == kMmaWarp) tc::tmem_free(tm, 512);
+  __syncwarp();
+  if (sm.bad && !sm.dead) mend_rows<T, DP, S::M, KT, S::kThreads>(q, kc, vc, out, lse, g, a, c, sm.tmp);
 }
 
 }  // namespace attend
