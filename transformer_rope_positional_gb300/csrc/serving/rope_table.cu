@@ -174,8 +174,8 @@ uint64_t turns_of(double f) {
   const double hi = f * c1;
   const double lo = std::fma(f, c1, -hi) + f * c2;
   const double frac = hi - std::floor(hi);
-  const double top = std::floor(std::ldexp(frac, 32));
-  const double rest = std::ldexp(std::ldexp(frac, 32) - top, 32) + std::ldexp(lo, 64);
+  const double top = std::floor(frac * 0x1p32);
+  const double rest = (frac * 0x1p32 - top) * 0x1p32 + lo * 0x1p64;
   return ((uint64_t)top << 32) + (uint64_t)(int64_t)std::llrint(rest);
 }
 
