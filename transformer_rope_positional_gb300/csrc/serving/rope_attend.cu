@@ -240,13 +240,13 @@ int padded_columns(int64_t D) { return (int)round_up(D, 64); }
 
 // A launch of units: its kernel, rows of a unit and grid.
 struct Units {
-  // 16-bit data: tall or not, M = 256 / 128 (rope_attend_tc.cuh) or 16 (rope_attend_mma.cuh);
+  // 16-bit data: tall or not, M = 256 / 128 (rope_attend_tc.cuh) or 16 / 8 (rope_attend_mma.cuh);
   // binary32 (rope_attend_f32.cuh): 64 or 8 / 4
   bool tall;
   int64_t M, grid;
 };
 
-// Kernels of 16-bit units of 16 rows, binary32 units of 8 and 4, and the tall ones.
+// The kernel of units of M rows.
 Units units_of(int64_t M, int64_t D, int32_t dtype) {
   const int cols = padded_columns(D);
   Units u;
@@ -261,7 +261,7 @@ Units units_of(int64_t M, int64_t D, int32_t dtype) {
 int64_t tall_rows(int64_t D, int32_t dtype) { return dtype == kF32 ? 64 : padded_columns(D) <= 128 ? 256 : 128; }
 
 // The kernel for B sequences of `rows` rows a key head, on average, and up to `keys` keys: small
-// units up to 16 rows (binary32: 4 rows up to 4, else 8; 33 sequences of 16 rows: 10 us, with units of
+// units up to 16 rows (16 bits: 8 rows up to 8, else 16; binary32: 4 rows up to 4, else 8; 33 sequences of 16 rows: 10 us, with units of
 // 64 rows 15 us).  Beyond, K and V are read again for every small unit, and tall ones take them once
 // on the 5th-generation tensor cores, or in wider products; but a tall unit takes 12 us at the least,
 // so where all the work is a few small tiles a CTA they stay (107 sequences of up to 8 tokens on 63,
@@ -270,7 +270,7 @@ int64_t tall_rows(int64_t D, int32_t dtype) { return dtype == kF32 ? 64 : padded
 // sequences of up to 15 tokens on 188, 10 heads of 256: 19.1 us, tall 16.4); eight in binary32.
 Units units_for(double rows, int64_t B, int64_t nk, int64_t keys, int64_t D, int32_t dtype) {
   const bool f32 = dtype == kF32;
-  const int64_t few = !f32 ? kMmaRows : rows > 4 ? 8 : 4;
+  const int64_t few = !f32 ? (rows <= 8 ? 8 : kMmaRows) : rows > 4 ? 8 : 4;
   const Units u = units_of(few, D, dtype);
   if (rows <= 16) return u;
   const double tiles = (rows / (double)few + 1) * (double)(B * nk) * (double)(keys / (f32 ? kFewKeys : kMmaKeys) + 1);
@@ -307,7 +307,7 @@ int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, 
 // at the smallest 64-byte rows).
 bool unit_path(int64_t D, int64_t cache_rows) { return D <= 256 && cache_rows < (int64_t(1) << 31); }
 
-Cut cut_of(const Part& s, char* at, const Units& u) {
+Cut cut_of(const Part& s, char* at, const Units& u, int32_t dtype) {
   Cut c;
   c.grid = (int32_t)u.grid;
   c.lo = 0;
@@ -315,6 +315,7 @@ Cut cut_of(const Part& s, char* at, const Units& u) {
   c.shared = 0;
   c.slot_rows = (int32_t)s.slot_rows;
   c.whole = whole_tiles(u.M);
+  c.cost = unit_cost(dtype);
   c.solo = 0;
   c.rec = reinterpret_cast<int2*>(at + s.rec);
   c.slots = reinterpret_cast<float*>(at + s.slots);
@@ -322,16 +323,23 @@ Cut cut_of(const Part& s, char* at, const Units& u) {
   return c;
 }
 
-template <typename T, int DP>
-cudaError_t launch_mma(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
+template <typename T, int DP, int MR>
+cudaError_t launch_mma_rows(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
                        cudaStream_t stream) {
-  auto kernel = attend_mma_kernel<T, DP>;
+  auto kernel = attend_mma_kernel<T, DP, MR>;
   const size_t smem = sizeof(MmaShared<DP>);
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_overlapped_smem(kernel, (unsigned)grid, kMmaThreads, smem, stream, static_cast<const T*>(p.query),
                                 static_cast<const T*>(p.k_cache), static_cast<const T*>(p.v_cache),
                                 static_cast<T*>(p.out), p.lse, g, a, c);
+}
+
+template <typename T, int DP>
+cudaError_t launch_mma(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, const Units& u,
+                       cudaStream_t stream) {
+  return u.M == 8 ? launch_mma_rows<T, DP, 8>(p, g, a, c, u.grid, stream)
+                  : launch_mma_rows<T, DP, kMmaRows>(p, g, a, c, u.grid, stream);
 }
 
 template <typename T, int DP>
@@ -382,10 +390,10 @@ cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const Attend
       if (cols <= 128) return launch_tc<T, 128>(p, g, a, c, u.grid, stream);
       return launch_tc<T, 256>(p, g, a, c, u.grid, stream);
     }
-    if (cols <= 64) return launch_mma<T, 64>(p, g, a, c, u.grid, stream);
-    if (cols <= 128) return launch_mma<T, 128>(p, g, a, c, u.grid, stream);
-    if (cols <= 192) return launch_mma<T, 192>(p, g, a, c, u.grid, stream);
-    return launch_mma<T, 256>(p, g, a, c, u.grid, stream);
+    if (cols <= 64) return launch_mma<T, 64>(p, g, a, c, u, stream);
+    if (cols <= 128) return launch_mma<T, 128>(p, g, a, c, u, stream);
+    if (cols <= 192) return launch_mma<T, 192>(p, g, a, c, u, stream);
+    return launch_mma<T, 256>(p, g, a, c, u, stream);
   }
 }
 
@@ -428,11 +436,11 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
               u_pre = units_for((double)p.T * a.G, 1, p.nk, p.prefix_len, p.D, p.dtype);
   const Part s_own = part_of(p.T, p.nq, p.nk, p.D, u_own, shared);
   char* const ws = static_cast<char*>(p.workspace);
-  Cut own = cut_of(s_own, ws, u_own), pre = own;
+  Cut own = cut_of(s_own, ws, u_own, p.dtype), pre = own;
   if (shared) {
     own.shared = 1;
     own.lo = a.P;
-    pre = cut_of(part_of(p.T, p.nq, p.nk, p.D, u_pre, true), ws + s_own.bytes, u_pre);
+    pre = cut_of(part_of(p.T, p.nq, p.nk, p.D, u_pre, true), ws + s_own.bytes, u_pre, p.dtype);
     pre.shared = pre.prefix = 1;
     const cudaError_t e = launch_units<T>(p, g, a, pre, u_pre, stream);
     if (e != cudaSuccess) return e;

@@ -90,7 +90,7 @@ __device__ __forceinline__ PageRow page_row(int j, const int64_t* table, const P
 // How the work is cut.  A unit is a tile of M query rows of one sequence and key head (row r
 // of a sequence is token r / G, head r % G of the key head's group) with the keys they see;
 // or, in the launch over a shared prefix, a tile of M rows of the whole batch with the
-// prefix's keys.  A unit's work is its number of key tiles and unit_cost().  All units' work,
+// prefix's keys.  A unit's work is its number of key tiles and Cut::cost.  All units' work,
 // one after the other, is cut into equal shares, one per CTA of the grid: a unit may be finished by
 // several CTAs; each leaves its rows' partial (m, l, O) in one of its two slots (slot 1: the
 // unit begins in this CTA, slot 0: it began in an earlier one), and the joining kernel adds
@@ -110,6 +110,7 @@ struct Cut {
   int32_t slot_rows;  // rows of a partial slot
   int32_t grid;       // CTAs of the launch
   int32_t whole;      // units of up to so many tiles are not split
+  int32_t cost;       // what a unit costs beside its key tiles, in tiles (see unit_cost)
   int32_t solo;       // no unit is split and no joining kernel follows: no records
   int2* rec;          // [T * nq]: first and last CTA of the row's unit (16 bits each) and the row's
                       // place in the unit
@@ -169,22 +170,11 @@ __device__ __forceinline__ int row_tiles(const SeqWork& s) {
   return (s.rows + M - 1) / M;
 }
 
-// What a unit costs beside its key tiles (query rows in, results out), in tiles: it counts in the
-// cut like key tiles that come before them, so that a CTA with many short units gets fewer tiles.
-// (128 sequences of 31 to 1024 own keys: without it some CTAs took 67 us and most 45.  The call,
-// which joins a prefix of 16384: 124.7 us with 0, 113.2 with 1, 110.4 with 2, 108.1 with 3.  32
-// sequences of up to 5 tokens, heads of 256: 70.6, 68.1, 62.7, 62.2.  64 rows of binary32 have
-// dearer tiles: 10 sequences of 8 tokens, heads of 160: 25.3 us with 1, 40.3 with 2.)
-template <int M>
-__host__ __device__ constexpr int unit_cost() {
-  return M == 16 || M > 64 ? 2 : 1;
-}
-
 template <int M, int KT>
 __device__ __forceinline__ int64_t seq_total(const SeqWork& s, const AttendArgs& a, const Cut& c) {
   const int tiles = row_tiles<M>(s);
-  if (c.prefix) return (int64_t)tiles * (unit_cost<M>() + tile_work<M, KT>(s, 0, a, c)) * a.nk;
-  int64_t sum = (int64_t)tiles * unit_cost<M>();
+  if (c.prefix) return (int64_t)tiles * (c.cost + tile_work<M, KT>(s, 0, a, c)) * a.nk;
+  int64_t sum = (int64_t)tiles * c.cost;
   for (int i = 0; i < tiles; ++i) sum += tile_work<M, KT>(s, i, a, c);
   return sum * a.nk;
 }
@@ -206,6 +196,14 @@ struct Walk {
 // Units of at most so many tiles are not split.
 inline int whole_tiles(int64_t M) { return M > 64 ? 4 : 1; }
 
+// What a unit costs beside its key tiles (query rows in, results out), in tiles: it counts in the
+// cut like key tiles that come before them, so that a CTA with many short units gets fewer tiles.
+// (128 sequences of 31 to 1024 own keys: without it some CTAs took 67 us and most 45.  The call,
+// which joins a prefix of 16384: 124.7 us with 0, 113.2 with 1, 110.4 with 2, 108.1 with 3.  32
+// sequences of up to 5 tokens, heads of 256: 70.6, 68.1, 62.7, 62.2.  64 rows of binary32 have
+// dearer tiles: 10 sequences of 8 tokens, heads of 160: 25.3 us with 1, 40.3 with 2.)
+inline int unit_cost(int32_t dtype) { return dtype == kF32 ? 1 : 2; }
+
 // Key tiles of the current unit in this CTA end here.
 __device__ __forceinline__ int walk_k1(const Walk& w, const Cut& c) {
   return w.work <= c.whole ? w.work : (int)min((int64_t)w.work, w.k0 + w.left);
@@ -218,7 +216,7 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
 // The next unit of the share; w.done at its end.
 template <int M, int KT>
 __device__ __forceinline__ void walk_next(Walk& w, const Pointers& g, const AttendArgs& a, const Cut& c) {
-  w.left -= walk_k1(w, c) - w.k0 + unit_cost<M>();
+  w.left -= walk_k1(w, c) - w.k0 + c.cost;
   if (w.left <= 0) {
     w.done = true;
     return;
@@ -333,21 +331,21 @@ __device__ __forceinline__ Walk find_share(const Pointers& g, const AttendArgs& 
   w.tiles = row_tiles<M>(w.s);
   if (c.prefix) {
     w.work = tile_work<M, KT>(w.s, 0, a, c);
-    const int64_t row = (int64_t)(unit_cost<M>() + w.work) * a.nk;
+    const int64_t row = (int64_t)(c.cost + w.work) * a.nk;
     w.i = (int)quotient(rest, row);
     rest -= w.i * row;
   } else {
     w.i = 0;
     for (;;) {
       w.work = tile_work<M, KT>(w.s, w.i, a, c);
-      const int64_t row = (int64_t)(unit_cost<M>() + w.work) * a.nk;
+      const int64_t row = (int64_t)(c.cost + w.work) * a.nk;
       if (rest < row) break;
       rest -= row;
       ++w.i;
     }
   }
-  w.h = (int)quotient(rest, unit_cost<M>() + w.work);
-  w.k0 = (int)(rest - (int64_t)w.h * (unit_cost<M>() + w.work)) - unit_cost<M>();
+  w.h = (int)quotient(rest, c.cost + w.work);
+  w.k0 = (int)(rest - (int64_t)w.h * (c.cost + w.work)) - c.cost;
   if (w.k0 < 0) {  // the unit begins in this CTA, or (no more than a part of its cost is left) in the next
     w.left += w.k0;
     w.k0 = 0;

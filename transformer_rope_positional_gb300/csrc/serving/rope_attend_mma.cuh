@@ -7,13 +7,16 @@
 //    barrier until the unit ends, and the copies of the next unit are already on their way
 //    then.  Two CTAs an SM, so that one copies while the other ends a unit (heads of 256 with
 //    one CTA: 105 us for the own keys of 32 drafts, with two 58).
-//  * Scores and outputs by mma.sync m16n8k16 (the rows pad to 16): the tensor core's newer
-//    instruction wants 64 or 128 rows a tile, and these units have 1 to 16.
+//  * Scores and outputs by mma.sync m16n8k16: the tensor core's newer instruction wants 64 or 128
+//    rows a tile, and these units have 1 to 16.  Units of 16 rows take them as the 16 of the
+//    instruction; units of 8 as its 8, keys (then columns of V) being the 16: half the products
+//    and half the registers for O (32 of up to 5 drafted tokens, heads of 256: 62.2 us with 16
+//    rows, 59.0 with 8).
 //  * The weights of a score tile are, register for register, the A operand of the product
-//    with V.  They are rounded to the data's type there (half a step relative each, the
-//    sums l taken before); m, l and O stay in binary32.
+//    with V (8 rows: transposed, its B operand).  They are rounded to the data's type there (half
+//    a step relative each, the sums l taken before); m, l and O stay in binary32.
 //
-// 64 requests of up to 8192 tokens, 32 q and 8 k heads of 128, bf16: 176 us, 6.3 TB/s, 0.93 of
+// 64 requests of up to 8192 tokens, 32 q and 8 k heads of 128, bf16: 174 us, 6.4 TB/s, 0.94 of
 // the measured copy bandwidth.  4 requests of 300 tokens: 8.9 us with the joining kernel, all of
 // it latency (lengths, pages, rows, two launches).
 #pragma once
@@ -77,6 +80,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// An 8 x 8 matrix of 16-bit values, two of a row a lane, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack2(const __half*, float x, float y) {
   const __half2 v = __floats2half2_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -87,7 +97,8 @@ __device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float x, float y
 }
 
 // DP: D rounded up to a multiple of 64; columns past D are zeros in shared memory.
-template <typename T, int DP>
+// MR: rows of a unit, 16 or 8.
+template <typename T, int DP, int MR>
 __global__ void __launch_bounds__(kMmaThreads, 2)
     attend_mma_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
                       float* __restrict__ lse, Pointers g, AttendArgs a, Cut c) {
@@ -95,22 +106,23 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   constexpr int S = Shape::kStages;
   constexpr int CH = DP / 8;   // 16-byte chunks of a row
   constexpr int KS = DP / 16;  // k steps of the score product
+  constexpr bool kEight = MR == 8;
   constexpr bool kHoldQ = DP <= 128;  // the row tile's A operands stay in registers
   extern __shared__ __align__(1024) unsigned char raw[];
   MmaShared<DP>& sm = *reinterpret_cast<MmaShared<DP>*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_prior_grid();
-  Walk w = find_share<kMmaRows, kMmaKeys, kMmaThreads>(g, a, c, sm.tmp);
+  Walk w = find_share<MR, kMmaKeys, kMmaThreads>(g, a, c, sm.tmp);
   if (w.done) return;
   if (threadIdx.x == 0) sm.bad = 0;
 
-  Ring<T, 16, DP, S, kMmaRows, kMmaKeys, true> ring;
+  Ring<T, 16, DP, S, MR, kMmaKeys, true> ring;
   ring.start(w, sm.ring[warp][0], g, a, c);
   // a unit's query rows, in 16-byte pieces of this thread: read while the unit before ends
-  constexpr int NQ = 16 * CH / kMmaThreads;
+  constexpr int NQ = (MR * CH + kMmaThreads - 1) / kMmaThreads;
   uint4 qv[NQ];
   auto read_q = [&](const Walk& x) {
-    const UnitRows u = unit_rows<kMmaRows>(x, a);
+    const UnitRows u = unit_rows<MR>(x, a);
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int idx = threadIdx.x + kMmaThreads * i;
@@ -135,32 +147,39 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_ch = lane >> 4;
 
   while (!w.done) {
-    const UnitRows u = unit_rows<kMmaRows>(w, a);
+    const UnitRows u = unit_rows<MR>(w, a);
     // ---- the unit's query rows, as A operands
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int idx = threadIdx.x + kMmaThreads * i;
       const int r = idx / CH, ch = idx - r * CH;
-      *reinterpret_cast<uint4*>(sm.q + r * (DP * 2) + ((ch ^ (r & 7)) << 4)) = qv[i];
+      if (idx < MR * CH) *reinterpret_cast<uint4*>(sm.q + r * (DP * 2) + ((ch ^ (r & 7)) << 4)) = qv[i];
     }
     __syncthreads();
-    uint32_t qa[kHoldQ ? KS : 1][4];
+    uint32_t qa[kEight ? KS / 2 : kHoldQ ? KS : 1][4];  // kEight: two steps' B operands each
     auto load_q = [&](uint32_t (&f)[4], int ks) {
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), ch = ks * 2 + (lane >> 4);
       ldmatrix4(f, q_at + r * (DP * 2) + ((ch ^ (r & 7)) << 4));
     };
-    if constexpr (kHoldQ) {
+    if constexpr (kEight) {
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i)
+        ldmatrix4(qa[i], q_at + (lane & 7) * (DP * 2) + (((i * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
+    } else if constexpr (kHoldQ) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) load_q(qa[ks], ks);
     }
+    // this lane's two rows and their limits
+    const int ra = kEight ? cq : r0, rb = kEight ? cq + 1 : r0 + 8;
     int lim0 = lane < u.rows ? row_limit(w, row_at(u, lane, w.h, a).t, g, a, c) : 0;
-    const int lim1 = __shfl_sync(0xffffffffu, lim0, r0 + 8);
-    lim0 = __shfl_sync(0xffffffffu, lim0, r0);
+    const int lim1 = __shfl_sync(0xffffffffu, lim0, rb);
+    lim0 = __shfl_sync(0xffffffffu, lim0, ra);
     const int k1 = walk_k1(w, c);
 
-    float o[DP / 8][4];
+    constexpr int NO = kEight ? DP / 16 : DP / 8;
+    float o[NO][4];  // kEight: columns by rows
 #pragma unroll
-    for (int n = 0; n < DP / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     for (int k = w.k0; k < k1; ++k) {
@@ -169,6 +188,70 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       const uint32_t there = ring.seen();
       const unsigned kt = smem_u32(ring.take(kc, vc, g, a, c));
       const int j0 = c.lo + k * kMmaKeys + warp * 16;
+      if constexpr (kEight) {
+        // ---- scores, keys by rows: two chains of products
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += 2) {
+          uint32_t f[4];
+          ldmatrix4(f, kt + v_row * (DP * 2) + (((ks * 2 + v_ch) ^ (v_row & 7)) << 4));
+          mma16816<T>(s, f, qa[ks / 2][0], qa[ks / 2][1]);
+          ldmatrix4(f, kt + v_row * (DP * 2) + (((ks * 2 + 2 + v_ch) ^ (v_row & 7)) << 4));
+          mma16816<T>(s2, f, qa[ks / 2][2], qa[ks / 2][3]);
+        }
+        // ---- unseen keys, maximum, weights
+        float t0 = m0, t1 = m1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = r0 + e * 8;
+          const bool in = (there >> i) & 1;
+          s[2 * e] = in && j0 + i < lim0 ? (s[2 * e] + s2[2 * e]) * a.scale_log2 : -INFINITY;
+          s[2 * e + 1] = in && j0 + i < lim1 ? (s[2 * e + 1] + s2[2 * e + 1]) * a.scale_log2 : -INFINITY;
+          t0 = fmaxf(t0, s[2 * e]);
+          t1 = fmaxf(t1, s[2 * e + 1]);
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) {
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+        }
+        const float b0 = t0 == -INFINITY ? 0.f : t0, b1 = t1 == -INFINITY ? 0.f : t1;
+        if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {  // some row's maximum grew
+          const float f0 = fast_exp2(m0 - b0), f1 = fast_exp2(m1 - b1);
+          l0 *= f0;
+          l1 *= f1;
+#pragma unroll
+          for (int n = 0; n < NO; ++n) {
+            o[n][0] *= f0;
+            o[n][1] *= f1;
+            o[n][2] *= f0;
+            o[n][3] *= f1;
+          }
+          m0 = t0;
+          m1 = t1;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[2 * e] = fast_exp2(s[2 * e] - b0);
+          s[2 * e + 1] = fast_exp2(s[2 * e + 1] - b1);
+          l0 += s[2 * e];
+          l1 += s[2 * e + 1];
+        }
+        // (rows, keys) from (keys, rows): the B operand
+        const uint32_t p0 = transposed(pack2((const T*)nullptr, s[0], s[1]));
+        const uint32_t p1 = transposed(pack2((const T*)nullptr, s[2], s[3]));
+        // ---- outputs
+        cp_async_wait<S - 2>();
+        __syncwarp();
+        const unsigned vt = smem_u32(ring.take(kc, vc, g, a, c));
+#pragma unroll
+        for (int n = 0; n < NO; ++n) {
+          uint32_t f[4];
+          ldmatrix4_trans(f, vt + k_row * (DP * 2) + (((n * 2 + k_ch) ^ (k_row & 7)) << 4));
+          mma16816<T>(o[n], f, p0, p1);
+        }
+        __syncwarp();
+      } else {
       // ---- scores
       float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -235,29 +318,41 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         mma16816<T>(o[2 * n + 1], p, b[2], b[3]);
       }
       __syncwarp();
+      }
     }
 
     // ---- the four warps' rows together, a few rows at a time, to the output or a partial result
 #pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
+    for (int d = kEight ? 4 : 1; d < (kEight ? 32 : 4); d *= 2) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
-    if ((lane & 3) == 0) {
-      sm.ml[warp][r0][0] = m0;
-      sm.ml[warp][r0][1] = l0;
-      sm.ml[warp][r0 + 8][0] = m1;
-      sm.ml[warp][r0 + 8][1] = l1;
+    if (kEight ? r0 == 0 : cq == 0) {
+      sm.ml[warp][ra][0] = m0;
+      sm.ml[warp][ra][1] = l0;
+      sm.ml[warp][rb][0] = m1;
+      sm.ml[warp][rb][1] = l1;
     }
     Walk nw = w;
-    walk_next<kMmaRows, kMmaKeys>(nw, g, a, c);
+    walk_next<MR, kMmaKeys>(nw, g, a, c);
     if (!nw.done) read_q(nw);
     const bool begins = w.k0 == 0, whole = begins && k1 == w.work, final = whole && !c.shared;
     float* const po = slot_o(c, a, blockIdx.x, begins ? 1 : 0);
     float* const pml = slot_ml(c, a, blockIdx.x, begins ? 1 : 0);
     constexpr int RJ = Shape::kJoin;
     for (int p0 = 0; p0 < u.rows; p0 += RJ) {
-      if ((r0 & (8 - RJ)) == (p0 & (8 - RJ))) {  // this lane has row r0 % RJ of them: r0, or r0 + 8
+      if constexpr (kEight) {
+        if (cq >= p0 && cq < p0 + RJ) {  // both of this lane's rows
+          float* to = &sm.o[warp][cq - p0][r0];
+#pragma unroll
+          for (int n = 0; n < NO; ++n) {
+            to[n * 16] = o[n][0];
+            to[n * 16 + DP + 8] = o[n][1];
+            to[n * 16 + 8] = o[n][2];
+            to[n * 16 + 8 + DP + 8] = o[n][3];
+          }
+        }
+      } else if ((r0 & (8 - RJ)) == (p0 & (8 - RJ))) {  // this lane has row r0 % RJ of them: r0, or r0 + 8
         float* to = &sm.o[warp][r0 & (RJ - 1)][cq];
 #pragma unroll
         for (int n = 0; n < DP / 8; ++n)
@@ -315,7 +410,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   }
   cp_async_wait<0>();
   __syncthreads();
-  if (sm.bad) mend_rows<T, DP, kMmaRows, kMmaKeys, kMmaThreads>(q, kc, vc, out, lse, g, a, c, sm.tmp);
+  if (sm.bad) mend_rows<T, DP, MR, kMmaKeys, kMmaThreads>(q, kc, vc, out, lse, g, a, c, sm.tmp);
 }
 
 }  // namespace attend
