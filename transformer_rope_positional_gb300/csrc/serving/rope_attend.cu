@@ -8,8 +8,9 @@
 //   m = max m_s,  l = sum l_s e^(m_s - m),  o = sum o_s e^(m_s - m) / l.
 //
 // Heads of up to 256 take the unit kernels (16-bit data: rope_attend_mma.cuh for up to 16 rows
-// a sequence and key head, rope_attend_tc.cuh beyond; binary32: rope_attend_f32.cuh), then a
-// kernel that joins partial results; larger heads a kernel with one warp per query row.
+// a sequence and key head and for little work, rope_attend_tc.cuh beyond; binary32:
+// rope_attend_f32.cuh), then, where units may be split, a kernel that joins partial results;
+// larger heads a kernel with one warp per query row.
 //
 // A shared prefix has a launch of its own when a sequence's rows fill less than a unit: the
 // rows of all sequences together fill the units of that launch, so the prefix is read once

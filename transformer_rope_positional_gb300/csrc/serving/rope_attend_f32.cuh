@@ -16,8 +16,8 @@
 // owns DP / 32 columns of Q, K, V and O; the partial scores of 8 keys x 4 rows are summed over
 // the lanes by halving: 31 shuffles for 32 sums, each lane ending with one of them.
 //
-// 64 requests of up to 335 tokens, 16 q and 4 k heads of 160: 30 us (8.5 us of bytes; units of 64
-// rows took 78); 6 ragged sequences behind 101 tokens: 15 us, latency.
+// 64 requests of up to 335 tokens, 16 q and 4 k heads of 160: 24 us (8.5 us of bytes; units of 64
+// rows took 78); 6 ragged sequences behind 101 tokens: 14 us, latency.
 #pragma once
 
 #include "rope_attend.cuh"

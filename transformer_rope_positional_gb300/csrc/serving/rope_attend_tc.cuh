@@ -5,8 +5,8 @@
 // outnumber about 280 operations per byte of K and V, so the kernel keeps tcgen05.mma fed:
 //  * one CTA per SM, its warps in roles.  Four warps (two for heads of 256) copy Q, K and V
 //    tiles into shared memory with cp.async (any page size and row order: a page's rows are
-//    found key by key; two warps were not enough for heads of 128: 582 us against 548 in the
-//    example below), one thread relays the finished copies to the tensor core, one issues the
+//    found key by key; two warps were not enough for heads of 128: 582 us against 548 for the
+//    example below as the kernel was then), one thread relays the finished copies to the tensor core, one issues the
 //    products, and one or two groups of four warps do the softmax, one thread a row.
 //    Everything between them is barriers in shared memory.
 //  * scores S = Q K^T (128 rows x KT keys) land in tensor memory; the softmax threads read
@@ -26,8 +26,8 @@
 // The products are issued in order by one thread and the tensor core runs them in order, which
 // is what keeps the next scores from overwriting weights that are still being read.
 //
-// 4 chunks of 1984 tokens behind 4096 shared ones, 32 q and 8 k heads of 128, bf16: 0.53 to 0.55
-// ms, 1.2 PFLOP/s, 0.63 of the measured matrix rate.  What is left is the softmax's latency
+// 4 chunks of 1984 tokens behind 4096 shared ones, 32 q and 8 k heads of 128, bf16: 0.50 to 0.52
+// ms, 1.3 PFLOP/s, 0.67 of the measured matrix rate.  What is left is the softmax's latency
 // between a tile's two products (the products wait for weights a fifth of the time), and the
 // ends of units, where 256 rows of results leave lane by lane.
 #pragma once
