@@ -1,0 +1,90 @@
+"""Paged attention where its units follow one another in ways that small batches do not reach: many units a CTA of every
+shape, against a float64 reference (bounds: tests/serving_ref.py)."""
+import pytest
+import torch
+
+import transformer_rope_positional_gb300 as R
+from serving_ref import E32, TINY, assert_close, half_step, run_attend, widened
+
+pytestmark = pytest.mark.gpu
+
+
+def batch(seed, dtype, new, own, P, hq, hk, D, bs):
+    """As serving_ref.attend_case, for large batches: on the GPU, all tokens at once."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    B, T = len(new), sum(new)
+    held = [-(-n // bs) for n in own]
+    shared = -(-P // bs)
+    NB = shared + sum(held) + 2
+    pages = torch.randperm(NB, generator=g, device="cuda")
+    table = torch.full((B, max(held) + 1), 1 << 40, dtype=torch.int64, device="cuda")
+    k = torch.full((NB, hk, bs, D), float("nan"), dtype=dtype, device="cuda")
+    v = k.clone()
+    at, prefix = shared, pages[:shared].clone()
+    page, row = [prefix[torch.arange(P, device="cuda") // bs]], [torch.arange(P, device="cuda") % bs]
+    for b in range(B):
+        table[b, :held[b]] = pages[at:at + held[b]]
+        j = torch.arange(own[b], device="cuda")
+        page.append(table[b, j // bs])
+        row.append(j % bs)
+        at += held[b]
+    page, row = torch.cat(page), torch.cat(row)
+    for cache in (k, v):
+        cache[page, :, row] = torch.randn(len(page), hk, D, generator=g, device="cuda").to(dtype)
+    return {"q": torch.randn(T, hq * D, generator=g, device="cuda").to(dtype), "width": hq * D, "k": k, "v": v,
+            "table": table, "lens": torch.tensor([P + n for n in own], device="cuda"),
+            "starts": torch.tensor([0] + list(new), device="cuda").cumsum(0), "prefix": prefix, "P": P, "hq": hq,
+            "hk": hk, "D": D, "bs": bs, "T": T, "scale": D ** -0.5}
+
+
+def reference(c, new, own):
+    """(out, lse, out bound, lse bound), a sequence at a time."""
+    hq, hk, D, bs, P = (c[x] for x in ("hq", "hk", "D", "bs", "P"))
+    dtype = c["q"].dtype
+    uw = 0.0 if dtype == torch.float32 else half_step(dtype)
+    res = [[], [], [], []]
+    t = 0
+    for b, (n, m) in enumerate(zip(new, own)):
+        j = torch.arange(P + m, device="cuda")
+        page = torch.cat([c["prefix"][j[:P] // bs], c["table"][b, (j[P:] - P) // bs]])
+        row = torch.cat([j[:P] % bs, (j[P:] - P) % bs])
+        k, v = (c[x][page, :, row].double().transpose(0, 1)[:, None] for x in ("k", "v"))  # [hk, 1, keys, D]
+        q = c["q"][t:t + n].double().view(n, hk, hq // hk, D).permute(1, 2, 0, 3)
+        late = j[None] > (P + m - n + torch.arange(n, device="cuda"))[:, None]
+        s = (q @ k.transpose(-1, -2) * c["scale"]).masked_fill(late, float("-inf"))
+        big = (q.abs() @ k.abs().transpose(-1, -2) * c["scale"]).masked_fill(late, 0).amax(-1)
+        w = torch.softmax(s, -1)
+        o, A, lse = w @ v, w @ v.abs(), torch.logsumexp(s, -1)
+        seen = (~late).sum(-1).double()
+        d = 2 * (D + 4) * E32 * big
+        tol = half_step(dtype) * o.abs() + (uw + 2 * d + (4 * seen + 64) * E32)[..., None] * A + TINY[dtype]
+        ltol = d + (seen + 64) * E32 + 4 * E32 * lse.abs()
+        for x, y in zip(res, (o, lse, tol, ltol)):
+            x.append((y.permute(2, 0, 1, 3).reshape(n, -1) if y.dim() == 4 else y.permute(2, 0, 1).reshape(n, -1)).cpu())
+        t += n
+    return [torch.cat(x) for x in res]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("D", [64, 96, 128])
+@pytest.mark.parametrize("P", [0, 70])
+def test_short_prompts_between_longer_ones(rope_gpu, dtype, D, P):
+    """About 30 units a CTA: runs of more than 16 of one row tile and one key tile, then units of two row tiles, or of
+    one with several key tiles, which the second softmax group has a part of again."""
+    new, own = [], []
+    for i in range(140):
+        n = 40 + (i * 37) % 61 if i % 4 else 130 + (i * 53) % 121
+        if i % 8 == 4:  # few rows behind many keys
+            new.append(1 + i % 9)
+            own.append(129 + (i * 31) % 272)
+        else:
+            new.append(n)
+            own.append(n)
+    c = batch(31, dtype, new, own, P, 32, 32, D, 16)
+    ro, rl, to, tl = reference(c, new, own)
+    wide = widened({k: v.cpu() if k == "table" else v for k, v in c.items()})
+    for case in (c, wide):
+        out, lse = run_attend(R, case)
+        assert_close(out, ro, to, "out")
+        assert_close(lse, rl, tl, "lse")
+        assert R.get_device_error() == 0

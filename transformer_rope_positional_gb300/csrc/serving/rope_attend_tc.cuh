@@ -411,6 +411,14 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       // parts of 64 keys: part y & 1 of job x, or one a job
       const int parts = NW == 2 ? nt == 2 ? 2 * kt : ((jobs + 1 - group) >> 1) * 2 : jobs;
       uint32_t there[2 * S::kParts];  // which keys of the job are there
+      // The second group has no part of a unit of one row tile and one key tile, waits for nothing there
+      // and may come out many tiles ahead of the copies.  The barriers of `seen` come round every 16
+      // tiles, so that a parity tells the wanted tile from those 16 before and after it only while the
+      // group is less than that away: its first scores of a unit bring it there.
+      if (NW == 2 && parts > 0) {
+        ok = tc::bar_wait(&sm.s_full[group], (pv >> 1) & 1, &sm.dead);
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
       for (int y = 0; y < parts; ++y) {
         const int x = NW == 2 ? (y >> 1) * 2 + group : y;
         const int part = NW == 2 ? y & 1 : 0;
