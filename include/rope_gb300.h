@@ -427,7 +427,8 @@ int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* qu
  * Arithmetic: scores, softmax statistics and sums are binary32 (one running maximum and sum per row; partial
  * results over key ranges are joined in a fixed order, so results are deterministic).  With F16/BF16 data the
  * products run on the tensor cores, and the softmax weights e^(s_j - m) are rounded to the data's type before
- * the product with V (at most half a unit in the last place each); out is rounded once.
+ * the product with V: at most half a unit in the last place each, F16 weights below 2^-25 of the row's largest
+ * by 2^-36 of it at most.  out is rounded once.
  * A page outside [0, NB), and tokens of a sequence past the W pages it has, are keys that no row sees; both
  * record ROPE_DEVICE_SLOT_OUT_OF_RANGE.
  * Returns ROPE_OK, ROPE_ERR_PARAM_NULLPTR, ROPE_ERR_PARAM_INVALID or ROPE_ERR_CUDA.

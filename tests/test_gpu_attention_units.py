@@ -88,3 +88,32 @@ def test_short_prompts_between_longer_ones(rope_gpu, dtype, D, P):
         assert_close(out, ro, to, "out")
         assert_close(lse, rl, tl, "lse")
         assert R.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("lead", [15.0, 17.6])
+@pytest.mark.parametrize("D,new,G", [(64, 1, 8), (128, 1, 16), (256, 1, 4), (256, 2, 8), (64, 40, 8), (128, 17, 8), (256, 20, 8)])
+def test_one_key_far_above_many(rope_gpu, dtype, lead, D, new, G):
+    """One key leads 20000 others by so much that the weights of these, relative to its own, are below the smallest
+    normal binary16 (15 nats) or below half its smallest value (17.6); together they are the whole of the output, as
+    the leading key's value is 0.  So many sequences, all on the same pages, that a CTA takes them whole."""
+    n, bs = 20000, 64
+    B = 304
+    g = torch.Generator(device="cuda").manual_seed(32)
+    pages = -(-n // bs)
+    k = torch.zeros(pages, 1, bs, D, dtype=dtype, device="cuda")
+    v = (1 + 0.1 * torch.randn(pages, 1, bs, D, generator=g, device="cuda")).to(dtype)
+    k[0, 0, 3], v[0, 0, 3] = lead * D ** -0.5, 0
+    q = (1 + torch.arange(new * G, device="cuda")[:, None] % 8 / 256).expand(-1, D).reshape(new, G * D).to(dtype)
+    one = {"q": q, "k": k, "v": v, "table": torch.arange(pages, device="cuda")[None], "width": G * D,
+           "lens": torch.tensor([n], device="cuda"), "starts": torch.tensor([0, new], device="cuda"),
+           "prefix": torch.zeros(0, dtype=torch.int64, device="cuda"), "P": 0, "hq": G, "hk": 1, "D": D, "bs": bs,
+           "T": new, "scale": D ** -0.5}
+    ro, rl, to, tl = reference(one, [new], [n])
+    many = dict(one, q=q.repeat(B, 1), table=one["table"].repeat(B, 1), lens=one["lens"].repeat(B), T=new * B,
+                starts=torch.arange(B + 1, device="cuda") * new)
+    for c, times in ((one, 1), (many, B)):
+        out, lse = run_attend(R, c)
+        assert_close(out, ro.repeat(times, 1), to.repeat(times, 1), "out of %d" % times)
+        assert_close(lse, rl.repeat(times, 1), tl.repeat(times, 1), "lse of %d" % times)
+        assert R.get_device_error() == 0

@@ -14,7 +14,11 @@
 //    rows, 59.0 with 8).
 //  * The weights of a score tile are, register for register, the A operand of the product
 //    with V (8 rows: transposed, its B operand).  They are rounded to the data's type there (half
-//    a step relative each, the sums l taken before); m, l and O stay in binary32.
+//    a step relative each, the sums l taken before); m, l and O stay in binary32.  binary16's
+//    exponents end at 2^-14 (2^-24 in its subnormals), so its weights are taken 2^15 times as large
+//    (see weight_lift): from 2^-29 of the largest on the half step is relative, and what is below is
+//    off by 2^-40 of the largest at most.  (Without, 20000 keys 17.6 nats below one vanished from O
+//    but not from l.)
 //
 // 64 requests of up to 8192 tokens, 32 q and 8 k heads of 128, bf16: 174 us, 6.4 TB/s, 0.94 of
 // the measured copy bandwidth.  4 requests of 300 tokens: 8.9 us with the joining kernel, all of
@@ -96,6 +100,14 @@ __device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float x, float y
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Weights of up to 2^over are taken 2^lift times as large: up to 2^15 in binary16, whose largest
+// value is just below 2^16; as they are in bfloat16, whose exponents are binary32's.  l and O are of
+// the same weights, so the m that leaves with them is smaller by lift.
+template <typename T>
+__host__ __device__ constexpr int weight_lift(int over) {
+  return std::is_same<T, __half>::value ? 15 - over : 0;
+}
+
 // DP: D rounded up to a multiple of 64; columns past D are zeros in shared memory.
 // MR: rows of a unit, 16 or 8.
 template <typename T, int DP, int MR>
@@ -108,6 +120,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
   constexpr int KS = DP / 16;  // k steps of the score product
   constexpr bool kEight = MR == 8;
   constexpr bool kHoldQ = DP <= 128;  // the row tile's A operands stay in registers
+  constexpr float kLift = (float)weight_lift<T>(0);
   extern __shared__ __align__(1024) unsigned char raw[];
   MmaShared<DP>& sm = *reinterpret_cast<MmaShared<DP>*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -215,9 +228,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
           t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
           t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
         }
-        const float b0 = t0 == -INFINITY ? 0.f : t0, b1 = t1 == -INFINITY ? 0.f : t1;
+        const float b0 = t0 == -INFINITY ? 0.f : t0 - kLift, b1 = t1 == -INFINITY ? 0.f : t1 - kLift;
         if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {  // some row's maximum grew
-          const float f0 = fast_exp2(m0 - b0), f1 = fast_exp2(m1 - b1);
+          const float f0 = fast_exp2(m0 - kLift - b0), f1 = fast_exp2(m1 - kLift - b1);
           l0 *= f0;
           l1 *= f1;
 #pragma unroll
@@ -280,9 +293,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
       }
-      const float b0 = t0 == -INFINITY ? 0.f : t0, b1 = t1 == -INFINITY ? 0.f : t1;
+      const float b0 = t0 == -INFINITY ? 0.f : t0 - kLift, b1 = t1 == -INFINITY ? 0.f : t1 - kLift;
       if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1)) {  // some row's maximum grew
-        const float f0 = fast_exp2(m0 - b0), f1 = fast_exp2(m1 - b1);
+        const float f0 = fast_exp2(m0 - kLift - b0), f1 = fast_exp2(m1 - kLift - b1);
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
@@ -328,9 +341,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
     if (kEight ? r0 == 0 : cq == 0) {
-      sm.ml[warp][ra][0] = m0;
+      sm.ml[warp][ra][0] = m0 - kLift;
       sm.ml[warp][ra][1] = l0;
-      sm.ml[warp][rb][0] = m1;
+      sm.ml[warp][rb][0] = m1 - kLift;
       sm.ml[warp][rb][1] = l1;
     }
     Walk nw = w;

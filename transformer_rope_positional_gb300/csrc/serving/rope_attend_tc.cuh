@@ -20,9 +20,11 @@
 //    product of full rate; products of 64 keys read the queries from shared memory twice as
 //    often and run at two thirds of it.)
 //  * heads of 256 have room for one O: one softmax group with two score buffers of 64 keys.
-//  * O is multiplied by e^(m_old - m_new) only when a row's maximum grew by more than 2^8
-//    (the weights then stay below 2^8, far inside both 16-bit types), which is rare after the
-//    first tiles.  The result is the same: l and O always refer to the same m.
+//  * O is multiplied by e^(m_old - m_new) only when a row's maximum grew by more than 2^kLag, which
+//    is rare after the first tiles.  The result is the same: l and O always refer to the same m.
+//    bfloat16: by 2^8, and the weights are up to 2^8.  binary16, whose exponents are few: by 2^4, and
+//    the weights are taken 2^11 times as large, up to 2^15 (see weight_lift): from 2^-25 of the
+//    largest on their rounding is half a step relative, below it 2^-36 of the largest at most.
 // The products are issued in order by one thread and the tensor core runs them in order, which
 // is what keeps the next scores from overwriting weights that are still being read.
 //
@@ -390,6 +392,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     unsigned ml_seen = 0;
     const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;  // a row of out is a multiple of 64 bytes
     bool ok = true;
+    constexpr int kLag = std::is_same<T, __half>::value ? 4 : 8;
+    constexpr float kLift = (float)weight_lift<T>(kLag);
     // The last product into this group's O.  Even and odd ones have a barrier each: by the time
     // that one is waited for, the one before it on the same barrier was done (two groups: before
     // these scores; one group: before the last but one), so its parity is not taken for it.
@@ -458,10 +462,10 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           for (int i = 0; i < 32; i += 2)
             top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
         const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-        const float mt = top * a.scale_log2;  // -infinity stays (scale > 0)
+        const float mt = top * a.scale_log2 - kLift;  // -infinity stays (scale > 0)
         if (!any) {
           m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + 8.f)) {
+        } else if (__any_sync(0xffffffffu, mt > m + (float)kLag)) {
           // the last product into O is done before O is changed
           ok = product_done();
           if (!ok) break;
