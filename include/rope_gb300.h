@@ -429,6 +429,10 @@ int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* qu
  * products run on the tensor cores, and the softmax weights e^(s_j - m) are rounded to the data's type before
  * the product with V: at most half a unit in the last place each, F16 weights below 2^-25 of the row's largest
  * by 2^-36 of it at most.  out is rounded once.
+ * The products <query, k> are taken before scale and have to stay within binary32.  Where they do not (F32 and
+ * BF16 reach that far): a row with a product of +infinity, or with none but of -infinity, is computed again with
+ * the query scaled first; in other rows a key whose product is -infinity has weight 0.  A row of scores that are all
+ * -infinity gives out 0 and lse -infinity.
  * A page outside [0, NB), and tokens of a sequence past the W pages it has, are keys that no row sees; both
  * record ROPE_DEVICE_SLOT_OUT_OF_RANGE.
  * Returns ROPE_OK, ROPE_ERR_PARAM_NULLPTR, ROPE_ERR_PARAM_INVALID or ROPE_ERR_CUDA.

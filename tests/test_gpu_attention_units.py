@@ -117,3 +117,47 @@ def test_one_key_far_above_many(rope_gpu, dtype, lead, D, new, G):
         assert_close(out, ro.repeat(times, 1), to.repeat(times, 1), "out of %d" % times)
         assert_close(lse, rl.repeat(times, 1), tl.repeat(times, 1), "lse of %d" % times)
         assert R.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("D,new,own,P", [(64, [1, 1, 1], [70, 5, 300], 0), (128, [1, 2, 1], [40, 3, 2000], 40),
+                                         (64, [90, 40, 3], [90, 500, 20], 0), (128, [90, 140], [400, 140], 30),
+                                         (256, [90, 40], [90, 500], 0), (288, [1, 20], [30, 20], 3)])
+def test_products_beyond_binary32(rope_gpu, dtype, sign, D, new, own, P):
+    """Scores of -9 to -5 (or 5 to 9) with a scale of 2^-126: every product of a query and a key is beyond
+    binary32.  A sequence of no tokens yet (length 0) beside them sees nothing."""
+    c = batch(33, dtype, new + [1], own + [1], P, 4, 2, D, 16)
+    q, k = c["q"], c["k"]
+    q[:] = 2.0 ** 64
+    k.copy_(torch.where(torch.isnan(k), k, sign * (5 + 4 * torch.rand_like(k, dtype=torch.float32).to(dtype)) * 2.0 ** 62 / D))
+    c["scale"] = 2.0 ** -126
+    c["lens"][-1] = 0
+    ro, rl, to, tl = reference(c, new, own)
+    for case in (c, widened({x: y.cpu() if x == "table" else y for x, y in c.items()})):
+        out, lse = run_attend(R, case)
+        assert_close(out[:-1], ro, to, "out")
+        assert_close(lse[:-1], rl, tl, "lse")
+        assert not out[-1].any() and torch.equal(lse[-1], torch.full((4,), float("-inf")))
+        assert R.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_products_beyond_binary32_behind_a_shared_prefix(rope_gpu, dtype):
+    """The same with a launch for the prefix."""
+    n = 60
+    new, own = [1] * n, [1 + (i * 7) % 50 for i in range(n)]
+    c = batch(34, dtype, new + [1], own + [1], 1000, 4, 2, 128, 16)
+    c["q"][:] = 2.0 ** 64
+    k = c["k"]
+    k.copy_(torch.where(torch.isnan(k), k, -(5 + 4 * torch.rand_like(k, dtype=torch.float32).to(dtype)) * 2.0 ** 62 / 128))
+    c["scale"] = 2.0 ** -126
+    c["lens"][-1] = 0
+    ro, rl, to, tl = reference(c, new, own)
+    before = R.launch_count()
+    out, lse = run_attend(R, c)
+    assert R.launch_count() - before == 3
+    assert_close(out[:-1], ro, to, "out")
+    assert_close(lse[:-1], rl, tl, "lse")
+    assert not out[-1].any() and torch.equal(lse[-1], torch.full((4,), float("-inf")))
+    assert R.get_device_error() == 0

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // The joining kernels add the partial results of rows up, a warp to a row.  A row whose result
-// is not finite is computed again key by key (see mend_rows).
+// is not finite, or of weights that are all 0, is computed again key by key (see mend_rows).
 
 // Where partial result s of a row lies: (m, l) and O.
 struct Source {
@@ -114,13 +114,14 @@ __device__ __forceinline__ void add_up(int n, const AttendArgs& a, F&& source, f
   }
 }
 
-// The row's result from m, l and O, if it is finite.
+// The row's result from m, l and O, if it is finite and some key had a weight (see inverse_sum; here rows
+// without keys are left to attend_row too).
 template <typename T, int E>
 __device__ __forceinline__ bool write_row(int64_t row, float m, float l, float2 (&o)[E], T* __restrict__ out,
                                           float* __restrict__ lse, const Pointers& g, const AttendArgs& a) {
   const int lane = threadIdx.x & 31;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  bool fine = l <= FLT_MAX;
+  const float inv = 1.f / l;
+  bool fine = l > 0.f && l <= FLT_MAX;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     o[e] = make_float2(o[e].x * inv, o[e].y * inv);
@@ -134,7 +135,7 @@ __device__ __forceinline__ bool write_row(int64_t row, float m, float l, float2 
     if (d < a.D && access_ok(p, 2 * sizeof(T), a.out_span, g.err)) narrow2(p, o[e]);
   }
   if (lse && lane == 0 && access_ok(lse + row, 4, a.lse_span, g.err))
-    lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+    lse[row] = (m + log2f(l)) * 0.693147180559945309f;
   return true;
 }
 

@@ -414,6 +414,15 @@ __device__ __forceinline__ int row_limit(const Walk& w, int64_t t, const Pointer
   return (int)(p < 0 ? 0 : p > w.s.hi ? w.s.hi : p);
 }
 
+// 1 / l for a row's sum of weights.  A sum of 0 is 0 of a row without keys, but NaN, for mend_rows to
+// find, of one with keys: the products of all of them may have left binary32 downwards where scaled
+// they would not have.
+__device__ __forceinline__ float inverse_sum(float l, const Walk& w, int64_t t, const Pointers& g, const AttendArgs& a,
+                                             const Cut& c) {
+  if (l != 0.f) return 1.f / l;
+  return row_limit(w, t, g, a, c) > 0 ? NAN : 0.f;
+}
+
 // One query row by one warp, a key at a time: keys the row does not see are not read at all.
 template <typename T, int E>
 __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict__ q, const T* __restrict__ kc,
@@ -498,7 +507,8 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
 }
 
 // The rows that this CTA finished and whose result is not finite, once more key by key: a key that a
-// row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of its value leaves NaN.
+// row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of its value leaves NaN; and
+// products of queries and keys beyond binary32 are infinite there, here queries are scaled before.
 // All NT threads call it after a barrier; `tmp` as for find_share.
 template <typename T, int DP, int M, int KT, int NT>
 __device__ __forceinline__ void mend_rows(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,

@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const bool begins = w.k0 == 0, whole = begins && k1 == w.work;
         const bool final = whole && !c.shared;
         const int64_t row = at.t * a.nq + at.h;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         if (final) {
+          const float inv = inverse_sum(l, w, at.t, g, a, c);
           f0 *= inv;
           f1 *= inv;
         }
