@@ -51,18 +51,21 @@ int32_t type_of(const at::Tensor& t) {
   }
 }
 
-// Descriptors of one call; all tensors on the device of the first.
+// Descriptors of one call; all tensors on the device of the first.  What the call writes says so
+// (kWrites): a tensor that shares its memory until one is written gets its own first.
+enum Use { kReads, kWrites };
+
 class Call {
  public:
-  const rope_tensor_t* whole(PyObject* o) {  // NULL for None
+  const rope_tensor_t* whole(PyObject* o, Use use = kReads) {  // NULL for None
     if (o == Py_None) return nullptr;
     const at::Tensor& t = tensor(o);
     if (!t.is_contiguous()) fail(PyExc_ValueError, "expected a contiguous tensor");
-    return add(t);
+    return add(t, use);
   }
 
   // Rows of a 2-D tensor that may be strided; rows must not overlap.
-  const rope_tensor_t* rows(PyObject* o, int64_t* stride) {
+  const rope_tensor_t* rows(PyObject* o, int64_t* stride, Use use = kReads) {
     *stride = 0;
     if (o == Py_None) return nullptr;
     const at::Tensor& t = tensor(o);
@@ -70,17 +73,17 @@ class Call {
       fail(PyExc_ValueError, "expected a 2-D tensor with contiguous rows");
     *stride = t.size(0) > 1 ? t.stride(0) : t.size(1);
     if (*stride < t.size(1)) fail(PyExc_ValueError, "rows overlap: the row stride is below the row width");
-    return add(t);
+    return add(t, use);
   }
 
  private:
-  const rope_tensor_t* add(const at::Tensor& t) {
+  const rope_tensor_t* add(const at::Tensor& t, Use use) {
     if (!t.is_cuda()) fail(PyExc_ValueError, "expected a CUDA tensor");
     if (device_ < 0) device_ = t.get_device();
     if (t.get_device() != device_) fail(PyExc_ValueError, "tensors on different devices");
     if (t.dim() < 1 || t.dim() > 4) fail(PyExc_ValueError, "expected 1 to 4 dimensions");
     rope_tensor_t& d = descs_[n_++];
-    d.data = const_cast<void*>(t.const_data_ptr());
+    d.data = use == kWrites ? t.mutable_data_ptr() : const_cast<void*>(t.const_data_ptr());
     d.dtype = type_of(t);
     d.ndim = (int32_t)t.dim();
     for (int i = 0; i < d.ndim; ++i) d.shape[i] = t.size(i);
@@ -105,13 +108,17 @@ double number(PyObject* o) {
 }
 
 // Frequencies: a contiguous float64 tensor on the host.
-const double* host_doubles(PyObject* o, int64_t* n) {
+const at::Tensor& host_doubles(PyObject* o, int64_t* n) {
   const at::Tensor& t = tensor(o);
   if (t.is_cuda()) fail(PyExc_ValueError, "expected frequencies on the host, got a CUDA tensor");
   if (t.scalar_type() != at::kDouble || !t.is_contiguous())
     fail(PyExc_ValueError, "expected contiguous float64 frequencies");
   *n = t.numel();
-  return static_cast<const double*>(t.const_data_ptr());
+  return t;
+}
+
+const double* frequencies_of(PyObject* o, int64_t* n) {
+  return static_cast<const double*>(host_doubles(o, n).const_data_ptr());
 }
 
 template <typename F>
@@ -170,9 +177,9 @@ PyObject* frequencies(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.attention = number(a[7]);
     int64_t count = 0, size = 0;
     const int64_t dim = integer(a[0]);
-    s.factors = a[8] == Py_None ? nullptr : host_doubles(a[8], &count);
+    s.factors = a[8] == Py_None ? nullptr : frequencies_of(a[8], &count);
     double scale = 0;
-    double* out = const_cast<double*>(host_doubles(a[9], &size));
+    double* out = static_cast<double*>(host_doubles(a[9], &size).mutable_data_ptr());
     int st = ROPE_ERR_PARAM_INVALID;
     if (size >= dim / 2 && (!s.factors || count == dim / 2))
       st = g_frequencies(dim, number(a[1]), s.kind < 0 ? nullptr : &s, out, &scale);
@@ -185,9 +192,9 @@ PyObject* scaled_cos_sin_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&]() -> PyObject* {
     Call c;
     int64_t F = 0;
-    const double* f = host_doubles(a[0], &F);
+    const double* f = frequencies_of(a[0], &F);
     const double scale = number(a[1]);
-    const rope_tensor_t *cache = c.whole(a[4]), *positions = c.whole(a[2]);
+    const rope_tensor_t *cache = c.whole(a[4], kWrites), *positions = c.whole(a[2]);
     const int64_t first = integer(a[3]), stream = integer(a[5]);
     return status_of([&] { return g_cos_sin_cache(f, F, scale, positions, first, cache, (void*)stream); });
   });
@@ -198,9 +205,10 @@ PyObject* scaled_cos_sin(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 8, [&]() -> PyObject* {
     Call c;
     int64_t F = 0;
-    const double* f = host_doubles(a[0], &F);
+    const double* f = frequencies_of(a[0], &F);
     const double scale = number(a[1]);
-    const rope_tensor_t *cos = c.whole(a[5]), *sin = c.whole(a[6]), *positions = c.whole(a[2]);
+    const rope_tensor_t *cos = c.whole(a[5], kWrites), *sin = c.whole(a[6], kWrites);
+    const rope_tensor_t* positions = c.whole(a[2]);
     const int64_t first = integer(a[3]), mode = integer(a[4]), stream = integer(a[7]);
     return status_of([&] { return g_cos_sin(f, F, scale, positions, first, mode, cos, sin, (void*)stream); });
   });
@@ -212,9 +220,13 @@ PyObject* append_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 15, [&]() -> PyObject* {
     Call c;
     int64_t ks, qs, vs;
-    const rope_tensor_t *key = c.rows(a[2], &ks), *query = c.rows(a[1], &qs), *value = c.rows(a[3], &vs);
+    // (written ones first: a query that is its own output, or the fused buffer of an in-place query's key, has
+    // the address that it is written at)
+    const rope_tensor_t* out = c.whole(a[6], kWrites);
+    const rope_tensor_t *kc = c.whole(a[7], kWrites), *vc = c.whole(a[8], kWrites);
+    const rope_tensor_t* query = c.rows(a[1], &qs, out ? kReads : kWrites);
+    const rope_tensor_t *key = c.rows(a[2], &ks), *value = c.rows(a[3], &vs);
     const rope_tensor_t *positions = c.whole(a[0]), *table = c.whole(a[4]), *slots = c.whole(a[5]);
-    const rope_tensor_t *out = c.whole(a[6]), *kc = c.whole(a[7]), *vc = c.whole(a[8]);
     const int64_t head = integer(a[9]);
     const int64_t rotary = a[10] != Py_None ? integer(a[10]) : table && table->ndim == 2 ? table->shape[1] : 0;
     const int neox = PyObject_IsTrue(a[11]);
@@ -263,8 +275,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     int64_t qs;
     const rope_tensor_t *query = c.rows(a[0], &qs), *kc = c.whole(a[1]), *vc = c.whole(a[2]), *bt = c.whole(a[3]);
-    const rope_tensor_t *lens = c.whole(a[4]), *starts = c.whole(a[5]), *prefix = c.whole(a[6]), *out = c.whole(a[9]);
-    const rope_tensor_t* lse = c.whole(a[10]);
+    const rope_tensor_t *lens = c.whole(a[4]), *starts = c.whole(a[5]), *prefix = c.whole(a[6]);
+    const rope_tensor_t *out = c.whole(a[9], kWrites), *lse = c.whole(a[10], kWrites);
     const int64_t prefix_len = integer(a[7]), stream = integer(a[12]);
     const float scale = (float)number(a[8]);
     at::Tensor ws;
@@ -277,7 +289,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (bytes < 0) return PyLong_FromLong(ROPE_ERR_PARAM_INVALID);
       ws = at::empty({bytes}, tensor(a[0]).options().dtype(at::kByte));
     }
-    void* const at = const_cast<void*>(ws.const_data_ptr());
+    void* const at = ws.mutable_data_ptr();
     const int64_t bytes = (int64_t)ws.nbytes();
     return status_of([&] {
       return g_attend(query, qs, kc, vc, bt, lens, starts, prefix, prefix_len, scale, out, lse, at, bytes,
