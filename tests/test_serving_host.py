@@ -332,3 +332,13 @@ def test_heads_of_no_columns(lib):
     with pytest.raises(ValueError):
         R.paged_attention(torch.zeros(4, 64), kv, kv, i.view(4, 1), i, torch.zeros(5, dtype=torch.int64),
                           torch.zeros(4, 64))
+
+
+@pytest.mark.parametrize("scaling", [None, {"kind": "factors", "factors": [2.0, 4.0]}])
+def test_frequencies_stay_on_the_host_under_another_default_device(lib, scaling):
+    want = R.rope_frequencies(4, 10000.0, scaling)[0]
+    with torch.device("meta"):
+        got = R.rope_frequencies(4, 10000.0, scaling)[0]
+        given = C._host_frequencies([1.0, 0.5])
+    assert got.device.type == "cpu" and torch.equal(got, want)
+    assert given.device.type == "cpu" and given.tolist() == [1.0, 0.5]

@@ -388,7 +388,7 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[d
     formulas are those of ``rope_scaled_frequencies`` in the C header."""
     what = "rope_scaled_frequencies"
     fn = (_binding or _load_binding()).frequencies
-    inv = torch.empty(min(max(1, int(rotary_dim) // 2), 1024), dtype=torch.float64)
+    inv = torch.empty(min(max(1, int(rotary_dim) // 2), 1024), dtype=torch.float64, device="cpu")
     if scaling is None:
         st, scale = fn(rotary_dim, base, -1, 0.0, 0.0, 0.0, 0.0, 0.0, None, inv)
     else:
@@ -410,7 +410,7 @@ _SCALING_KEYS = frozenset(("kind", "factor", "original_length", "low", "high", "
 
 def _host_frequencies(inv_freq) -> torch.Tensor:
     if not isinstance(inv_freq, torch.Tensor):
-        return torch.tensor(list(inv_freq), dtype=torch.float64)
+        return torch.tensor(list(inv_freq), dtype=torch.float64, device="cpu")
     if inv_freq.dtype == torch.float64:
         return inv_freq.contiguous()
     if inv_freq.is_cuda:
