@@ -40,7 +40,7 @@ SOURCES = ["rope_api.cu", "rope_launch.cu", "rope_inplace_fwd.cu", "rope_inplace
            "rope_qkv.cu", "serving/rope_table.cu", "serving/rope_append.cu", "serving/rope_attend.cu"]
 HEADERS = ["rope_device.cuh", "rope_launch.h", "rope_inplace.cuh", "serving/serving.h",
            "serving/rope_attend.cuh", "serving/rope_attend_ring.cuh", "serving/rope_attend_mma.cuh", "serving/rope_attend_tc.cuh", "serving/rope_attend_f32.cuh",
-           "serving/tcgen05.cuh"]
+           "serving/tcgen05.cuh", "serving/wait_clock.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

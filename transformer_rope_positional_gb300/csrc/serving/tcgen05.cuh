@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "serving/wait_clock.h"
+
 namespace rope {
 namespace tc {
 
@@ -42,18 +44,16 @@ __device__ __forceinline__ uint64_t now_ns() {
   return t;
 }
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s; a wait is a few microseconds
-
 // Waits until the phase of the given parity has completed; false when the CTA is dead.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity, int* dead) {
   if (bar_try(bar, parity)) return true;
-  const uint64_t start = now_ns();
+  WaitClock clock(now_ns());
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
       if (bar_try(bar, parity)) return true;
     if (*(volatile int*)dead) return false;
-    if (now_ns() - start > kWaitLimitNs) {
+    if (clock.expired(now_ns())) {
       *(volatile int*)dead = 1;
       return false;
     }
