@@ -115,7 +115,6 @@ def _build_locked(lib_path: str, verbose: bool, debug: bool) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_build_binding)
         results = list(ex.map(compile_one, SOURCES))
-        binding.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -125,6 +124,7 @@ def _build_locked(lib_path: str, verbose: bool, debug: bool) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, lib_path)
+    binding.result()  # raises if it failed; the library, which needs nothing of torch, is there all the same
     return lib_path
 
 
