@@ -350,8 +350,14 @@ _binding = None
 def _load_binding():
     global _binding
     if _binding is None:
+        from . import build as B
+
         load()  # the library first: it says how to build both
-        path = os.path.join(_HERE, "lib", "rope_binding.so")
+        path = B.BINDING_PATH
+        if B.binding_built_for() != B.binding_target():
+            raise RuntimeError("%s is not built for this Python and torch; run "
+                               "`python -m transformer_rope_positional_gb300.build%s`"
+                               % (path, " --debug" if DEBUG_BOUNDS else ""))
         loader = importlib.machinery.ExtensionFileLoader("rope_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("rope_binding", loader))
         loader.exec_module(module)

@@ -57,8 +57,24 @@ def _inputs():
     return srcs + [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "rope_gb300.h")]
 
 
+def binding_target() -> str:
+    """What the binding is linked against: this Python's ABI and the installed torch, in the words of its
+    version file (torch is not imported)."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return "%s\n%s" % (sysconfig.get_config_var("SOABI"), f.read())
+
+
+def binding_built_for() -> str:
+    """The :func:`binding_target` of the binding that is there; empty where there is none."""
+    try:
+        with open(BINDING_PATH + ".target") as f:
+            return f.read() if os.path.exists(BINDING_PATH) else ""
+    except FileNotFoundError:
+        return ""
+
+
 def up_to_date(lib: str = LIB_PATH) -> bool:
-    if not os.path.exists(lib) or not os.path.exists(BINDING_PATH):
+    if not os.path.exists(lib) or binding_built_for() != binding_target():
         return False
     t = min(os.path.getmtime(lib), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(p) <= t for p in _inputs())
@@ -83,8 +99,12 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
             fcntl.flock(lock, fcntl.LOCK_UN)
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
 def _build_binding() -> None:
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch_dir, target = _torch_dir(), binding_target()
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     tmp = BINDING_PATH + ".%d.tmp" % os.getpid()
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
@@ -94,7 +114,13 @@ def _build_binding() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s\n%s" % (BINDING, r.stdout, r.stderr))
+    note = BINDING_PATH + ".target"
+    if os.path.exists(note):
+        os.remove(note)  # none beside a binding that it does not describe
     os.replace(tmp, BINDING_PATH)
+    with open(tmp, "w") as f:
+        f.write(target)
+    os.replace(tmp, note)
 
 
 def _build_locked(lib_path: str, verbose: bool, debug: bool) -> str:
