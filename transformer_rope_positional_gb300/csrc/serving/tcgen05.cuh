@@ -107,13 +107,6 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&v)[16], uint32_t at) {
       : "r"(at)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      ROPE_I8(v, 0), ROPE_I8(v, 8), ROPE_I8(v, 16), ROPE_I8(v, 24)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
