@@ -161,3 +161,32 @@ def test_products_beyond_binary32_behind_a_shared_prefix(rope_gpu, dtype):
     assert_close(lse[:-1], rl, tl, "lse")
     assert not out[-1].any() and torch.equal(lse[-1], torch.full((4,), float("-inf")))
     assert R.get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 32), (torch.float32, 16)], ids=str)
+def test_cache_of_more_than_2_31_rows(rope_gpu, dtype, D):
+    """The smallest heads with so many pages that a cache row no longer fits 32 bits (137 GB, keys and values in one
+    tensor, of which only the pages in use are ever written)."""
+    bs, NB = 128, (1 << 24) + 8
+    if torch.cuda.mem_get_info()[0] < NB * bs * 64 + (8 << 30):
+        pytest.skip("needs 146 GB")
+    cache = torch.empty(NB, 1, bs, D, dtype=dtype, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(35)
+    table = torch.tensor([[NB - 1, 0, NB - 7], [1, NB - 2, 3], [(1 << 24) - 1, 1 << 24, 5]], device="cuda")
+    prefix = torch.tensor([NB - 3, 7], device="cuda")
+    for page in torch.cat([table.flatten(), prefix]).tolist():
+        cache[page] = torch.randn(1, bs, D, generator=g, device="cuda").to(dtype)
+    new, own, P = [1, 130, 40], [300, 200, 384], 150
+    c = {"q": torch.randn(sum(new), 4 * D, generator=g, device="cuda").to(dtype), "width": 4 * D, "k": cache, "v": cache,
+         "table": table, "lens": torch.tensor([P + n for n in own], device="cuda"),
+         "starts": torch.tensor([0] + new, device="cuda").cumsum(0), "prefix": prefix, "P": P, "hq": 4, "hk": 1,
+         "D": D, "bs": bs, "scale": D ** -0.5}
+    ro, rl, to, tl = reference(c, new, own)
+    out = torch.empty(sum(new), 4 * D, dtype=dtype, device="cuda")
+    lse = torch.empty(sum(new), 4, device="cuda")
+    R.paged_attention(c["q"], cache, cache, table, c["lens"], c["starts"], out, prefix_blocks=prefix, prefix_len=P, lse=lse)
+    assert_close(out, ro, to, "out")
+    assert_close(lse, rl, tl, "lse")
+    assert R.get_device_error() == 0
+    del cache, c
+    torch.cuda.empty_cache()

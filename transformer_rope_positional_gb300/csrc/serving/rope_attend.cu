@@ -32,7 +32,7 @@ using namespace attend;
 constexpr int kWarps = 4;
 
 // One warp per query row.
-template <typename T, int E>
+template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_rows_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
                        float* __restrict__ lse, Pointers g, AttendArgs a) {
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * kWarps) {
     const int64_t t = row / a.nq;
     if (t >= tokens) break;
-    attend_row<T, E>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
+    attend_row<T, 16>(t, (int)(row - t * a.nq), q, kc, vc, out, lse, g, a);
   }
 }
 
@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-template <typename T, int E>
+template <typename T>
 cudaError_t launch_rows(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
-  auto kernel = attend_rows_kernel<T, E>;
+  auto kernel = attend_rows_kernel<T>;
   const int64_t resident = (int64_t)sm_count() * resident_blocks(reinterpret_cast<const void*>(kernel), kWarps * 32);
   const int64_t grid = std::max<int64_t>(1, std::min((p.T * p.nq + kWarps - 1) / kWarps, resident));
   return launch_overlapped(kernel, (unsigned)grid, kWarps * 32, stream, static_cast<const T*>(p.query),
@@ -493,8 +493,7 @@ cudaError_t launch_typed(const AttendProblem& p, cudaStream_t stream) {
   const cudaError_t er = device_error_address(&g.err);
   if (er != cudaSuccess) return er;
   if (unit_path(p.D, p.num_blocks * p.nk * p.block_size)) return launch_cut<T>(p, g, a, stream);
-  if (p.D <= 64) return launch_rows<T, 2>(p, g, a, stream);
-  return launch_rows<T, 16>(p, g, a, stream);
+  return launch_rows<T>(p, g, a, stream);
 }
 
 }  // namespace
