@@ -11,8 +11,8 @@ PROGRAM = r"""
 #include <initializer_list>
 
 int main() {
-  const uint64_t ms = 1000000ull, s = 1000 * ms;
-  for (uint64_t start : {uint64_t(0), 5 * s, ~uint64_t(0) - s}) {
+  const uint64_t ms = 1000000ull, s = 1000 * ms;  // of the clock, of which the lower 32 bits are seen
+  for (uint64_t start : {uint64_t(0), 5 * s, uint64_t(0xfffffffe)}) {
     {  // suspended for an hour, then again for ten seconds, within one wait
       rope::WaitClock c(start);
       if (c.expired(start + 3600 * s)) return 1;
