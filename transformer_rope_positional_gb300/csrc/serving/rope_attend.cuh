@@ -414,13 +414,12 @@ __device__ __forceinline__ int row_limit(const Walk& w, int64_t t, const Pointer
   return (int)(p < 0 ? 0 : p > w.s.hi ? w.s.hi : p);
 }
 
-// 1 / l for a row's sum of weights.  A sum of 0 is 0 of a row without keys, but NaN, for mend_rows to
-// find, of one with keys: the products of all of them may have left binary32 downwards where scaled
-// they would not have.
-__device__ __forceinline__ float inverse_sum(float l, const Walk& w, int64_t t, const Pointers& g, const AttendArgs& a,
-                                             const Cut& c) {
+// 1 / l for the sum of weights of a row that this CTA finishes (in the launch over a prefix none does).
+// A sum of 0 is 0 of a row without keys, but NaN, for mend_rows to find, of one with keys: the
+// products of all of them may have left binary32 downwards where scaled they would not have.
+__device__ __forceinline__ float inverse_sum(float l, const Walk& w, int64_t t) {
   if (l != 0.f) return 1.f / l;
-  return row_limit(w, t, g, a, c) > 0 ? NAN : 0.f;
+  return w.s.hi > 0 && w.s.pos0 + (t - w.s.t0) >= 0 ? NAN : 0.f;
 }
 
 // One query row by one warp, a key at a time: keys the row does not see are not read at all.

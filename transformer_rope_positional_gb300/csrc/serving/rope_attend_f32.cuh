@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kF32Threads, f32_ctas<DP>())
       const bool mine = r < u.rows;
       const RowAt at = row_at(u, mine ? r : 0, w.h, a);
       const int64_t row = at.t * a.nq + at.h;
-      const float f = !final ? 1.f : mine ? inverse_sum(l[i], w, at.t, g, a, c) : 0.f;
+      const float f = !final ? 1.f : mine ? inverse_sum(l[i], w, at.t) : 0.f;
       float* const to = final ? out + row * a.D
                         : whole ? c.dense + row * a.D
                                 : slot_o(c, a, blockIdx.x, begins ? 1 : 0) + (int64_t)r * a.D;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const RowAt at = row_at(u, rr, w.h, a);
         const int64_t row = at.t * a.nq + at.h;
         if (final) {
-          const float inv = inverse_sum(sum, w, at.t, g, a, c);
+          const float inv = inverse_sum(sum, w, at.t);
           v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
           if (!(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX &&
                 sum <= FLT_MAX))

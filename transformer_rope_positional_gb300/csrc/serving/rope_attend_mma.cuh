@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         const RowAt at = row_at(u, rr, w.h, a);
         const int64_t row = at.t * a.nq + at.h;
         if (final) {
-          const float inv = inverse_sum(l, w, at.t, g, a, c);
+          const float inv = inverse_sum(l, w, at.t);
           v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
           if (!(fabsf(v.x) <= FLT_MAX && fabsf(v.y) <= FLT_MAX && fabsf(v.z) <= FLT_MAX && fabsf(v.w) <= FLT_MAX &&
                 l <= FLT_MAX))

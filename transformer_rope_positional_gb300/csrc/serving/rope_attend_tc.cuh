@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const bool final = whole && !c.shared;
         const int64_t row = at.t * a.nq + at.h;
         if (final) {
-          const float inv = inverse_sum(l, w, at.t, g, a, c);
+          const float inv = inverse_sum(l, w, at.t);
           f0 *= inv;
           f1 *= inv;
         }
