@@ -31,7 +31,10 @@ using namespace attend;
 
 constexpr int kWarps = 4;
 
-// One warp per query row.
+// One warp per query row: heads over 256, and caches of 2^31 rows.  Every key is a round trip to
+// memory and two sums over the lanes, and K and V are read again for each head of a group: 64 requests
+// of up to 2048 tokens, 16 q and 4 k heads of 512, bf16: 11.5 ms where the bytes take 82 us, issue
+// slots busy 3 % of the time.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
     attend_rows_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
@@ -59,7 +62,8 @@ __device__ __forceinline__ Source slot_source(const Cut& c, const AttendArgs& a,
   return {slot_ml(c, a, cta, begins ? 1 : 0) + at * 2, slot_o(c, a, cta, begins ? 1 : 0) + (int64_t)at * a.D};
 }
 
-// Adds up n partial results of each of R rows, NS at a time, all loads before any arithmetic:
+// Adds up n partial results of each of R rows, NS at a time, all loads before any arithmetic
+// (fast_exp2 for binary32 too: one factor a part, of relative error 2^-22 as exp2f's):
 // m, l, and this lane's columns 2 lane + 64 e of O.  source(r, s) is called for s < n only.
 template <int E, int R, int NS, typename F>
 __device__ __forceinline__ void add_up(int n, const AttendArgs& a, F&& source, float (&m)[R], float (&l)[R],

@@ -21,7 +21,7 @@
 //    but not from l.)
 //
 // 64 requests of up to 8192 tokens, 32 q and 8 k heads of 128, bf16: 174 us, 6.4 TB/s, 0.94 of
-// the measured copy bandwidth.  4 requests of 300 tokens: 8.9 us with the joining kernel, all of
+// the measured copy bandwidth.  4 requests of 300 tokens: 8.0 us with the joining kernel, all of
 // it latency (lengths, pages, rows, two launches).
 #pragma once
 

@@ -28,10 +28,11 @@
 // The products are issued in order by one thread and the tensor core runs them in order, which
 // is what keeps the next scores from overwriting weights that are still being read.
 //
-// 4 chunks of 1984 tokens behind 4096 shared ones, 32 q and 8 k heads of 128, bf16: 0.50 to 0.52
-// ms, 1.3 PFLOP/s, 0.67 of the measured matrix rate.  What is left is the softmax's latency
-// between a tile's two products (the products wait for weights a fifth of the time), and the
-// ends of units, where 256 rows of results leave lane by lane.
+// 4 chunks of 1984 tokens behind 4096 shared ones, 32 q and 8 k heads of 128, bf16: 0.50 to 0.53
+// ms, 1.3 PFLOP/s, 0.67 of the measured matrix rate.  The tensor pipe is active 58 % of the time,
+// issue slots 54, the pipe of the exponentials 29: none of them is the bound.  What is left is the
+// softmax's latency between a tile's two products, and the ends of units, where 256 rows of results
+// leave lane by lane.
 #pragma once
 
 #include <type_traits>

@@ -13,8 +13,9 @@
 //    Chebyshev nodes on [0, 1/4] (errors 6.8e-12 and 4.7e-11): 9 FMAs for both, two columns
 //    in one packed instruction.
 //  * One thread owns V consecutive frequencies (16 bytes of the output) and walks rows.
-// Bound by instruction issue, about 25 a value pair, twice the time of the stores: 131072 rows
-// of 128 columns in bf16 take 10.2 us, 3.3 TB/s; 2048 x 64 binary32 for the in-place op 2.8 us.
+// About 25 instructions a value pair: the issue slots and the integer pipe are busy two thirds of the
+// time, and that is twice the time of the stores: 131072 rows of 128 columns in bf16 take 10.2 us,
+// 3.3 TB/s; 2048 x 64 binary32 for the in-place op 2.8 us.
 #include <algorithm>
 #include <cmath>
 
