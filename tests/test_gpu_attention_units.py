@@ -190,3 +190,32 @@ def test_cache_of_more_than_2_31_rows(rope_gpu, dtype, D):
     assert R.get_device_error() == 0
     del cache, c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,own", [([1, 1], [300, 40]), ([3, 1], [300, 1000]), ([40, 60], [300, 900])])
+def test_scores_of_which_one_unit_is_less_than_a_step(rope_gpu, dtype, D, new, own):
+    """Scores of 2^23 to 2^31, where binary32 steps by 1 to 256, thousands apart: the key that leads has all the
+    weight, so its value is the result (rounded once: half a step, and 2^-20 for sums and weights).  The score itself is a sum of up to 13 rounded
+    parts with 5 more roundings of scales and units, each 2^-24: 2^-19."""
+    for power in range(0, 9):
+        c = batch(36, dtype, new, own, 0, 8, 2, D, 16)
+        k = c["k"]
+        step = 2 ** -7 if dtype == torch.bfloat16 else 2 ** -10  # of the keys, relative
+        fall = 1 - step * (1 + torch.randint(0, 50, k.shape[:3], device="cuda")[..., None])
+        k.copy_(torch.where(torch.isnan(k), k, (512 * fall).to(dtype).expand_as(k)))
+        lead = [(int(c["table"][b, 0]), min(n - 1, 3) if n > a + 3 else 0) for b, (a, n) in enumerate(zip(new, own))]
+        for page, row in lead:
+            k[page, :, row] = 512
+        c["q"][:] = 4096 / (D // 64)
+        c["scale"] = 0.0625 * 2.0 ** power
+        want = torch.cat([c["v"][page, :, row].double()[None, :, None].expand(a, 2, 4, D).reshape(a, -1)
+                          for (page, row), a in zip(lead, new)]).cpu()
+        for case in (c, widened({x: y.cpu() if x == "table" else y for x, y in c.items()})):
+            out, lse = run_attend(R, case)
+            assert_close(out, want, (half_step(dtype) + 2.0 ** -20) * want.abs() + TINY[dtype], "out at 2^%d" % power)
+            top = 64 * 4096 * 512 * c["scale"]
+            assert_close(lse, torch.full((sum(new), 8), top, dtype=torch.float64),
+                         torch.full((sum(new), 8), top * 2.0 ** -19), "lse at 2^%d" % power)
+            assert R.get_device_error() == 0

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import contextlib
 import fcntl
 import importlib.util
 import os
@@ -115,7 +116,7 @@ def _build_binding() -> None:
     if r.returncode != 0:
         raise RuntimeError("g++ failed on %s:\n%s\n%s" % (BINDING, r.stdout, r.stderr))
     note = BINDING_PATH + ".target"
-    if os.path.exists(note):
+    with contextlib.suppress(FileNotFoundError):
         os.remove(note)  # none beside a binding that it does not describe
     os.replace(tmp, BINDING_PATH)
     with open(tmp, "w") as f:
