@@ -1,7 +1,7 @@
 /*
  * rope_gb300.h -- C ABI of the GB300 (sm_103a) rotary position embedding library.
  *
- * Six operators, each an asynchronous call on a caller-given CUDA stream:
+ * Operators, each an asynchronous call on a caller-given CUDA stream:
  *
  *   rope_inplace_partial          in-place partial-slice RoPE on a BSND tensor
  *                                 (interleave or half mode), and its backward
@@ -15,6 +15,11 @@
  *                                 their slots of a paged KV cache (no norm)
  *   rope_paged_attention          attention over the paged KV cache, with a prefix shared by
  *                                 the whole batch read once for all
+ *   rope_append_paged_kv_8bit     the append and the attention for a cache held in 8 bits, with a
+ *   rope_paged_attention_8bit     scale for each block of tokens and head
+ *   rope_rearrange_sequences      sequences of a paged cache forked, reordered, dropped and given room;
+ *   rope_compact_pages            live pages moved to the front; pages copied in many tensors at once
+ *   rope_copy_pages
  *
  * Sources (web pages, cited by title and section):
  *  [IPRM] "CANN ops-transformer 的 aclnnInplacePartialRotaryMul 算子：Inplace
@@ -28,8 +33,8 @@
  * borrowed for the duration of the call and of the work it enqueues.  All
  * tensors of a call live on the current device (cudaSetDevice), and `stream`
  * belongs to it: the launch goes to the current device.  The
- * library allocates nothing, needs no workspace (except rope_paged_attention,
- * whose caller gives it one), and never synchronises the
+ * library allocates nothing on the device, needs no workspace (except rope_paged_attention
+ * and rope_paged_attention_8bit, whose caller gives them one), and never synchronises the
  * stream (except rope_get_device_error, which says so).  The two-phase
  * "GetWorkspaceSize, then execute" interface of the pages collapses to one call
  * because the workspace is always zero bytes.  (The fused op's kernel uses up to
@@ -75,7 +80,11 @@ typedef enum {
   ROPE_F32 = 0,  /* IEEE binary32 */
   ROPE_F16 = 1,  /* IEEE binary16 */
   ROPE_BF16 = 2, /* bfloat16 */
-  ROPE_I64 = 3   /* int64 (positions only) */
+  ROPE_I64 = 3,  /* int64 (positions, slots, page numbers and the like) */
+  ROPE_F8E4M3 = 4, /* 8-bit codes of a cache: sign, 4 exponent bits of bias 7, 3 of the fraction; 0x7f is NaN, no infinity */
+  ROPE_E8M0 = 5,   /* scales of a cache of codes: byte b is 2^(b - 127), 255 is NaN */
+  ROPE_I32 = 6,    /* int32 (counts of holders of a page) */
+  ROPE_U8 = 7      /* bytes of any meaning (rope_copy_pages) */
 } rope_dtype_t;
 
 /* A borrowed, contiguous, row-major device tensor of 1 to 4 dimensions. */
@@ -101,6 +110,7 @@ enum {
                                             table was outside the cache, or a sequence longer than its pages */
   ROPE_DEVICE_INDEX_OUT_OF_BOUNDS = 4,   /* bounds-checking builds only: a kernel formed an address
                                             outside the tensor it addresses (the access was skipped) */
+  ROPE_DEVICE_PAGES_EXHAUSTED = 16,      /* rope_rearrange_sequences found fewer free pages than were asked for */
   ROPE_DEVICE_WAIT_EXPIRED = 8           /* a wait inside a kernel ran out (results are not valid); a defect of
                                             the library, never caused by the values of a tensor */
 };
@@ -457,6 +467,119 @@ int rope_paged_attention(const rope_tensor_t* query, int64_t query_row_stride, c
  */
 int rope_paged_attention_workspace(int64_t num_tokens, int64_t num_q_heads, int64_t num_k_heads, int64_t head_size,
                                    int32_t dtype, int64_t prefix_len, int64_t* bytes);
+
+/*
+ * RoPE of query and key on the way to the query output and to a paged KV cache of 8-bit codes.
+ *
+ * A cached value is code * 2^(b - 127), b being the scale byte of its block: the BS / S tokens of a page (S scale
+ * blocks a page) of one head.  The rotation is rope_append_paged_kv's, in binary32.  Then for every scale block that
+ * the call writes, of the keys and of the values,
+ *   most = max |x| over its values written that are finite;  e = the least integer with most <= 448 * 2^e
+ *   byte = e + 127, from 1 to 254;  0 where most = 0
+ * and where tokens stand in the block before the first one written: no less than the byte that was there, and where it
+ * grew their codes become the nearest (ties to even) of code * 2^(old - new).  Written codes are the nearest of
+ * x * 2^-e; a value that is not finite becomes NaN.  So a value is off by 2^-4 of itself at most, and by 2^(e - 10) where
+ * that is more, once; the codes of tokens before are re-encoded exactly, but where 2^(old - new) makes them subnormal.
+ *
+ *   All arguments as in rope_append_paged_kv, and
+ *   k_cache, v_cache  ROPE_F8E4M3 [NB, numKHeads, BS, head_size], [NB, numVHeads, BS, head_size].  head_size at most 512.
+ *   k_scale, v_scale  ROPE_E8M0 [NB, numKHeads, S], [NB, numVHeads, S]; S divides BS.  Scales of blocks whose first
+ *                     token the call writes need not be initialised.
+ *   slot_mapping      The tokens of one scale block stand one after the other in the call, in the order of their slots
+ *                     (tokens of a sequence in order do), and what a block holds before the first of them is kept.  Where
+ *                     a call brings tokens to a block in more than one such run, the block's content is unspecified.
+ *                     Rows of a block behind the last token written are not re-encoded.
+ * Results, refusals and device errors otherwise as rope_append_paged_kv's.
+ */
+int rope_append_paged_kv_8bit(const rope_tensor_t* positions, const rope_tensor_t* query, const rope_tensor_t* key,
+                              const rope_tensor_t* value, const rope_tensor_t* cos_sin_cache,
+                              const rope_tensor_t* slot_mapping, const rope_tensor_t* query_out,
+                              const rope_tensor_t* k_cache, const rope_tensor_t* v_cache,
+                              const rope_tensor_t* k_scale, const rope_tensor_t* v_scale, int64_t head_size,
+                              int64_t rotary_dim, int32_t is_neox, const int64_t* mrope_section,
+                              int64_t mrope_section_len, int32_t cache_mode, int64_t query_row_stride,
+                              int64_t key_row_stride, int64_t value_row_stride, void* stream);
+
+/*
+ * rope_paged_attention over a cache of codes (see rope_append_paged_kv_8bit): keys and values are code * 2^(b - 127).
+ *
+ *   All arguments as in rope_paged_attention (query and out F32, F16 or BF16), and
+ *   k_cache, v_cache  ROPE_F8E4M3 [NB, Nk, BS, D].
+ *   k_scale, v_scale  ROPE_E8M0 [NB, Nk, S]; S divides BS.
+ *   workspace_bytes   at least what rope_paged_attention_8bit_workspace says.
+ */
+int rope_paged_attention_8bit(const rope_tensor_t* query, int64_t query_row_stride, const rope_tensor_t* k_cache,
+                              const rope_tensor_t* v_cache, const rope_tensor_t* k_scale,
+                              const rope_tensor_t* v_scale, const rope_tensor_t* block_table,
+                              const rope_tensor_t* seq_lens, const rope_tensor_t* query_start_loc,
+                              const rope_tensor_t* prefix_blocks, int64_t prefix_len, float scale,
+                              const rope_tensor_t* out, const rope_tensor_t* lse, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+int rope_paged_attention_8bit_workspace(int64_t num_tokens, int64_t num_q_heads, int64_t num_k_heads,
+                                        int64_t head_size, int32_t dtype, int64_t prefix_len, int64_t* bytes);
+
+/*
+ * New sequences of old ones: forks (samples, beams), reordering, dropping, and room for what comes.
+ *
+ * Sequence b of the old batch has seq_lens[b] tokens, prefix_len of them in pages that all share and that stay out of
+ * the tables, the others in the pages block_table[b, 0 ...], BS tokens a page.  ref_counts[page] says how many tables'
+ * entries hold a page (and whoever else the program counts, a shared prefix say); 0 is a free page.
+ * Row i of the new batch has the tokens of old row p = parents[i] (p < 0: only the prefix), and room for room[i] more:
+ *   all old rows let go of their pages; a page that nobody then holds is free, with what follows taken into account;
+ *   row i holds the whole pages of p;
+ *   if p's last page is not full, the first row i that asks for it keeps it, provided nobody else holds it; any other
+ *   gets a fresh page, and (that page, the fresh one) is a pair of pages to be copied before the cache is written;
+ *   fresh pages follow until the row has room: free pages are given out lowest first, rows in order.
+ * copy_src and copy_dst receive the pairs in the order of rows, then -1.  counts[0] is their number, counts[1] how many
+ * pages are free then.  new_seq_lens[i] = seq_lens[p] + room[i].  Entries of the new table behind a row's pages are left
+ * as they were.  With rope_copy_pages over every layer's caches the new batch is ready to be written and read.
+ * Where pages run out, the entries are -1 from there on, a pair's copy_dst too, and ROPE_DEVICE_PAGES_EXHAUSTED is
+ * recorded.  A page number outside [0, NB), more tokens than a row's pages hold, and p >= B record
+ * ROPE_DEVICE_SLOT_OUT_OF_RANGE; such pages are passed over, tokens past the table dropped, such a p is none.
+ *
+ *   block_table I64 [B, W], new_block_table I64 [rows, new W]; seq_lens I64 [B]; parents, room (or NULL), new_seq_lens,
+ *   copy_src, copy_dst I64 [rows], rows at most 8192; ref_counts, new_ref_counts I32 [NB], which may be one tensor;
+ *   counts I64 [2].  W * BS, rows * new W and NB at most 2^30.  B and rows may be 0.
+ * What is written shares no memory with any other tensor of the call, new_ref_counts in the place of ref_counts apart.
+ * Whole numbers: results are the same whatever the order in which threads run.
+ */
+int rope_rearrange_sequences(const rope_tensor_t* block_table, const rope_tensor_t* seq_lens,
+                             const rope_tensor_t* ref_counts, const rope_tensor_t* parents, const rope_tensor_t* room,
+                             const rope_tensor_t* new_block_table, const rope_tensor_t* new_seq_lens,
+                             const rope_tensor_t* new_ref_counts, const rope_tensor_t* copy_src,
+                             const rope_tensor_t* copy_dst, const rope_tensor_t* counts, int64_t block_size,
+                             int64_t prefix_len, void* stream);
+
+/*
+ * Live pages to the front: with L pages held (ref_counts > 0), the k-th held page at or behind L goes to the k-th free
+ * page before L, so that pages [L, NB) are free.  copy_src and copy_dst receive the moves, ascending, then -1;
+ * counts[0] is their number, counts[1] is L.  Tables, prefix and counts follow; the pages themselves are moved by
+ * rope_copy_pages.  Table entries behind a row's pages are left as they were.
+ *
+ *   block_table, new_block_table I64 [B, W]; seq_lens I64 [B]; ref_counts, new_ref_counts I32 [NB]; prefix_blocks,
+ *   new_prefix_blocks I64, at least ceil(prefix_len / BS) pages (NULL with prefix_len 0); copy_src, copy_dst I64 [pairs],
+ *   pairs at least NB / 2; counts I64 [2].  Each new tensor may be the old one.  Limits as rope_rearrange_sequences'.
+ * An entry outside [0, NB), or of a page that ref_counts calls free, is copied as it is and records
+ * ROPE_DEVICE_SLOT_OUT_OF_RANGE, as more tokens than a row's pages hold do.
+ */
+int rope_compact_pages(const rope_tensor_t* block_table, const rope_tensor_t* seq_lens,
+                       const rope_tensor_t* ref_counts, const rope_tensor_t* prefix_blocks,
+                       const rope_tensor_t* new_block_table, const rope_tensor_t* new_ref_counts,
+                       const rope_tensor_t* new_prefix_blocks, const rope_tensor_t* copy_src,
+                       const rope_tensor_t* copy_dst, const rope_tensor_t* counts, int64_t block_size,
+                       int64_t prefix_len, void* stream);
+
+/*
+ * Page src[i] of every tensor to its page dst[i], i < count[0] (count NULL: all).  A pair with a negative number is passed
+ * over; one outside [0, NB) too, and records ROPE_DEVICE_SLOT_OUT_OF_RANGE.
+ *
+ *   src, dst I64 [pairs]; count I64, at least one element.  A page that some pair writes is not of another pair of the
+ *   call: where it is, each 16 bytes of it are of one of the states that it has on the way.
+ *   tensors  HOST array of num_tensors descriptors (read before the call returns) of any type and shape whose first
+ *            dimension is NB, the same for all: caches and scales of any number of layers.  No two share memory.
+ */
+int rope_copy_pages(const rope_tensor_t* src, const rope_tensor_t* dst, const rope_tensor_t* count,
+                    const rope_tensor_t* tensors, int64_t num_tensors, void* stream);
 
 /*
  * Takes the device-side error word of the current device (an atomic exchange

@@ -11,7 +11,11 @@ hand-written CUDA kernels for sm_103a:
 * ``rope_frequencies``, ``scaled_cos_sin_cache``, ``scaled_cos_sin`` -- the cos/sin
   tables that the others read, scaled for long contexts;
 * ``append_paged_kv`` -- RoPE of query and key on the way to a paged KV cache;
-* ``paged_attention`` -- attention over that cache, a shared prefix read once for all.
+* ``paged_attention`` -- attention over that cache, a shared prefix read once for all;
+* ``append_paged_kv_8bit``, ``paged_attention_8bit`` -- the two for a cache of 8-bit codes with a
+  scale for each block of tokens and head;
+* ``rearrange_sequences``, ``compact_pages``, ``copy_pages`` -- sequences of a paged cache forked,
+  reordered and dropped, its live pages moved to the front, pages copied in all layers' caches.
 
 PyTorch supplies device memory and streams only.
 """
@@ -36,6 +40,14 @@ from ._capi import (  # noqa: F401
     ROPE_DEVICE_SLOT_OUT_OF_RANGE,
     ROPE_DEVICE_INDEX_OUT_OF_BOUNDS,
     ROPE_DEVICE_WAIT_EXPIRED,
+    ROPE_DEVICE_PAGES_EXHAUSTED,
+    append_paged_kv_8bit,
+    compact_pages,
+    copy_pages,
+    paged_attention_8bit,
+    prepare_append_paged_kv_8bit,
+    prepare_paged_attention_8bit,
+    rearrange_sequences,
     append_paged_kv,
     paged_attention,
     paged_attention_workspace,
@@ -61,6 +73,11 @@ __all__ = [
     "append_paged_kv",
     "paged_attention",
     "paged_attention_workspace",
+    "append_paged_kv_8bit",
+    "paged_attention_8bit",
+    "rearrange_sequences",
+    "compact_pages",
+    "copy_pages",
     "get_device_error",
     "launch_count",
     "status_string",

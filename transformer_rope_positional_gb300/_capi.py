@@ -21,7 +21,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 DEBUG_BOUNDS = os.environ.get("ROPE_GB300_DEBUG_BOUNDS", "0") not in ("", "0")
 LIB_PATH = os.path.join(_HERE, "lib", "librope_gb300_debug.so" if DEBUG_BOUNDS else "librope_gb300.so")
 
-F32, F16, BF16, I64 = 0, 1, 2, 3
+F32, F16, BF16, I64, F8E4M3, E8M0, I32, U8 = 0, 1, 2, 3, 4, 5, 6, 7
 DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.int64: I64}
 
 ROPE_OK = 0
@@ -32,11 +32,14 @@ ROPE_DEVICE_POSITION_OUT_OF_RANGE = 1
 ROPE_DEVICE_SLOT_OUT_OF_RANGE = 2
 ROPE_DEVICE_INDEX_OUT_OF_BOUNDS = 4
 ROPE_DEVICE_WAIT_EXPIRED = 8
+ROPE_DEVICE_PAGES_EXHAUSTED = 16
 
 EXPORTED = ("rope_inplace_partial", "rope_inplace_partial_backward", "rope_with_sin_cos_cache",
             "rope_with_sin_cos_cache_v2", "rope_qkv_rmsnorm_rope_cache", "rope_scaled_frequencies",
             "rope_scaled_cos_sin_cache", "rope_scaled_cos_sin", "rope_append_paged_kv", "rope_paged_attention",
-            "rope_paged_attention_workspace", "rope_get_device_error",
+            "rope_paged_attention_workspace", "rope_append_paged_kv_8bit", "rope_paged_attention_8bit",
+            "rope_paged_attention_8bit_workspace", "rope_rearrange_sequences", "rope_compact_pages", "rope_copy_pages",
+            "rope_get_device_error",
             "rope_status_string", "rope_launch_count", "rope_abi_version")
 
 
@@ -102,6 +105,15 @@ def load() -> ctypes.CDLL:
     lib.rope_paged_attention.restype = ctypes.c_int
     lib.rope_paged_attention_workspace.argtypes = [D, D, D, D, ctypes.c_int32, D, ctypes.POINTER(D)]
     lib.rope_paged_attention_workspace.restype = ctypes.c_int
+    lib.rope_append_paged_kv_8bit.argtypes = [B] * 11 + lib.rope_append_paged_kv.argtypes[9:]
+    lib.rope_paged_attention_8bit.argtypes = [B, D] + [B] * 8 + lib.rope_paged_attention.argtypes[8:]
+    lib.rope_paged_attention_8bit_workspace.argtypes = lib.rope_paged_attention_workspace.argtypes
+    lib.rope_rearrange_sequences.argtypes = [B] * 11 + [D, D, V]
+    lib.rope_compact_pages.argtypes = [B] * 10 + [D, D, V]
+    lib.rope_copy_pages.argtypes = [B, B, B, P, D, V]
+    for name in ("rope_append_paged_kv_8bit", "rope_paged_attention_8bit", "rope_paged_attention_8bit_workspace",
+                 "rope_rearrange_sequences", "rope_compact_pages", "rope_copy_pages"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.rope_get_device_error.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]
     lib.rope_get_device_error.restype = ctypes.c_int
     lib.rope_status_string.argtypes = [ctypes.c_int]
@@ -534,6 +546,107 @@ def prepare_paged_attention(query: torch.Tensor, k_cache: torch.Tensor, v_cache:
     args = (query, k_cache, v_cache, block_table, seq_lens, query_start_loc, prefix_blocks, prefix_len, scale, out,
             lse, workspace, handle)
     return PreparedCall(_load_binding().paged_attention, args, (query,), "rope_paged_attention")
+
+
+def append_paged_kv_8bit(positions: torch.Tensor, query: Optional[torch.Tensor], key: torch.Tensor,
+                         value: torch.Tensor, cos_sin_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                         k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                         head_size: int, rotary_dim: Optional[int] = None, is_neox: bool = True,
+                         mrope_section: Optional[Sequence[int]] = None, stream=None, *, cache_mode: int = 0,
+                         query_out: Optional[torch.Tensor] = None) -> None:
+    """:func:`append_paged_kv` to caches of 8-bit codes (float8_e4m3fn) with a power of two (float8_e8m0fnu
+    [blocks, heads, S]) for each of the S blocks of tokens of a page and head (see the C header).  The tokens of
+    one such block stand one after the other in the call, in the order of their slots."""
+    _issue("append_paged_kv_8bit", (positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache,
+                                    v_cache, k_scale, v_scale, head_size, rotary_dim, is_neox, mrope_section,
+                                    cache_mode), key, stream, "rope_append_paged_kv_8bit")
+
+
+def prepare_append_paged_kv_8bit(positions: torch.Tensor, query: Optional[torch.Tensor], key: torch.Tensor,
+                                 value: torch.Tensor, cos_sin_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                                 k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                                 v_scale: torch.Tensor, head_size: int, rotary_dim: Optional[int] = None,
+                                 is_neox: bool = True, mrope_section: Optional[Sequence[int]] = None, stream=None, *,
+                                 cache_mode: int = 0, query_out: Optional[torch.Tensor] = None) -> "PreparedCall":
+    """:func:`append_paged_kv_8bit` as a call to be issued many times, on the stream of now."""
+    args = (positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache, k_scale, v_scale,
+            head_size, rotary_dim, is_neox, None if mrope_section is None else tuple(mrope_section), cache_mode,
+            _stream_handle(key, stream))
+    return PreparedCall(_load_binding().append_paged_kv_8bit, args, (key,), "rope_append_paged_kv_8bit")
+
+
+def paged_attention_8bit(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                         query_start_loc: torch.Tensor, out: torch.Tensor, *, scale: Optional[float] = None,
+                         prefix_blocks: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """:func:`paged_attention` over caches of 8-bit codes with their scales (see :func:`append_paged_kv_8bit`);
+    :func:`paged_attention_workspace` knows such caches by their type."""
+    if scale is None:
+        scale = _default_scale(k_cache)
+    if workspace is None and stream is not None:
+        _stream_handle(query, stream)  # its device is the tensors'
+        workspace = _workspace_for(query, k_cache, prefix_len, stream)
+    _issue("paged_attention_8bit", (query, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc,
+                                    prefix_blocks, prefix_len, scale, out, lse, workspace), query, stream,
+           "rope_paged_attention_8bit")
+
+
+def prepare_paged_attention_8bit(query: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, query_start_loc: torch.Tensor, out: torch.Tensor, *,
+                                 scale: Optional[float] = None, prefix_blocks: Optional[torch.Tensor] = None,
+                                 prefix_len: int = 0, lse: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None, stream=None) -> "PreparedCall":
+    """:func:`paged_attention_8bit` as a call to be issued many times, on the stream of now, with its workspace
+    (given or allocated here) kept."""
+    handle = _stream_handle(query, stream)
+    if scale is None:
+        scale = _default_scale(k_cache)
+    if workspace is None:
+        workspace = _workspace_for(query, k_cache, prefix_len, stream)
+    args = (query, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, prefix_blocks,
+            prefix_len, scale, out, lse, workspace, handle)
+    return PreparedCall(_load_binding().paged_attention_8bit, args, (query,), "rope_paged_attention_8bit")
+
+
+def rearrange_sequences(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
+                        parents: torch.Tensor, new_block_table: torch.Tensor, new_seq_lens: torch.Tensor,
+                        new_ref_counts: torch.Tensor, copy_src: torch.Tensor, copy_dst: torch.Tensor,
+                        counts: torch.Tensor, block_size: int, *, room: Optional[torch.Tensor] = None,
+                        prefix_len: int = 0, stream=None) -> None:
+    """A new batch of the old one's sequences: row i continues old row ``parents[i]`` (-1: starts empty), with room
+    for ``room[i]`` more tokens.  A parent of several rows is forked, one of none is dropped.
+
+    Whole pages are shared (``ref_counts`` [blocks], int32, counts the holders of each; ``new_ref_counts`` may be the
+    same tensor); a page that is written on is kept by one row and copied for the others: (``copy_src``, ``copy_dst``)
+    [rows] name the pages that :func:`copy_pages` has to copy then, ``counts`` [2] how many pairs there are and how
+    many pages are left free.  Free pages are given out lowest first (see the C header)."""
+    _issue("rearrange_sequences", (block_table, seq_lens, ref_counts, parents, room, new_block_table, new_seq_lens,
+                                   new_ref_counts, copy_src, copy_dst, counts, block_size, prefix_len), block_table,
+           stream, "rope_rearrange_sequences")
+
+
+def compact_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
+                  new_block_table: torch.Tensor, new_ref_counts: torch.Tensor, copy_src: torch.Tensor,
+                  copy_dst: torch.Tensor, counts: torch.Tensor, block_size: int, *,
+                  prefix_blocks: Optional[torch.Tensor] = None, new_prefix_blocks: Optional[torch.Tensor] = None,
+                  prefix_len: int = 0, stream=None) -> None:
+    """Tables, counts and prefix for a cache whose live pages are moved to the front, and in ``copy_src`` and
+    ``copy_dst`` (at least blocks / 2 elements) the pages that :func:`copy_pages` has to move for it; ``counts`` [2]
+    receives their number and that of live pages.  Each new tensor may be the old one."""
+    _issue("compact_pages", (block_table, seq_lens, ref_counts, prefix_blocks, new_block_table, new_ref_counts,
+                             new_prefix_blocks, copy_src, copy_dst, counts, block_size, prefix_len), block_table, stream,
+           "rope_compact_pages")
+
+
+def copy_pages(src: torch.Tensor, dst: torch.Tensor, tensors: Sequence[torch.Tensor], *,
+               count: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Page ``src[i]`` of every tensor (caches and scales of any layers, of any type, pages first) to its page
+    ``dst[i]``, for the first ``count[0]`` pairs or all; pairs with a negative number are passed over."""
+    _issue("copy_pages", (src, dst, count, tensors if isinstance(tensors, (list, tuple)) else list(tensors)), src,
+           stream, "rope_copy_pages")
 
 
 def get_device_error(stream=None, device=None) -> int:

@@ -7,8 +7,11 @@
 // RopeWithSinCosCache 深度解析…", sections 约束说明 and 入参校验逻辑).  Every check
 // runs on the host before anything is enqueued, and no check touches the GPU,
 // so a rejected call has no side effect at all.
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <new>
+#include <vector>
 
 #include "rope_gb300.h"
 #include "rope_launch.h"
@@ -59,7 +62,21 @@ int64_t strided_extent(int64_t rows, int64_t stride, int64_t width) {
 
 bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-int64_t elem_size(int32_t dt) { return dt == kF32 ? 4 : dt == kI64 ? 8 : 2; }
+int64_t elem_size(int32_t dt) {
+  switch (dt) {
+    case kI64:
+      return 8;
+    case kF32:
+    case rope::kI32:
+      return 4;
+    case rope::kE4M3:
+    case rope::kE8M0:
+    case rope::kU8:
+      return 1;
+    default:
+      return 2;
+  }
+}
 
 // Whether two sets of `rows` rows share a byte: set a starts at byte address
 // a, its rows are aw bytes wide and as bytes apart (likewise b).  Sets whose
@@ -469,25 +486,35 @@ Range whole_range(const rope_tensor_t* t) {
 
 bool meet(const Range& x, const Range& y) { return ranges_overlap(x.at, x.bytes, y.at, y.bytes); }
 
-// Checks of the append call, then the launch.
+// Scales of caches of codes: [NB, heads, S], S scale blocks of equal size a page, the same S for K and V.
+bool scales_ok(const rope_tensor_t* cache, const rope_tensor_t* scale) {
+  return scale->dtype == rope::kE8M0 && scale->ndim == 3 && scale->shape[0] == cache->shape[0] &&
+         scale->shape[1] == cache->shape[1] && scale->shape[2] >= 1 && scale->shape[2] <= cache->shape[2] &&
+         cache->shape[2] % scale->shape[2] == 0;
+}
+
+// Checks of the append call, then the launch.  `coded`: the caches hold codes, with scales.
 int append_call(const rope_tensor_t* positions, const rope_tensor_t* query, const rope_tensor_t* key,
                 const rope_tensor_t* value, const rope_tensor_t* table, const rope_tensor_t* slots,
-                const rope_tensor_t* query_out, const rope_tensor_t* k_cache, const rope_tensor_t* v_cache, int64_t D,
-                int64_t R, int32_t is_neox, const int64_t* section, int64_t section_len, int32_t cache_mode,
+                const rope_tensor_t* query_out, const rope_tensor_t* k_cache, const rope_tensor_t* v_cache, bool coded,
+                const rope_tensor_t* k_scale, const rope_tensor_t* v_scale, int64_t D, int64_t R, int32_t is_neox, const int64_t* section, int64_t section_len, int32_t cache_mode,
                 int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride, void* stream) {
   for (const rope_tensor_t* t : {positions, key, value, table, slots, k_cache, v_cache})
     if (!t) return ROPE_ERR_PARAM_NULLPTR;
-  if (query_out && !query) return ROPE_ERR_PARAM_NULLPTR;
-  for (const rope_tensor_t* t : {positions, query, key, value, table, slots, query_out, k_cache, v_cache})
+  if ((query_out && !query) || (coded && !(k_scale && v_scale))) return ROPE_ERR_PARAM_NULLPTR;
+  for (const rope_tensor_t* t :
+       {positions, query, key, value, table, slots, query_out, k_cache, v_cache, k_scale, v_scale})
     if (t && !shape_ok(t)) return ROPE_ERR_PARAM_INVALID;
   const int32_t dt = key->dtype;
   if (!is_float(dt) || (table->dtype != dt && table->dtype != kF32)) return ROPE_ERR_PARAM_INVALID;
-  for (const rope_tensor_t* t : {query, value, query_out, k_cache, v_cache})
+  for (const rope_tensor_t* t : {query, value, query_out})
     if (t && t->dtype != dt) return ROPE_ERR_PARAM_INVALID;
+  for (const rope_tensor_t* t : {k_cache, v_cache})
+    if (t->dtype != (coded ? (int32_t)rope::kE4M3 : dt)) return ROPE_ERR_PARAM_INVALID;
   if (positions->dtype != kI64 || slots->dtype != kI64 || slots->ndim != 1) return ROPE_ERR_PARAM_INVALID;
   // head size and rotary dim: 64-byte multiples; a head's row groups fit a block
   const int64_t mult = dt == kF32 ? 16 : 32;
-  if (D <= 0 || D % mult || D > (dt == kF32 ? 1024 : 2048)) return ROPE_ERR_PARAM_INVALID;
+  if (D <= 0 || D % mult || D > (coded ? 512 : dt == kF32 ? 1024 : 2048)) return ROPE_ERR_PARAM_INVALID;
   if (R <= 0 || R % mult || R > D) return ROPE_ERR_PARAM_INVALID;
   if (table->ndim != 2 || table->shape[0] < 1 || table->shape[1] != R) return ROPE_ERR_PARAM_INVALID;
   bool mrope = false;
@@ -520,8 +547,11 @@ int append_call(const rope_tensor_t* positions, const rope_tensor_t* query, cons
       v_cache->shape[1] != hv || v_cache->shape[2] != BS || v_cache->shape[3] != D)
     return ROPE_ERR_PARAM_INVALID;
   if (hq + hk + hv > (int64_t(1) << 30) || BS > (int64_t(1) << 30)) return ROPE_ERR_PARAM_INVALID;
+  if (coded && !(scales_ok(k_cache, k_scale) && scales_ok(v_cache, v_scale) && k_scale->shape[2] == v_scale->shape[2]))
+    return ROPE_ERR_PARAM_INVALID;
   if (T == 0) return ROPE_OK;
-  for (const rope_tensor_t* t : {positions, query, key, value, table, slots, query_out, k_cache, v_cache})
+  for (const rope_tensor_t* t :
+       {positions, query, key, value, table, slots, query_out, k_cache, v_cache, k_scale, v_scale})
     if (t && !t->data) return ROPE_ERR_PARAM_NULLPTR;
   for (const rope_tensor_t* t : {query, key, value, table, query_out, k_cache, v_cache})
     if (t && !aligned(t->data, 16)) return ROPE_ERR_PARAM_INVALID;
@@ -530,14 +560,19 @@ int append_call(const rope_tensor_t* positions, const rope_tensor_t* query, cons
   const bool in_place = query && (!query_out || (query_out->data == query->data && strides[0] == query->shape[1]));
   const Range kr = rows_range(key, strides[1]), vr = rows_range(value, strides[2]);
   const Range read[] = {whole_range(positions), whole_range(table), whole_range(slots)};
-  const Range caches[] = {whole_range(k_cache), whole_range(v_cache)};
+  const Range none = {0, 0};
+  const Range caches[] = {whole_range(k_cache), whole_range(v_cache), coded ? whole_range(k_scale) : none,
+                          coded ? whole_range(v_scale) : none};
   const Range qr = query ? rows_range(query, strides[0]) : Range{0, 0};
   const Range qo = !query ? Range{0, 0} : in_place ? qr : whole_range(query_out);
   for (const Range& r : read)
-    if (meet(qo, r) || meet(caches[0], r) || meet(caches[1], r)) return ROPE_ERR_PARAM_INVALID;
-  for (const Range& r : {kr, vr, qr, qo})
-    if (meet(caches[0], r) || meet(caches[1], r)) return ROPE_ERR_PARAM_INVALID;
-  if (meet(caches[0], caches[1])) return ROPE_ERR_PARAM_INVALID;
+    if (meet(qo, r)) return ROPE_ERR_PARAM_INVALID;
+  for (int i = 0; i < 4; ++i) {
+    for (const Range& r : {read[0], read[1], read[2], kr, vr, qr, qo})
+      if (meet(caches[i], r)) return ROPE_ERR_PARAM_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (meet(caches[i], caches[j])) return ROPE_ERR_PARAM_INVALID;
+  }
   if (query) {
     const int64_t e = elem_size(dt);
     if (in_place) {
@@ -578,7 +613,11 @@ int append_call(const rope_tensor_t* positions, const rope_tensor_t* query, cons
   p.q_stride = query ? strides[0] : 0;
   p.k_stride = strides[1];
   p.v_stride = strides[2];
-  return cuda_status(rope::launch_append(p, static_cast<cudaStream_t>(stream)));
+  if (!coded) return cuda_status(rope::launch_append(p, static_cast<cudaStream_t>(stream)));
+  p.k_scale = static_cast<uint8_t*>(k_scale->data);
+  p.v_scale = static_cast<uint8_t*>(v_scale->data);
+  p.scale_blocks = k_scale->shape[2];
+  return cuda_status(rope::launch_append_codes(p, static_cast<cudaStream_t>(stream)));
 }
 
 // Head counts, head size and row count that the attention takes (rows bounded so that the
@@ -589,20 +628,24 @@ bool attend_sizes_ok(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dt) {
          T <= (int64_t(1) << 31) && T * nq < (int64_t(1) << 31) - 512 && D >= mult && D % mult == 0 && D <= 512;
 }
 
-// Checks of the attention call, then the launch.
+// Checks of the attention call, then the launch.  `coded`: the caches hold codes, with scales.
 int attend_call(const rope_tensor_t* query, int64_t q_row_stride, const rope_tensor_t* k_cache,
-                const rope_tensor_t* v_cache, const rope_tensor_t* block_table, const rope_tensor_t* seq_lens,
-                const rope_tensor_t* qsl, const rope_tensor_t* prefix_blocks, int64_t P, float scale,
+                const rope_tensor_t* v_cache, bool coded, const rope_tensor_t* k_scale, const rope_tensor_t* v_scale,
+                const rope_tensor_t* block_table, const rope_tensor_t* seq_lens, const rope_tensor_t* qsl,
+                const rope_tensor_t* prefix_blocks, int64_t P, float scale,
                 const rope_tensor_t* out, const rope_tensor_t* lse, void* workspace, int64_t workspace_bytes,
                 void* stream) {
   for (const rope_tensor_t* t : {query, k_cache, v_cache, block_table, seq_lens, qsl, out})
     if (!t) return ROPE_ERR_PARAM_NULLPTR;
-  for (const rope_tensor_t* t : {query, k_cache, v_cache, block_table, seq_lens, qsl, prefix_blocks, out, lse})
+  if (coded && !(k_scale && v_scale)) return ROPE_ERR_PARAM_NULLPTR;
+  for (const rope_tensor_t* t :
+       {query, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, qsl, prefix_blocks, out, lse})
     if (t && !shape_ok(t)) return ROPE_ERR_PARAM_INVALID;
   const int32_t dt = query->dtype;
   if (!is_float(dt)) return ROPE_ERR_PARAM_INVALID;
-  for (const rope_tensor_t* t : {k_cache, v_cache, out})
-    if (t->dtype != dt) return ROPE_ERR_PARAM_INVALID;
+  if (out->dtype != dt) return ROPE_ERR_PARAM_INVALID;
+  for (const rope_tensor_t* t : {k_cache, v_cache})
+    if (t->dtype != (coded ? (int32_t)rope::kE4M3 : dt)) return ROPE_ERR_PARAM_INVALID;
   for (const rope_tensor_t* t : {block_table, seq_lens, qsl, prefix_blocks})
     if (t && t->dtype != kI64) return ROPE_ERR_PARAM_INVALID;
   if (lse && lse->dtype != kF32) return ROPE_ERR_PARAM_INVALID;
@@ -610,6 +653,8 @@ int attend_call(const rope_tensor_t* query, int64_t q_row_stride, const rope_ten
   if (k_cache->ndim != 4 || v_cache->ndim != 4) return ROPE_ERR_PARAM_INVALID;
   for (int i = 0; i < 4; ++i)
     if (k_cache->shape[i] != v_cache->shape[i] || k_cache->shape[i] < 1) return ROPE_ERR_PARAM_INVALID;
+  if (coded && !(scales_ok(k_cache, k_scale) && scales_ok(v_cache, v_scale) && k_scale->shape[2] == v_scale->shape[2]))
+    return ROPE_ERR_PARAM_INVALID;
   const int64_t NB = k_cache->shape[0], nk = k_cache->shape[1], BS = k_cache->shape[2], D = k_cache->shape[3];
   if (query->ndim != 2 || query->shape[1] < 1 || query->shape[1] % D) return ROPE_ERR_PARAM_INVALID;
   const int64_t T = query->shape[0], nq = query->shape[1] / D;
@@ -633,8 +678,10 @@ int attend_call(const rope_tensor_t* query, int64_t q_row_stride, const rope_ten
   if (lse && (lse->ndim != 2 || lse->shape[0] != T || lse->shape[1] != nq)) return ROPE_ERR_PARAM_INVALID;
   if (T == 0) return ROPE_OK;
   if (!workspace) return ROPE_ERR_PARAM_NULLPTR;
-  if (workspace_bytes < rope::attend_workspace(T, nq, nk, D, dt, P)) return ROPE_ERR_PARAM_INVALID;
-  for (const rope_tensor_t* t : {query, k_cache, v_cache, block_table, seq_lens, qsl, out, lse})
+  if (workspace_bytes < (coded ? rope::attend_codes_workspace(T, nq, nk, D, dt, P)
+                               : rope::attend_workspace(T, nq, nk, D, dt, P)))
+    return ROPE_ERR_PARAM_INVALID;
+  for (const rope_tensor_t* t : {query, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, qsl, out, lse})
     if (t && !t->data) return ROPE_ERR_PARAM_NULLPTR;
   if (P > 0 && !prefix_blocks->data) return ROPE_ERR_PARAM_NULLPTR;
   for (const rope_tensor_t* t : {query, k_cache, v_cache, out})
@@ -649,7 +696,8 @@ int attend_call(const rope_tensor_t* query, int64_t q_row_stride, const rope_ten
                            {reinterpret_cast<uintptr_t>(workspace), workspace_bytes}};
   const Range read[] = {rows_range(query, q_row_stride), whole_range(k_cache), whole_range(v_cache),
                         whole_range(block_table), whole_range(seq_lens), whole_range(qsl),
-                        P > 0 ? whole_range(prefix_blocks) : none};
+                        P > 0 ? whole_range(prefix_blocks) : none, coded ? whole_range(k_scale) : none,
+                        coded ? whole_range(v_scale) : none};
   for (int i = 0; i < 3; ++i) {
     for (const Range& r : read)
       if (meet(written[i], r)) return ROPE_ERR_PARAM_INVALID;
@@ -680,7 +728,185 @@ int attend_call(const rope_tensor_t* query, int64_t q_row_stride, const rope_ten
   p.W = W;
   p.prefix_len = P;
   p.scale = scale;
-  return cuda_status(rope::launch_attend(p, static_cast<cudaStream_t>(stream)));
+  if (!coded) return cuda_status(rope::launch_attend(p, static_cast<cudaStream_t>(stream)));
+  p.k_scale = static_cast<const uint8_t*>(k_scale->data);
+  p.v_scale = static_cast<const uint8_t*>(v_scale->data);
+  p.scale_blocks = k_scale->shape[2];
+  return cuda_status(rope::launch_attend_codes(p, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t* i64_data(const rope_tensor_t* t) { return t ? static_cast<int64_t*>(t->data) : nullptr; }
+int32_t* i32_data(const rope_tensor_t* t) { return t ? static_cast<int32_t*>(t->data) : nullptr; }
+
+constexpr int64_t kMostPages = int64_t(1) << 30;
+
+// What the calls on page tables have in common: int64 tensors but for the counts, of one dimension but for the
+// tables, non-NULL and aligned.  Tensors that may be NULL are left out where they are.
+int page_tensors_ok(std::initializer_list<const rope_tensor_t*> tables, std::initializer_list<const rope_tensor_t*> lists,
+                    std::initializer_list<const rope_tensor_t*> refs) {
+  for (const auto& group : {tables, lists, refs})
+    for (const rope_tensor_t* t : group)
+      if (!t) return ROPE_ERR_PARAM_NULLPTR;
+  for (const rope_tensor_t* t : tables)
+    if (!shape_ok(t) || t->dtype != kI64 || t->ndim != 2) return ROPE_ERR_PARAM_INVALID;
+  for (const rope_tensor_t* t : lists)
+    if (!shape_ok(t) || t->dtype != kI64 || t->ndim != 1) return ROPE_ERR_PARAM_INVALID;
+  for (const rope_tensor_t* t : refs)
+    if (!shape_ok(t) || t->dtype != rope::kI32 || t->ndim != 1) return ROPE_ERR_PARAM_INVALID;
+  for (const auto& group : {tables, lists, refs})
+    for (const rope_tensor_t* t : group) {
+      if (numel(t) > 0 && !t->data) return ROPE_ERR_PARAM_NULLPTR;
+      if (!aligned(t->data, (uintptr_t)elem_size(t->dtype))) return ROPE_ERR_PARAM_INVALID;
+    }
+  return ROPE_OK;
+}
+
+// Whether a tensor that is written meets any other: `written` and `read` hold each tensor once, NULL for one that
+// is not there or that is the same as one of the others.
+bool any_meet(std::initializer_list<const rope_tensor_t*> written, std::initializer_list<const rope_tensor_t*> read) {
+  for (const rope_tensor_t* w : written) {
+    if (!w) continue;
+    for (const rope_tensor_t* r : read)
+      if (r && tensors_overlap(w, r)) return true;
+    for (const rope_tensor_t* o : written) {
+      if (o == w) break;
+      if (o && tensors_overlap(w, o)) return true;
+    }
+  }
+  return false;
+}
+
+// `to` in the place of `from`: one tensor, which is read and then written.
+bool in_place(const rope_tensor_t* from, const rope_tensor_t* to) {
+  return from && to && from->data == to->data && numel(from) == numel(to);
+}
+
+int rearrange_call(const rope_tensor_t* table, const rope_tensor_t* lens, const rope_tensor_t* refs,
+                   const rope_tensor_t* parents, const rope_tensor_t* room, const rope_tensor_t* new_table,
+                   const rope_tensor_t* new_lens, const rope_tensor_t* new_refs, const rope_tensor_t* src,
+                   const rope_tensor_t* dst, const rope_tensor_t* counts, int64_t bs, int64_t P, void* stream) {
+  int st = page_tensors_ok({table, new_table}, {lens, parents, new_lens, src, dst, counts}, {refs, new_refs});
+  if (st == ROPE_OK && room) st = page_tensors_ok({}, {room}, {});
+  if (st != ROPE_OK) return st;
+  const int64_t B = lens->shape[0], rows = parents->shape[0], NB = refs->shape[0];
+  const int64_t W = table->shape[1], new_W = new_table->shape[1];
+  if (table->shape[0] != B || new_table->shape[0] != rows || new_lens->shape[0] != rows || src->shape[0] != rows ||
+      dst->shape[0] != rows || (room && room->shape[0] != rows) || new_refs->shape[0] != NB || counts->shape[0] != 2)
+    return ROPE_ERR_PARAM_INVALID;
+  if (bs < 1 || bs > kMostPages || P < 0 || P > kMostPages || NB < 1 || NB > kMostPages) return ROPE_ERR_PARAM_INVALID;
+  if (B > kMostPages || rows > rope::kMostRearranged || W > kMostPages / bs || new_W > kMostPages / bs ||
+      rows * new_W > kMostPages)
+    return ROPE_ERR_PARAM_INVALID;
+  const rope_tensor_t* const refs_read = in_place(refs, new_refs) ? nullptr : refs;
+  if (any_meet({new_table, new_lens, new_refs, src, dst, counts}, {table, lens, refs_read, parents, room}))
+    return ROPE_ERR_PARAM_INVALID;
+  rope::RearrangeProblem p;
+  p.table = i64_data(table);
+  p.lens = i64_data(lens);
+  p.refs = i32_data(refs);
+  p.parents = i64_data(parents);
+  p.room = i64_data(room);
+  p.new_table = i64_data(new_table);
+  p.new_lens = i64_data(new_lens);
+  p.new_refs = i32_data(new_refs);
+  p.src = i64_data(src);
+  p.dst = i64_data(dst);
+  p.counts = i64_data(counts);
+  p.B = B;
+  p.W = W;
+  p.rows = rows;
+  p.new_W = new_W;
+  p.NB = NB;
+  p.block_size = bs;
+  p.prefix_len = P;
+  return cuda_status(rope::launch_rearrange(p, static_cast<cudaStream_t>(stream)));
+}
+
+int compact_call(const rope_tensor_t* table, const rope_tensor_t* lens, const rope_tensor_t* refs,
+                 const rope_tensor_t* prefix, const rope_tensor_t* new_table, const rope_tensor_t* new_refs,
+                 const rope_tensor_t* new_prefix, const rope_tensor_t* src, const rope_tensor_t* dst,
+                 const rope_tensor_t* counts, int64_t bs, int64_t P, void* stream) {
+  int st = page_tensors_ok({table, new_table}, {lens, src, dst, counts}, {refs, new_refs});
+  if (st == ROPE_OK && P > 0) st = page_tensors_ok({}, {prefix, new_prefix}, {});
+  if (st != ROPE_OK) return st;
+  const int64_t B = lens->shape[0], NB = refs->shape[0], W = table->shape[1];
+  if (table->shape[0] != B || new_table->shape[0] != B || new_table->shape[1] != W || new_refs->shape[0] != NB ||
+      src->shape[0] != dst->shape[0] || src->shape[0] < NB / 2 || counts->shape[0] != 2)
+    return ROPE_ERR_PARAM_INVALID;
+  if (bs < 1 || bs > kMostPages || P < 0 || P > kMostPages || NB < 1 || NB > kMostPages || B > kMostPages ||
+      W > kMostPages / bs)
+    return ROPE_ERR_PARAM_INVALID;
+  const int64_t pages = (P + bs - 1) / bs;
+  if (P > 0 && (prefix->shape[0] < pages || new_prefix->shape[0] < pages)) return ROPE_ERR_PARAM_INVALID;
+  if (P == 0) prefix = new_prefix = nullptr;
+  if (any_meet({new_table, new_refs, new_prefix, src, dst, counts},
+               {in_place(table, new_table) ? nullptr : table, lens, in_place(refs, new_refs) ? nullptr : refs,
+                in_place(prefix, new_prefix) ? nullptr : prefix}))
+    return ROPE_ERR_PARAM_INVALID;
+  rope::CompactProblem p;
+  p.table = i64_data(table);
+  p.lens = i64_data(lens);
+  p.refs = i32_data(refs);
+  p.new_table = i64_data(new_table);
+  p.new_refs = i32_data(new_refs);
+  p.prefix = i64_data(prefix);
+  p.new_prefix = i64_data(new_prefix);
+  p.src = i64_data(src);
+  p.dst = i64_data(dst);
+  p.counts = i64_data(counts);
+  p.B = B;
+  p.W = W;
+  p.NB = NB;
+  p.block_size = bs;
+  p.prefix_len = P;
+  p.pairs = src->shape[0];
+  return cuda_status(rope::launch_compact(p, static_cast<cudaStream_t>(stream)));
+}
+
+int copy_pages_call(const rope_tensor_t* src, const rope_tensor_t* dst, const rope_tensor_t* count,
+                    const rope_tensor_t* tensors, int64_t n, void* stream) {
+  int st = page_tensors_ok({}, {src, dst}, {});
+  if (st == ROPE_OK && count) st = page_tensors_ok({}, {count}, {});
+  if (st != ROPE_OK) return st;
+  if (src->shape[0] != dst->shape[0] || src->shape[0] > kMostPages || (count && count->shape[0] < 1))
+    return ROPE_ERR_PARAM_INVALID;
+  if (n < 0 || n > (1 << 16)) return ROPE_ERR_PARAM_INVALID;
+  if (n > 0 && !tensors) return ROPE_ERR_PARAM_NULLPTR;
+  std::vector<rope::CopyTensor> list;
+  std::vector<Range> ranges;
+  int64_t pieces = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const rope_tensor_t* t = tensors + i;
+    if (t->dtype < kF32 || t->dtype > rope::kU8 || !shape_ok(t) || t->shape[0] != tensors[0].shape[0] ||
+        t->shape[0] < 1 || t->shape[0] > kMostPages)
+      return ROPE_ERR_PARAM_INVALID;
+    const int64_t e = elem_size(t->dtype), bytes = numel(t) / t->shape[0] * e;
+    if (bytes == 0) continue;
+    if (!t->data) return ROPE_ERR_PARAM_NULLPTR;
+    pieces += bytes / 4096 + 1;
+    if (!aligned(t->data, (uintptr_t)e) || bytes > (int64_t(1) << 40) || pieces > kMostPages)
+      return ROPE_ERR_PARAM_INVALID;
+    list.push_back({static_cast<char*>(t->data), bytes});
+    ranges.push_back(whole_range(t));
+  }
+  // tensors that share memory would be copied within each other
+  for (const rope_tensor_t* t : {src, dst, count})
+    if (t)
+      for (const Range& r : ranges)
+        if (meet(r, whole_range(t))) return ROPE_ERR_PARAM_INVALID;
+  std::sort(ranges.begin(), ranges.end(), [](const Range& x, const Range& y) { return x.at < y.at; });
+  for (size_t i = 1; i < ranges.size(); ++i)
+    if (meet(ranges[i - 1], ranges[i])) return ROPE_ERR_PARAM_INVALID;
+  if (src->shape[0] == 0 || list.empty()) return ROPE_OK;
+  rope::CopyProblem p;
+  p.src = i64_data(src);
+  p.dst = i64_data(dst);
+  p.count = i64_data(count);
+  p.pairs = src->shape[0];
+  p.NB = tensors[0].shape[0];
+  p.tensors = list.data();
+  p.num_tensors = (int64_t)list.size();
+  return cuda_status(rope::launch_copy_pages(p, static_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -751,8 +977,8 @@ int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* qu
                          int64_t rotary_dim, int32_t is_neox, const int64_t* mrope_section,
                          int64_t mrope_section_len, int32_t cache_mode, int64_t query_row_stride,
                          int64_t key_row_stride, int64_t value_row_stride, void* stream) {
-  return append_call(positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache, head_size,
-                     rotary_dim, is_neox, mrope_section, mrope_section_len, cache_mode, query_row_stride,
+  return append_call(positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache, false,
+                     nullptr, nullptr, head_size, rotary_dim, is_neox, mrope_section, mrope_section_len, cache_mode, query_row_stride,
                      key_row_stride, value_row_stride, stream);
 }
 
@@ -762,7 +988,7 @@ int rope_paged_attention(const rope_tensor_t* query, int64_t query_row_stride, c
                          const rope_tensor_t* prefix_blocks, int64_t prefix_len, float scale,
                          const rope_tensor_t* out, const rope_tensor_t* lse, void* workspace,
                          int64_t workspace_bytes, void* stream) {
-  return attend_call(query, query_row_stride, k_cache, v_cache, block_table, seq_lens, query_start_loc, prefix_blocks,
+  return attend_call(query, query_row_stride, k_cache, v_cache, false, nullptr, nullptr, block_table, seq_lens, query_start_loc, prefix_blocks,
                      prefix_len, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
@@ -773,6 +999,68 @@ int rope_paged_attention_workspace(int64_t num_tokens, int64_t num_q_heads, int6
     return ROPE_ERR_PARAM_INVALID;
   *bytes = rope::attend_workspace(num_tokens, num_q_heads, num_k_heads, head_size, dtype, prefix_len);
   return ROPE_OK;
+}
+
+int rope_append_paged_kv_8bit(const rope_tensor_t* positions, const rope_tensor_t* query, const rope_tensor_t* key,
+                              const rope_tensor_t* value, const rope_tensor_t* cos_sin_cache,
+                              const rope_tensor_t* slot_mapping, const rope_tensor_t* query_out,
+                              const rope_tensor_t* k_cache, const rope_tensor_t* v_cache,
+                              const rope_tensor_t* k_scale, const rope_tensor_t* v_scale, int64_t head_size,
+                              int64_t rotary_dim, int32_t is_neox, const int64_t* mrope_section,
+                              int64_t mrope_section_len, int32_t cache_mode, int64_t query_row_stride,
+                              int64_t key_row_stride, int64_t value_row_stride, void* stream) {
+  return append_call(positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache, true,
+                     k_scale, v_scale, head_size, rotary_dim, is_neox, mrope_section, mrope_section_len, cache_mode,
+                     query_row_stride, key_row_stride, value_row_stride, stream);
+}
+
+int rope_paged_attention_8bit(const rope_tensor_t* query, int64_t query_row_stride, const rope_tensor_t* k_cache,
+                              const rope_tensor_t* v_cache, const rope_tensor_t* k_scale,
+                              const rope_tensor_t* v_scale, const rope_tensor_t* block_table,
+                              const rope_tensor_t* seq_lens, const rope_tensor_t* query_start_loc,
+                              const rope_tensor_t* prefix_blocks, int64_t prefix_len, float scale,
+                              const rope_tensor_t* out, const rope_tensor_t* lse, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  return attend_call(query, query_row_stride, k_cache, v_cache, true, k_scale, v_scale, block_table, seq_lens,
+                     query_start_loc, prefix_blocks, prefix_len, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int rope_paged_attention_8bit_workspace(int64_t num_tokens, int64_t num_q_heads, int64_t num_k_heads,
+                                        int64_t head_size, int32_t dtype, int64_t prefix_len, int64_t* bytes) {
+  if (!bytes) return ROPE_ERR_PARAM_NULLPTR;
+  if (prefix_len < 0 || !attend_sizes_ok(num_tokens, num_q_heads, num_k_heads, head_size, dtype))
+    return ROPE_ERR_PARAM_INVALID;
+  *bytes = rope::attend_codes_workspace(num_tokens, num_q_heads, num_k_heads, head_size, dtype, prefix_len);
+  return ROPE_OK;
+}
+
+int rope_rearrange_sequences(const rope_tensor_t* block_table, const rope_tensor_t* seq_lens,
+                             const rope_tensor_t* ref_counts, const rope_tensor_t* parents, const rope_tensor_t* room,
+                             const rope_tensor_t* new_block_table, const rope_tensor_t* new_seq_lens,
+                             const rope_tensor_t* new_ref_counts, const rope_tensor_t* copy_src,
+                             const rope_tensor_t* copy_dst, const rope_tensor_t* counts, int64_t block_size,
+                             int64_t prefix_len, void* stream) {
+  return rearrange_call(block_table, seq_lens, ref_counts, parents, room, new_block_table, new_seq_lens,
+                        new_ref_counts, copy_src, copy_dst, counts, block_size, prefix_len, stream);
+}
+
+int rope_compact_pages(const rope_tensor_t* block_table, const rope_tensor_t* seq_lens,
+                       const rope_tensor_t* ref_counts, const rope_tensor_t* prefix_blocks,
+                       const rope_tensor_t* new_block_table, const rope_tensor_t* new_ref_counts,
+                       const rope_tensor_t* new_prefix_blocks, const rope_tensor_t* copy_src,
+                       const rope_tensor_t* copy_dst, const rope_tensor_t* counts, int64_t block_size,
+                       int64_t prefix_len, void* stream) {
+  return compact_call(block_table, seq_lens, ref_counts, prefix_blocks, new_block_table, new_ref_counts,
+                      new_prefix_blocks, copy_src, copy_dst, counts, block_size, prefix_len, stream);
+}
+
+int rope_copy_pages(const rope_tensor_t* src, const rope_tensor_t* dst, const rope_tensor_t* count,
+                    const rope_tensor_t* tensors, int64_t num_tensors, void* stream) {
+  try {
+    return copy_pages_call(src, dst, count, tensors, num_tensors, stream);
+  } catch (const std::bad_alloc&) {
+    return ROPE_ERR_CUDA;
+  }
 }
 
 int rope_get_device_error(void* stream, int32_t* code) {

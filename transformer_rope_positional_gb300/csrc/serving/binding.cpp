@@ -13,6 +13,8 @@
 
 #include <ATen/ops/empty.h>
 
+#include <vector>
+
 #include "rope_gb300.h"
 
 namespace {
@@ -23,6 +25,12 @@ decltype(&rope_scaled_cos_sin) g_cos_sin;
 decltype(&rope_append_paged_kv) g_append;
 decltype(&rope_paged_attention) g_attend;
 decltype(&rope_paged_attention_workspace) g_workspace;
+decltype(&rope_append_paged_kv_8bit) g_append_8bit;
+decltype(&rope_paged_attention_8bit) g_attend_8bit;
+decltype(&rope_paged_attention_8bit_workspace) g_workspace_8bit;
+decltype(&rope_rearrange_sequences) g_rearrange;
+decltype(&rope_compact_pages) g_compact;
+decltype(&rope_copy_pages) g_copy_pages;
 
 struct Failed {};  // a Python error is set
 
@@ -46,6 +54,12 @@ int32_t type_of(const at::Tensor& t) {
       return ROPE_BF16;
     case at::kLong:
       return ROPE_I64;
+    case at::kFloat8_e4m3fn:
+      return ROPE_F8E4M3;
+    case at::kFloat8_e8m0fnu:
+      return ROPE_E8M0;
+    case at::kInt:
+      return ROPE_I32;
     default:
       fail(PyExc_ValueError, "unsupported dtype");
   }
@@ -64,6 +78,21 @@ class Call {
     return add(t, use);
   }
 
+  // Pages of a tensor of any type and number of dimensions, as bytes.
+  rope_tensor_t pages(PyObject* o) {
+    const at::Tensor& t = tensor(o);
+    if (!t.is_contiguous()) fail(PyExc_ValueError, "expected a contiguous tensor");
+    check(t);
+    if (t.dim() < 1) fail(PyExc_ValueError, "expected a tensor with a dimension of pages");
+    rope_tensor_t d;
+    d.data = t.mutable_data_ptr();
+    d.dtype = ROPE_U8;
+    d.ndim = 2;
+    d.shape[0] = t.size(0);
+    d.shape[1] = t.size(0) ? (int64_t)t.nbytes() / t.size(0) : 0;
+    return d;
+  }
+
   // Rows of a 2-D tensor that may be strided; rows must not overlap.
   const rope_tensor_t* rows(PyObject* o, int64_t* stride, Use use = kReads) {
     *stride = 0;
@@ -77,10 +106,14 @@ class Call {
   }
 
  private:
-  const rope_tensor_t* add(const at::Tensor& t, Use use) {
+  void check(const at::Tensor& t) {
     if (!t.is_cuda()) fail(PyExc_ValueError, "expected a CUDA tensor");
     if (device_ < 0) device_ = t.get_device();
     if (t.get_device() != device_) fail(PyExc_ValueError, "tensors on different devices");
+  }
+
+  const rope_tensor_t* add(const at::Tensor& t, Use use) {
+    check(t);
     if (t.dim() < 1 || t.dim() > 4) fail(PyExc_ValueError, "expected 1 to 4 dimensions");
     rope_tensor_t& d = descs_[n_++];
     d.data = use == kWrites ? t.mutable_data_ptr() : const_cast<void*>(t.const_data_ptr());
@@ -90,7 +123,7 @@ class Call {
     return &d;
   }
 
-  rope_tensor_t descs_[12];
+  rope_tensor_t descs_[14];
   int n_ = 0;
   int64_t device_ = -1;
 };
@@ -160,6 +193,12 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     find(g_append, "rope_append_paged_kv");
     find(g_attend, "rope_paged_attention");
     find(g_workspace, "rope_paged_attention_workspace");
+    find(g_append_8bit, "rope_append_paged_kv_8bit");
+    find(g_attend_8bit, "rope_paged_attention_8bit");
+    find(g_workspace_8bit, "rope_paged_attention_8bit_workspace");
+    find(g_rearrange, "rope_rearrange_sequences");
+    find(g_compact, "rope_compact_pages");
+    find(g_copy_pages, "rope_copy_pages");
     Py_RETURN_NONE;
   });
 }
@@ -214,49 +253,65 @@ PyObject* scaled_cos_sin(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The arguments of an append: a[0 .. caches) tensors up to the caches (and scales), then
+// (head_size, rotary_dim or None, is_neox, mrope_section or None, cache_mode, stream).
+PyObject* append(PyObject* const* a, bool coded) {
+  Call c;
+  int64_t ks, qs, vs;
+  // (written ones first: a query that is its own output, or the fused buffer of an in-place query's key, has
+  // the address that it is written at)
+  const rope_tensor_t* out = c.whole(a[6], kWrites);
+  const rope_tensor_t *kc = c.whole(a[7], kWrites), *vc = c.whole(a[8], kWrites);
+  const rope_tensor_t *kz = coded ? c.whole(a[9], kWrites) : nullptr, *vz = coded ? c.whole(a[10], kWrites) : nullptr;
+  const rope_tensor_t* query = c.rows(a[1], &qs, out ? kReads : kWrites);
+  const rope_tensor_t *key = c.rows(a[2], &ks), *value = c.rows(a[3], &vs);
+  const rope_tensor_t *positions = c.whole(a[0]), *table = c.whole(a[4]), *slots = c.whole(a[5]);
+  a += coded ? 11 : 9;
+  const int64_t head = integer(a[0]);
+  const int64_t rotary = a[1] != Py_None ? integer(a[1]) : table && table->ndim == 2 ? table->shape[1] : 0;
+  const int neox = PyObject_IsTrue(a[2]);
+  if (neox < 0) throw Failed();
+  int64_t section[4] = {0, 0, 0, 0}, sections = 0;
+  const bool mrope = a[3] != Py_None;
+  if (mrope) {
+    sections = PySequence_Size(a[3]);
+    if (sections < 0) throw Failed();
+    for (int64_t i = 0; i < sections && i < 4; ++i) {
+      PyObject* v = PySequence_GetItem(a[3], i);
+      if (!v) throw Failed();
+      section[i] = PyLong_AsLongLong(v);
+      Py_DECREF(v);
+      if (section[i] == -1 && PyErr_Occurred()) throw Failed();
+    }
+  }
+  const int32_t mode = (int32_t)integer(a[4]);
+  const int64_t stream = integer(a[5]);
+  return status_of([&] {
+    if (coded)
+      return g_append_8bit(positions, query, key, value, table, slots, out, kc, vc, kz, vz, head, rotary, neox,
+                           mrope ? section : nullptr, sections, mode, qs, ks, vs, (void*)stream);
+    return g_append(positions, query, key, value, table, slots, out, kc, vc, head, rotary, neox,
+                    mrope ? section : nullptr, sections, mode, qs, ks, vs, (void*)stream);
+  });
+}
+
 // (positions, query or None, key, value, table, slots, query_out or None, k_cache, v_cache, head_size,
 //  rotary_dim or None, is_neox, mrope_section or None, cache_mode, stream) -> status
 PyObject* append_paged_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 15, [&]() -> PyObject* {
-    Call c;
-    int64_t ks, qs, vs;
-    // (written ones first: a query that is its own output, or the fused buffer of an in-place query's key, has
-    // the address that it is written at)
-    const rope_tensor_t* out = c.whole(a[6], kWrites);
-    const rope_tensor_t *kc = c.whole(a[7], kWrites), *vc = c.whole(a[8], kWrites);
-    const rope_tensor_t* query = c.rows(a[1], &qs, out ? kReads : kWrites);
-    const rope_tensor_t *key = c.rows(a[2], &ks), *value = c.rows(a[3], &vs);
-    const rope_tensor_t *positions = c.whole(a[0]), *table = c.whole(a[4]), *slots = c.whole(a[5]);
-    const int64_t head = integer(a[9]);
-    const int64_t rotary = a[10] != Py_None ? integer(a[10]) : table && table->ndim == 2 ? table->shape[1] : 0;
-    const int neox = PyObject_IsTrue(a[11]);
-    if (neox < 0) throw Failed();
-    int64_t section[4] = {0, 0, 0, 0}, sections = 0;
-    const bool mrope = a[12] != Py_None;
-    if (mrope) {
-      sections = PySequence_Size(a[12]);
-      if (sections < 0) throw Failed();
-      for (int64_t i = 0; i < sections && i < 4; ++i) {
-        PyObject* v = PySequence_GetItem(a[12], i);
-        if (!v) throw Failed();
-        section[i] = PyLong_AsLongLong(v);
-        Py_DECREF(v);
-        if (section[i] == -1 && PyErr_Occurred()) throw Failed();
-      }
-    }
-    const int32_t mode = (int32_t)integer(a[13]);
-    const int64_t stream = integer(a[14]);
-    return status_of([&] {
-      return g_append(positions, query, key, value, table, slots, out, kc, vc, head, rotary, neox,
-                      mrope ? section : nullptr, sections, mode, qs, ks, vs, (void*)stream);
-    });
-  });
+  return guarded(n, 15, [&]() -> PyObject* { return append(a, false); });
+}
+
+// The same with k_scale and v_scale behind v_cache.
+PyObject* append_paged_kv_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 17, [&]() -> PyObject* { return append(a, true); });
 }
 
 int64_t workspace_bytes(const at::Tensor& q, const at::Tensor& k, int64_t prefix_len) {
   int64_t bytes = 0;
   if (q.dim() != 2 || k.dim() != 4 || k.size(3) < 1) return -1;
-  const int st = g_workspace(q.size(0), q.size(1) / k.size(3), k.size(1), k.size(3), type_of(q), prefix_len, &bytes);
+  const bool coded = k.scalar_type() == at::kFloat8_e4m3fn;
+  const int st = (coded ? g_workspace_8bit : g_workspace)(q.size(0), q.size(1) / k.size(3), k.size(1), k.size(3),
+                                                          type_of(q), prefix_len, &bytes);
   return st == ROPE_OK ? bytes : -1;
 }
 
@@ -267,34 +322,89 @@ PyObject* attention_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (query, k_cache, v_cache, block_table, seq_lens, query_start_loc, prefix_blocks or None, prefix_len, scale, out,
-//  lse or None, workspace or None, stream) -> status.  Without a workspace one is taken from the allocator for the
-// current stream, which then has to be the stream of the call.
+// (query, k_cache, v_cache, [k_scale, v_scale,] block_table, seq_lens, query_start_loc, prefix_blocks or None,
+//  prefix_len, scale, out, lse or None, workspace or None, stream) -> status.  Without a workspace one is taken from
+// the allocator for the current stream, which then has to be the stream of the call.
+PyObject* attention(PyObject* const* a, bool coded) {
+  Call c;
+  int64_t qs;
+  PyObject* const* b = a + (coded ? 5 : 3);  // from block_table on
+  const rope_tensor_t *query = c.rows(a[0], &qs), *kc = c.whole(a[1]), *vc = c.whole(a[2]);
+  const rope_tensor_t *kz = coded ? c.whole(a[3]) : nullptr, *vz = coded ? c.whole(a[4]) : nullptr;
+  const rope_tensor_t *bt = c.whole(b[0]), *lens = c.whole(b[1]), *starts = c.whole(b[2]), *prefix = c.whole(b[3]);
+  const rope_tensor_t *out = c.whole(b[6], kWrites), *lse = c.whole(b[7], kWrites);
+  const int64_t prefix_len = integer(b[4]), stream = integer(b[9]);
+  const float scale = (float)number(b[5]);
+  at::Tensor ws;
+  if (b[8] != Py_None) {
+    ws = tensor(b[8]);
+    if (!ws.is_cuda() || !ws.is_contiguous() || ws.get_device() != tensor(a[0]).get_device())
+      fail(PyExc_ValueError, "expected a contiguous workspace on the tensors' device");
+  } else {
+    const int64_t bytes = workspace_bytes(tensor(a[0]), tensor(a[1]), prefix_len);
+    if (bytes < 0) return PyLong_FromLong(ROPE_ERR_PARAM_INVALID);
+    ws = at::empty({bytes}, tensor(a[0]).options().dtype(at::kByte));
+  }
+  void* const at = ws.mutable_data_ptr();
+  const int64_t bytes = (int64_t)ws.nbytes();
+  return status_of([&] {
+    if (coded)
+      return g_attend_8bit(query, qs, kc, vc, kz, vz, bt, lens, starts, prefix, prefix_len, scale, out, lse, at, bytes,
+                           (void*)stream);
+    return g_attend(query, qs, kc, vc, bt, lens, starts, prefix, prefix_len, scale, out, lse, at, bytes,
+                    (void*)stream);
+  });
+}
+
 PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> PyObject* { return attention(a, false); });
+}
+
+PyObject* paged_attention_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> PyObject* { return attention(a, true); });
+}
+
+// (block_table, seq_lens, ref_counts, parents, room or None, new_block_table, new_seq_lens, new_ref_counts, copy_src,
+//  copy_dst, counts, block_size, prefix_len, stream) -> status
+PyObject* rearrange_sequences(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&]() -> PyObject* {
+    Call c;
+    const rope_tensor_t* t[11];
+    for (int i = 10; i >= 0; --i) t[i] = c.whole(a[i], i >= 5 ? kWrites : kReads);  // (written ones first, as above)
+    const int64_t block = integer(a[11]), prefix = integer(a[12]), stream = integer(a[13]);
+    return status_of([&] {
+      return g_rearrange(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], t[8], t[9], t[10], block, prefix,
+                         (void*)stream);
+    });
+  });
+}
+
+// (block_table, seq_lens, ref_counts, prefix_blocks or None, new_block_table, new_ref_counts, new_prefix_blocks or
+//  None, copy_src, copy_dst, counts, block_size, prefix_len, stream) -> status
+PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&]() -> PyObject* {
     Call c;
-    int64_t qs;
-    const rope_tensor_t *query = c.rows(a[0], &qs), *kc = c.whole(a[1]), *vc = c.whole(a[2]), *bt = c.whole(a[3]);
-    const rope_tensor_t *lens = c.whole(a[4]), *starts = c.whole(a[5]), *prefix = c.whole(a[6]);
-    const rope_tensor_t *out = c.whole(a[9], kWrites), *lse = c.whole(a[10], kWrites);
-    const int64_t prefix_len = integer(a[7]), stream = integer(a[12]);
-    const float scale = (float)number(a[8]);
-    at::Tensor ws;
-    if (a[11] != Py_None) {
-      ws = tensor(a[11]);
-      if (!ws.is_cuda() || !ws.is_contiguous() || ws.get_device() != tensor(a[0]).get_device())
-        fail(PyExc_ValueError, "expected a contiguous workspace on the tensors' device");
-    } else {
-      const int64_t bytes = workspace_bytes(tensor(a[0]), tensor(a[1]), prefix_len);
-      if (bytes < 0) return PyLong_FromLong(ROPE_ERR_PARAM_INVALID);
-      ws = at::empty({bytes}, tensor(a[0]).options().dtype(at::kByte));
-    }
-    void* const at = ws.mutable_data_ptr();
-    const int64_t bytes = (int64_t)ws.nbytes();
+    const rope_tensor_t* t[10];
+    for (int i = 9; i >= 0; --i) t[i] = c.whole(a[i], i >= 4 ? kWrites : kReads);
+    const int64_t block = integer(a[10]), prefix = integer(a[11]), stream = integer(a[12]);
     return status_of([&] {
-      return g_attend(query, qs, kc, vc, bt, lens, starts, prefix, prefix_len, scale, out, lse, at, bytes,
-                      (void*)stream);
+      return g_compact(t[0], t[1], t[2], t[3], t[4], t[5], t[6], t[7], t[8], t[9], block, prefix, (void*)stream);
     });
+  });
+}
+
+// (src, dst, count or None, a tuple or list of tensors, stream) -> status
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    Call c;
+    if (!PyList_Check(a[3]) && !PyTuple_Check(a[3])) fail(PyExc_TypeError, "expected a list or tuple of tensors");
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[3]);
+    std::vector<rope_tensor_t> list;
+    list.reserve(count);
+    const rope_tensor_t *src = c.whole(a[0]), *dst = c.whole(a[1]), *pairs = c.whole(a[2]);
+    for (Py_ssize_t i = 0; i < count; ++i) list.push_back(c.pages(PySequence_Fast_GET_ITEM(a[3], i)));
+    const int64_t stream = integer(a[4]);
+    return status_of([&] { return g_copy_pages(src, dst, pairs, list.data(), (int64_t)count, (void*)stream); });
   });
 }
 
@@ -306,6 +416,11 @@ PyMethodDef methods[] = {ROPE_METHOD(init),
                          ROPE_METHOD(append_paged_kv),
                          ROPE_METHOD(attention_workspace),
                          ROPE_METHOD(paged_attention),
+                         ROPE_METHOD(append_paged_kv_8bit),
+                         ROPE_METHOD(paged_attention_8bit),
+                         ROPE_METHOD(rearrange_sequences),
+                         ROPE_METHOD(compact_pages),
+                         ROPE_METHOD(copy_pages),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "rope_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -2,8 +2,11 @@
 // key of a sequence sits in the paged cache.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "rope_device.cuh"
 #include "serving.h"
@@ -23,7 +26,8 @@ struct AttendArgs {
   int32_t block_size, bs_shift;  // bs_shift: log2(block_size), or -1
   int32_t P;            // keys of the shared prefix
   float scale_log2;     // scale * log2(e)
-  Span q_span, k_span, v_span, bt_span, sl_span, qsl_span, pb_span, out_span, lse_span;
+  int32_t S, per;       // caches of codes: scale blocks of a page, tokens of a scale block
+  Span q_span, k_span, v_span, bt_span, sl_span, qsl_span, pb_span, out_span, lse_span, ks_span, vs_span;
 };
 
 struct Pointers {
@@ -32,7 +36,31 @@ struct Pointers {
   const int64_t* qsl;
   const int64_t* prefix_blocks;
   unsigned int* err;
+  const uint8_t *k_scale, *v_scale;  // caches of codes: E8M0 bytes [num_blocks, nk, S]
 };
+
+// An element of a cache of codes: E4M3, in units of its block's scale.
+struct Code {
+  uint8_t bits;
+};
+template <typename C>
+constexpr bool kCoded = std::is_same<C, Code>::value;
+
+// 2^(b - 127), exact; NaN for b = 255.
+__device__ __forceinline__ float power_of(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+}
+
+__device__ __forceinline__ float widen(Code c) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(c.bits, __NV_E4M3);
+  return __half2float(__half(h));
+}
+using rope::widen;
+
+// The scale byte's place of a key in row `row` of a page: k_scale and v_scale have it there.
+__device__ __forceinline__ int64_t scale_at(int64_t page, int kh, int row, const AttendArgs& a) {
+  return (page * a.nk + kh) * a.S + row / a.per;
+}
 
 // Batch of token t: the largest b in [0, B) with query_start_loc[b] <= t.
 __device__ __forceinline__ int64_t batch_of(int64_t t, const Pointers& g, const AttendArgs& a) {
@@ -422,10 +450,20 @@ __device__ __forceinline__ float inverse_sum(float l, const Walk& w, int64_t t) 
   return w.s.hi > 0 && w.s.pos0 + (t - w.s.t0) >= 0 ? NAN : 0.f;
 }
 
+// One element of a cache, as its code says.
+template <typename C>
+__device__ __forceinline__ float element(const C* p, const Span& s, unsigned int* err) {
+  if constexpr (kCoded<C>)
+    return widen(Code{ldg(&p->bits, s, err)});
+  else
+    return widen(ldg(p, s, err));
+}
+
 // One query row by one warp, a key at a time: keys the row does not see are not read at all.
-template <typename T, int E>
-__device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict__ q, const T* __restrict__ kc,
-                                           const T* __restrict__ vc, T* __restrict__ out, float* __restrict__ lse,
+// C: elements of the cache, T or Code.
+template <typename T, int E, typename C>
+__device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict__ q, const C* __restrict__ kc,
+                                           const C* __restrict__ vc, T* __restrict__ out, float* __restrict__ lse,
                                            const Pointers& g, const AttendArgs& a) {
   constexpr int KU = 4;
   const int lane = threadIdx.x & 31;
@@ -449,13 +487,26 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
   float m = -INFINITY, l = 0.f;
   for (int j0 = 0; j0 < seen; j0 += KU) {
     int64_t at[KU];
-    float s[KU];
+    float s[KU], ks[KU], vs[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
-      const int64_t r = j0 + u < seen ? key_row(j0 + u, table, g, a) : -1;
-      if (r < 0 && j0 + u < seen && lane == 0) atomicOr(g.err, kSlotOutOfRange);
-      at[u] = r < 0 ? -1 : (r + (int64_t)kh * a.block_size) * a.D;
       s[u] = 0.f;
+      ks[u] = vs[u] = 1.f;
+      if constexpr (kCoded<C>) {
+        const PageRow r = j0 + u < seen ? page_row(j0 + u, table, g, a) : PageRow{-1, 0};
+        const bool there = r.page >= 0 && r.page < a.num_blocks;
+        if (!there && j0 + u < seen && lane == 0) atomicOr(g.err, kSlotOutOfRange);
+        at[u] = there ? ((r.page * a.nk + kh) * a.block_size + r.row) * a.D : -1;
+        if (there) {
+          const int64_t i = scale_at(r.page, kh, r.row, a);
+          ks[u] = power_of(ldg(g.k_scale + i, a.ks_span, g.err));
+          vs[u] = power_of(ldg(g.v_scale + i, a.vs_span, g.err));
+        }
+      } else {
+        const int64_t r = j0 + u < seen ? key_row(j0 + u, table, g, a) : -1;
+        if (r < 0 && j0 + u < seen && lane == 0) atomicOr(g.err, kSlotOutOfRange);
+        at[u] = r < 0 ? -1 : (r + (int64_t)kh * a.block_size) * a.D;
+      }
     }
 #pragma unroll
     for (int u = 0; u < KU; ++u)
@@ -463,7 +514,7 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const int d = lane + 32 * e;
-          if (d < a.D) s[u] = fmaf(qv[e], widen(ldg(kc + at[u] + d, a.k_span, g.err)), s[u]);
+          if (d < a.D) s[u] = fmaf(qv[e], element(kc + at[u] + d, a.k_span, g.err) * ks[u], s[u]);
         }
       }
 #pragma unroll
@@ -489,7 +540,7 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int d = lane + 32 * e;
-        if (d < a.D) o[e] = fmaf(w, widen(ldg(vc + at[u] + d, a.v_span, g.err)), o[e]);
+        if (d < a.D) o[e] = fmaf(w, element(vc + at[u] + d, a.v_span, g.err) * vs[u], o[e]);
       }
     }
     m = top;
@@ -509,8 +560,8 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
 // row does not see has weight 0 in the unit kernels, and 0 * infinity or NaN of its value leaves NaN; and
 // products of queries and keys beyond binary32 are infinite there, here queries are scaled before.
 // All NT threads call it after a barrier; `tmp` as for find_share.
-template <typename T, int DP, int M, int KT, int NT>
-__device__ __forceinline__ void mend_rows(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
+template <typename T, int DP, int M, int KT, int NT, typename C>
+__device__ __forceinline__ void mend_rows(const T* __restrict__ q, const C* __restrict__ kc, const C* __restrict__ vc,
                                           T* __restrict__ out, float* __restrict__ lse, const Pointers& g,
                                           const AttendArgs& a, const Cut& c, int64_t* tmp) {
   const int lane = threadIdx.x & 31;

@@ -1,0 +1,585 @@
+// Pages of a paged cache: sequences forked, reordered, dropped and given room; live pages moved to the front;
+// pages copied in many tensors at once.
+//
+// The first two work on tables of page numbers and on how many times each page is held (ref_counts).  They are
+// bound by latency: each runs as one cluster of 8 CTAs, whose barrier is what lets every step see the one before
+// it, so that a call is one launch.  Free pages are given out lowest first, rows in order, so results do not
+// depend on the order in which threads run.
+//
+// rearrange_sequences: every old row lets go of its pages; new row i takes the whole pages of its parent once
+// more.  The page that is written on (the last, partly filled one) stays with the first of the new rows that
+// claim it if nobody else holds it: rows claim it by atomicMin of row - kClaim in its count, which is then 0.
+// The others get a copy.  Where fresh pages go is found the other way round: the r-th free page belongs to the
+// row whose range of requests holds r.
+//
+// compact_pages: with L live pages, the k-th live page at or behind L goes to the k-th free page before L.
+#include <algorithm>
+
+#include "rope_device.cuh"
+#include "serving.h"
+
+namespace rope {
+namespace {
+
+constexpr unsigned kSlotOutOfRange = 2u;
+constexpr unsigned kPagesExhausted = 16u;
+constexpr int kCluster = 8;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAll = kCluster * kThreads;
+constexpr int kAllWarps = kCluster * kWarps;
+constexpr int kClaim = 1 << 30;
+
+__device__ __forceinline__ int cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+
+// What any thread of the cluster wrote before it, all see after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The word of CTA `rank` that is where `p` is in this one's shared memory.
+__device__ __forceinline__ int peer_int(const int* p, int rank) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(p), far;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(far) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// Warps' ranges of pages: warp w of all has [w * per, min(NB, (w + 1) * per)), per a multiple of 32.
+struct Pages {
+  int from, to;
+};
+__device__ __forceinline__ Pages pages_of(int warp, int NB) {
+  const int per = (NB + kAllWarps * 32 - 1) / (kAllWarps * 32) * 32;
+  const int64_t from = (int64_t)warp * per;
+  return {(int)min(from, (int64_t)NB), (int)min(from + per, (int64_t)NB)};
+}
+
+// Sum of `count` (a value a warp, in every CTA's shared memory) over all warps before `warp`, and over all.
+// Every warp calls it.
+__device__ __forceinline__ int sum_before(const int* count, int warp, int* total) {
+  const int lane = threadIdx.x & 31;
+  int before = 0, all = 0;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) {
+    const int v = peer_int(count + lane, r);
+    all += v;
+    before += r * kWarps + lane < warp ? v : 0;
+  }
+  *total = warp_sum(all);
+  return warp_sum(before);
+}
+
+// ---------------------------------------------------------------------------
+// New sequences of old ones
+// ---------------------------------------------------------------------------
+struct RearrangeArgs {
+  RearrangeProblem p;
+  Span table_span, lens_span, refs_span, parents_span, room_span, new_table_span, new_lens_span, new_refs_span, src_span,
+      dst_span, counts_span;
+};
+
+struct RearrangeShared {
+  int free_pages[kWarps];        // in the warp's range
+  int2 sums[kWarps];
+  int start[kMostRearranged + 1];  // first request of every row
+  int have[kMostRearranged];     // pages that it has before
+  int pair[kMostRearranged];     // its place among the copies, or -1
+};
+
+// What new row i takes of its parent.
+struct Taken {
+  int64_t parent;  // or -1
+  int64_t len;     // of the parent
+  int full, rest;  // whole pages, tokens on the page that is written on
+  int64_t last;    // that page, or -1
+};
+
+__device__ __forceinline__ Taken taken_of(int i, const RearrangeArgs& a, unsigned* err) {
+  const RearrangeProblem& p = a.p;
+  Taken t = {ldg(p.parents + i, a.parents_span, err), p.prefix_len, 0, 0, -1};
+  if (t.parent >= p.B) {
+    atomicOr(err, kSlotOutOfRange);
+    t.parent = -1;
+  }
+  if (t.parent < 0) {
+    t.parent = -1;
+    return t;
+  }
+  t.len = ldg(p.lens + t.parent, a.lens_span, err);
+  int64_t own = max(t.len - p.prefix_len, (int64_t)0);
+  const int64_t most = min(p.W, p.new_W) * p.block_size;
+  if (own > most) {
+    atomicOr(err, kSlotOutOfRange);
+    own = most;
+    t.len = p.prefix_len + own;
+  }
+  t.full = (int)(own / p.block_size);
+  t.rest = (int)(own - (int64_t)t.full * p.block_size);
+  if (t.rest) {
+    const int64_t page = ldg(p.table + t.parent * p.W + t.full, a.table_span, err);
+    if (page >= 0 && page < p.NB) t.last = page;
+    else atomicOr(err, kSlotOutOfRange);
+  }
+  return t;
+}
+
+__global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, unsigned int* err) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  RearrangeShared& sm = *reinterpret_cast<RearrangeShared*>(raw);
+  const RearrangeProblem& p = a.p;
+  const int rank = cta_rank(), me = rank * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31, cw = threadIdx.x >> 5, warp = rank * kWarps + cw;
+  const int rows = (int)p.rows, NB = (int)p.NB;
+  const int64_t bs = p.block_size;
+  int32_t* const refs = p.new_refs;
+  auto ref_ok = [&](const int32_t* r) { return access_ok(r, 4, a.new_refs_span, err); };
+  wait_for_prior_grid();
+  // ---- counts as they were
+  if (refs != p.refs) {
+    for (int i = me; i < NB; i += kAll)
+      if (ref_ok(refs + i)) __stcg(refs + i, ldg(p.refs + i, a.refs_span, err));
+    cluster_sync();
+  }
+  // ---- old rows let go
+  for (int64_t b = warp; b < p.B; b += kAllWarps) {
+    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
+    const int64_t pages = (own + bs - 1) / bs;
+    if (pages > p.W && lane == 0) atomicOr(err, kSlotOutOfRange);
+    for (int c = lane; c < min(pages, p.W); c += 32) {
+      const int64_t page = ldg(p.table + b * p.W + c, a.table_span, err);
+      if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
+      else if (ref_ok(refs + page)) atomicSub(refs + page, 1);
+    }
+  }
+  cluster_sync();
+  // ---- claims of pages that are written on
+  for (int i = me; i < rows; i += kAll) {
+    const Taken t = taken_of(i, a, err);
+    if (t.last >= 0 && ref_ok(refs + t.last) && __ldcg(refs + t.last) <= 0) atomicMin(refs + t.last, i - kClaim);
+  }
+  cluster_sync();
+  for (int i = me; i < rows; i += kAll) {
+    const Taken t = taken_of(i, a, err);
+    const bool keeps = t.last >= 0 && ref_ok(refs + t.last) && __ldcg(refs + t.last) == i - kClaim;
+    if (access_ok(p.src + i, 8, a.src_span, err)) __stcg(p.src + i, (int64_t)keeps);
+  }
+  cluster_sync();
+  // ---- new rows take hold, and every CTA adds up what they ask for
+  for (int i = warp; i < rows; i += kAllWarps) {
+    const Taken t = taken_of(i, a, err);
+    for (int c = lane; c < t.full + (t.rest > 0); c += 32) {
+      const int64_t page = ldg(p.table + t.parent * p.W + c, a.table_span, err);
+      int32_t add = 1;
+      if (c == t.full) {
+        if (!__ldcg(p.src + i)) continue;
+        add = 1 - (i - kClaim);  // off with the claim
+      }
+      if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
+      else if (ref_ok(refs + page)) atomicAdd(refs + page, add);
+      int64_t* const to = p.new_table + i * p.new_W + c;
+      if (access_ok(to, 8, a.new_table_span, err)) *to = page;
+    }
+  }
+  int2 run = make_int2(0, 0);  // requests, copies
+  for (int base = 0; base < rows; base += kThreads) {
+    const int i = base + threadIdx.x;
+    int2 mine = make_int2(0, 0);
+    int have = 0;
+    bool copy = false;
+    if (i < rows) {
+      const Taken t = taken_of(i, a, err);
+      const bool keeps = __ldcg(p.src + i) != 0;
+      copy = t.rest > 0 && !keeps;
+      have = t.full + keeps;
+      const int64_t own = max(t.len - p.prefix_len, (int64_t)0);
+      const int64_t room = p.room ? max(ldg(p.room + i, a.room_span, err), (int64_t)0) : 0;
+      const int64_t most = p.new_W * bs, grown = room > most - own ? most : own + room;
+      if (own + room != grown && rank == 0) atomicOr(err, kSlotOutOfRange);
+      mine = make_int2((int)((grown + bs - 1) / bs) - have, copy);
+      if (rank == 0 && access_ok(p.new_lens + i, 8, a.new_lens_span, err))
+        p.new_lens[i] = p.prefix_len + grown;
+    }
+    int2 upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, upto.x, d), y = __shfl_up_sync(0xffffffffu, upto.y, d);
+      if (lane >= d) upto.x += x, upto.y += y;
+    }
+    __syncthreads();
+    if (lane == 31) sm.sums[cw] = upto;
+    __syncthreads();
+    int2 sum = sm.sums[lane];
+    const int2 own_sum = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, sum.x, d), y = __shfl_up_sync(0xffffffffu, sum.y, d);
+      if (lane >= d) sum.x += x, sum.y += y;
+    }
+    const int before_x = __shfl_sync(0xffffffffu, sum.x - own_sum.x, cw), before_y = __shfl_sync(0xffffffffu, sum.y - own_sum.y, cw);
+    if (i < rows) {
+      sm.start[i] = run.x + before_x + upto.x - mine.x;
+      sm.have[i] = have;
+      sm.pair[i] = copy ? run.y + before_y + upto.y - 1 : -1;
+    }
+    run.x += __shfl_sync(0xffffffffu, sum.x, 31);
+    run.y += __shfl_sync(0xffffffffu, sum.y, 31);
+  }
+  if (threadIdx.x == 0) sm.start[rows] = run.x;
+  cluster_sync();
+  // ---- free pages
+  const Pages mine = pages_of(warp, NB);
+  int free_pages = 0;
+  for (int i = mine.from + lane; i < mine.to; i += 32) free_pages += ref_ok(refs + i) && __ldcg(refs + i) == 0;
+  free_pages = warp_sum(free_pages);
+  if (lane == 0) sm.free_pages[cw] = free_pages;
+  cluster_sync();
+  int all_free;
+  int r0 = sum_before(sm.free_pages, warp, &all_free);
+  const int asked = run.x;
+  for (int base = mine.from; base < mine.to && r0 < asked; base += 32) {
+    const int page = base + lane;
+    const bool is_free = page < mine.to && ref_ok(refs + page) && __ldcg(refs + page) == 0;
+    const uint32_t ones = __ballot_sync(0xffffffffu, is_free);
+    const int r = r0 + __popc(ones & ((1u << lane) - 1u));
+    r0 += __popc(ones);
+    if (!is_free || r >= asked) continue;
+    int lo = 0, hi = rows - 1;  // the last row that starts at or before r (rows without requests start with the next)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sm.start[mid] <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    const int j = r - sm.start[lo];
+    int64_t* const to = p.new_table + lo * p.new_W + sm.have[lo] + j;
+    if (access_ok(to, 8, a.new_table_span, err)) *to = page;
+    refs[page] = 1;
+    if (j == 0 && sm.pair[lo] >= 0 && access_ok(p.dst + sm.pair[lo], 8, a.dst_span, err)) p.dst[sm.pair[lo]] = page;
+  }
+  // ---- pairs, requests that no page was left for, and the counts
+  for (int i = me; i < rows; i += kAll) {
+    const int pair = sm.pair[i], first = sm.start[i], end = sm.start[i + 1];
+    if (pair >= 0 && access_ok(p.src + pair, 8, a.src_span, err)) {
+      p.src[pair] = taken_of(i, a, err).last;
+      if (first >= all_free) p.dst[pair] = -1;
+    }
+    if (i >= run.y && access_ok(p.src + i, 8, a.src_span, err)) p.src[i] = p.dst[i] = -1;
+    for (int r = max(first, all_free); r < end; ++r) {
+      int64_t* const to = p.new_table + i * p.new_W + sm.have[i] + r - first;
+      if (access_ok(to, 8, a.new_table_span, err)) *to = -1;
+      atomicOr(err, kPagesExhausted);
+    }
+  }
+  if (me == 0 && access_ok(p.counts, 16, a.counts_span, err)) {
+    p.counts[0] = run.y;
+    p.counts[1] = max(all_free - asked, 0);
+  }
+  cluster_sync();  // nobody leaves while another reads its shared memory
+}
+
+// ---------------------------------------------------------------------------
+// Live pages to the front
+// ---------------------------------------------------------------------------
+struct CompactArgs {
+  CompactProblem p;
+  int64_t prefix_pages;
+  Span table_span, lens_span, refs_span, new_table_span, new_refs_span, prefix_span, new_prefix_span, src_span, dst_span,
+      counts_span;
+};
+
+__global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, unsigned int* err) {
+  __shared__ int live_of[kWarps], hole_of[kWarps], mover_of[kWarps];
+  const CompactProblem& p = a.p;
+  const int rank = cta_rank(), me = rank * kThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31, cw = threadIdx.x >> 5, warp = rank * kWarps + cw;
+  const int NB = (int)p.NB;
+  wait_for_prior_grid();
+  auto live_at = [&](int i) { return ldg(p.refs + i, a.refs_span, err) > 0; };
+  const Pages mine = pages_of(warp, NB);
+  int n = 0;
+  for (int i = mine.from + lane; i < mine.to; i += 32) n += live_at(i);
+  n = warp_sum(n);
+  if (lane == 0) live_of[cw] = n;
+  cluster_sync();
+  int L;
+  sum_before(live_of, warp, &L);
+  // ---- free pages before L, live ones at or behind it
+  int holes = 0, movers = 0;
+  for (int i = mine.from + lane; i < mine.to; i += 32) {
+    const bool live = live_at(i);
+    holes += !live && i < L;
+    movers += live && i >= L;
+  }
+  holes = warp_sum(holes);
+  movers = warp_sum(movers);
+  if (lane == 0) {
+    hole_of[cw] = holes;
+    mover_of[cw] = movers;
+  }
+  cluster_sync();
+  int all_holes, moved;
+  int h0 = sum_before(hole_of, warp, &all_holes), m0 = sum_before(mover_of, warp, &moved);
+  if (holes + movers > 0)
+    for (int base = mine.from; base < mine.to; base += 32) {
+      const int i = base + lane;
+      const bool live = i < mine.to && live_at(i);
+      const bool hole = i < mine.to && !live && i < L, mover = live && i >= L;
+      const uint32_t hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, mover);
+      const uint32_t before = (1u << lane) - 1u;
+      if (hole) {
+        int64_t* const to = p.dst + h0 + __popc(hs & before);
+        if (access_ok(to, 8, a.dst_span, err)) __stcg(to, (int64_t)i);
+      }
+      if (mover) {
+        int64_t* const to = p.src + m0 + __popc(ms & before);
+        if (access_ok(to, 8, a.src_span, err)) __stcg(to, (int64_t)i);
+      }
+      h0 += __popc(hs);
+      m0 += __popc(ms);
+    }
+  for (int64_t i = moved + me; i < p.pairs; i += kAll) {
+    if (access_ok(p.src + i, 8, a.src_span, err)) p.src[i] = -1;
+    if (access_ok(p.dst + i, 8, a.dst_span, err)) p.dst[i] = -1;
+  }
+  if (me == 0 && access_ok(p.counts, 16, a.counts_span, err)) {
+    p.counts[0] = moved;
+    p.counts[1] = L;
+  }
+  cluster_sync();
+  auto to_of = [&](int64_t page) -> int64_t {  // where a page goes; -1 for none
+    if (page < 0 || page >= p.NB || !live_at((int)page)) {
+      atomicOr(err, kSlotOutOfRange);
+      return page;
+    }
+    if (page < L) return page;
+    int lo = 0, hi = moved - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(p.src + mid) < page) lo = mid + 1;
+      else hi = mid;
+    }
+    return __ldcg(p.dst + lo);
+  };
+  // ---- tables
+  for (int64_t b = warp; b < p.B; b += kAllWarps) {
+    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
+    const int64_t pages = (own + p.block_size - 1) / p.block_size;
+    if (pages > p.W && lane == 0) atomicOr(err, kSlotOutOfRange);
+    for (int c = lane; c < min(pages, p.W); c += 32) {
+      const int64_t* from = p.table + b * p.W + c;
+      int64_t* const to = p.new_table + b * p.W + c;
+      const int64_t page = access_ok(from, 8, a.table_span, err) ? *from : 0;
+      if (access_ok(to, 8, a.new_table_span, err)) *to = to_of(page);
+    }
+  }
+  for (int64_t i = me; i < a.prefix_pages; i += kAll) {
+    const int64_t page = access_ok(p.prefix + i, 8, a.prefix_span, err) ? p.prefix[i] : 0;
+    if (access_ok(p.new_prefix + i, 8, a.new_prefix_span, err)) p.new_prefix[i] = to_of(page);
+  }
+  cluster_sync();
+  // ---- counts
+  for (int i = me; i < L; i += kAll) {
+    const int32_t* const from = p.refs + i;
+    int32_t* const to = p.new_refs + i;
+    const int32_t v = access_ok(from, 4, a.refs_span, err) ? *(const volatile int32_t*)from : 0;
+    if (v > 0 && access_ok(to, 4, a.new_refs_span, err)) *to = v;  // (a free page gets the count of what moves there)
+  }
+  for (int k = me; k < moved; k += kAll) {
+    const int64_t from = __ldcg(p.src + k), to = __ldcg(p.dst + k);
+    const int32_t v = access_ok(p.refs + from, 4, a.refs_span, err) ? *(const volatile int32_t*)(p.refs + from) : 0;
+    if (access_ok(p.new_refs + to, 4, a.new_refs_span, err)) p.new_refs[to] = v;
+  }
+  cluster_sync();
+  for (int i = L + me; i < NB; i += kAll)
+    if (access_ok(p.new_refs + i, 4, a.new_refs_span, err)) p.new_refs[i] = 0;
+}
+
+// One cluster of kCluster CTAs.
+template <typename K, typename A>
+cudaError_t launch_cluster(K kernel, size_t smem, const A& a, cudaStream_t stream) {
+  unsigned int* err = nullptr;
+  cudaError_t e = device_error_address(&err);
+  if (e != cudaSuccess) return e;
+  if (smem) {
+    e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, err);
+  count_launch();
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// ---------------------------------------------------------------------------
+// Pages copied
+// ---------------------------------------------------------------------------
+constexpr int kTensors = 64;   // of one launch
+constexpr int kPiece = 4096;   // bytes that a warp copies at a time
+constexpr int kCopyThreads = 256;
+
+struct CopyArgs {
+  const int64_t *src, *dst, *count;
+  int64_t pairs, NB;
+  int64_t pieces;  // of a pair, all tensors together
+  int32_t tensors;
+  CopyTensor t[kTensors];
+  int32_t first[kTensors + 1];  // first piece of each tensor
+  int32_t vec[kTensors];        // bytes of an access: 16, 8, 4, 2 or 1
+  Span src_span, dst_span, count_span, span[kTensors];
+};
+
+template <typename V>
+__device__ __forceinline__ void copy_piece(char* to, const char* from, int n, const Span& s, unsigned* err) {
+  const int lane = threadIdx.x & 31;
+  constexpr int U = 8;
+  const V* x = reinterpret_cast<const V*>(from);
+  V* y = reinterpret_cast<V*>(to);
+  const int m = n / (int)sizeof(V);
+  for (int i = lane; i < m; i += 32 * U) {
+    V v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + 32 * u < m && access_ok(x + i + 32 * u, sizeof(V), s, err)) v[u] = __ldcs(x + i + 32 * u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + 32 * u < m && access_ok(y + i + 32 * u, sizeof(V), s, err)) __stcs(y + i + 32 * u, v[u]);
+  }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a, unsigned int* err) {
+  wait_for_prior_grid();
+  const int lane = threadIdx.x & 31;
+  int64_t pairs = a.pairs;
+  if (a.count) pairs = max(min(ldg(a.count, a.count_span, err), pairs), (int64_t)0);
+  const int64_t all = pairs * a.pieces, warps = (int64_t)gridDim.x * (kCopyThreads / 32);
+  for (int64_t f = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); f < all; f += warps) {
+    const int64_t pair = f / a.pieces;
+    const int piece = (int)(f - pair * a.pieces);
+    const int64_t from = ldg(a.src + pair, a.src_span, err), to = ldg(a.dst + pair, a.dst_span, err);
+    if (from < 0 || to < 0 || from == to) continue;
+    if (from >= a.NB || to >= a.NB) {
+      if (lane == 0) atomicOr(err, kSlotOutOfRange);
+      continue;
+    }
+    int lo = 0, hi = a.tensors - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.first[mid] <= piece) lo = mid;
+      else hi = mid - 1;
+    }
+    const int64_t bytes = a.t[lo].bytes, off = (int64_t)(piece - a.first[lo]) * kPiece;
+    const int n = (int)min((int64_t)kPiece, bytes - off);
+    char* const y = a.t[lo].data + to * bytes + off;
+    const char* const x = a.t[lo].data + from * bytes + off;
+    switch (a.vec[lo]) {
+      case 16:
+        copy_piece<uint4>(y, x, n, a.span[lo], err);
+        break;
+      case 8:
+        copy_piece<uint2>(y, x, n, a.span[lo], err);
+        break;
+      case 4:
+        copy_piece<unsigned int>(y, x, n, a.span[lo], err);
+        break;
+      case 2:
+        copy_piece<unsigned short>(y, x, n, a.span[lo], err);
+        break;
+      default:
+        copy_piece<unsigned char>(y, x, n, a.span[lo], err);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rearrange(const RearrangeProblem& p, cudaStream_t stream) {
+  RearrangeArgs a;
+  a.p = p;
+  a.table_span = make_span(p.table, p.B * p.W * 8);
+  a.lens_span = make_span(p.lens, p.B * 8);
+  a.refs_span = make_span(p.refs, p.NB * 4);
+  a.parents_span = make_span(p.parents, p.rows * 8);
+  a.room_span = make_span(p.room, p.rows * 8);
+  a.new_table_span = make_span(p.new_table, p.rows * p.new_W * 8);
+  a.new_lens_span = make_span(p.new_lens, p.rows * 8);
+  a.new_refs_span = make_span(p.new_refs, p.NB * 4);
+  a.src_span = make_span(p.src, p.rows * 8);
+  a.dst_span = make_span(p.dst, p.rows * 8);
+  a.counts_span = make_span(p.counts, 16);
+  return launch_cluster(rearrange_kernel, sizeof(RearrangeShared), a, stream);
+}
+
+cudaError_t launch_compact(const CompactProblem& p, cudaStream_t stream) {
+  CompactArgs a;
+  a.p = p;
+  a.prefix_pages = p.prefix ? (p.prefix_len + p.block_size - 1) / p.block_size : 0;
+  a.table_span = make_span(p.table, p.B * p.W * 8);
+  a.lens_span = make_span(p.lens, p.B * 8);
+  a.refs_span = make_span(p.refs, p.NB * 4);
+  a.new_table_span = make_span(p.new_table, p.B * p.W * 8);
+  a.new_refs_span = make_span(p.new_refs, p.NB * 4);
+  a.prefix_span = make_span(p.prefix, a.prefix_pages * 8);
+  a.new_prefix_span = make_span(p.new_prefix, a.prefix_pages * 8);
+  a.src_span = make_span(p.src, p.pairs * 8);
+  a.dst_span = make_span(p.dst, p.pairs * 8);
+  a.counts_span = make_span(p.counts, 16);
+  return launch_cluster(compact_kernel, 0, a, stream);
+}
+
+cudaError_t launch_copy_pages(const CopyProblem& p, cudaStream_t stream) {
+  unsigned int* err = nullptr;
+  const cudaError_t er = device_error_address(&err);
+  if (er != cudaSuccess) return er;
+  for (int64_t at = 0; at < p.num_tensors; at += kTensors) {
+    CopyArgs a;
+    a.src = p.src;
+    a.dst = p.dst;
+    a.count = p.count;
+    a.pairs = p.pairs;
+    a.NB = p.NB;
+    a.tensors = (int32_t)std::min<int64_t>(kTensors, p.num_tensors - at);
+    int64_t pieces = 0;
+    for (int i = 0; i < a.tensors; ++i) {
+      const CopyTensor& t = p.tensors[at + i];
+      a.t[i] = t;
+      a.first[i] = (int32_t)pieces;
+      pieces += (t.bytes + kPiece - 1) / kPiece;
+      const uintptr_t bits = reinterpret_cast<uintptr_t>(t.data) | (uintptr_t)t.bytes;
+      a.vec[i] = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+      a.span[i] = make_span(t.data, t.bytes * p.NB);
+    }
+    a.first[a.tensors] = (int32_t)pieces;
+    a.pieces = pieces;
+    a.src_span = make_span(p.src, p.pairs * 8);
+    a.dst_span = make_span(p.dst, p.pairs * 8);
+    a.count_span = make_span(p.count, 8);
+    const int64_t warps = kCopyThreads / 32;
+    const int64_t resident =
+        (int64_t)sm_count() * resident_blocks(reinterpret_cast<const void*>(copy_pages_kernel), kCopyThreads);
+    const int64_t grid = std::max<int64_t>(1, std::min((p.pairs * pieces + warps - 1) / warps, resident));
+    const cudaError_t e = launch_overlapped(copy_pages_kernel, (unsigned)grid, kCopyThreads, stream, a, err);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace rope
