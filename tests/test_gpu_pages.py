@@ -79,10 +79,12 @@ def test_rearrange_holders_outside_the_batch(rope_gpu):
 
 def test_rearrange_pages_run_out(rope_gpu):
     c = pages_case(6, [20, 33, 5], 16, spare=3, share=False)
+    over = []
     for parents, room in (([0, 1, 2, 0, 1, 2], [0] * 6), ([0, 1, 2], [16, 40, 30]), ([1, 1, 1, 1, 0], [1, 1, 1, 1, 100])):
         want = rearrange_reference(c, parents, room, 12)
-        assert bool((want["new_table"] == -1).any()) or parents == [0, 1, 2]
+        over.append(bool((want["new_table"] == -1).any()))
         same(run_rearrange(c, parents, room, 12), want)
+    assert over.count(True) >= 2
 
 
 def test_rearrange_bad_numbers(rope_gpu):

@@ -92,7 +92,7 @@ cudaError_t launch_mma(const AttendProblem& p, const Pointers& g, const AttendAr
 template <typename T, int DP>
 cudaError_t launch_tc(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
                       cudaStream_t stream) {
-  auto kernel = attend_tc_kernel<T, DP>;
+  auto kernel = attend_tc_kernel<T, DP, T>;
   const size_t smem = sizeof(TcShared<DP>);
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;

@@ -26,7 +26,7 @@ struct AttendArgs {
   int32_t block_size, bs_shift;  // bs_shift: log2(block_size), or -1
   int32_t P;            // keys of the shared prefix
   float scale_log2;     // scale * log2(e)
-  int32_t S, per;       // caches of codes: scale blocks of a page, tokens of a scale block
+  int32_t per;          // caches of codes: tokens of a scale block, so that cache row r has scale r / per
   Span q_span, k_span, v_span, bt_span, sl_span, qsl_span, pb_span, out_span, lse_span, ks_span, vs_span;
 };
 
@@ -57,10 +57,14 @@ __device__ __forceinline__ float widen(Code c) {
 }
 using rope::widen;
 
-// The scale byte's place of a key in row `row` of a page: k_scale and v_scale have it there.
-__device__ __forceinline__ int64_t scale_at(int64_t page, int kh, int row, const AttendArgs& a) {
-  return (page * a.nk + kh) * a.S + row / a.per;
+// Two codes as two binary16 values: the lower and the upper half of w.
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& lower, uint32_t& upper) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lower), "=r"(upper)
+      : "r"(w));
 }
+
 
 // Batch of token t: the largest b in [0, B) with query_start_loc[b] <= t.
 __device__ __forceinline__ int64_t batch_of(int64_t t, const Pointers& g, const AttendArgs& a) {
@@ -496,9 +500,10 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
         const PageRow r = j0 + u < seen ? page_row(j0 + u, table, g, a) : PageRow{-1, 0};
         const bool there = r.page >= 0 && r.page < a.num_blocks;
         if (!there && j0 + u < seen && lane == 0) atomicOr(g.err, kSlotOutOfRange);
-        at[u] = there ? ((r.page * a.nk + kh) * a.block_size + r.row) * a.D : -1;
+        const int64_t row = (r.page * a.nk + kh) * a.block_size + r.row;
+        at[u] = there ? row * a.D : -1;
         if (there) {
-          const int64_t i = scale_at(r.page, kh, r.row, a);
+          const int64_t i = row / a.per;
           ks[u] = power_of(ldg(g.k_scale + i, a.ks_span, g.err));
           vs[u] = power_of(ldg(g.v_scale + i, a.vs_span, g.err));
         }

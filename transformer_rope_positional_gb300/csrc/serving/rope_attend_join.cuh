@@ -227,7 +227,6 @@ inline cudaError_t arguments_of(const AttendProblem& p, int64_t e, int64_t ce, A
     if ((int64_t(1) << sh) == p.block_size) a.bs_shift = sh;
   a.P = (int32_t)p.prefix_len;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634074);
-  a.S = (int32_t)p.scale_blocks;
   a.per = p.scale_blocks ? (int32_t)(p.block_size / p.scale_blocks) : 1;
   const int64_t cache = p.num_blocks * p.nk * p.block_size * p.D * ce;
   a.q_span = make_span(p.query, ((p.T - 1) * p.q_stride + p.nq * p.D) * e);

@@ -113,9 +113,18 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
                : "memory");
 }
 
-template <typename T, int DP>
+// Two codes times a power of two, in the data's type: rounded where they are no numbers of it.
+template <typename T>
+__device__ __forceinline__ uint32_t scaled_codes(uint32_t two, float f) {
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&two));
+  const float2 y = __fmul2_rn(x, make_float2(f, f));
+  return pack2((const T*)nullptr, y.x, y.y);
+}
+
+// C: elements of the cache, T or Code.
+template <typename T, int DP, typename C>
 __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
-    attend_tc_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc, T* __restrict__ out,
+    attend_tc_kernel(const T* __restrict__ q, const C* __restrict__ kc, const C* __restrict__ vc, T* __restrict__ out,
                      float* __restrict__ lse, Pointers g, AttendArgs a, Cut c) {
   using S = TcShape<DP>;
   constexpr int KT = S::KT, NW = S::NW, NS = S::NS;
@@ -219,11 +228,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         }
         tc::bar_arrive_after_copies(&sm.q_copied);
       }
-      for (int n = 0; n < 2 * kt; ++n) {
-        // ---- K and V
-        const CopyItem it = copy_item(n, kt, lead);
-        if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
-        if (!__all_sync(0xffffffffu, ok)) break;
+      // The cache rows of the keys of copy n, one a lane (-1: none), with what is known of them: in the
+      // order of copies.
+      auto rows_of = [&](const CopyItem& it) {
         int now = rows[0];
         if (!it.is_v) {
           now = -1;
@@ -247,21 +254,86 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           for (int e = 0; e + 1 < S::kAhead; ++e) rows[e] = rows[e + 1];
           --waiting;
         }
-        const unsigned dst = tc::smem_at(sm.ring[stage]) + cw * S::KW * 128;
-        const T* const src = it.is_v ? vc : kc;
-        const Span& span = it.is_v ? a.v_span : a.k_span;
+        return now;
+      };
+      if constexpr (kCoded<C>) {
+        // Codes go through registers: a copy's are read while those before are widened, scaled and stored.
+        constexpr int CC = DP / 16;  // 16-byte pieces of a row of codes
+        uint4 codes[CC];
+        float factor = 0.f;  // of this lane's key
+        auto read = [&](int n) {
+          const CopyItem it = copy_item(n, kt, lead);
+          const int now = rows_of(it);
+          const Code* const src = it.is_v ? vc : kc;
+          const Span& span = it.is_v ? a.v_span : a.k_span;
+          factor = 0.f;
+          if (now >= 0)
+            factor = power_of(ldg((it.is_v ? g.v_scale : g.k_scale) + (uint32_t)now / (uint32_t)a.per,
+                                  it.is_v ? a.vs_span : a.ks_span, g.err));
 #pragma unroll
-        for (int i = 0; i < S::KW * CH / 32; ++i) {
-          const int idx = lane + 32 * i;
-          const int key = idx / CH, ch = idx - key * CH;
-          const int r = __shfl_sync(0xffffffffu, now, key);
-          const bool there = r >= 0 && ch * 8 < a.D;
-          const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 8 : 0));
-          cp_async16_or_zero(dst + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), p,
-                             there && access_ok(p, 16, span, g.err));
+          for (int i = 0; i < CC; ++i) {
+            const int idx = lane + 32 * i;
+            const int key = idx / CC, ch = idx - key * CC;
+            const int r = __shfl_sync(0xffffffffu, now, key);
+            const Code* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + ch * 16);
+            codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r >= 0 && ch * 16 < a.D && access_ok(p, 16, span, g.err))
+              codes[i] = __ldg(reinterpret_cast<const uint4*>(p));
+          }
+        };
+        if (kt > 0) read(0);
+        for (int n = 0; n < 2 * kt; ++n) {
+          uint4 x[CC];
+#pragma unroll
+          for (int i = 0; i < CC; ++i) x[i] = codes[i];
+          const float f = factor;
+          if (n + 1 < 2 * kt) read(n + 1);
+          if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          unsigned char* const to = sm.ring[stage] + cw * S::KW * 128;
+#pragma unroll
+          for (int i = 0; i < CC; ++i) {
+            const int idx = lane + 32 * i;
+            const int key = idx / CC, ch = 2 * (idx - key * CC);
+            const float fk = __shfl_sync(0xffffffffu, f, key);
+            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              halves(in[e], y[2 * e], y[2 * e + 1]);
+              y[2 * e] = scaled_codes<T>(y[2 * e], fk);
+              y[2 * e + 1] = scaled_codes<T>(y[2 * e + 1], fk);
+            }
+            unsigned char* const row = to + (ch >> 3) * (KT * 128) + key * 128;
+            *reinterpret_cast<uint4*>(row + (((ch & 7) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(row + ((((ch & 7) | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          tc::bar_arrive(&sm.copied[stage]);
+          if (++stage == NS) stage = 0, ++round;
         }
-        tc::bar_arrive_after_copies(&sm.copied[stage]);
-        if (++stage == NS) stage = 0, ++round;
+      } else {
+        for (int n = 0; n < 2 * kt; ++n) {
+          // ---- K and V
+          const CopyItem it = copy_item(n, kt, lead);
+          if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          const int now = rows_of(it);
+          const unsigned dst = tc::smem_at(sm.ring[stage]) + cw * S::KW * 128;
+          const T* const src = it.is_v ? vc : kc;
+          const Span& span = it.is_v ? a.v_span : a.k_span;
+#pragma unroll
+          for (int i = 0; i < S::KW * CH / 32; ++i) {
+            const int idx = lane + 32 * i;
+            const int key = idx / CH, ch = idx - key * CH;
+            const int r = __shfl_sync(0xffffffffu, now, key);
+            const bool there = r >= 0 && ch * 8 < a.D;
+            const T* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 8 : 0));
+            cp_async16_or_zero(dst + (ch >> 3) * (KT * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4), p,
+                               there && access_ok(p, 16, span, g.err));
+          }
+          tc::bar_arrive_after_copies(&sm.copied[stage]);
+          if (++stage == NS) stage = 0, ++round;
+        }
       }
       if (!__all_sync(0xffffffffu, ok)) break;
       walk_next<S::M, KT>(w, g, a, c);

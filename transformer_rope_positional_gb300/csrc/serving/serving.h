@@ -85,6 +85,14 @@ struct AttendProblem {
 
 cudaError_t launch_attend(const AttendProblem& p, cudaStream_t stream);
 cudaError_t launch_attend_codes(const AttendProblem& p, cudaStream_t stream);
+// (a part of it, by itself for the sake of the build's time)
+namespace attend {
+struct Pointers;
+struct AttendArgs;
+struct Cut;
+cudaError_t launch_codes_tall(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c,
+                              cudaStream_t stream);
+}  // namespace attend
 int64_t attend_codes_workspace(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, int64_t prefix_len);
 int64_t attend_workspace(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, int64_t prefix_len);
 
