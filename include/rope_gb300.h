@@ -82,7 +82,7 @@ typedef enum {
   ROPE_BF16 = 2, /* bfloat16 */
   ROPE_I64 = 3,  /* int64 (positions, slots, page numbers and the like) */
   ROPE_F8E4M3 = 4, /* 8-bit codes of a cache: sign, 4 exponent bits of bias 7, 3 of the fraction; 0x7f is NaN, no infinity */
-  ROPE_E8M0 = 5,   /* scales of a cache of codes: byte b is 2^(b - 127), 255 is NaN */
+  ROPE_E8M0 = 5,   /* scales of a cache of codes: byte b is 2^(b - 127), 255 is NaN; 0 here stands for 0 */
   ROPE_I32 = 6,    /* int32 (counts of holders of a page) */
   ROPE_U8 = 7      /* bytes of any meaning (rope_copy_pages) */
 } rope_dtype_t;
@@ -472,7 +472,7 @@ int rope_paged_attention_workspace(int64_t num_tokens, int64_t num_q_heads, int6
  * RoPE of query and key on the way to the query output and to a paged KV cache of 8-bit codes.
  *
  * A cached value is code * 2^(b - 127), b being the scale byte of its block: the BS / S tokens of a page (S scale
- * blocks a page) of one head.  The rotation is rope_append_paged_kv's, in binary32.  Then for every scale block that
+ * blocks a page) of one head; b = 0 is a block of zeros.  The rotation is rope_append_paged_kv's, in binary32.  Then for every scale block that
  * the call writes, of the keys and of the values,
  *   most = max |x| over its values written that are finite;  e = the least integer with most <= 448 * 2^e
  *   byte = e + 127, from 1 to 254;  0 where most = 0

@@ -1,7 +1,7 @@
 """Inputs, 64-bit references and error bounds of the operators on a paged cache of 8-bit codes, and plain
 references of those on its pages, for their tests.
 
-A cached value is code * 2^(byte - 127), exact in binary64.  Bounds beside those of serving_ref.py (e = 2^-24):
+A cached value is code * 2^(byte - 127), 0 times the code for byte 0, exact in binary64.  Bounds beside those of serving_ref.py (e = 2^-24):
 
 * append: x is off by 4 e |x| before it is coded (serving_ref.append_bound without the output's rounding), and a
   code is the nearest of E4M3's values: |value - x| <= step(x) / 2 + 4 e |x|, step being that of E4M3 at x in units
@@ -29,7 +29,7 @@ def e8m0(t):
 def values_of(codes, scale):
     """[NB, H, BS, D] codes and [NB, H, S] scales as float64 values."""
     b = bytes_of(scale).double()
-    f = torch.where(b == 255, torch.nan, torch.pow(2.0, b - 127))
+    f = torch.where(b == 255, torch.nan, torch.where(b == 0, 0.0, torch.pow(2.0, b - 127)))
     return bytes_of(codes).view(E4M3).double() * f.repeat_interleave(codes.shape[2] // scale.shape[2], 2)[..., None]
 
 

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads)
       int byte = byte_for(most);
       if (first > 0) {
         if (old < byte) {
-          const float f = power_of(max(127 + old - byte, 0));
+          const float f = old == 0 ? 0.f : power_of(max(127 + old - byte, 0));
           for (int i = 0; i < first; ++i)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {

@@ -93,7 +93,7 @@ template <typename T, int DP>
 cudaError_t launch_tc(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
                       cudaStream_t stream) {
   auto kernel = attend_tc_kernel<T, DP, T>;
-  const size_t smem = sizeof(TcShared<DP>);
+  const size_t smem = sizeof(TcShared<DP, false>);
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_overlapped_smem(kernel, (unsigned)grid, TcShape<DP>::kThreads, smem, stream,

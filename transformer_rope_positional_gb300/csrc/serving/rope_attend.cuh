@@ -27,6 +27,7 @@ struct AttendArgs {
   int32_t P;            // keys of the shared prefix
   float scale_log2;     // scale * log2(e)
   int32_t per;          // caches of codes: tokens of a scale block, so that cache row r has scale r / per
+  int32_t per_shift;    // log2(per), or -1
   Span q_span, k_span, v_span, bt_span, sl_span, qsl_span, pb_span, out_span, lse_span, ks_span, vs_span;
 };
 
@@ -46,16 +47,23 @@ struct Code {
 template <typename C>
 constexpr bool kCoded = std::is_same<C, Code>::value;
 
-// 2^(b - 127), exact; NaN for b = 255.
-__device__ __forceinline__ float power_of(uint32_t b) {
-  return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
-}
+// The scale that byte b stands for: 2^(b - 127), 0 for b = 0 (a block of zeros), NaN for 255.
+__device__ __forceinline__ float power_of(uint32_t b) { return __uint_as_float(b == 255 ? 0x7fc00000u : b << 23); }
 
 __device__ __forceinline__ float widen(Code c) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(c.bits, __NV_E4M3);
   return __half2float(__half(h));
 }
 using rope::widen;
+
+// 2^n for n from -126 to 127.
+__device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)(127 + n) << 23); }
+
+// The n, from -119 to 110, by whose power of two a query row with this largest magnitude is multiplied to be binary16:
+// the largest is in [2^8, 2^9) then, where it is not below 2^-102.  A row of zeros, and one that is not finite, as it is.
+__device__ __forceinline__ int row_power(float most) {
+  return most > 0.f && most <= FLT_MAX ? min(8 + 127 - (int)(__float_as_uint(most) >> 23), 110) : 0;
+}
 
 // Two codes as two binary16 values: the lower and the upper half of w.
 __device__ __forceinline__ void halves(uint32_t w, uint32_t& lower, uint32_t& upper) {

@@ -15,13 +15,16 @@ namespace {
 
 using namespace attend;
 
+constexpr int kMostShared = 228 * 1024;  // bytes of an SM, 1024 of them a CTA's own
 constexpr int kSmallRows = 16;  // of the larger of the small units
 
-Units units_of(int64_t M) {
+Units units_of(int64_t M, int64_t D, int32_t dtype) {
   Units u;
   u.tall = M > kSmallRows;
   u.M = M;
-  u.grid = (int64_t)sm_count() * (u.tall ? 1 : 2);
+  // (CodesShape's kCtas)
+  const int ctas = u.tall ? 1 : M == 8 && padded_columns(D) <= 128 && dtype != kF32 ? CodesShape<__half, 128, 8>::kCtas : 2;
+  u.grid = (int64_t)sm_count() * ctas;
   return u;
 }
 
@@ -29,23 +32,23 @@ int64_t tall_rows(int64_t D) { return padded_columns(D) <= 128 ? 256 : 128; }
 
 int64_t tile_keys(const Units& u, int64_t D) {
   const bool narrow = padded_columns(D) <= 128;
-  return u.tall ? (narrow ? 128 : 64) : narrow ? CodesShape<128>::KT : CodesShape<256>::KT;
+  return u.tall ? (narrow ? 128 : 64) : narrow ? CodesShape<float, 128, 8>::KT : CodesShape<float, 256, 8>::KT;
 }
 
 // The kernel for B sequences of `rows` rows a key head, on average, and up to `keys` keys.
 Units units_for(double rows, int64_t B, int64_t nk, int64_t keys, int64_t D, int32_t dtype) {
-  const Units u = units_of(rows <= 8 ? 8 : kSmallRows);
+  const Units u = units_of(rows <= 8 ? 8 : kSmallRows, D, dtype);
   if (rows <= 16 || dtype == kF32) return u;
   const double tiles = (rows / (double)u.M + 1) * (double)(B * nk) * (double)(keys / tile_keys(u, D) + 1);
   const double most = (double)u.grid * (256 / padded_columns(D));
-  return tiles <= most ? u : units_of(tall_rows(D));
+  return tiles <= most ? u : units_of(tall_rows(D), D, dtype);
 }
 
 // The largest part of the kernels': which one runs depends on the batch as well.
 int64_t part_bytes(int64_t T, int64_t nq, int64_t nk, int64_t D, int32_t dtype, bool dense) {
   int64_t most = 0;
   for (int64_t M : {(int64_t)8, (int64_t)kSmallRows, tall_rows(D)})
-    if (M <= kSmallRows || dtype != kF32) most = std::max(most, part_of(T, nq, nk, D, units_of(M), dense).bytes);
+    if (M <= kSmallRows || dtype != kF32) most = std::max(most, part_of(T, nq, nk, D, units_of(M, D, dtype), dense).bytes);
   return most;
 }
 
@@ -53,7 +56,9 @@ template <typename T, int DP, int MR>
 cudaError_t launch_small(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, int64_t grid,
                          cudaStream_t stream) {
   auto kernel = attend_codes_kernel<T, DP, MR>;
-  const size_t smem = sizeof(CodesShared<T, DP, MR>);
+  using Shape = CodesShape<T, DP, MR>;
+  constexpr size_t smem = sizeof(CodesShared<T, DP, MR>);
+  static_assert(smem <= (kMostShared - 1024 * Shape::kCtas) / Shape::kCtas, "so many CTAs share an SM");
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_overlapped_smem(kernel, (unsigned)grid, kCodesThreads, smem, stream, static_cast<const T*>(p.query),

@@ -20,6 +20,8 @@
 //    With binary32 they are two parts as well.
 #pragma once
 
+#include <climits>
+
 #include "rope_attend_mma.cuh"
 
 namespace rope {
@@ -27,32 +29,36 @@ namespace attend {
 
 constexpr int kCodesThreads = 128;
 
-// KW: keys that a warp takes of a tile.  Stages of its ring: as many as let two CTAs share an SM.
-template <int DP>
+// KW: keys that a warp takes of a tile.  Three CTAs an SM where registers and shared memory allow it (64 requests of up
+// to 8192 tokens, 8 rows: two 101 us, issue slots half used and hardly a wait for data), else two; as many stages of a
+// warp's ring as fit then.
+template <typename T, int DP, int MR>
 struct CodesShape {
   static constexpr int KW = DP <= 128 ? 32 : 16;
   static constexpr int KT = 4 * KW;
-  static constexpr int kStages = DP <= 64 ? 10 : DP <= 128 ? 5 : DP <= 192 ? 6 : 5;
+  static constexpr int kCtas = MR == 8 && DP <= 128 && sizeof(T) == 2 ? 3 : 2;
+  static constexpr int kStages = kCtas == 3 ? (DP <= 64 ? 7 : 4) : DP <= 64 ? 10 : DP <= 128 ? 5 : DP <= 192 ? 6 : sizeof(T) == 4 ? 4 : 5;
   static constexpr int kStage = KW * DP;  // bytes
-  static constexpr int kJoin = DP <= 128 ? 4 : 2;
-  static constexpr int kRecent = 8;  // tiles whose keys' scales are kept; at most kStages / 2 + 1 are under way
+  static constexpr int kJoin = DP <= 128 && kCtas == 2 ? 4 : 2;
+  static constexpr int kRecent = kStages <= 5 ? 4 : 8;  // tiles whose keys' scales are kept
+  static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;  // binary16 parts of a query
+  static_assert(kStages >= 4 && kStages / 2 + 2 <= kRecent, "a tile's scales are there before it is used");
 };
 
 template <typename T, int DP, int MR>
 struct CodesShared {
-  using S = CodesShape<DP>;
-  static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;  // binary16 parts of a query
+  using S = CodesShape<T, DP, MR>;
   alignas(1024) unsigned char ring[4][S::kStages][S::kStage];
   union {
     float o[4][S::kJoin][DP + 8];
     alignas(16) unsigned char q[MR * DP * sizeof(T)];
   };
   // query operands: of k step ks for lane l, MR = 16: four registers, 8: two
-  alignas(16) uint32_t operand[kParts][DP / 16][32][MR / 4];
-  float2 scales[4][S::kRecent][32];  // of a tile's keys: K's as a factor, V's byte as an integer
+  alignas(16) uint32_t operand[S::kParts][DP / 16][32][MR / 4];
+  float2 scales[4][S::kRecent][32];  // of a tile's keys: K's and V's
   uint2 there[4][S::kRecent];        // which keys are there, and the largest of V's bytes
-  float ml[4][16][2];
-  int power[16];                     // rows are times 2^power
+  float ml[4][MR][2];
+  int power[MR];                     // rows are times 2^power
   int bad;                           // some finished row is not finite
   int64_t tmp[kCodesThreads / 32 + 2];
 };
@@ -67,15 +73,14 @@ __device__ __forceinline__ int piece_at(int r, int ch) {
 }
 
 // A warp's own pipeline of K and V codes (see rope_attend_ring.cuh), and of their scales.
-template <int DP, int MR>
+template <typename T, int DP, int MR>
 struct CodesRing {
-  using S = CodesShape<DP>;
+  using S = CodesShape<T, DP, MR>;
   static constexpr int CH = DP / 16;
 
   Walk pw;            // unit of the next copy
-  int pk, pend;       // its tile, and where the unit's keys end
+  int pk, pk1, pend;  // its tile, the end of the unit's tiles here, and where its keys end
   int slot;           // stage of the next copy
-  bool next_v;        // it is V
   PageRow page;       // of this lane's key of the next tile
   int row;            // cache row of the key of the tile whose K was copied last
   int made;           // tiles whose K was copied
@@ -97,9 +102,9 @@ struct CodesRing {
                                         const AttendArgs& a, const Cut& c) {
     pw = w;
     pk = pw.k0;
+    pk1 = walk_k1(pw, c);
     pend = tile_end<MR>(pw.s, pw.i, a, c);
     slot = cur = tile = made = 0;
-    next_v = false;
     row = -1;
     kb = vb = 0;
     ring = at;
@@ -108,17 +113,18 @@ struct CodesRing {
     look_up(g, a, c);
   }
 
+  // IS_V: of V, else of the next tile's K: they take turns, and the caller knows whose it is.
+  template <bool IS_V>
   __device__ __forceinline__ void copy(const Code* __restrict__ kc, const Code* __restrict__ vc, const Pointers& g,
                                        const AttendArgs& a, const Cut& c) {
     const int lane = threadIdx.x & 31;
-    if (!next_v) {
+    if constexpr (!IS_V) {
       // the scales of the tile before have arrived
       if (made > 0) {
         const int at = (made - 1) & (S::kRecent - 1);
-        const bool is_there = row >= 0;
-        const uint32_t which = __ballot_sync(0xffffffffu, is_there);
-        const uint32_t most = __reduce_max_sync(0xffffffffu, is_there && vb != 255 ? vb : 0);
-        scales[at][lane] = make_float2(power_of(kb), __int_as_float((int)vb));
+        const uint32_t which = __ballot_sync(0xffffffffu, row >= 0);
+        const uint32_t most = __reduce_max_sync(0xffffffffu, vb != 255 ? vb : 0);
+        scales[at][lane] = make_float2(power_of(kb), power_of(vb));
         if (lane == 0) there[at] = make_uint2(which, most);
       }
       ++made;
@@ -126,80 +132,91 @@ struct CodesRing {
       kb = vb = 0;
       if (page.page >= 0 && page.page < a.num_blocks) {
         row = ((int)page.page * a.nk + pw.h) * a.block_size + page.row;
-        const uint32_t z = (uint32_t)row / (uint32_t)a.per;
+        const uint32_t z = a.per_shift >= 0 ? (uint32_t)row >> a.per_shift : (uint32_t)row / (uint32_t)a.per;
         kb = ldg(g.k_scale + z, a.ks_span, g.err);
         vb = ldg(g.v_scale + z, a.vs_span, g.err);
       } else if (page.page != -2) {
         atomicOr(g.err, kSlotOutOfRange);
       }
       if (!pw.done) {
-        if (++pk == walk_k1(pw, c)) {
+        if (++pk == pk1) {
           walk_next<MR, S::KT>(pw, g, a, c);
           pk = pw.k0;
-          if (!pw.done) pend = tile_end<MR>(pw.s, pw.i, a, c);
+          if (!pw.done) {
+            pk1 = walk_k1(pw, c);
+            pend = tile_end<MR>(pw.s, pw.i, a, c);
+          }
         }
       }
       look_up(g, a, c);
     }
-    const Code* const src = next_v ? vc : kc;
-    const Span& span = next_v ? a.v_span : a.k_span;
+    const Code* const src = IS_V ? vc : kc;
+    const Span& span = IS_V ? a.v_span : a.k_span;
     unsigned char* const to = ring + slot * S::kStage;
-    if (__any_sync(0xffffffffu, row >= 0)) {
-      const unsigned dst = smem_u32(to);
+    const uint32_t which = __ballot_sync(0xffffffffu, row >= 0);
+    const unsigned dst = smem_u32(to);
+    if (which == (uint32_t)((1ull << S::KW) - 1) && a.D == DP) {  // whole rows of all keys
 #pragma unroll
+      for (int i = 0; i < S::KW * CH / 32; ++i) {
+        const int idx = lane + 32 * i;
+        const int key = idx / CH, ch = idx - key * CH;
+        const int r = __shfl_sync(0xffffffffu, row, key);
+        const Code* p = src + ch * 16 + (uint64_t)(uint32_t)r * (uint32_t)DP;
+        if (access_ok(p, 16, span, g.err))
+          cp_async16_or_zero(dst + piece_at<DP, IS_V>(key, ch), p, true);
+      }
+    } else if (which) {
+#pragma unroll 1
       for (int i = 0; i < S::KW * CH / 32; ++i) {
         const int idx = lane + 32 * i;
         const int key = idx / CH, ch = idx - key * CH;
         const int r = __shfl_sync(0xffffffffu, row, key);
         const bool ok = r >= 0 && ch * 16 < a.D;
         const Code* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (ok ? ch * 16 : 0));
-        cp_async16_or_zero(dst + (next_v ? piece_at<DP, true>(key, ch) : piece_at<DP, false>(key, ch)), p,
+        cp_async16_or_zero(dst + piece_at<DP, IS_V>(key, ch), p,
                            ok && access_ok(p, 16, span, g.err));
       }
-    } else if (next_v) {  // no key of the tile: its weights are 0, and V must not be NaN
+    } else if (IS_V) {  // no key of the tile: its weights are 0, and V must not be NaN
 #pragma unroll
       for (int i = 0; i < S::KW * CH / 32; ++i)
         *reinterpret_cast<uint4*>(to + (lane + 32 * i) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
-    next_v = !next_v;
     cp_async_commit();
     slot = slot + 1 == S::kStages ? 0 : slot + 1;
   }
 
   // The next stage, once its copies are there (and its last readers done: the caller has
-  // converged the warp after them); another copy is issued into the stage before it.
+  // converged the warp after them); another copy, IS_V or not, is issued into the stage before it.
+  template <bool IS_V>
   __device__ __forceinline__ const unsigned char* take(const Code* __restrict__ kc, const Code* __restrict__ vc,
                                                        const Pointers& g, const AttendArgs& a, const Cut& c) {
-    copy(kc, vc, g, a, c);
+    copy<IS_V>(kc, vc, g, a, c);
     const unsigned char* at = ring + cur * S::kStage;
     cur = cur + 1 == S::kStages ? 0 : cur + 1;
     return at;
   }
 };
 
-// A weight that is taken as 0 in the product with V (not in l).  Above it the scales of V may be 2^15 below the
-// largest before: then binary16 has too few exponents for the weight, O is made NaN, and mend_rows finds the row.
+// Where some key's V is in units of less than 2^-15 of the largest, binary16 has too few exponents for its weight: it is
+// made NaN, and mend_rows finds the row, unless it is as small as this, which is taken as 0 (not in l).
 constexpr float kNoWeight = 0x1p-30f;
-
-// 2^n for n from -126 to 127.
-__device__ __forceinline__ float power(int n) { return __uint_as_float((uint32_t)(127 + n) << 23); }
 
 // DP: D rounded up to a multiple of 64; columns past D are zeros in shared memory.
 // MR: rows of a unit, 16 or 8.
 template <typename T, int DP, int MR>
-__global__ void __launch_bounds__(kCodesThreads, 2)
+__global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
     attend_codes_kernel(const T* __restrict__ q, const Code* __restrict__ kc, const Code* __restrict__ vc,
                         T* __restrict__ out, float* __restrict__ lse, Pointers g, AttendArgs a, Cut c) {
-  using Shape = CodesShape<DP>;
+  using Shape = CodesShape<T, DP, MR>;
   using Shared = CodesShared<T, DP, MR>;
   constexpr int S = Shape::kStages, KW = Shape::KW, KT = Shape::KT;
   constexpr int KS = DP / 16;        // k steps of the score product
   constexpr int MT = KW / 16;        // products of 16 keys
-  constexpr int QP = Shared::kParts;
+  constexpr int QP = Shape::kParts;
   constexpr bool kEight = MR == 8;
-  constexpr bool kHoldQ = KS * QP * (MR / 4) <= 64;  // the queries' operands stay in registers
+  constexpr int NO = kEight ? DP / 16 : DP / 8;
+  constexpr bool kHoldQ = KS * QP * (MR / 4) + NO * 4 <= 160;  // the queries' operands stay in registers
   constexpr int VEC = 16 / sizeof(T), CHT = DP / VEC;  // 16-byte pieces of a query row
-  static_assert(S >= 4 && S / 2 + 2 <= Shape::kRecent, "a tile's scales are there before it is used");
   extern __shared__ __align__(1024) unsigned char raw[];
   Shared& sm = *reinterpret_cast<Shared*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -208,7 +225,7 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
   if (w.done) return;
   if (threadIdx.x == 0) sm.bad = 0;
 
-  CodesRing<DP, MR> ring;
+  CodesRing<T, DP, MR> ring;
   ring.start(w, sm.ring[warp][0], sm.scales[warp], sm.there[warp], g, a, c);
   // a unit's query rows, in 16-byte pieces of this thread: read while the unit before ends
   constexpr int NQ = (MR * CHT + kCodesThreads - 1) / kCodesThreads;
@@ -230,9 +247,23 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
 
   read_q(w);
 #pragma unroll 1
-  for (int i = 0; i < S - 1; ++i) ring.copy(kc, vc, g, a, c);
+  for (int i = 0; i < S - 1; i += 2) {
+    ring.template copy<false>(kc, vc, g, a, c);
+    if (i + 1 < S - 1) ring.template copy<true>(kc, vc, g, a, c);
+  }
+  // (S - 1 copies are ahead: with S even the one that is issued when a K is taken is a V's)
 
   const int r0 = lane >> 2, cl = lane & 3, cq = cl * 2;
+  // where this lane reads in a stage: key r0 (and r0 + 8, ...) of K; keys cq (and cq + 1, cq + 8, ...) of V
+  unsigned k_at[DP / 64], v_at[DP / 64];
+#pragma unroll
+  for (int i = 0; i < DP / 64; ++i) {
+    k_at[i] = piece_at<DP, false>(r0, 4 * i + cl);
+    v_at[i] = piece_at<DP, true>(cq, 4 * i + (r0 >> 1)) + (r0 & 1) * 8;
+  }
+  // (8 keys further the same place of a row 8 rows down; the next key, where it is even, too: for rows of 64 bytes the
+  // other half of the pair)
+  const int next_key = DP == 64 ? piece_at<DP, true>(cq + 1, 0) - piece_at<DP, true>(cq, 0) : DP;
 
   while (!w.done) {
     const UnitRows u = unit_rows<MR>(w, a);
@@ -251,10 +282,7 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
         for (int d = threadIdx.x & 7; d < DP; d += 8) most = fmaxf(most, fabsf(widen(qs[r * DP + d])));
 #pragma unroll
         for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-        // (a row of zeros, and one that is not finite, as it is)
-        int n = 0;
-        if (most > 0.f && most <= FLT_MAX) n = min(8 + 127 - (int)(__float_as_uint(most) >> 23), 110);
-        if ((threadIdx.x & 7) == 0) sm.power[r] = n;
+        if ((threadIdx.x & 7) == 0) sm.power[r] = row_power(most);
       }
       __syncthreads();
     }
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
     }
     // this lane's two rows, their limits and their factors
     const int ra = kEight ? cq : r0, rb = kEight ? cq + 1 : r0 + 8;
-    int lim0 = lane < u.rows ? row_limit(w, row_at(u, lane, w.h, a).t, g, a, c) : 0;
+    int lim0 = lane < u.rows ? row_limit(w, row_at(u, lane, w.h, a).t, g, a, c) : INT_MAX;  // (no such row: any result)
     const int lim1 = __shfl_sync(0xffffffffu, lim0, rb);
     lim0 = __shfl_sync(0xffffffffu, lim0, ra);
     float fac0 = a.scale_log2, fac1 = a.scale_log2;
@@ -310,17 +338,16 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
     }
     const int k1 = walk_k1(w, c);
 
-    constexpr int NO = kEight ? DP / 16 : DP / 8;
     float o[NO][4];  // kEight: columns by rows
 #pragma unroll
     for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    int unit = 0;  // O is in units of 2^(unit - 127 - 15)
+    int unit = 15;  // O is in units of 2^(unit - 142): V's largest byte so far, at least 15
 
     for (int k = w.k0; k < k1; ++k) {
       cp_async_wait<S - 2>();
       __syncwarp();
-      const unsigned char* const kt = ring.take(kc, vc, g, a, c);
+      const unsigned char* const kt = ring.template take<S % 2 == 0>(kc, vc, g, a, c);
       const int at = ring.tile++ & (Shape::kRecent - 1);
       const uint2 about = sm.there[warp][at];
       const int j0 = c.lo + k * KT + warp * KW;
@@ -334,8 +361,8 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
       for (int i = 0; i < DP / 64; ++i) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kt + piece_at<DP, false>(mt * 16 + r0, 4 * i + cl));
-          const uint4 y = *reinterpret_cast<const uint4*>(kt + piece_at<DP, false>(mt * 16 + r0 + 8, 4 * i + cl));
+          const uint4 x = *reinterpret_cast<const uint4*>(kt + k_at[i] + mt * 16 * DP);
+          const uint4 y = *reinterpret_cast<const uint4*>(kt + k_at[i] + (mt * 16 + 8) * DP);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             uint32_t f[4];  // keys r0: 0 and 2, r0 + 8: 1 and 3
@@ -360,29 +387,48 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
           }
         }
       }
-      // ---- scales, unseen keys, maximum
-      float vf[MT][kEight ? 2 : 4];  // V's bytes, then factors, of this lane's keys
-      float t0 = m0, t1 = m1;
+      // ---- K's scales, unseen keys, maximum
+      constexpr int NK = kEight ? 2 : 4;  // keys of this lane in each 16
+      auto score = [&](int mt, int e, int row) -> float& {
+        return kEight ? s[mt][0][2 * e + row] : s[mt][e >> 1][2 * row + (e & 1)];
+      };
+      auto key_of = [&](int mt, int e) { return mt * 16 + (kEight ? r0 + e * 8 : (e >> 1) * 8 + cq + (e & 1)); };
+      float vf[MT][NK];  // V's scales of this lane's keys
+      float t0 = -INFINITY, t1 = -INFINITY;
+      const bool open = __all_sync(0xffffffffu, about.x == (uint32_t)((1ull << KW) - 1) && j0 + KW <= min(lim0, lim1));
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < (kEight ? 2 : 4); ++e) {
-          const int i = mt * 16 + (kEight ? r0 + e * 8 : (e >> 1) * 8 + cq + (e & 1));
-          const float2 z = sm.scales[warp][at][i];
-          const bool in = (about.x >> i) & 1;
+        for (int e = 0; e < NK; ++e) {
+          const float2 z = sm.scales[warp][at][key_of(mt, e)];
           vf[mt][e] = z.y;
-          float& x = kEight ? s[mt][0][2 * e] : s[mt][e >> 1][e & 1];
-          float& y = kEight ? s[mt][0][2 * e + 1] : s[mt][e >> 1][2 + (e & 1)];
-          x = in && j0 + i < lim0 ? x * z.x * fac0 : -INFINITY;
-          y = in && j0 + i < lim1 ? y * z.x * fac1 : -INFINITY;
-          t0 = fmaxf(t0, x);
-          t1 = fmaxf(t1, y);
+          score(mt, e, 0) *= z.x;
+          score(mt, e, 1) *= z.x;
+        }
+      if (!open)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < NK; ++e) {
+            const int i = key_of(mt, e);
+            const bool in = (about.x >> i) & 1;
+            if (!in || j0 + i >= lim0) score(mt, e, 0) = -INFINITY;
+            if (!in || j0 + i >= lim1) score(mt, e, 1) = -INFINITY;
+          }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < NK; ++e) {
+          t0 = fmaxf(t0, score(mt, e, 0));
+          t1 = fmaxf(t1, score(mt, e, 1));
         }
 #pragma unroll
       for (int d = kEight ? 4 : 1; d < (kEight ? 32 : 4); d *= 2) {
         t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
         t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
       }
+      t0 = fmaxf(m0, t0 * fac0);  // (-infinity stays: the factors are > 0)
+      t1 = fmaxf(m1, t1 * fac1);
       const float b0 = t0 == -INFINITY ? 0.f : t0, b1 = t1 == -INFINITY ? 0.f : t1;
       const bool bigger = (int)about.y > unit;  // V's unit grows
       if (__any_sync(0xffffffffu, t0 != m0 || t1 != m1 || bigger)) {  // some row's maximum grew
@@ -407,24 +453,40 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
         }
       }
       // ---- weights: the operands of the product with V
+      const float to_unit = power(142 - unit);
+      bool lost = false;  // V's scale is NaN, or too small for the weight's exponents
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < NK; ++e) {
+          const float f = vf[mt][e] * to_unit;
+          vf[mt][e] = f >= 1.f || vf[mt][e] == 0.f ? f : NAN;
+          lost = lost || vf[mt][e] != vf[mt][e];
+        }
+      lost = __any_sync(0xffffffffu, lost);
       uint32_t p[QP][MT][kEight ? 2 : 4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        float e0[kEight ? 2 : 4], e1[kEight ? 2 : 4];
+        float e0[NK], e1[NK];
 #pragma unroll
-        for (int e = 0; e < (kEight ? 2 : 4); ++e) {
-          const float x = kEight ? s[mt][0][2 * e] : s[mt][e >> 1][e & 1];
-          const float y = kEight ? s[mt][0][2 * e + 1] : s[mt][e >> 1][2 + (e & 1)];
-          e0[e] = fast_exp2(x - b0);
-          e1[e] = fast_exp2(y - b1);
+        for (int e = 0; e < NK; ++e) {
+          e0[e] = fast_exp2(fmaf(score(mt, e, 0), fac0, -b0));
+          e1[e] = fast_exp2(fmaf(score(mt, e, 1), fac1, -b1));
           l0 += e0[e];
           l1 += e1[e];
-          // (a block's byte is 0 where its values are; of weights below 2^-30 nothing is asked)
-          const int byte = __float_as_int(vf[mt][e]), n = byte - unit + 15;
-          const float f = byte == 255 || (n < 0 && byte > 0) ? NAN : n < -126 ? 0.f : power(n);
-          e0[e] = e0[e] > kNoWeight || e0[e] != e0[e] ? e0[e] * f : 0.f;
-          e1[e] = e1[e] > kNoWeight || e1[e] != e1[e] ? e1[e] * f : 0.f;
         }
+        if (lost)
+#pragma unroll
+          for (int e = 0; e < NK; ++e) {
+            e0[e] = e0[e] <= kNoWeight ? 0.f : e0[e] * vf[mt][e];
+            e1[e] = e1[e] <= kNoWeight ? 0.f : e1[e] * vf[mt][e];
+          }
+        else
+#pragma unroll
+          for (int e = 0; e < NK; ++e) {
+            e0[e] *= vf[mt][e];
+            e1[e] *= vf[mt][e];
+          }
 #pragma unroll
         for (int part = 0; part < QP; ++part) {
           if constexpr (kEight) {  // (rows, keys) from (keys, rows)
@@ -448,7 +510,7 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
       // ---- outputs: this lane has keys cq, cq + 1, cq + 8, cq + 9 of every 16, and columns 8 r0 + 64 i .. + 7
       cp_async_wait<S - 2>();
       __syncwarp();
-      const unsigned char* const vt = ring.take(kc, vc, g, a, c);
+      const unsigned char* const vt = ring.template take<S % 2 != 0>(kc, vc, g, a, c);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -456,8 +518,7 @@ __global__ void __launch_bounds__(kCodesThreads, 2)
           uint2 v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[e] = *reinterpret_cast<const uint2*>(
-                vt + piece_at<DP, true>(mt * 16 + cq + (e & 1) + (e >> 1) * 8, 4 * i + (r0 >> 1)) + (r0 & 1) * 8);
+            v[e] = *reinterpret_cast<const uint2*>(vt + v_at[i] + (mt * 16 + (e >> 1) * 8) * DP + (e & 1 ? next_key : 0));
 #pragma unroll
           for (int t = 0; t < 4; ++t) {  // two columns
             const uint32_t x0 = t < 2 ? v[0].x : v[0].y, x1 = t < 2 ? v[1].x : v[1].y;

@@ -222,12 +222,14 @@ inline cudaError_t arguments_of(const AttendProblem& p, int64_t e, int64_t ce, A
   a.G = (int32_t)(p.nq / p.nk);
   a.D = (int32_t)p.D;
   a.block_size = (int32_t)p.block_size;
-  a.bs_shift = -1;
-  for (int sh = 0; sh < 31; ++sh)
+  a.per = p.scale_blocks ? (int32_t)(p.block_size / p.scale_blocks) : 1;
+  a.bs_shift = a.per_shift = -1;
+  for (int sh = 0; sh < 31; ++sh) {
     if ((int64_t(1) << sh) == p.block_size) a.bs_shift = sh;
+    if ((int64_t(1) << sh) == a.per) a.per_shift = sh;
+  }
   a.P = (int32_t)p.prefix_len;
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634074);
-  a.per = p.scale_blocks ? (int32_t)(p.block_size / p.scale_blocks) : 1;
   const int64_t cache = p.num_blocks * p.nk * p.block_size * p.D * ce;
   a.q_span = make_span(p.query, ((p.T - 1) * p.q_stride + p.nq * p.D) * e);
   a.k_span = make_span(p.k_cache, cache);

@@ -63,8 +63,20 @@ struct TcShape {
   static constexpr int kO = 256;                    // first column of O; the second O follows
 };
 
-template <int DP>
-struct TcShared {
+// What the units over a cache of codes keep besides: of the last 16 K tiles, 32 keys at a time, the scales that their
+// codes are in units of (bytes of K's and of V's, and whether some key's is too far below); of the rows of this unit and
+// the next, the power of two that they are times; the unit of the second group's O.
+template <bool CODED>
+struct TcMore {};
+template <>
+struct TcMore<true> {
+  uint32_t units[16][4];
+  signed char power[2][256];
+  int second;
+};
+
+template <int DP, bool CODED>
+struct TcShared : TcMore<CODED> {
   using S = TcShape<DP>;
   alignas(1024) unsigned char ring[S::NS][S::kStage];
   alignas(1024) unsigned char q[S::NW][S::kQ];
@@ -113,13 +125,21 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
                : "memory");
 }
 
-// Two codes times a power of two, in the data's type: rounded where they are no numbers of it.
-template <typename T>
-__device__ __forceinline__ uint32_t scaled_codes(uint32_t two, float f) {
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&two));
-  const float2 y = __fmul2_rn(x, make_float2(f, f));
-  return pack2((const T*)nullptr, y.x, y.y);
+// Two binary16 values times another.
+__device__ __forceinline__ uint32_t times(uint32_t x, __half2 f) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), f);
+  return *reinterpret_cast<const uint32_t*>(&y);
 }
+
+// Caches of codes.  All operands are binary16: codes are widened, two an instruction, by the copying warps, which take
+// them through registers.  A product sees scales only relative to the largest of 32 keys, up to 2^-15 of it, which
+// binary16 holds exactly; that largest is one factor of 32 scores for K, and for V a term in the exponents of 32
+// weights: with B the largest of V's so far, weights are e^(s - m) 2^(V's - B), O is in units of 2^B (and multiplied by
+// 2^(B_old - B) where B grows) and the sum of 32 weights goes into l times 2^(B - V's).  So the softmax costs nothing more
+// per score.  Rows of bfloat16 queries are multiplied by powers of two as in rope_attend_codes_mma.cuh.
+// Where scales are further apart (a key's from its 32 keys', or V's from B by more than kSpread), rows that see such
+// keys are made NaN, for mend_rows to find.
+constexpr int kSpread = 10;
 
 // C: elements of the cache, T or Code.
 template <typename T, int DP, typename C>
@@ -130,7 +150,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
   constexpr int KT = S::KT, NW = S::NW, NS = S::NS;
   constexpr int CH = DP / 8;
   extern __shared__ __align__(1024) unsigned char raw[];
-  TcShared<DP>& sm = *reinterpret_cast<TcShared<DP>*>(raw);
+  constexpr bool kCodes = kCoded<C>;
+  using M = typename std::conditional<kCodes, __half, T>::type;  // the operands
+  TcShared<DP, kCodes>& sm = *reinterpret_cast<TcShared<DP, kCodes>*>(raw);
   const int tid = threadIdx.x, warp = (int)tc::uniform(tid >> 5), lane = tid & 31;
   constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + S::kCopy / 32,
                 kRelayWarp = kMmaWarp + 1;
@@ -195,7 +217,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       const int end = tile_end<S::M>(w.s, w.i, a, c);
       const int64_t* table = g.block_table + w.b * a.W;
       PageRow page;                    // of this lane's key of the next K tile
-      int rows[S::kAhead];             // cache rows of its keys of the K tiles whose V has not followed
+      int rows[S::kAhead] = {};        // cache rows of its keys of the K tiles whose V has not followed
       int waiting = 0;                 // so many
       auto look_up = [&](int tile) {
         const int j = c.lo + (w.k0 + tile) * KT + cw * S::KW + lane;
@@ -216,17 +238,63 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         const T* p = q + at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8;
         const int64_t next_token = a.q_stride - (int64_t)a.G * a.D;
         unsigned dst = tc::smem_at(sm.q[0]) + (ch >> 3) * (128 * 128);
-#pragma unroll 4
-        for (int r = ct / CH; r < 128 * nt; r += kStep) {
-          const bool there = r < u.rows && ch * 8 < a.D;
-          const int rr = r & 127;
-          cp_async16_or_zero(dst + (NW == 2 ? r >> 7 : 0) * S::kQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
-                             there ? p : q, there && access_ok(p, 16, a.q_span, g.err));
-          p += kStep * a.D;
-          head += kStep;
-          while (head >= a.G) head -= a.G, p += next_token;
+        if constexpr (kCodes && !std::is_same<T, __half>::value) {
+          // through registers: rows are brought to binary16's range
+          constexpr int U = 4;
+#pragma unroll 1
+          for (int r1 = ct / CH; r1 < 128 * nt; r1 += U * kStep) {
+            uint4 x[U];
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+              const int r = r1 + e * kStep;
+              x[e] = make_uint4(0u, 0u, 0u, 0u);
+              if (r < u.rows && ch * 8 < a.D && access_ok(p, 16, a.q_span, g.err))
+                x[e] = __ldg(reinterpret_cast<const uint4*>(p));
+              p += kStep * a.D;
+              head += kStep;
+              while (head >= a.G) head -= a.G, p += next_token;
+            }
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+              const int r = r1 + e * kStep, rr = r & 127;
+              const uint32_t w4[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+              float f[8], most = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f[2 * i] = __uint_as_float(w4[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w4[i] & 0xffff0000u);
+                most = fmaxf(most, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+              }
+#pragma unroll
+              for (int d = 1; d < CH; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+              const int n = row_power(most);
+              const float up = power(n);
+              uint4 y;
+              y.x = pack2((const __half*)nullptr, f[0] * up, f[1] * up);
+              y.y = pack2((const __half*)nullptr, f[2] * up, f[3] * up);
+              y.z = pack2((const __half*)nullptr, f[4] * up, f[5] * up);
+              y.w = pack2((const __half*)nullptr, f[6] * up, f[7] * up);
+              unsigned char* const to = sm.q[NW == 2 ? r >> 7 : 0] + (ch >> 3) * (128 * 128) + rr * 128;
+              *reinterpret_cast<uint4*>(to + (((ch & 7) ^ (rr & 7)) << 4)) = y;
+              if (ch == 0) sm.power[(unit - 1) & 1][r] = (signed char)n;
+            }
+          }
+          __syncwarp();  // (the powers are there for who sees this warp's next arrivals)
+        } else {
+        unsigned dst = tc::smem_at(sm.q[0]) + (ch >> 3) * (128 * 128);
+  #pragma unroll 4
+          for (int r = ct / CH; r < 128 * nt; r += kStep) {
+            const bool there = r < u.rows && ch * 8 < a.D;
+            const int rr = r & 127;
+            cp_async16_or_zero(dst + (NW == 2 ? r >> 7 : 0) * S::kQ + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                               there ? p : q, there && access_ok(p, 16, a.q_span, g.err));
+            p += kStep * a.D;
+            head += kStep;
+            while (head >= a.G) head -= a.G, p += next_token;
+          }
         }
-        tc::bar_arrive_after_copies(&sm.q_copied);
+        if constexpr (kCodes && !std::is_same<T, __half>::value) tc::bar_arrive(&sm.q_copied);
+        else tc::bar_arrive_after_copies(&sm.q_copied);
       }
       // The cache rows of the keys of copy n, one a lane (-1: none), with what is known of them: in the
       // order of copies.
@@ -242,12 +310,14 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           for (int e = 0; e < S::kAhead; ++e)
             if (e == waiting) rows[e] = now;
           ++waiting;
-          const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
-          if (lane == 0) {
-            sm.seen[k_count & 15][cw] = there;
-            tc::bar_arrive(&sm.seen_full[k_count & 15]);
+          if constexpr (!kCodes) {
+            const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
+            if (lane == 0) {
+              sm.seen[k_count & 15][cw] = there;
+              tc::bar_arrive(&sm.seen_full[k_count & 15]);
+            }
+            ++k_count;
           }
-          ++k_count;
           look_up(it.tile + 1);
         } else {
 #pragma unroll
@@ -256,20 +326,29 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         }
         return now;
       };
-      if constexpr (kCoded<C>) {
-        // Codes go through registers: a copy's are read while those before are widened, scaled and stored.
+      if constexpr (kCodes) {
+        // Codes go through registers: a copy's are read while those before are widened and stored.
         constexpr int CC = DP / 16;  // 16-byte pieces of a row of codes
         uint4 codes[CC];
-        float factor = 0.f;  // of this lane's key
+        bool is_there = false, is_v = false;  // this lane's key of the copy that is read, and whose it is
+        uint32_t kb = 0, vb = 0;              // its scales
+        __half2 v_factor[S::kAhead];          // of the K tiles whose V has not followed
+        int behind = 0;                       // so many
         auto read = [&](int n) {
           const CopyItem it = copy_item(n, kt, lead);
           const int now = rows_of(it);
           const Code* const src = it.is_v ? vc : kc;
           const Span& span = it.is_v ? a.v_span : a.k_span;
-          factor = 0.f;
-          if (now >= 0)
-            factor = power_of(ldg((it.is_v ? g.v_scale : g.k_scale) + (uint32_t)now / (uint32_t)a.per,
-                                  it.is_v ? a.vs_span : a.ks_span, g.err));
+          is_v = it.is_v;
+          if (!it.is_v) {
+            is_there = now >= 0;
+            kb = vb = 0;
+            if (is_there) {
+              const uint32_t z = a.per_shift >= 0 ? (uint32_t)now >> a.per_shift : (uint32_t)now / (uint32_t)a.per;
+              kb = ldg(g.k_scale + z, a.ks_span, g.err);
+              vb = ldg(g.v_scale + z, a.vs_span, g.err);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < CC; ++i) {
             const int idx = lane + 32 * i;
@@ -281,28 +360,59 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
               codes[i] = __ldg(reinterpret_cast<const uint4*>(p));
           }
         };
+        // byte b relative to the largest, as a factor: exact down to 2^-15
+        auto relative = [&](uint32_t b, uint32_t most) {
+          const float f = b == 255 ? NAN : b == 0 || most - b > 24 ? 0.f : power(-(int)(most - b));
+          return __float2half2_rn(f);
+        };
         if (kt > 0) read(0);
         for (int n = 0; n < 2 * kt; ++n) {
           uint4 x[CC];
 #pragma unroll
           for (int i = 0; i < CC; ++i) x[i] = codes[i];
-          const float f = factor;
+          __half2 f;
+          if (!is_v) {
+            const uint32_t there = __ballot_sync(0xffffffffu, is_there);
+            uint32_t km = __reduce_max_sync(0xffffffffu, kb == 255 ? 0u : kb);
+            uint32_t vm = __reduce_max_sync(0xffffffffu, vb == 255 ? 0u : vb);
+            const bool far = __any_sync(0xffffffffu, (kb > 0 && kb + 15 < km) || (vb > 0 && vb + 15 < vm));
+            if (km == 0) km = 127;  // zeros, or no key: in any units
+            f = relative(kb, km);
+            const __half2 fv = relative(vb, vm);
+#pragma unroll
+            for (int e = 0; e < S::kAhead; ++e)
+              if (e == behind) v_factor[e] = fv;
+            ++behind;
+            if (lane == 0) {
+              sm.seen[k_count & 15][cw] = there;
+              sm.units[k_count & 15][cw] = km | vm << 8 | (uint32_t)far << 16;
+              tc::bar_arrive(&sm.seen_full[k_count & 15]);
+            }
+            ++k_count;
+          } else {
+            f = v_factor[0];
+#pragma unroll
+            for (int e = 0; e + 1 < S::kAhead; ++e) v_factor[e] = v_factor[e + 1];
+            --behind;
+          }
           if (n + 1 < 2 * kt) read(n + 1);
           if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
           if (!__all_sync(0xffffffffu, ok)) break;
           unsigned char* const to = sm.ring[stage] + cw * S::KW * 128;
+          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&f);
 #pragma unroll
           for (int i = 0; i < CC; ++i) {
             const int idx = lane + 32 * i;
             const int key = idx / CC, ch = 2 * (idx - key * CC);
-            const float fk = __shfl_sync(0xffffffffu, f, key);
+            const uint32_t fk = __shfl_sync(0xffffffffu, bits, key);
+            const __half2 fh = *reinterpret_cast<const __half2*>(&fk);
             const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             uint32_t y[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               halves(in[e], y[2 * e], y[2 * e + 1]);
-              y[2 * e] = scaled_codes<T>(y[2 * e], fk);
-              y[2 * e + 1] = scaled_codes<T>(y[2 * e + 1], fk);
+              y[2 * e] = times(y[2 * e], fh);
+              y[2 * e + 1] = times(y[2 * e + 1], fh);
             }
             unsigned char* const row = to + (ch >> 3) * (KT * 128) + key * 128;
             *reinterpret_cast<uint4*>(row + (((ch & 7) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
@@ -366,7 +476,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ products
-    constexpr uint32_t kScores = tc::instruction<T>(128, KT, false), kOutput = tc::instruction<T>(128, DP, true);
+    constexpr uint32_t kScores = tc::instruction<M>(128, KT, false), kOutput = tc::instruction<M>(128, DP, true);
     const uint32_t q0 = tc::uniform(tc::k_major(tc::smem_at(sm.q[0])));
     const uint32_t k0 = tc::uniform(tc::k_major(tc::smem_at(sm.ring[0])));
     const uint32_t v0 = tc::uniform(tc::mn_major(tc::smem_at(sm.ring[0]), KT * 128));
@@ -465,8 +575,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
     unsigned ml_seen = 0;
     const bool wide = reinterpret_cast<uintptr_t>(out) % 32 == 0;  // a row of out is a multiple of 64 bytes
     bool ok = true;
-    constexpr int kLag = std::is_same<T, __half>::value ? 4 : 8;
-    constexpr float kLift = (float)weight_lift<T>(kLag);
+    constexpr int kLag = std::is_same<M, __half>::value ? 4 : 8;
+    constexpr float kLift = (float)weight_lift<M>(kLag);
+    unsigned unit_count = 0;
     // The last product into this group's O.  Even and odd ones have a barrier each: by the time
     // that one is waited for, the one before it on the same barrier was done (two groups: before
     // these scores; one group: before the last but one), so its parity is not taken for it.
@@ -488,6 +599,9 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
       // parts of 64 keys: part y & 1 of job x, or one a job
       const int parts = NW == 2 ? nt == 2 ? 2 * kt : ((jobs + 1 - group) >> 1) * 2 : jobs;
       uint32_t there[2 * S::kParts];  // which keys of the job are there
+      uint32_t units[kCodes ? 2 * S::kParts : 1];  // codes: the units of their 32 keys each
+      float row_scale = a.scale_log2;
+      int o_unit = 1;  // codes: O is in units of 2^(o_unit - 127)
       // The second group has no part of a unit of one row tile and one key tile, waits for nothing there
       // and may come out many tiles ahead of the copies.  The barriers of `seen` come round every 16
       // tiles, so that a parity tells the wanted tile from those 16 before and after it only while the
@@ -507,12 +621,22 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           ok = tc::bar_wait(&sm.seen_full[(k_base + kk) & 15], (unsigned)((k_base + kk) >> 4) & 1, &sm.dead);
 #pragma unroll
           for (int i = 0; i < 2 * S::kParts; ++i) there[i] = sm.seen[(k_base + kk) & 15][i];
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int i = 0; i < 2 * S::kParts; ++i) units[i] = sm.units[(k_base + kk) & 15][i];
+            if constexpr (!std::is_same<T, __half>::value)
+              if (!any) row_scale = a.scale_log2 * power(-(int)sm.power[unit_count & 1][r]);
+          }
           ok = ok && tc::bar_wait(&sm.s_full[NW == 2 ? group : buf], (pv >> 1) & 1, &sm.dead);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc::fence_after();
         } else {
           there[0] = there[2 * S::kParts - 2];
           there[1] = there[2 * S::kParts - 1];
+          if constexpr (kCodes) {
+            units[0] = units[2 * S::kParts - 2];
+            units[1] = units[2 * S::kParts - 1];
+          }
         }
         const bool open = __all_sync(0xffffffffu, (there[0] & there[1]) == 0xffffffffu && j0 + 64 <= limit);
         uint32_t v[2][32];
@@ -528,25 +652,53 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
               if (!((word >> i) & 1) || j0 + ch * 32 + i >= limit) v[ch][i] = 0xff800000u;
           }
         }
-        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float sc[2], less[2];  // codes: of each 32 keys, the scores' factor and V's exponent relative to O's
+        float mt;
+        bool grows = false;    // codes: O's unit
+        int next_unit = o_unit;
+        if constexpr (kCodes) {
+          float top[2];
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch)
+          for (int ch = 0; ch < 2; ++ch) {
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
-        const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
-        const float mt = top * a.scale_log2 - kLift;  // -infinity stays (scale > 0)
+            for (int i = 0; i < 32; i += 2)
+              top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
+            sc[ch] = row_scale * power_of(units[ch] & 255u);
+            top[ch] = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * sc[ch];
+            next_unit = max(next_unit, (int)(units[ch] >> 8 & 255u));
+          }
+          grows = next_unit > o_unit;
+          mt = fmaxf(top[0], top[1]) - kLift;  // -infinity stays (the factors are > 0)
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch) {
+            const int vm = (int)(units[ch] >> 8 & 255u);
+            less[ch] = vm == 0 ? 0.f : (float)(vm - next_unit);  // (a V of zeros: in any units)
+            // (of weights of less than 2^-30 nothing is asked)
+            if (((units[ch] >> 16) != 0 || less[ch] < (float)-kSpread) && top[ch] > fmaxf(m, mt) + kLift - 30.f) l = NAN;
+          }
+        } else {
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
+          const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+          mt = top * a.scale_log2 - kLift;  // -infinity stays (scale > 0)
+        }
         if (!any) {
           m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + (float)kLag)) {
+        } else if (__any_sync(0xffffffffu, mt > m + (float)kLag || grows)) {
           // the last product into O is done before O is changed
           ok = product_done();
           if (!ok) break;
           tc::fence_after();
-          const float up = fmaxf(m, mt);
-          const float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
+          const float up = kCodes && !(mt > m + (float)kLag) ? m : fmaxf(m, mt);
+          float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
           l *= f;
           m = up;
+          if constexpr (kCodes) f *= o_unit - next_unit >= -90 ? power(o_unit - next_unit) : l > 0.f ? NAN : 0.f;
 #pragma unroll 1
           for (int ch = 0; ch < DP / 16; ++ch) {  // rare: few registers rather than few waits
             uint32_t x[16];
@@ -558,20 +710,31 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           }
         }
         any = true;
+        o_unit = next_unit;
         const float base = m == -INFINITY ? 0.f : m;
         const float2 scale2 = make_float2(a.scale_log2, a.scale_log2), minus2 = make_float2(-base, -base);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           uint32_t p[16];
+          float2 part_sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            float2 e =
-                __ffma2_rn(make_float2(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])), scale2, minus2);
+            float2 e;
+            if constexpr (kCodes)
+              e = __ffma2_rn(make_float2(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])),
+                             make_float2(sc[ch], sc[ch]), make_float2(less[ch] - base, less[ch] - base));
+            else
+              e = __ffma2_rn(make_float2(__uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1])), scale2, minus2);
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
-            sum = __fadd2_rn(sum, e);
-            p[i / 2] = pack2((const T*)nullptr, e.x, e.y);
+            if constexpr (kCodes) part_sum = __fadd2_rn(part_sum, e);
+            else sum = __fadd2_rn(sum, e);
+            p[i / 2] = pack2((const M*)nullptr, e.x, e.y);
+          }
+          if constexpr (kCodes) {
+            const float back = less[ch] >= -126.f ? power(-(int)less[ch]) : 0.f;  // (lost, and NaN already, where it is 0)
+            sum = __ffma2_rn(part_sum, make_float2(back, back), sum);
           }
           tc::tmem_store16(t_s + ch * 16, p);  // over the scores
         }
@@ -582,18 +745,20 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         ++pv;
       }
       k_base += kt;
+      ++unit_count;
       if (!__all_sync(0xffffffffu, ok)) break;
 
       // ---- the unit's rows: wait for the last product, then out
       if (any) ok = product_done();
       if (!ok) break;
       tc::fence_after();
-      const bool halves = NW == 2 && nt == 1 && jobs > 1;  // the second group has keys of the same rows
+      const bool halves_of_rows = NW == 2 && nt == 1 && jobs > 1;  // the second group has keys of the same rows
       float f0 = 1.f, f1 = 0.f;
-      if (halves) {
+      if (halves_of_rows) {
         if (group == 1) {
           sm.ml[r_tile][0] = m;
           sm.ml[r_tile][1] = l;
+          if constexpr (kCodes) sm.second = o_unit;
           tc::bar_arrive(&sm.ml_full);
         } else {
           ok = tc::bar_wait(&sm.ml_full, ml_seen & 1, &sm.dead);
@@ -617,6 +782,11 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           f0 *= inv;
           f1 *= inv;
         }
+        float u0 = 1.f, u1 = 1.f;
+        if constexpr (kCodes) {
+          u0 = power_of(o_unit);
+          if (halves_of_rows) u1 = power_of(sm.second);
+        }
         float* const to = whole ? c.dense + row * a.D : slot_o(c, a, blockIdx.x, begins ? 1 : 0) + (int64_t)r * a.D;
         bool fine = l <= FLT_MAX;
 #pragma unroll
@@ -627,11 +797,14 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
           float y[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(v[i]) * f0;
-          if (halves) {
+          if constexpr (kCodes)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] *= u0;
+          if (halves_of_rows) {
             tc::tmem_load32(v, t_o + DP + ch * 32);
             tc::wait_loads();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(v[i]), f1, y[i]);
+            for (int i = 0; i < 32; ++i) y[i] = fmaf(kCodes ? __uint_as_float(v[i]) * u1 : __uint_as_float(v[i]), f1, y[i]);
           }
           if (mine && ch * 32 < a.D) {
             if (final) {
@@ -678,7 +851,7 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         tc::bar_arrive(&sm.o_free[NW == 2 ? group : 0]);
       } else if (group == 0) {
         tc::bar_arrive(&sm.o_free[0]);
-        if (halves) tc::bar_arrive(&sm.o_free[1]);
+        if (halves_of_rows) tc::bar_arrive(&sm.o_free[1]);
       }
       walk_next<S::M, KT>(w, g, a, c);
     }
