@@ -96,7 +96,7 @@ cudaError_t launch_tc(const AttendProblem& p, const Pointers& g, const AttendArg
   const size_t smem = sizeof(TcShared<DP, false>);
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped_smem(kernel, (unsigned)grid, TcShape<DP>::kThreads, smem, stream,
+  return launch_overlapped_smem(kernel, (unsigned)grid, TcShape<DP, false>::kThreads, smem, stream,
                                 static_cast<const T*>(p.query), static_cast<const T*>(p.k_cache),
                                 static_cast<const T*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, c);
 }

@@ -84,6 +84,14 @@ cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const Attend
   return launch_as<T, 256>(p, g, a, c, u, stream);
 }
 
+// Where no sequence can have more keys than this, no unit is split and the joining launch is saved: two tiles one after
+// the other are not longer than it, and four are not where every unit has a CTA of its own.
+int64_t solo_keys(const AttendProblem& p, const Units& u, double rows) {
+  if (u.tall) return 512;
+  const bool one_each = (double)p.B * (double)p.nk * (rows / (double)u.M + 1) <= (double)u.grid;
+  return (one_each ? 4 : 2) * tile_keys(u, p.D);
+}
+
 template <typename T>
 cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
   // rows of a sequence and key head, on average: only the lengths' sum is known here
@@ -104,7 +112,7 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
     pre.shared = pre.prefix = 1;
     const cudaError_t e = launch_units<T>(p, g, a, pre, u_pre, stream);
     if (e != cudaSuccess) return e;
-  } else if (p.prefix_len + p.W * p.block_size <= (u_own.tall ? 512 : 2 * tile_keys(u_own, p.D))) {
+  } else if (p.prefix_len + p.W * p.block_size <= solo_keys(p, u_own, rows)) {
     own.whole = INT32_MAX;
     own.solo = 1;
   }

@@ -12,7 +12,7 @@ cudaError_t launch(const AttendProblem& p, const Pointers& g, const AttendArgs& 
   const size_t smem = sizeof(TcShared<DP, true>);
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  return launch_overlapped_smem(kernel, (unsigned)c.grid, TcShape<DP>::kThreads, smem, stream,
+  return launch_overlapped_smem(kernel, (unsigned)c.grid, TcShape<DP, true>::kThreads, smem, stream,
                                 static_cast<const T*>(p.query), static_cast<const Code*>(p.k_cache),
                                 static_cast<const Code*>(p.v_cache), static_cast<T*>(p.out), p.lse, g, a, c);
 }

@@ -46,14 +46,16 @@ namespace attend {
 
 constexpr unsigned kWaitExpired = 8u;
 
-template <int DP>
+// CODED: over a cache of codes, which come through slots of their own (kRaw items under way).
+template <int DP, bool CODED>
 struct TcShape {
   static constexpr int KT = DP <= 128 ? 128 : 64;   // keys of a tile
   static constexpr int NW = DP <= 128 ? 2 : 1;      // softmax groups
   static constexpr int kParts = KT / 64;            // parts of 64 keys in which its weights are handed over
   static constexpr int M = 128 * NW;                // rows of a unit
   static constexpr int kStage = KT * DP * 2;        // bytes of a K or V tile
-  static constexpr int NS = DP <= 64 ? 8 : 5;       // tiles in the ring
+  static constexpr int NS = CODED ? (DP <= 64 ? 7 : 4) : DP <= 64 ? 8 : 5;  // tiles in the ring
+  static constexpr int kRaw = 2;
   static constexpr int kQ = 128 * DP * 2;           // bytes of a row tile
   static constexpr int kSoftmax = 128 * NW;         // softmax threads
   static constexpr int kCopy = DP <= 128 ? 128 : 64;  // copying threads
@@ -66,18 +68,19 @@ struct TcShape {
 // What the units over a cache of codes keep besides: of the last 16 K tiles, 32 keys at a time, the scales that their
 // codes are in units of (bytes of K's and of V's, and whether some key's is too far below); of the rows of this unit and
 // the next, the power of two that they are times; the unit of the second group's O.
-template <bool CODED>
+template <int DP, bool CODED>
 struct TcMore {};
-template <>
-struct TcMore<true> {
+template <int DP>
+struct TcMore<DP, true> {
+  alignas(1024) uint4 raw[TcShape<DP, true>::kRaw][TcShape<DP, true>::kCopy / 32][DP / 16][32];  // a lane's codes
   uint32_t units[16][4];
   signed char power[2][256];
   int second;
 };
 
 template <int DP, bool CODED>
-struct TcShared : TcMore<CODED> {
-  using S = TcShape<DP>;
+struct TcShared : TcMore<DP, CODED> {
+  using S = TcShape<DP, CODED>;
   alignas(1024) unsigned char ring[S::NS][S::kStage];
   alignas(1024) unsigned char q[S::NW][S::kQ];
   uint64_t copied[S::NS], full[S::NS], empty[S::NS];  // a tile is there, visible to the tensor core, read
@@ -143,10 +146,10 @@ constexpr int kSpread = 10;
 
 // C: elements of the cache, T or Code.
 template <typename T, int DP, typename C>
-__global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
+__global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
     attend_tc_kernel(const T* __restrict__ q, const C* __restrict__ kc, const C* __restrict__ vc, T* __restrict__ out,
                      float* __restrict__ lse, Pointers g, AttendArgs a, Cut c) {
-  using S = TcShape<DP>;
+  using S = TcShape<DP, kCoded<C>>;
   constexpr int KT = S::KT, NW = S::NW, NS = S::NS;
   constexpr int CH = DP / 8;
   extern __shared__ __align__(1024) unsigned char raw[];
@@ -327,58 +330,61 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
         return now;
       };
       if constexpr (kCodes) {
-        // Codes go through registers: a copy's are read while those before are widened and stored.
+        // Codes are copied kRaw items ahead, each lane's to slots of its own, and from there widened and stored.
         constexpr int CC = DP / 16;  // 16-byte pieces of a row of codes
-        uint4 codes[CC];
-        bool is_there = false, is_v = false;  // this lane's key of the copy that is read, and whose it is
-        uint32_t kb = 0, vb = 0;              // its scales
-        __half2 v_factor[S::kAhead];          // of the K tiles whose V has not followed
-        int behind = 0;                       // so many
-        auto read = [&](int n) {
-          const CopyItem it = copy_item(n, kt, lead);
-          const int now = rows_of(it);
-          const Code* const src = it.is_v ? vc : kc;
-          const Span& span = it.is_v ? a.v_span : a.k_span;
-          is_v = it.is_v;
-          if (!it.is_v) {
-            is_there = now >= 0;
-            kb = vb = 0;
-            if (is_there) {
-              const uint32_t z = a.per_shift >= 0 ? (uint32_t)now >> a.per_shift : (uint32_t)now / (uint32_t)a.per;
-              kb = ldg(g.k_scale + z, a.ks_span, g.err);
-              vb = ldg(g.v_scale + z, a.vs_span, g.err);
+        // This lane's piece of row `key` + i * 128 / DP * 4: eight lanes have four pieces of two rows each, so that what
+        // they store meets every bank once.
+        const int ch = (lane & 3) | ((lane >> 3) << 2 & (CC - 1)), first_key = (lane >> 2 & 1) | (lane >> (CC == 4 ? 3 : CC == 8 ? 4 : 5)) << 1;
+        constexpr int kKeys = 32 / CC;  // rows of an access
+        bool is_there[S::kRaw], is_v[S::kRaw];  // this lane's key of the items under way, and whose they are
+        uint32_t kb[S::kRaw], vb[S::kRaw];      // its scales
+        __half2 v_factor[S::kAhead];            // of the K tiles whose V has not followed
+        int behind = 0;                         // so many
+        auto read = [&](int n, auto slot) {
+          constexpr int at = decltype(slot)::value;
+          if (n < 2 * kt) {
+            const CopyItem it = copy_item(n, kt, lead);
+            const int now = rows_of(it);
+            const Code* const src = it.is_v ? vc : kc;
+            const Span& span = it.is_v ? a.v_span : a.k_span;
+            is_v[at] = it.is_v;
+            if (!it.is_v) {
+              is_there[at] = now >= 0;
+              kb[at] = vb[at] = 0;
+              if (now >= 0) {
+                const uint32_t z = a.per_shift >= 0 ? (uint32_t)now >> a.per_shift : (uint32_t)now / (uint32_t)a.per;
+                kb[at] = ldg(g.k_scale + z, a.ks_span, g.err);
+                vb[at] = ldg(g.v_scale + z, a.vs_span, g.err);
+              }
+            }
+            const unsigned dst = tc::smem_at(&sm.raw[at][cw][0][lane]);
+#pragma unroll
+            for (int i = 0; i < CC; ++i) {
+              const int r = __shfl_sync(0xffffffffu, now, first_key + i * kKeys);
+              const bool there = r >= 0 && ch * 16 < a.D;
+              const Code* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + (there ? ch * 16 : 0));
+              cp_async16_or_zero(dst + i * 512, p, there && access_ok(p, 16, span, g.err));
             }
           }
-#pragma unroll
-          for (int i = 0; i < CC; ++i) {
-            const int idx = lane + 32 * i;
-            const int key = idx / CC, ch = idx - key * CC;
-            const int r = __shfl_sync(0xffffffffu, now, key);
-            const Code* p = src + ((uint64_t)(uint32_t)max(r, 0) * (uint32_t)a.D + ch * 16);
-            codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r >= 0 && ch * 16 < a.D && access_ok(p, 16, span, g.err))
-              codes[i] = __ldg(reinterpret_cast<const uint4*>(p));
-          }
+          cp_async_commit();
         };
         // byte b relative to the largest, as a factor: exact down to 2^-15
         auto relative = [&](uint32_t b, uint32_t most) {
           const float f = b == 255 ? NAN : b == 0 || most - b > 24 ? 0.f : power(-(int)(most - b));
           return __float2half2_rn(f);
         };
-        if (kt > 0) read(0);
-        for (int n = 0; n < 2 * kt; ++n) {
-          uint4 x[CC];
-#pragma unroll
-          for (int i = 0; i < CC; ++i) x[i] = codes[i];
+        auto step = [&](int n, auto slot) {
+          constexpr int at = decltype(slot)::value;
+          cp_async_wait<S::kRaw - 1>();
           __half2 f;
-          if (!is_v) {
-            const uint32_t there = __ballot_sync(0xffffffffu, is_there);
-            uint32_t km = __reduce_max_sync(0xffffffffu, kb == 255 ? 0u : kb);
-            uint32_t vm = __reduce_max_sync(0xffffffffu, vb == 255 ? 0u : vb);
-            const bool far = __any_sync(0xffffffffu, (kb > 0 && kb + 15 < km) || (vb > 0 && vb + 15 < vm));
+          if (!is_v[at]) {
+            const uint32_t there = __ballot_sync(0xffffffffu, is_there[at]);
+            uint32_t km = __reduce_max_sync(0xffffffffu, kb[at] == 255 ? 0u : kb[at]);
+            uint32_t vm = __reduce_max_sync(0xffffffffu, vb[at] == 255 ? 0u : vb[at]);
+            const bool far = __any_sync(0xffffffffu, (kb[at] > 0 && kb[at] + 15 < km) || (vb[at] > 0 && vb[at] + 15 < vm));
             if (km == 0) km = 127;  // zeros, or no key: in any units
-            f = relative(kb, km);
-            const __half2 fv = relative(vb, vm);
+            f = relative(kb[at], km);
+            const __half2 fv = relative(vb[at], vm);
 #pragma unroll
             for (int e = 0; e < S::kAhead; ++e)
               if (e == behind) v_factor[e] = fv;
@@ -395,18 +401,18 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
             for (int e = 0; e + 1 < S::kAhead; ++e) v_factor[e] = v_factor[e + 1];
             --behind;
           }
-          if (n + 1 < 2 * kt) read(n + 1);
           if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          unsigned char* const to = sm.ring[stage] + cw * S::KW * 128;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) return;
+          unsigned char* const to = sm.ring[stage] + (cw * S::KW + first_key) * 128 + (ch >> 2) * (KT * 128);
           const uint32_t bits = *reinterpret_cast<const uint32_t*>(&f);
 #pragma unroll
           for (int i = 0; i < CC; ++i) {
-            const int idx = lane + 32 * i;
-            const int key = idx / CC, ch = 2 * (idx - key * CC);
+            const int key = first_key + i * kKeys;
+            const uint4 x = sm.raw[at][cw][i][lane];
             const uint32_t fk = __shfl_sync(0xffffffffu, bits, key);
             const __half2 fh = *reinterpret_cast<const __half2*>(&fk);
-            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
             uint32_t y[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -414,12 +420,23 @@ __global__ void __launch_bounds__(TcShape<DP>::kThreads, 1)
               y[2 * e] = times(y[2 * e], fh);
               y[2 * e + 1] = times(y[2 * e + 1], fh);
             }
-            unsigned char* const row = to + (ch >> 3) * (KT * 128) + key * 128;
-            *reinterpret_cast<uint4*>(row + (((ch & 7) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(row + ((((ch & 7) | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+            unsigned char* const row = to + i * kKeys * 128;
+            const int piece = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + ((piece ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(row + (((piece | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
           tc::bar_arrive(&sm.copied[stage]);
           if (++stage == NS) stage = 0, ++round;
+          read(n + S::kRaw, slot);  // into the slots that were just read
+        };
+        static_assert(S::kRaw == 2, "the two steps");
+        const std::integral_constant<int, 0> even;
+        const std::integral_constant<int, 1> odd;
+        read(0, even);
+        read(1, odd);
+        for (int n = 0; n < 2 * kt && ok; n += 2) {
+          step(n, even);
+          if (ok) step(n + 1, odd);
         }
       } else {
         for (int n = 0; n < 2 * kt; ++n) {
