@@ -3,9 +3,10 @@ references of those on its pages, for their tests.
 
 A cached value is code * 2^(byte - 127), 0 times the code for byte 0, exact in binary64.  Bounds beside those of serving_ref.py (e = 2^-24):
 
-* append: x is off by 4 e |x| before it is coded (serving_ref.append_bound without the output's rounding), and a
-  code is the nearest of E4M3's values: |value - x| <= step(x) / 2 + 4 e |x|, step being that of E4M3 at x in units
-  of the scale (2^-3 of the power of two below, 2^-9 at least).  The scale byte is a step function of the largest
+* append: a code is the nearest of E4M3's values to x' = fl(a c - fl(b s)), whose two roundings are off by e |b s| and
+  e |a c - b s| (1 + e): |value - x| <= step(x) / 2 + 4 e (|a c| + |b s|), step being that of E4M3 at x in units of the
+  scale (2^-3 of the power of two below, 2^-9 at least).  With |a|, |b| <= the row's largest magnitude r and
+  |c|, |s| <= the table's t (r and t are those of the case) the terms are at most 2 r t; values are copied (one term).  The scale byte is a step function of the largest
   magnitude: a reference within 2^-20 of a step's edge may come out on either side.
 * attention: the cache's values are exact, so the bounds are those of serving_ref.attend_reference.
 """
@@ -132,11 +133,13 @@ def codes_append_reference(c):
     dk = dict(d, q=c["k"], hq=c["hk"])
     k_rot = append_reference(dk)[0].reshape(T, c["hk"], D)
     out = []
+    largest = float(c["table"].double().abs().max())
     for n, x, H in (("k", k_rot, c["hk"]), ("v", c["v"].double().reshape(T, c["hv"], D), c["hv"])):
         codes, scale = bytes_of(c[n + "c"]).clone(), bytes_of(c[n + "s"]).clone().int()
         value = torch.full(codes.shape, math.nan, dtype=torch.float64)  # of written rows, in units of the scale
         written = torch.zeros(codes.shape[:3], dtype=torch.bool)
         near = torch.zeros(scale.shape, dtype=torch.bool)
+        terms = torch.zeros(codes.shape[:3], dtype=torch.float64)
         slots = c["slots"].tolist()
         t = 0
         total = codes.shape[0] * bs
@@ -176,9 +179,13 @@ def codes_append_reference(c):
                 scale[page, h, part] = byte
                 for i in use:
                     value[page, h, at + i - t] = x[i, h] * 2.0 ** (127 - byte)
+                    if n == "k":
+                        raw = c["k"].double().reshape(T, H, D)[i, h].abs()
+                        raw = float(torch.where(torch.isfinite(raw), raw, torch.zeros_like(raw)).max())
+                        terms[page, h, at + i - t] = 2 * raw * largest * 2.0 ** (127 - byte)
                     written[page, h, at + i - t] = True
             t += m
-        out.append({"codes": codes, "scale": scale, "value": value, "written": written, "near": near})
+        out.append({"codes": codes, "scale": scale, "value": value, "written": written, "near": near, "terms": terms})
     return q_out, skipped, out
 
 
@@ -193,12 +200,13 @@ def check_codes(got_codes, got_scale, want, what):
     kept = ~want["written"] & sure
     assert torch.equal(codes[kept], want["codes"][kept]), what + " rows that stay"
     v, g = want["value"][w], codes[w].view(E4M3).double()
+    terms = want["terms"][w][:, None].expand_as(v)
     bad = ~torch.isfinite(v)
     assert bool(torch.isnan(g[bad]).all()), what + " values that are not finite"
-    v, g = v[~bad], g[~bad]
+    v, g, terms = v[~bad], g[~bad], terms[~bad]
     step = torch.pow(2.0, torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
     err = (g - v).abs()
-    assert bool((err <= step / 2 + 4 * E32 * v.abs()).all()), (what, float((err - step / 2).max()))
+    assert bool((err <= step / 2 + 4 * E32 * (v.abs() + terms)).all()), (what, float((err - step / 2).max()))
 
 
 # ---------------------------------------------------------------------------
