@@ -2,8 +2,10 @@
 // pages copied in many tensors at once.
 //
 // The first two work on tables of page numbers and on how many times each page is held (ref_counts).  They are
-// bound by latency: each runs as one cluster of 8 CTAs, whose barrier is what lets every step see the one before
-// it, so that a call is one launch.  Free pages are given out lowest first, rows in order, so results do not
+// bound by latency: a handful of steps, each of which has to see all of the one before.  Each is one launch: of one CTA
+// that keeps the counts in shared memory where there are up to kSmallPages pages and kSmallEntries table entries, so that
+// a step is a few hundred nanoseconds, else of one cluster of 8 CTAs with the counts in global memory (16 rows of up to
+// 300 tokens reordered: 12 us in the cluster, 7 in one CTA).  Free pages are given out lowest first, rows in order, so results do not
 // depend on the order in which threads run.
 //
 // rearrange_sequences: every old row lets go of its pages; new row i takes the whole pages of its parent once
@@ -26,56 +28,84 @@ constexpr unsigned kPagesExhausted = 16u;
 constexpr int kCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAll = kCluster * kThreads;
-constexpr int kAllWarps = kCluster * kWarps;
 constexpr int kClaim = 1 << 30;
+constexpr int kKeeps = 1 << 30;  // a row keeps the page that it writes on
+constexpr int64_t kSmallPages = 24576;
+constexpr int64_t kSmallEntries = 16384;
 
-__device__ __forceinline__ int cta_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return (int)r;
-}
+// The CTAs of a call: CL is 1 or kCluster.
+template <int CL>
+struct Team {
+  static constexpr int kAll = CL * kThreads, kAllWarps = CL * kWarps;
 
-// What any thread of the cluster wrote before it, all see after it.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+  static __device__ __forceinline__ int rank() {
+    if constexpr (CL == 1) return 0;
+    uint32_t r;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return (int)r;
+  }
 
-// The word of CTA `rank` that is where `p` is in this one's shared memory.
-__device__ __forceinline__ int peer_int(const int* p, int rank) {
-  uint32_t at = (uint32_t)__cvta_generic_to_shared(p), far;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(far) : "memory");
-  return v;
+  // What any thread wrote before it, all see after it.
+  static __device__ __forceinline__ void sync() {
+    if constexpr (CL == 1)
+      __syncthreads();
+    else
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+
+  // The word of CTA `rank` that is where `p` is in this one's shared memory.
+  static __device__ __forceinline__ int peer(const int* p, int rank) {
+    if constexpr (CL == 1) return *p;
+    uint32_t at = (uint32_t)__cvta_generic_to_shared(p), far;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(at), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(far) : "memory");
+    return v;
+  }
+
+  // Warps' ranges of pages: warp w of all has [w * per, min(NB, (w + 1) * per)), per a multiple of 32.
+  static __device__ __forceinline__ int2 pages_of(int warp, int NB) {
+    const int per = (NB + kAllWarps * 32 - 1) / (kAllWarps * 32) * 32;
+    const int64_t from = (int64_t)warp * per;
+    return make_int2((int)min(from, (int64_t)NB), (int)min(from + per, (int64_t)NB));
+  }
+
+  // Sum of `count` (a value a warp, in every CTA's shared memory) over all warps before `warp`, and over all.
+  // Every warp calls it.
+  static __device__ __forceinline__ int sum_before(const int* count, int warp, int* total) {
+    const int lane = threadIdx.x & 31;
+    int before = 0, all = 0;
+#pragma unroll
+    for (int r = 0; r < CL; ++r) {
+      const int v = peer(count + lane, r);
+      all += v;
+      before += r * kWarps + lane < warp ? v : 0;
+    }
+    *total = __reduce_add_sync(0xffffffffu, all);
+    return __reduce_add_sync(0xffffffffu, before);
+  }
+};
+
+// f(row, column) for the entries of a table, ALL threads in turn, several entries' loads at a time.
+template <int ALL, typename F>
+__device__ __forceinline__ void for_entries(int me, int64_t rows, int64_t columns, F&& f) {
+  const int64_t n = rows * columns;
+  if (n < (int64_t(1) << 31) - 4 * ALL) {
+#pragma unroll 4
+    for (int e = me; e < (int)n; e += ALL) {
+      const int r = (int)((uint32_t)e / (uint32_t)columns);
+      f(r, e - r * (int)columns);
+    }
+  } else {
+    for (int64_t e = me; e < n; e += ALL) f(e / columns, (int)(e % columns));
+  }
 }
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// Warps' ranges of pages: warp w of all has [w * per, min(NB, (w + 1) * per)), per a multiple of 32.
-struct Pages {
-  int from, to;
-};
-__device__ __forceinline__ Pages pages_of(int warp, int NB) {
-  const int per = (NB + kAllWarps * 32 - 1) / (kAllWarps * 32) * 32;
-  const int64_t from = (int64_t)warp * per;
-  return {(int)min(from, (int64_t)NB), (int)min(from + per, (int64_t)NB)};
-}
-
-// Sum of `count` (a value a warp, in every CTA's shared memory) over all warps before `warp`, and over all.
-// Every warp calls it.
-__device__ __forceinline__ int sum_before(const int* count, int warp, int* total) {
-  const int lane = threadIdx.x & 31;
-  int before = 0, all = 0;
-#pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
-    const int v = peer_int(count + lane, r);
-    all += v;
-    before += r * kWarps + lane < warp ? v : 0;
-  }
-  *total = warp_sum(all);
-  return warp_sum(before);
-}
+// A word that others write meanwhile, in shared or global memory.
+__device__ __forceinline__ int32_t now(const int32_t* p) { return *(const volatile int32_t*)p; }
+__device__ __forceinline__ int64_t now(const int64_t* p) { return *(const volatile int64_t*)p; }
 
 // ---------------------------------------------------------------------------
 // New sequences of old ones
@@ -87,11 +117,8 @@ struct RearrangeArgs {
 };
 
 struct RearrangeShared {
-  int free_pages[kWarps];        // in the warp's range
+  int free_pages[kWarps];  // in the warp's range
   int2 sums[kWarps];
-  int start[kMostRearranged + 1];  // first request of every row
-  int have[kMostRearranged];     // pages that it has before
-  int pair[kMostRearranged];     // its place among the copies, or -1
 };
 
 // What new row i takes of its parent.
@@ -131,81 +158,68 @@ __device__ __forceinline__ Taken taken_of(int i, const RearrangeArgs& a, unsigne
   return t;
 }
 
+template <int CL>
 __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, unsigned int* err) {
+  using All = Team<CL>;
   extern __shared__ __align__(16) unsigned char raw[];
   RearrangeShared& sm = *reinterpret_cast<RearrangeShared*>(raw);
   const RearrangeProblem& p = a.p;
-  const int rank = cta_rank(), me = rank * kThreads + threadIdx.x;
+  const int rank = All::rank(), me = rank * kThreads + threadIdx.x;
   const int lane = threadIdx.x & 31, cw = threadIdx.x >> 5, warp = rank * kWarps + cw;
   const int rows = (int)p.rows, NB = (int)p.NB;
   const int64_t bs = p.block_size;
-  int32_t* const refs = p.new_refs;
-  auto ref_ok = [&](const int32_t* r) { return access_ok(r, 4, a.new_refs_span, err); };
+  // the counts: one CTA's in shared memory, behind the rows' words
+  int* const start = reinterpret_cast<int*>(raw + sizeof(RearrangeShared));  // first request of every row
+  int* const have = start + rows + 1;                                        // pages that it has before, | kKeeps
+  int* const pair = have + rows;                                             // its place among the copies, or -1
+  int32_t* const refs = CL == 1 ? pair + rows : p.new_refs;
+  auto ref_ok = [&](const int32_t* r) { return CL == 1 || access_ok(r, 4, a.new_refs_span, err); };
   wait_for_prior_grid();
+  // (what a thread's row takes of its parent is three dependent loads: once, and on the way with the counts)
+  const bool one_row = CL == 1 && rows <= kThreads;
+  const Taken kept = one_row && me < rows ? taken_of(me, a, err) : Taken{-1, 0, 0, 0, -1};
+  auto taken = [&](int i) { return one_row ? kept : taken_of(i, a, err); };
   // ---- counts as they were
   if (refs != p.refs) {
-    for (int i = me; i < NB; i += kAll)
-      if (ref_ok(refs + i)) __stcg(refs + i, ldg(p.refs + i, a.refs_span, err));
-    cluster_sync();
+    for (int i = me; i < NB; i += All::kAll)
+      if (ref_ok(refs + i)) *(volatile int32_t*)(refs + i) = access_ok(p.refs + i, 4, a.refs_span, err) ? p.refs[i] : 0;
+    All::sync();
   }
   // ---- old rows let go
-  for (int64_t b = warp; b < p.B; b += kAllWarps) {
-    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
-    const int64_t pages = (own + bs - 1) / bs;
-    if (pages > p.W && lane == 0) atomicOr(err, kSlotOutOfRange);
-    for (int c = lane; c < min(pages, p.W); c += 32) {
-      const int64_t page = ldg(p.table + b * p.W + c, a.table_span, err);
-      if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
-      else if (ref_ok(refs + page)) atomicSub(refs + page, 1);
-    }
-  }
-  cluster_sync();
+  for_entries<All::kAll>(me, p.B, p.W, [&](int64_t b, int c) {
+    const int64_t own = ldg(p.lens + b, a.lens_span, err) - p.prefix_len;
+    if (own <= c * bs) return;
+    if (c == p.W - 1 && own > p.W * bs) atomicOr(err, kSlotOutOfRange);
+    const int64_t page = ldg(p.table + b * p.W + c, a.table_span, err);
+    if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
+    else if (ref_ok(refs + page)) atomicSub(refs + page, 1);
+  });
+  All::sync();
   // ---- claims of pages that are written on
-  for (int i = me; i < rows; i += kAll) {
-    const Taken t = taken_of(i, a, err);
-    if (t.last >= 0 && ref_ok(refs + t.last) && __ldcg(refs + t.last) <= 0) atomicMin(refs + t.last, i - kClaim);
+  for (int i = me; i < rows; i += All::kAll) {
+    const Taken t = taken(i);
+    if (t.last >= 0 && ref_ok(refs + t.last) && now(refs + t.last) <= 0) atomicMin(refs + t.last, i - kClaim);
   }
-  cluster_sync();
-  for (int i = me; i < rows; i += kAll) {
-    const Taken t = taken_of(i, a, err);
-    const bool keeps = t.last >= 0 && ref_ok(refs + t.last) && __ldcg(refs + t.last) == i - kClaim;
-    if (access_ok(p.src + i, 8, a.src_span, err)) __stcg(p.src + i, (int64_t)keeps);
-  }
-  cluster_sync();
-  // ---- new rows take hold, and every CTA adds up what they ask for
-  for (int i = warp; i < rows; i += kAllWarps) {
-    const Taken t = taken_of(i, a, err);
-    for (int c = lane; c < t.full + (t.rest > 0); c += 32) {
-      const int64_t page = ldg(p.table + t.parent * p.W + c, a.table_span, err);
-      int32_t add = 1;
-      if (c == t.full) {
-        if (!__ldcg(p.src + i)) continue;
-        add = 1 - (i - kClaim);  // off with the claim
-      }
-      if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
-      else if (ref_ok(refs + page)) atomicAdd(refs + page, add);
-      int64_t* const to = p.new_table + i * p.new_W + c;
-      if (access_ok(to, 8, a.new_table_span, err)) *to = page;
-    }
-  }
+  All::sync();
+  // ---- every CTA adds up what the rows keep, copy and ask for
   int2 run = make_int2(0, 0);  // requests, copies
   for (int base = 0; base < rows; base += kThreads) {
     const int i = base + threadIdx.x;
     int2 mine = make_int2(0, 0);
-    int have = 0;
-    bool copy = false;
+    int has = 0;
+    bool copy = false, keeps_last = false;
     if (i < rows) {
-      const Taken t = taken_of(i, a, err);
-      const bool keeps = __ldcg(p.src + i) != 0;
+      const Taken t = taken(i);
+      const bool keeps = t.last >= 0 && ref_ok(refs + t.last) && now(refs + t.last) == i - kClaim;
       copy = t.rest > 0 && !keeps;
-      have = t.full + keeps;
+      has = t.full + keeps;
+      keeps_last = keeps;
       const int64_t own = max(t.len - p.prefix_len, (int64_t)0);
       const int64_t room = p.room ? max(ldg(p.room + i, a.room_span, err), (int64_t)0) : 0;
       const int64_t most = p.new_W * bs, grown = room > most - own ? most : own + room;
       if (own + room != grown && rank == 0) atomicOr(err, kSlotOutOfRange);
-      mine = make_int2((int)((grown + bs - 1) / bs) - have, copy);
-      if (rank == 0 && access_ok(p.new_lens + i, 8, a.new_lens_span, err))
-        p.new_lens[i] = p.prefix_len + grown;
+      mine = make_int2((int)((grown + bs - 1) / bs) - has, copy);
+      if (rank == 0 && access_ok(p.new_lens + i, 8, a.new_lens_span, err)) p.new_lens[i] = p.prefix_len + grown;
     }
     int2 upto = mine;
 #pragma unroll
@@ -225,28 +239,41 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
     }
     const int before_x = __shfl_sync(0xffffffffu, sum.x - own_sum.x, cw), before_y = __shfl_sync(0xffffffffu, sum.y - own_sum.y, cw);
     if (i < rows) {
-      sm.start[i] = run.x + before_x + upto.x - mine.x;
-      sm.have[i] = have;
-      sm.pair[i] = copy ? run.y + before_y + upto.y - 1 : -1;
+      start[i] = run.x + before_x + upto.x - mine.x;
+      have[i] = has | (keeps_last ? kKeeps : 0);
+      pair[i] = copy ? run.y + before_y + upto.y - 1 : -1;
     }
     run.x += __shfl_sync(0xffffffffu, sum.x, 31);
     run.y += __shfl_sync(0xffffffffu, sum.y, 31);
   }
-  if (threadIdx.x == 0) sm.start[rows] = run.x;
-  cluster_sync();
+  if (threadIdx.x == 0) start[rows] = run.x;
+  All::sync();
+  // ---- new rows take hold
+  for_entries<All::kAll>(me, rows, p.new_W, [&](int64_t i, int c) {
+    const int h = have[i], n = h & ~kKeeps;
+    if (c >= n) return;
+    const int64_t parent = ldg(p.parents + i, a.parents_span, err);
+    const int64_t page = ldg(p.table + parent * p.W + c, a.table_span, err);
+    const int32_t add = h != n && c == n - 1 ? 1 - ((int)i - kClaim) : 1;  // off with the claim
+    if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
+    else if (ref_ok(refs + page)) atomicAdd(refs + page, add);
+    int64_t* const to = p.new_table + i * p.new_W + c;
+    if (access_ok(to, 8, a.new_table_span, err)) *to = page;
+  });
+  All::sync();
   // ---- free pages
-  const Pages mine = pages_of(warp, NB);
+  const int2 mine = All::pages_of(warp, NB);
   int free_pages = 0;
-  for (int i = mine.from + lane; i < mine.to; i += 32) free_pages += ref_ok(refs + i) && __ldcg(refs + i) == 0;
+  for (int i = mine.x + lane; i < mine.y; i += 32) free_pages += ref_ok(refs + i) && now(refs + i) == 0;
   free_pages = warp_sum(free_pages);
   if (lane == 0) sm.free_pages[cw] = free_pages;
-  cluster_sync();
+  All::sync();
   int all_free;
-  int r0 = sum_before(sm.free_pages, warp, &all_free);
+  int r0 = All::sum_before(sm.free_pages, warp, &all_free);
   const int asked = run.x;
-  for (int base = mine.from; base < mine.to && r0 < asked; base += 32) {
+  for (int base = mine.x; base < mine.y && r0 < asked; base += 32) {
     const int page = base + lane;
-    const bool is_free = page < mine.to && ref_ok(refs + page) && __ldcg(refs + page) == 0;
+    const bool is_free = page < mine.y && ref_ok(refs + page) && now(refs + page) == 0;
     const uint32_t ones = __ballot_sync(0xffffffffu, is_free);
     const int r = r0 + __popc(ones & ((1u << lane) - 1u));
     r0 += __popc(ones);
@@ -254,25 +281,25 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
     int lo = 0, hi = rows - 1;  // the last row that starts at or before r (rows without requests start with the next)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sm.start[mid] <= r) lo = mid;
+      if (start[mid] <= r) lo = mid;
       else hi = mid - 1;
     }
-    const int j = r - sm.start[lo];
-    int64_t* const to = p.new_table + lo * p.new_W + sm.have[lo] + j;
+    const int j = r - start[lo];
+    int64_t* const to = p.new_table + lo * p.new_W + (have[lo] & ~kKeeps) + j;
     if (access_ok(to, 8, a.new_table_span, err)) *to = page;
     refs[page] = 1;
-    if (j == 0 && sm.pair[lo] >= 0 && access_ok(p.dst + sm.pair[lo], 8, a.dst_span, err)) p.dst[sm.pair[lo]] = page;
+    if (j == 0 && pair[lo] >= 0 && access_ok(p.dst + pair[lo], 8, a.dst_span, err)) p.dst[pair[lo]] = page;
   }
   // ---- pairs, requests that no page was left for, and the counts
-  for (int i = me; i < rows; i += kAll) {
-    const int pair = sm.pair[i], first = sm.start[i], end = sm.start[i + 1];
-    if (pair >= 0 && access_ok(p.src + pair, 8, a.src_span, err)) {
-      p.src[pair] = taken_of(i, a, err).last;
-      if (first >= all_free) p.dst[pair] = -1;
+  for (int i = me; i < rows; i += All::kAll) {
+    const int at = pair[i], first = start[i], end = start[i + 1];
+    if (at >= 0 && access_ok(p.src + at, 8, a.src_span, err)) {
+      p.src[at] = taken(i).last;
+      if (first >= all_free) p.dst[at] = -1;
     }
     if (i >= run.y && access_ok(p.src + i, 8, a.src_span, err)) p.src[i] = p.dst[i] = -1;
     for (int r = max(first, all_free); r < end; ++r) {
-      int64_t* const to = p.new_table + i * p.new_W + sm.have[i] + r - first;
+      int64_t* const to = p.new_table + i * p.new_W + (have[i] & ~kKeeps) + r - first;
       if (access_ok(to, 8, a.new_table_span, err)) *to = -1;
       atomicOr(err, kPagesExhausted);
     }
@@ -281,7 +308,10 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
     p.counts[0] = run.y;
     p.counts[1] = max(all_free - asked, 0);
   }
-  cluster_sync();  // nobody leaves while another reads its shared memory
+  All::sync();  // (nobody leaves while another reads its shared memory)
+  if constexpr (CL == 1)
+    for (int i = me; i < NB; i += All::kAll)
+      if (access_ok(p.new_refs + i, 4, a.new_refs_span, err)) p.new_refs[i] = refs[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -294,25 +324,41 @@ struct CompactArgs {
       counts_span;
 };
 
+template <int CL>
 __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, unsigned int* err) {
+  using All = Team<CL>;
   __shared__ int live_of[kWarps], hole_of[kWarps], mover_of[kWarps];
+  extern __shared__ __align__(16) unsigned char raw[];
   const CompactProblem& p = a.p;
-  const int rank = cta_rank(), me = rank * kThreads + threadIdx.x;
+  const int rank = All::rank(), me = rank * kThreads + threadIdx.x;
   const int lane = threadIdx.x & 31, cw = threadIdx.x >> 5, warp = rank * kWarps + cw;
   const int NB = (int)p.NB;
+  // one CTA: the counts, where pages go, and the free pages in order, in shared memory
+  int32_t* const held = reinterpret_cast<int32_t*>(raw);
+  uint16_t* const moved_to = reinterpret_cast<uint16_t*>(held + (CL == 1 ? NB : 0));
+  uint16_t* const hole_at = moved_to + (CL == 1 ? NB : 0);
+  static_assert(kSmallPages < 65536, "page numbers in 16 bits");
   wait_for_prior_grid();
-  auto live_at = [&](int i) { return ldg(p.refs + i, a.refs_span, err) > 0; };
-  const Pages mine = pages_of(warp, NB);
+  auto ref_at = [&](int i) -> int32_t {
+    if constexpr (CL == 1) return held[i];
+    return access_ok(p.refs + i, 4, a.refs_span, err) ? now(p.refs + i) : 0;
+  };
+  if constexpr (CL == 1) {
+    for (int i = me; i < NB; i += All::kAll) held[i] = access_ok(p.refs + i, 4, a.refs_span, err) ? p.refs[i] : 0;
+    All::sync();
+  }
+  auto live_at = [&](int i) { return ref_at(i) > 0; };
+  const int2 mine = All::pages_of(warp, NB);
   int n = 0;
-  for (int i = mine.from + lane; i < mine.to; i += 32) n += live_at(i);
+  for (int i = mine.x + lane; i < mine.y; i += 32) n += live_at(i);
   n = warp_sum(n);
   if (lane == 0) live_of[cw] = n;
-  cluster_sync();
+  All::sync();
   int L;
-  sum_before(live_of, warp, &L);
+  All::sum_before(live_of, warp, &L);
   // ---- free pages before L, live ones at or behind it
   int holes = 0, movers = 0;
-  for (int i = mine.from + lane; i < mine.to; i += 32) {
+  for (int i = mine.x + lane; i < mine.y; i += 32) {
     const bool live = live_at(i);
     holes += !live && i < L;
     movers += live && i >= L;
@@ -323,28 +369,30 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, unsign
     hole_of[cw] = holes;
     mover_of[cw] = movers;
   }
-  cluster_sync();
+  All::sync();
   int all_holes, moved;
-  int h0 = sum_before(hole_of, warp, &all_holes), m0 = sum_before(mover_of, warp, &moved);
+  int h0 = All::sum_before(hole_of, warp, &all_holes), m0 = All::sum_before(mover_of, warp, &moved);
   if (holes + movers > 0)
-    for (int base = mine.from; base < mine.to; base += 32) {
+    for (int base = mine.x; base < mine.y; base += 32) {
       const int i = base + lane;
-      const bool live = i < mine.to && live_at(i);
-      const bool hole = i < mine.to && !live && i < L, mover = live && i >= L;
+      const bool live = i < mine.y && live_at(i);
+      const bool hole = i < mine.y && !live && i < L, mover = live && i >= L;
       const uint32_t hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, mover);
       const uint32_t before = (1u << lane) - 1u;
       if (hole) {
-        int64_t* const to = p.dst + h0 + __popc(hs & before);
-        if (access_ok(to, 8, a.dst_span, err)) __stcg(to, (int64_t)i);
+        const int k = h0 + __popc(hs & before);
+        if (access_ok(p.dst + k, 8, a.dst_span, err)) *(volatile int64_t*)(p.dst + k) = i;
+        if constexpr (CL == 1) hole_at[k] = (uint16_t)i;
       }
       if (mover) {
-        int64_t* const to = p.src + m0 + __popc(ms & before);
-        if (access_ok(to, 8, a.src_span, err)) __stcg(to, (int64_t)i);
+        const int k = m0 + __popc(ms & before);
+        if (access_ok(p.src + k, 8, a.src_span, err)) *(volatile int64_t*)(p.src + k) = i;
+        if constexpr (CL == 1) moved_to[i] = (uint16_t)k;  // (its rank: where that goes is known to all after the barrier)
       }
       h0 += __popc(hs);
       m0 += __popc(ms);
     }
-  for (int64_t i = moved + me; i < p.pairs; i += kAll) {
+  for (int64_t i = moved + me; i < p.pairs; i += All::kAll) {
     if (access_ok(p.src + i, 8, a.src_span, err)) p.src[i] = -1;
     if (access_ok(p.dst + i, 8, a.dst_span, err)) p.dst[i] = -1;
   }
@@ -352,67 +400,62 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, unsign
     p.counts[0] = moved;
     p.counts[1] = L;
   }
-  cluster_sync();
-  auto to_of = [&](int64_t page) -> int64_t {  // where a page goes; -1 for none
+  All::sync();
+  // ---- tables
+  auto to_of = [&](int64_t page) -> int64_t {  // where a page goes
     if (page < 0 || page >= p.NB || !live_at((int)page)) {
       atomicOr(err, kSlotOutOfRange);
       return page;
     }
     if (page < L) return page;
+    if constexpr (CL == 1) return hole_at[moved_to[page]];
     int lo = 0, hi = moved - 1;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (__ldcg(p.src + mid) < page) lo = mid + 1;
+      if (now(p.src + mid) < page) lo = mid + 1;
       else hi = mid;
     }
-    return __ldcg(p.dst + lo);
+    return now(p.dst + lo);
   };
-  // ---- tables
-  for (int64_t b = warp; b < p.B; b += kAllWarps) {
-    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
-    const int64_t pages = (own + p.block_size - 1) / p.block_size;
-    if (pages > p.W && lane == 0) atomicOr(err, kSlotOutOfRange);
-    for (int c = lane; c < min(pages, p.W); c += 32) {
-      const int64_t* from = p.table + b * p.W + c;
-      int64_t* const to = p.new_table + b * p.W + c;
-      const int64_t page = access_ok(from, 8, a.table_span, err) ? *from : 0;
-      if (access_ok(to, 8, a.new_table_span, err)) *to = to_of(page);
-    }
-  }
-  for (int64_t i = me; i < a.prefix_pages; i += kAll) {
+  for_entries<All::kAll>(me, p.B, p.W, [&](int64_t b, int c) {
+    const int64_t own = ldg(p.lens + b, a.lens_span, err) - p.prefix_len;
+    if (own <= c * p.block_size) return;
+    if (c == p.W - 1 && own > p.W * p.block_size) atomicOr(err, kSlotOutOfRange);
+    const int64_t* from = p.table + b * p.W + c;
+    int64_t* const to = p.new_table + b * p.W + c;
+    const int64_t page = access_ok(from, 8, a.table_span, err) ? *from : 0;
+    if (access_ok(to, 8, a.new_table_span, err)) *to = to_of(page);
+  });
+  for (int64_t i = me; i < a.prefix_pages; i += All::kAll) {
     const int64_t page = access_ok(p.prefix + i, 8, a.prefix_span, err) ? p.prefix[i] : 0;
     if (access_ok(p.new_prefix + i, 8, a.new_prefix_span, err)) p.new_prefix[i] = to_of(page);
   }
-  cluster_sync();
-  // ---- counts
-  for (int i = me; i < L; i += kAll) {
-    const int32_t* const from = p.refs + i;
-    int32_t* const to = p.new_refs + i;
-    const int32_t v = access_ok(from, 4, a.refs_span, err) ? *(const volatile int32_t*)from : 0;
-    if (v > 0 && access_ok(to, 4, a.new_refs_span, err)) *to = v;  // (a free page gets the count of what moves there)
+  // ---- counts (in place too: what is read of a page is read before it is written)
+  if constexpr (CL > 1) All::sync();
+  for (int i = me; i < L; i += All::kAll) {
+    const int32_t v = ref_at(i);
+    // (a free page gets the count of what moves there)
+    if (v > 0 && access_ok(p.new_refs + i, 4, a.new_refs_span, err)) p.new_refs[i] = v;
   }
-  for (int k = me; k < moved; k += kAll) {
-    const int64_t from = __ldcg(p.src + k), to = __ldcg(p.dst + k);
-    const int32_t v = access_ok(p.refs + from, 4, a.refs_span, err) ? *(const volatile int32_t*)(p.refs + from) : 0;
+  for (int k = me; k < moved; k += All::kAll) {
+    const int64_t from = now(p.src + k), to = now(p.dst + k);
+    const int32_t v = ref_at((int)from);
     if (access_ok(p.new_refs + to, 4, a.new_refs_span, err)) p.new_refs[to] = v;
   }
-  cluster_sync();
-  for (int i = L + me; i < NB; i += kAll)
+  if constexpr (CL > 1) All::sync();
+  for (int i = L + me; i < NB; i += All::kAll)
     if (access_ok(p.new_refs + i, 4, a.new_refs_span, err)) p.new_refs[i] = 0;
 }
 
-// One cluster of kCluster CTAs.
-template <typename K, typename A>
-cudaError_t launch_cluster(K kernel, size_t smem, const A& a, cudaStream_t stream) {
+// One CTA, or one cluster of kCluster.
+template <int CL, typename K, typename A>
+cudaError_t launch_team(K kernel, size_t smem, const A& a, cudaStream_t stream) {
   unsigned int* err = nullptr;
   cudaError_t e = device_error_address(&err);
+  if (e == cudaSuccess && smem > 48 * 1024) e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  if (smem) {
-    e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(CL);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -420,10 +463,10 @@ cudaError_t launch_cluster(K kernel, size_t smem, const A& a, cudaStream_t strea
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.x = CL;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = CL == 1 ? 1 : 2;
   e = cudaLaunchKernelEx(&cfg, kernel, a, err);
   count_launch();
   return e == cudaSuccess ? cudaGetLastError() : e;
@@ -525,7 +568,10 @@ cudaError_t launch_rearrange(const RearrangeProblem& p, cudaStream_t stream) {
   a.src_span = make_span(p.src, p.rows * 8);
   a.dst_span = make_span(p.dst, p.rows * 8);
   a.counts_span = make_span(p.counts, 16);
-  return launch_cluster(rearrange_kernel, sizeof(RearrangeShared), a, stream);
+  const size_t smem = sizeof(RearrangeShared) + (3 * p.rows + 1) * 4;
+  if (p.NB <= kSmallPages && p.B * p.W <= kSmallEntries && p.rows * p.new_W <= kSmallEntries)
+    return launch_team<1>(rearrange_kernel<1>, smem + p.NB * 4, a, stream);
+  return launch_team<kCluster>(rearrange_kernel<kCluster>, smem, a, stream);
 }
 
 cudaError_t launch_compact(const CompactProblem& p, cudaStream_t stream) {
@@ -542,7 +588,9 @@ cudaError_t launch_compact(const CompactProblem& p, cudaStream_t stream) {
   a.src_span = make_span(p.src, p.pairs * 8);
   a.dst_span = make_span(p.dst, p.pairs * 8);
   a.counts_span = make_span(p.counts, 16);
-  return launch_cluster(compact_kernel, 0, a, stream);
+  if (p.NB <= kSmallPages && p.B * p.W <= kSmallEntries)
+    return launch_team<1>(compact_kernel<1>, p.NB * (4 + 2 + 2), a, stream);
+  return launch_team<kCluster>(compact_kernel<kCluster>, 0, a, stream);
 }
 
 cudaError_t launch_copy_pages(const CopyProblem& p, cudaStream_t stream) {
