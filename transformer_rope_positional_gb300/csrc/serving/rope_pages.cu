@@ -86,19 +86,50 @@ struct Team {
   }
 };
 
-// f(row, column) for the entries of a table, ALL threads in turn, several entries' loads at a time.
-template <int ALL, typename F>
-__device__ __forceinline__ void for_entries(int me, int64_t rows, int64_t columns, F&& f) {
-  const int64_t n = rows * columns;
-  if (n < (int64_t(1) << 31) - 4 * ALL) {
-#pragma unroll 4
-    for (int e = me; e < (int)n; e += ALL) {
-      const int r = (int)((uint32_t)e / (uint32_t)columns);
-      f(r, e - r * (int)columns);
+// For the first count(row).columns entries of every row of a table, a warp to a row, four rows at a time (their loads
+// before the use of any): x = *(count(row).from + column), then use(row, column, x).
+struct Entries {
+  const int64_t* from;
+  int columns;
+};
+template <int WARPS, typename N, typename F>
+__device__ __forceinline__ void for_entries(int warp, int64_t rows, const Span& span, unsigned* err, N&& count, F&& use) {
+  constexpr int U = 4;
+  for (int64_t r0 = warp; r0 < rows; r0 += U * WARPS) {
+    Entries n[U];
+    int most = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      n[u] = {nullptr, 0};
+      if (r0 + u * WARPS < rows) n[u] = count(r0 + u * WARPS);
+      most = max(most, n[u].columns);
     }
-  } else {
-    for (int64_t e = me; e < n; e += ALL) f(e / columns, (int)(e % columns));
+    for (int c = threadIdx.x & 31; c < most; c += 32) {
+      int64_t x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] = c < n[u].columns && access_ok(n[u].from + c, 8, span, err) ? *(const volatile int64_t*)(n[u].from + c) : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c < n[u].columns) use(r0 + u * WARPS, c, x[u]);
+    }
   }
+}
+
+// Counts in shared memory (one CTA) or in global memory.
+template <int CL>
+__device__ __forceinline__ void add_to(int32_t* p, int32_t v) {
+  if constexpr (CL == 1)
+    asm volatile("red.shared.add.s32 [%0], %1;" ::"r"((unsigned)__cvta_generic_to_shared(p)), "r"(v) : "memory");
+  else
+    atomicAdd(p, v);
+}
+template <int CL>
+__device__ __forceinline__ void min_to(int32_t* p, int32_t v) {
+  if constexpr (CL == 1)
+    asm volatile("red.shared.min.s32 [%0], %1;" ::"r"((unsigned)__cvta_generic_to_shared(p)), "r"(v) : "memory");
+  else
+    atomicMin(p, v);
 }
 
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
@@ -186,19 +217,22 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
     All::sync();
   }
   // ---- old rows let go
-  for_entries<All::kAll>(me, p.B, p.W, [&](int64_t b, int c) {
-    const int64_t own = ldg(p.lens + b, a.lens_span, err) - p.prefix_len;
-    if (own <= c * bs) return;
-    if (c == p.W - 1 && own > p.W * bs) atomicOr(err, kSlotOutOfRange);
-    const int64_t page = ldg(p.table + b * p.W + c, a.table_span, err);
+  // (a sequence's pages, at most those of its row)
+  auto pages_of_row = [&](int64_t b) -> Entries {
+    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
+    const int64_t pages = (own + bs - 1) / bs;
+    if (pages > p.W) atomicOr(err, kSlotOutOfRange);
+    return {p.table + b * p.W, (int)min(pages, p.W)};
+  };
+  for_entries<All::kAllWarps>(warp, p.B, a.table_span, err, pages_of_row, [&](int64_t, int, int64_t page) {
     if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
-    else if (ref_ok(refs + page)) atomicSub(refs + page, 1);
+    else if (ref_ok(refs + page)) add_to<CL>(refs + page, -1);
   });
   All::sync();
   // ---- claims of pages that are written on
   for (int i = me; i < rows; i += All::kAll) {
     const Taken t = taken(i);
-    if (t.last >= 0 && ref_ok(refs + t.last) && now(refs + t.last) <= 0) atomicMin(refs + t.last, i - kClaim);
+    if (t.last >= 0 && ref_ok(refs + t.last) && now(refs + t.last) <= 0) min_to<CL>(refs + t.last, i - kClaim);
   }
   All::sync();
   // ---- every CTA adds up what the rows keep, copy and ask for
@@ -249,14 +283,15 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
   if (threadIdx.x == 0) start[rows] = run.x;
   All::sync();
   // ---- new rows take hold
-  for_entries<All::kAll>(me, rows, p.new_W, [&](int64_t i, int c) {
+  auto kept_of_row = [&](int64_t i) -> Entries {
+    const int n = have[i] & ~kKeeps;
+    return {n ? p.table + ldg(p.parents + i, a.parents_span, err) * p.W : nullptr, n};
+  };
+  for_entries<All::kAllWarps>(warp, rows, a.table_span, err, kept_of_row, [&](int64_t i, int c, int64_t page) {
     const int h = have[i], n = h & ~kKeeps;
-    if (c >= n) return;
-    const int64_t parent = ldg(p.parents + i, a.parents_span, err);
-    const int64_t page = ldg(p.table + parent * p.W + c, a.table_span, err);
     const int32_t add = h != n && c == n - 1 ? 1 - ((int)i - kClaim) : 1;  // off with the claim
     if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
-    else if (ref_ok(refs + page)) atomicAdd(refs + page, add);
+    else if (ref_ok(refs + page)) add_to<CL>(refs + page, add);
     int64_t* const to = p.new_table + i * p.new_W + c;
     if (access_ok(to, 8, a.new_table_span, err)) *to = page;
   });
@@ -417,13 +452,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, unsign
     }
     return now(p.dst + lo);
   };
-  for_entries<All::kAll>(me, p.B, p.W, [&](int64_t b, int c) {
-    const int64_t own = ldg(p.lens + b, a.lens_span, err) - p.prefix_len;
-    if (own <= c * p.block_size) return;
-    if (c == p.W - 1 && own > p.W * p.block_size) atomicOr(err, kSlotOutOfRange);
-    const int64_t* from = p.table + b * p.W + c;
+  auto pages_of_row = [&](int64_t b) -> Entries {
+    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
+    const int64_t pages = (own + p.block_size - 1) / p.block_size;
+    if (pages > p.W) atomicOr(err, kSlotOutOfRange);
+    return {p.table + b * p.W, (int)min(pages, p.W)};
+  };
+  for_entries<All::kAllWarps>(warp, p.B, a.table_span, err, pages_of_row, [&](int64_t b, int c, int64_t page) {
     int64_t* const to = p.new_table + b * p.W + c;
-    const int64_t page = access_ok(from, 8, a.table_span, err) ? *from : 0;
     if (access_ok(to, 8, a.new_table_span, err)) *to = to_of(page);
   });
   for (int64_t i = me; i < a.prefix_pages; i += All::kAll) {
