@@ -9,7 +9,8 @@ namespace {
 template <typename T, int DP>
 cudaError_t launch(const AttendProblem& p, const Pointers& g, const AttendArgs& a, const Cut& c, cudaStream_t stream) {
   auto kernel = attend_tc_kernel<T, DP, Code>;
-  const size_t smem = sizeof(TcShared<DP, true>);
+  constexpr size_t smem = sizeof(TcShared<DP, true>);
+  static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   const cudaError_t e = opt_in_shared(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_overlapped_smem(kernel, (unsigned)c.grid, TcShape<DP, true>::kThreads, smem, stream,

@@ -66,7 +66,7 @@ struct TcShape {
 };
 
 // What the units over a cache of codes keep besides: of the last 16 K tiles, 32 keys at a time, the scales that their
-// codes are in units of (bytes of K's and of V's, and whether some key's is too far below); of the rows of this unit and
+// codes are in units of (K's as a factor, NaN where some key's scale is too far below, with V's byte in its low bits); of the rows of this unit and
 // the next, the power of two that they are times; the unit of the second group's O.
 template <int DP, bool CODED>
 struct TcMore {};
@@ -75,7 +75,7 @@ struct TcMore<DP, true> {
   alignas(1024) uint4 raw[TcShape<DP, true>::kRaw][TcShape<DP, true>::kCopy / 32][DP / 16][32];  // a lane's codes
   uint32_t units[16][4];
   signed char power[2][256];
-  int second;
+  float second;
 };
 
 template <int DP, bool CODED>
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
             ++behind;
             if (lane == 0) {
               sm.seen[k_count & 15][cw] = there;
-              sm.units[k_count & 15][cw] = km | vm << 8 | (uint32_t)far << 16;
+              sm.units[k_count & 15][cw] = __float_as_uint(far ? NAN : power_of(km)) | vm;
               tc::bar_arrive(&sm.seen_full[k_count & 15]);
             }
             ++k_count;
@@ -406,24 +406,33 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           if (!ok) return;
           unsigned char* const to = sm.ring[stage] + (cw * S::KW + first_key) * 128 + (ch >> 2) * (KT * 128);
           const uint32_t bits = *reinterpret_cast<const uint32_t*>(&f);
+          constexpr int U = CC < 8 ? CC : 8;  // pieces at a time: their loads before any store
 #pragma unroll
-          for (int i = 0; i < CC; ++i) {
-            const int key = first_key + i * kKeys;
-            const uint4 x = sm.raw[at][cw][i][lane];
-            const uint32_t fk = __shfl_sync(0xffffffffu, bits, key);
-            const __half2 fh = *reinterpret_cast<const __half2*>(&fk);
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[8];
+          for (int i0 = 0; i0 < CC; i0 += U) {
+            uint4 x[U];
+            uint32_t fk[U];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              halves(in[e], y[2 * e], y[2 * e + 1]);
-              y[2 * e] = times(y[2 * e], fh);
-              y[2 * e + 1] = times(y[2 * e + 1], fh);
+            for (int i = 0; i < U; ++i) {
+              x[i] = sm.raw[at][cw][i0 + i][lane];
+              fk[i] = __shfl_sync(0xffffffffu, bits, first_key + (i0 + i) * kKeys);
             }
-            unsigned char* const row = to + i * kKeys * 128;
-            const int piece = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(row + ((piece ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4*>(row + (((piece | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              const int key = first_key + (i0 + i) * kKeys;
+              const __half2 fh = *reinterpret_cast<const __half2*>(&fk[i]);
+              const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                halves(in[e], y[2 * e], y[2 * e + 1]);
+                y[2 * e] = times(y[2 * e], fh);
+                y[2 * e + 1] = times(y[2 * e + 1], fh);
+              }
+              unsigned char* const row = to + (i0 + i) * kKeys * 128;
+              const int piece = (ch & 3) * 2;
+              *reinterpret_cast<uint4*>(row + ((piece ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(row + (((piece | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
           }
           tc::bar_arrive(&sm.copied[stage]);
           if (++stage == NS) stage = 0, ++round;
@@ -618,7 +627,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
       uint32_t there[2 * S::kParts];  // which keys of the job are there
       uint32_t units[kCodes ? 2 * S::kParts : 1];  // codes: the units of their 32 keys each
       float row_scale = a.scale_log2;
-      int o_unit = 1;  // codes: O is in units of 2^(o_unit - 127)
+      float o_unit = 1.f;  // codes: O is in units of 2^(o_unit - 127)
       // The second group has no part of a unit of one row tile and one key tile, waits for nothing there
       // and may come out many tiles ahead of the copies.  The barriers of `seen` come round every 16
       // tiles, so that a parity tells the wanted tile from those 16 before and after it only while the
@@ -671,8 +680,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         }
         float sc[2], less[2];  // codes: of each 32 keys, the scores' factor and V's exponent relative to O's
         float mt;
-        bool grows = false;    // codes: O's unit
-        int next_unit = o_unit;
+        float next_unit = o_unit;  // codes: O's unit
         if constexpr (kCodes) {
           float top[2];
 #pragma unroll
@@ -681,18 +689,18 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
               top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
-            sc[ch] = row_scale * power_of(units[ch] & 255u);
+            sc[ch] = row_scale * __uint_as_float(units[ch] & 0xffffff00u);
             top[ch] = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * sc[ch];
-            next_unit = max(next_unit, (int)(units[ch] >> 8 & 255u));
           }
-          grows = next_unit > o_unit;
+          const float vm[2] = {(float)(units[0] & 255u), (float)(units[1] & 255u)};
+          next_unit = max3(o_unit, vm[0], vm[1]);
           mt = fmaxf(top[0], top[1]) - kLift;  // -infinity stays (the factors are > 0)
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const int vm = (int)(units[ch] >> 8 & 255u);
-            less[ch] = vm == 0 ? 0.f : (float)(vm - next_unit);  // (a V of zeros: in any units)
-            // (of weights of less than 2^-30 nothing is asked)
-            if (((units[ch] >> 16) != 0 || less[ch] < (float)-kSpread) && top[ch] > fmaxf(m, mt) + kLift - 30.f) l = NAN;
+          for (int ch = 0; ch < 2; ++ch) less[ch] = vm[ch] == 0.f ? 0.f : vm[ch] - next_unit;  // (a V of zeros: in any units)
+          if (fminf(less[0], less[1]) < (float)-kSpread) {  // (of weights of less than 2^-30 nothing is asked)
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+              if (less[ch] < (float)-kSpread && top[ch] > fmaxf(m, mt) + kLift - 30.f) l = NAN;
           }
         } else {
           float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -706,7 +714,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         }
         if (!any) {
           m = mt;
-        } else if (__any_sync(0xffffffffu, mt > m + (float)kLag || grows)) {
+        } else if (__any_sync(0xffffffffu, mt > m + (float)kLag || next_unit > o_unit)) {
           // the last product into O is done before O is changed
           ok = product_done();
           if (!ok) break;
@@ -715,7 +723,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
           l *= f;
           m = up;
-          if constexpr (kCodes) f *= o_unit - next_unit >= -90 ? power(o_unit - next_unit) : l > 0.f ? NAN : 0.f;
+          if constexpr (kCodes) f *= o_unit - next_unit >= -90.f ? power((int)(o_unit - next_unit)) : l > 0.f ? NAN : 0.f;
 #pragma unroll 1
           for (int ch = 0; ch < DP / 16; ++ch) {  // rare: few registers rather than few waits
             uint32_t x[16];
@@ -750,7 +758,8 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
             p[i / 2] = pack2((const M*)nullptr, e.x, e.y);
           }
           if constexpr (kCodes) {
-            const float back = less[ch] >= -126.f ? power(-(int)less[ch]) : 0.f;  // (lost, and NaN already, where it is 0)
+            // (where it is more than 2^kSpread the row is NaN, or has no weights to speak of)
+            const float back = fast_exp2(-fmaxf(less[ch], -126.f));
             sum = __ffma2_rn(part_sum, make_float2(back, back), sum);
           }
           tc::tmem_store16(t_s + ch * 16, p);  // over the scores
@@ -801,8 +810,8 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         }
         float u0 = 1.f, u1 = 1.f;
         if constexpr (kCodes) {
-          u0 = power_of(o_unit);
-          if (halves_of_rows) u1 = power_of(sm.second);
+          u0 = power_of((uint32_t)o_unit);
+          if (halves_of_rows) u1 = power_of((uint32_t)sm.second);
         }
         float* const to = whole ? c.dense + row * a.D : slot_o(c, a, blockIdx.x, begins ? 1 : 0) + (int64_t)r * a.D;
         bool fine = l <= FLT_MAX;
