@@ -6,6 +6,7 @@
 // units may be split, a kernel that joins partial results (rope_attend_join.cuh); larger heads a kernel with one
 // warp per query row.
 #include <algorithm>
+#include <cmath>
 
 #include "rope_attend_codes_mma.cuh"
 #include "rope_attend_join.cuh"
@@ -35,10 +36,16 @@ int64_t tile_keys(const Units& u, int64_t D) {
   return u.tall ? (narrow ? 128 : 64) : narrow ? CodesShape<float, 128, 8>::KT : CodesShape<float, 256, 8>::KT;
 }
 
-// The kernel for B sequences of `rows` rows a key head, on average, and up to `keys` keys.
+// The kernel for B sequences of `rows` rows a key head, on average, and up to `keys` keys.  A tall unit takes as long as
+// four small ones of 16 rows, of more than 128 columns as three, however few its rows are (32 sequences of up to 1000
+// keys, 32 q and 8 k heads of 128: 32 rows 62 us by tall units, 35 by small ones; 64: 64, 61; 96: 67, 86; 16 heads of 256:
+// 32 rows 181, 123; 64: 184, 226).  Where all small units' tiles are in one round, these are
+// the shorter ones (one sequence of 64 tokens and up to 200 keys, 256 rows: 14 us, tall 20).
 Units units_for(double rows, int64_t B, int64_t nk, int64_t keys, int64_t D, int32_t dtype) {
   const Units u = units_of(rows <= 8 ? 8 : kSmallRows, D, dtype);
   if (rows <= 16 || dtype == kF32) return u;
+  const int64_t worth = padded_columns(D) <= 128 ? 4 : 3;
+  if (std::ceil(rows / kSmallRows) <= (double)worth * std::ceil(rows / (double)tall_rows(D))) return u;
   const double tiles = (rows / (double)u.M + 1) * (double)(B * nk) * (double)(keys / tile_keys(u, D) + 1);
   const double most = (double)u.grid * (256 / padded_columns(D));
   return tiles <= most ? u : units_of(tall_rows(D), D, dtype);
@@ -84,13 +91,9 @@ cudaError_t launch_units(const AttendProblem& p, const Pointers& g, const Attend
   return launch_as<T, 256>(p, g, a, c, u, stream);
 }
 
-// Where no sequence can have more keys than this, no unit is split and the joining launch is saved: two tiles one after
-// the other are not longer than it, and four are not where every unit has a CTA of its own.
-int64_t solo_keys(const AttendProblem& p, const Units& u, double rows) {
-  if (u.tall) return 512;
-  const bool one_each = (double)p.B * (double)p.nk * (rows / (double)u.M + 1) <= (double)u.grid;
-  return (one_each ? 4 : 2) * tile_keys(u, p.D);
-}
+// Where no sequence can have more keys than this, no unit is split and the joining launch is saved (4 sequences of up to
+// 200 keys: 9.3 us, split 10.8; tall, 4 of 300 tokens and up to 500 keys: 35.9, 38.5).
+int64_t solo_keys(const Units& u, int64_t D) { return u.tall ? 512 : 2 * tile_keys(u, D); }
 
 template <typename T>
 cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendArgs& a, cudaStream_t stream) {
@@ -112,7 +115,7 @@ cudaError_t launch_cut(const AttendProblem& p, const Pointers& g, const AttendAr
     pre.shared = pre.prefix = 1;
     const cudaError_t e = launch_units<T>(p, g, a, pre, u_pre, stream);
     if (e != cudaSuccess) return e;
-  } else if (p.prefix_len + p.W * p.block_size <= solo_keys(p, u_own, rows)) {
+  } else if (p.prefix_len + p.W * p.block_size <= solo_keys(u_own, p.D)) {
     own.whole = INT32_MAX;
     own.solo = 1;
   }
