@@ -483,7 +483,7 @@ def prepare_append_paged_kv(positions: torch.Tensor, query: Optional[torch.Tenso
 
 
 def paged_attention_workspace(query: torch.Tensor, k_cache: torch.Tensor, prefix_len: int = 0) -> int:
-    """Bytes of workspace that :func:`paged_attention` needs for these tensors."""
+    """Bytes of workspace that :func:`paged_attention` (or, for a cache of codes, :func:`paged_attention_8bit`) needs."""
     n = _on_device(query.get_device(), _load_binding().attention_workspace, (query, k_cache, prefix_len))
     if n < 0:
         raise RopeError(ROPE_ERR_PARAM_INVALID, "rope_paged_attention_workspace")
