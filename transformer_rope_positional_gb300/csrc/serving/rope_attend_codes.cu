@@ -37,14 +37,14 @@ int64_t tile_keys(const Units& u, int64_t D) {
 }
 
 // The kernel for B sequences of `rows` rows a key head, on average, and up to `keys` keys.  A tall unit takes as long as
-// four small ones of 16 rows, of more than 128 columns as three, however few its rows are (32 sequences of up to 1000
+// four small ones of 16 rows, of more than 128 columns as 2.5, however few its rows are (32 sequences of up to 1000
 // keys, 32 q and 8 k heads of 128: 32 rows 62 us by tall units, 35 by small ones; 64: 64, 61; 96: 67, 86; 16 heads of 256:
-// 32 rows 181, 123; 64: 184, 226).  Where all small units' tiles are in one round, these are
+// 32 rows 148, 123; 48: 149, 178).  Where all small units' tiles are in one round, these are
 // the shorter ones (one sequence of 64 tokens and up to 200 keys, 256 rows: 14 us, tall 20).
 Units units_for(double rows, int64_t B, int64_t nk, int64_t keys, int64_t D, int32_t dtype) {
   const Units u = units_of(rows <= 8 ? 8 : kSmallRows, D, dtype);
   if (rows <= 16 || dtype == kF32) return u;
-  const int64_t worth = padded_columns(D) <= 128 ? 4 : 3;
+  const int64_t worth = padded_columns(D) <= 128 ? 4 : 2;
   if (std::ceil(rows / kSmallRows) <= (double)worth * std::ceil(rows / (double)tall_rows(D))) return u;
   const double tiles = (rows / (double)u.M + 1) * (double)(B * nk) * (double)(keys / tile_keys(u, D) + 1);
   const double most = (double)u.grid * (256 / padded_columns(D));

@@ -46,7 +46,9 @@ namespace attend {
 
 constexpr unsigned kWaitExpired = 8u;
 
-// CODED: over a cache of codes, which come through slots of their own (kRaw items under way).
+// CODED: over a cache of codes, which come through slots of their own (kRaw items under way), for heads of 256, where there
+// are registers for more threads, K's and V's by a set of copying threads each (32 of 5 tokens behind 2048: 63 us by one
+// set, 56 by two; heads of 128, with registers moved between the roles by setmaxnreg: 32 of 300 tokens 197, 215 to 230).
 template <int DP, bool CODED>
 struct TcShape {
   static constexpr int KT = DP <= 128 ? 128 : 64;   // keys of a tile
@@ -55,11 +57,12 @@ struct TcShape {
   static constexpr int M = 128 * NW;                // rows of a unit
   static constexpr int kStage = KT * DP * 2;        // bytes of a K or V tile
   static constexpr int NS = CODED ? (DP <= 64 ? 7 : 4) : DP <= 64 ? 8 : 5;  // tiles in the ring
-  static constexpr int kRaw = 2;
+  static constexpr int kSets = CODED && DP > 128 ? 2 : 1;
+  static constexpr int kRaw = 2 / kSets;            // a set's
   static constexpr int kQ = 128 * DP * 2;           // bytes of a row tile
   static constexpr int kSoftmax = 128 * NW;         // softmax threads
-  static constexpr int kCopy = DP <= 128 ? 128 : 64;  // copying threads
-  static constexpr int kThreads = kSoftmax + kCopy + 64;
+  static constexpr int kCopy = DP <= 128 ? 128 : 64;  // copying threads of a set
+  static constexpr int kThreads = kSoftmax + kSets * kCopy + 64;
   static constexpr int KW = KT / (kCopy / 32);      // keys a copying warp takes, one a lane
   static constexpr int kAhead = 2;                  // scores ahead of the outputs
   static constexpr int kO = 256;                    // first column of O; the second O follows
@@ -72,7 +75,7 @@ template <int DP, bool CODED>
 struct TcMore {};
 template <int DP>
 struct TcMore<DP, true> {
-  alignas(1024) uint4 raw[TcShape<DP, true>::kRaw][TcShape<DP, true>::kCopy / 32][DP / 16][32];  // a lane's codes
+  alignas(1024) uint4 raw[2][TcShape<DP, true>::kCopy / 32][DP / 16][32];  // a lane's codes
   uint32_t units[16][4];
   signed char power[2][256];
   float second;
@@ -113,6 +116,13 @@ __device__ __forceinline__ CopyItem copy_item(int n, int kt, int lead) {
   const int m = n - first, rest = kt - first;
   if (m < 2 * rest) return {m & 1 ? first + (m >> 1) : m >> 1, !(m & 1)};
   return {m - rest, true};
+}
+
+// The inverse: which copy a tile's K or V is.
+__device__ __forceinline__ int item_of(int tile, bool is_v, int kt, int lead) {
+  const int first = min(lead, kt);
+  if (!is_v) return tile < first ? tile : 2 * tile - first + 1;
+  return tile < kt - first ? first + 2 * tile : kt + tile;
 }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
@@ -157,7 +167,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
   using M = typename std::conditional<kCodes, __half, T>::type;  // the operands
   TcShared<DP, kCodes>& sm = *reinterpret_cast<TcShared<DP, kCodes>*>(raw);
   const int tid = threadIdx.x, warp = (int)tc::uniform(tid >> 5), lane = tid & 31;
-  constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + S::kCopy / 32,
+  constexpr int kCopyWarp = S::kSoftmax / 32, kMmaWarp = kCopyWarp + S::kSets * S::kCopy / 32,
                 kRelayWarp = kMmaWarp + 1;
 
   if (tc::smem_at(raw) & 1023) {  // the operands' swizzle counts on it
@@ -206,10 +216,13 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
     // thread when its part is there.  Pages are looked up one K tile ahead; the rows of a tile
     // are kept until its V follows.
     static_assert(S::KW == 32, "a lane looks up one key");
-    const int cw = warp - kCopyWarp, ct = tid - S::kSoftmax;
+    constexpr bool kTwo = S::kSets == 2;
+    const bool v_set = kTwo && warp - kCopyWarp >= S::kCopy / 32;
+    const int cw = warp - kCopyWarp - (v_set ? S::kCopy / 32 : 0), ct = tid - S::kSoftmax;
     int stage = 0;
     unsigned round = 0;   // of the ring
     int k_count = 0;      // K tiles so far
+    unsigned items = 0;   // K and V tiles of the units before
     unsigned unit = 0;
     bool ok = true;
     while (!w.done) {
@@ -229,10 +242,10 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
       };
       look_up(0);
       // ---- Q, once the last unit's scores are done
-      if (unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
+      if (!v_set && unit > 0) ok = tc::bar_wait(&sm.q_free, (unit - 1) & 1, &sm.dead);
       ++unit;
       if (!__all_sync(0xffffffffu, ok)) break;
-      {
+      if (!v_set) {
         // this thread's piece of rows ct / CH, + kStep, ...: (token, head) stepped without division
         constexpr int kStep = S::kCopy / (CH < S::kCopy ? CH : S::kCopy);
         const int ch = ct % CH;
@@ -303,16 +316,18 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
       // order of copies.
       auto rows_of = [&](const CopyItem& it) {
         int now = rows[0];
-        if (!it.is_v) {
+        if (kTwo || !it.is_v) {
           now = -1;
           if (page.page >= 0 && page.page < a.num_blocks)
             now = ((int)page.page * a.nk + w.h) * a.block_size + page.row;
           else if (page.page != -2)
             atomicOr(g.err, kSlotOutOfRange);
+          if constexpr (!kTwo) {
 #pragma unroll
-          for (int e = 0; e < S::kAhead; ++e)
-            if (e == waiting) rows[e] = now;
-          ++waiting;
+            for (int e = 0; e < S::kAhead; ++e)
+              if (e == waiting) rows[e] = now;
+            ++waiting;
+          }
           if constexpr (!kCodes) {
             const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
             if (lane == 0) {
@@ -330,7 +345,8 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         return now;
       };
       if constexpr (kCodes) {
-        // Codes are copied kRaw items ahead, each lane's to slots of its own, and from there widened and stored.
+        // Codes are copied kRaw items ahead, each lane's to slots of its own, from there to its registers, and widened and
+        // stored.
         constexpr int CC = DP / 16;  // 16-byte pieces of a row of codes
         // This lane's piece of row `key` + i * 128 / DP * 4: eight lanes have four pieces of two rows each, so that what
         // they store meets every bank once.
@@ -340,15 +356,16 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         uint32_t kb[S::kRaw], vb[S::kRaw];      // its scales
         __half2 v_factor[S::kAhead];            // of the K tiles whose V has not followed
         int behind = 0;                         // so many
+        const int mine = kTwo ? kt : 2 * kt;    // items of this set
         auto read = [&](int n, auto slot) {
           constexpr int at = decltype(slot)::value;
-          if (n < 2 * kt) {
-            const CopyItem it = copy_item(n, kt, lead);
+          if (n < mine) {
+            const CopyItem it = kTwo ? CopyItem{n, v_set} : copy_item(n, kt, lead);
             const int now = rows_of(it);
             const Code* const src = it.is_v ? vc : kc;
             const Span& span = it.is_v ? a.v_span : a.k_span;
             is_v[at] = it.is_v;
-            if (!it.is_v) {
+            if (kTwo || !it.is_v) {
               is_there[at] = now >= 0;
               kb[at] = vb[at] = 0;
               if (now >= 0) {
@@ -357,7 +374,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
                 vb[at] = ldg(g.v_scale + z, a.vs_span, g.err);
               }
             }
-            const unsigned dst = tc::smem_at(&sm.raw[at][cw][0][lane]);
+            const unsigned dst = tc::smem_at(&sm.raw[kTwo ? v_set : at][cw][0][lane]);
 #pragma unroll
             for (int i = 0; i < CC; ++i) {
               const int r = __shfl_sync(0xffffffffu, now, first_key + i * kKeys);
@@ -377,76 +394,81 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           constexpr int at = decltype(slot)::value;
           cp_async_wait<S::kRaw - 1>();
           __half2 f;
+          const uint32_t vm = kTwo || !is_v[at] ? __reduce_max_sync(0xffffffffu, vb[at] == 255 ? 0u : vb[at]) : 0u;
           if (!is_v[at]) {
             const uint32_t there = __ballot_sync(0xffffffffu, is_there[at]);
             uint32_t km = __reduce_max_sync(0xffffffffu, kb[at] == 255 ? 0u : kb[at]);
-            uint32_t vm = __reduce_max_sync(0xffffffffu, vb[at] == 255 ? 0u : vb[at]);
             const bool far = __any_sync(0xffffffffu, (kb[at] > 0 && kb[at] + 15 < km) || (vb[at] > 0 && vb[at] + 15 < vm));
             if (km == 0) km = 127;  // zeros, or no key: in any units
             f = relative(kb[at], km);
-            const __half2 fv = relative(vb[at], vm);
+            if constexpr (!kTwo) {
+              const __half2 fv = relative(vb[at], vm);
 #pragma unroll
-            for (int e = 0; e < S::kAhead; ++e)
-              if (e == behind) v_factor[e] = fv;
-            ++behind;
+              for (int e = 0; e < S::kAhead; ++e)
+                if (e == behind) v_factor[e] = fv;
+              ++behind;
+            }
             if (lane == 0) {
               sm.seen[k_count & 15][cw] = there;
               sm.units[k_count & 15][cw] = __float_as_uint(far ? NAN : power_of(km)) | vm;
               tc::bar_arrive(&sm.seen_full[k_count & 15]);
             }
             ++k_count;
+          } else if constexpr (kTwo) {
+            f = relative(vb[at], vm);
           } else {
             f = v_factor[0];
 #pragma unroll
             for (int e = 0; e + 1 < S::kAhead; ++e) v_factor[e] = v_factor[e + 1];
             --behind;
           }
-          if (round > 0) ok = tc::bar_wait(&sm.empty[stage], (round - 1) & 1, &sm.dead);
+          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&f);
+          uint4 x[CC];
+          auto take = [&] {
+#pragma unroll
+            for (int i = 0; i < CC; ++i) x[i] = sm.raw[kTwo ? v_set : at][cw][i][lane];
+          };
+          if constexpr (kTwo) {
+            take();
+            __syncwarp();  // (read before the copies that overwrite them begin)
+            read(n + S::kRaw, slot);
+          }
+          const unsigned item = items + (unsigned)(kTwo ? item_of(n, v_set, kt, lead) : n);
+          const int to_stage = (int)(item % NS);
+          if (item >= NS) ok = tc::bar_wait(&sm.empty[to_stage], (item / NS - 1) & 1, &sm.dead);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) return;
-          unsigned char* const to = sm.ring[stage] + (cw * S::KW + first_key) * 128 + (ch >> 2) * (KT * 128);
-          const uint32_t bits = *reinterpret_cast<const uint32_t*>(&f);
-          constexpr int U = CC < 8 ? CC : 8;  // pieces at a time: their loads before any store
+          if constexpr (!kTwo) take();
+          unsigned char* const to = sm.ring[to_stage] + (cw * S::KW + first_key) * 128 + (ch >> 2) * (KT * 128);
 #pragma unroll
-          for (int i0 = 0; i0 < CC; i0 += U) {
-            uint4 x[U];
-            uint32_t fk[U];
+          for (int i = 0; i < CC; ++i) {
+            const uint32_t fk = __shfl_sync(0xffffffffu, bits, first_key + i * kKeys);
+            const int key = first_key + i * kKeys;
+            const __half2 fh = *reinterpret_cast<const __half2*>(&fk);
+            const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-              x[i] = sm.raw[at][cw][i0 + i][lane];
-              fk[i] = __shfl_sync(0xffffffffu, bits, first_key + (i0 + i) * kKeys);
+            for (int e = 0; e < 4; ++e) {
+              halves(in[e], y[2 * e], y[2 * e + 1]);
+              y[2 * e] = times(y[2 * e], fh);
+              y[2 * e + 1] = times(y[2 * e + 1], fh);
             }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-              const int key = first_key + (i0 + i) * kKeys;
-              const __half2 fh = *reinterpret_cast<const __half2*>(&fk[i]);
-              const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                halves(in[e], y[2 * e], y[2 * e + 1]);
-                y[2 * e] = times(y[2 * e], fh);
-                y[2 * e + 1] = times(y[2 * e + 1], fh);
-              }
-              unsigned char* const row = to + (i0 + i) * kKeys * 128;
-              const int piece = (ch & 3) * 2;
-              *reinterpret_cast<uint4*>(row + ((piece ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<uint4*>(row + (((piece | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-            }
+            unsigned char* const row = to + i * kKeys * 128;
+            const int piece = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + ((piece ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(row + (((piece | 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
-          tc::bar_arrive(&sm.copied[stage]);
-          if (++stage == NS) stage = 0, ++round;
-          read(n + S::kRaw, slot);  // into the slots that were just read
+          tc::bar_arrive(&sm.copied[to_stage]);
+          if constexpr (!kTwo) read(n + S::kRaw, slot);  // (earlier: 4 chunks of 1984 behind 4096 845 us instead of 800)
         };
-        static_assert(S::kRaw == 2, "the two steps");
         const std::integral_constant<int, 0> even;
-        const std::integral_constant<int, 1> odd;
-        read(0, even);
-        read(1, odd);
-        for (int n = 0; n < 2 * kt && ok; n += 2) {
+        const std::integral_constant<int, S::kRaw - 1> odd;
+        for (int n = 0; n < S::kRaw; ++n) n == 0 ? read(0, even) : read(1, odd);
+        for (int n = 0; n < mine && ok; n += S::kRaw) {
           step(n, even);
-          if (ok) step(n + 1, odd);
+          if (S::kRaw == 2 && ok) step(n + 1, odd);
         }
+        items += 2 * kt;
       } else {
         for (int n = 0; n < 2 * kt; ++n) {
           // ---- K and V
