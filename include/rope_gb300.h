@@ -472,8 +472,9 @@ int rope_paged_attention_workspace(int64_t num_tokens, int64_t num_q_heads, int6
  * RoPE of query and key on the way to the query output and to a paged KV cache of 8-bit codes.
  *
  * A cached value is code * 2^(b - 127), b being the scale byte of its block: the BS / S tokens of a page (S scale
- * blocks a page) of one head; b = 0 is a block of zeros.  The rotation is rope_append_paged_kv's, in binary32.  Then for every scale block that
- * the call writes, of the keys and of the values,
+ * blocks a page) of one head; b = 0 is a block of zeros, 255 is NaN.  The rotation is rope_append_paged_kv's; keys are
+ * rotated with two roundings to binary32 an element (a code's step is 2^20 times as large), not to their type.  Then for
+ * every scale block that the call writes, of the keys and of the values,
  *   most = max |x| over its values written that are finite;  e = the least integer with most <= 448 * 2^e
  *   byte = e + 127, from 1 to 254;  0 where most = 0
  * and where tokens stand in the block before the first one written: no less than the byte that was there, and where it
@@ -507,6 +508,17 @@ int rope_append_paged_kv_8bit(const rope_tensor_t* positions, const rope_tensor_
  *   k_cache, v_cache  ROPE_F8E4M3 [NB, Nk, BS, D].
  *   k_scale, v_scale  ROPE_E8M0 [NB, Nk, S]; S divides BS.
  *   workspace_bytes   at least what rope_paged_attention_8bit_workspace says.
+ *
+ * Arithmetic: as rope_paged_attention's, scores, statistics and sums in binary32.  The products run on the tensor cores
+ * with binary16 operands, which hold codes exactly; scales come in as powers of two.  BF16 and F32 queries are taken times
+ * a power of two that brings a row's largest element to about 2^8: BF16 exact down to 2^-22 of it, off by 2^-33 of it
+ * below; F32 as a sum of two binary16 values, off by 2^-23 of an element or 2^-33 of the largest.  Softmax weights are
+ * rounded to binary16 (half a step, those below 2^-25 of a row's largest by 2^-36 of it), with F32 queries to the sum of two.
+ * Scales that lie far apart leave binary16: rows that see such keys are computed again one key at a time, as rows are
+ * whose result is not finite (about 1 us a key).  A row meets that where a scale of V is below 2^-15 of the largest
+ * of V that it has seen of its part of the keys; in calls with more than 16 rows a sequence and key head where,
+ * among 32 keys that follow each other, one's scale of K or V is below 2^-15 of the largest (0 apart), or where the
+ * largest of V of 32 keys is below 2^-10 of the largest before.
  */
 int rope_paged_attention_8bit(const rope_tensor_t* query, int64_t query_row_stride, const rope_tensor_t* k_cache,
                               const rope_tensor_t* v_cache, const rope_tensor_t* k_scale,
@@ -527,7 +539,7 @@ int rope_paged_attention_8bit_workspace(int64_t num_tokens, int64_t num_q_heads,
  * Row i of the new batch has the tokens of old row p = parents[i] (p < 0: only the prefix), and room for room[i] more:
  *   all old rows let go of their pages; a page that nobody then holds is free, with what follows taken into account;
  *   row i holds the whole pages of p;
- *   if p's last page is not full, the first row i that asks for it keeps it, provided nobody else holds it; any other
+ *   if p's last page is not full, the first row i that asks for it keeps it, provided nobody else holds it then; any other
  *   gets a fresh page, and (that page, the fresh one) is a pair of pages to be copied before the cache is written;
  *   fresh pages follow until the row has room: free pages are given out lowest first, rows in order.
  * copy_src and copy_dst receive the pairs in the order of rows, then -1.  counts[0] is their number, counts[1] how many
@@ -536,6 +548,8 @@ int rope_paged_attention_8bit_workspace(int64_t num_tokens, int64_t num_q_heads,
  * Where pages run out, the entries are -1 from there on, a pair's copy_dst too, and ROPE_DEVICE_PAGES_EXHAUSTED is
  * recorded.  A page number outside [0, NB), more tokens than a row's pages hold, and p >= B record
  * ROPE_DEVICE_SLOT_OUT_OF_RANGE; such pages are passed over, tokens past the table dropped, such a p is none.
+ * A row's pages are those of its seq_lens.  A program that cuts a sequence short (drafted tokens that were refused) lets
+ * go of pages that are then behind its end by itself, in ref_counts.
  *
  *   block_table I64 [B, W], new_block_table I64 [rows, new W]; seq_lens I64 [B]; parents, room (or NULL), new_seq_lens,
  *   copy_src, copy_dst I64 [rows], rows at most 8192; ref_counts, new_ref_counts I32 [NB], which may be one tensor;

@@ -253,6 +253,9 @@ def rearrange_reference(c, parents, room=None, new_W=None, canary=-77):
     new, new_lens, need, pairs, claimed = [], [], [], [], set()
     own_of = [max(lens[p] - P, 0) if p >= 0 else 0 for p in parents]
     keeps = []
+    for i, p in enumerate(parents):  # whole pages first: who holds one keeps others from writing on it
+        for j in range(own_of[i] // bs):
+            refs[table[p][j]] += 1
     for i, p in enumerate(parents):
         full, rest = divmod(own_of[i], bs)
         k = False
@@ -264,8 +267,8 @@ def rearrange_reference(c, parents, room=None, new_W=None, canary=-77):
     for i, p in enumerate(parents):
         full, rest = divmod(own_of[i], bs)
         row = [table[p][j] for j in range(full + keeps[i])] if p >= 0 else []
-        for page in row:
-            refs[page] += 1
+        if keeps[i]:
+            refs[row[-1]] += 1
         new.append(row)
         grown = own_of[i] + (room[i] if room is not None else 0)
         new_lens.append(P + grown)

@@ -55,6 +55,20 @@ def test_rearrange(rope_gpu, bs, P, in_place):
                  rearrange_reference(c, parents, room, width))
 
 
+@pytest.mark.parametrize("parents", [[0, 1], [1, 0], [1, 1, 0], [1, -1], [0, 0]])
+def test_rearrange_a_sequence_cut_short(rope_gpu, parents):
+    """Sequence 1 shares whole pages with sequence 0 and was then cut to end inside one: its child may not write on what
+    another's child reads."""
+    for spare_columns in (2, 6000):  # one CTA, a cluster
+        c = pages_case(12, [40, 40], 8, spare=9, share=False, spare_columns=spare_columns)
+        c["refs"][c["table"][1, :4]] = 0
+        c["table"][1, :4] = c["table"][0, :4]
+        c["refs"][c["table"][0, :4]] = 2
+        c["refs"][c["table"][1, 4]] = 0
+        c["lens"][1] = 27  # pages 0 to 3, the last with three tokens
+        same(run_rearrange(c, parents), rearrange_reference(c, parents))
+
+
 def test_rearrange_many_rows(rope_gpu):
     """More rows than a CTA has threads, more pages than a warp's range has lanes, the most rows that are taken."""
     g = torch.Generator().manual_seed(3)

@@ -10,7 +10,7 @@
 //
 // rearrange_sequences: every old row lets go of its pages; new row i takes the whole pages of its parent once
 // more.  The page that is written on (the last, partly filled one) stays with the first of the new rows that
-// claim it if nobody else holds it: rows claim it by atomicMin of row - kClaim in its count, which is then 0.
+// claim it if nobody then holds it: rows claim it by atomicMin of row - kClaim in its count, which is then 0.
 // The others get a copy.  Where fresh pages go is found the other way round: the r-th free page belongs to the
 // row whose range of requests holds r.
 //
@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
   const bool one_row = CL == 1 && rows <= kThreads;
   const Taken kept = one_row && me < rows ? taken_of(me, a, err) : Taken{-1, 0, 0, 0, -1};
   auto taken = [&](int i) { return one_row ? kept : taken_of(i, a, err); };
+  for (int i = threadIdx.x; i < rows; i += kThreads) have[i] = taken(i).full;  // (of every CTA)
   // ---- counts as they were
   if (refs != p.refs) {
     for (int i = me; i < NB; i += All::kAll)
@@ -227,6 +228,18 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
   for_entries<All::kAllWarps>(warp, p.B, a.table_span, err, pages_of_row, [&](int64_t, int, int64_t page) {
     if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
     else if (ref_ok(refs + page)) add_to<CL>(refs + page, -1);
+  });
+  All::sync();
+  // ---- new rows take hold of whole pages
+  auto whole_of_row = [&](int64_t i) -> Entries {
+    const int n = have[i];
+    return {n ? p.table + ldg(p.parents + i, a.parents_span, err) * p.W : nullptr, n};
+  };
+  for_entries<All::kAllWarps>(warp, rows, a.table_span, err, whole_of_row, [&](int64_t i, int c, int64_t page) {
+    if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
+    else if (ref_ok(refs + page)) add_to<CL>(refs + page, 1);
+    int64_t* const to = p.new_table + i * p.new_W + c;
+    if (access_ok(to, 8, a.new_table_span, err)) *to = page;
   });
   All::sync();
   // ---- claims of pages that are written on
@@ -282,19 +295,14 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
   }
   if (threadIdx.x == 0) start[rows] = run.x;
   All::sync();
-  // ---- new rows take hold
-  auto kept_of_row = [&](int64_t i) -> Entries {
-    const int n = have[i] & ~kKeeps;
-    return {n ? p.table + ldg(p.parents + i, a.parents_span, err) * p.W : nullptr, n};
-  };
-  for_entries<All::kAllWarps>(warp, rows, a.table_span, err, kept_of_row, [&](int64_t i, int c, int64_t page) {
-    const int h = have[i], n = h & ~kKeeps;
-    const int32_t add = h != n && c == n - 1 ? 1 - ((int)i - kClaim) : 1;  // off with the claim
-    if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
-    else if (ref_ok(refs + page)) add_to<CL>(refs + page, add);
-    int64_t* const to = p.new_table + i * p.new_W + c;
+  // ---- pages that are kept to be written on: off with the claims
+  for (int i = me; i < rows; i += All::kAll) {
+    if (!(have[i] & kKeeps)) continue;
+    const int64_t page = taken(i).last;
+    if (ref_ok(refs + page)) *(volatile int32_t*)(refs + page) = 1;
+    int64_t* const to = p.new_table + i * p.new_W + (have[i] & ~kKeeps) - 1;
     if (access_ok(to, 8, a.new_table_span, err)) *to = page;
-  });
+  }
   All::sync();
   // ---- free pages
   const int2 mine = All::pages_of(warp, NB);
