@@ -405,3 +405,29 @@ def test_no_tokens(rope_gpu):
     i = torch.empty(0, dtype=torch.int64, device="cuda")
     R.copy_pages(i, i.clone(), [k])
     assert R.launch_count() == n
+
+
+@pytest.mark.skipif(not hasattr(torch, "_lazy_clone"), reason="this torch makes no such tensors")
+def test_the_source_of_a_lazy_clone_keeps_its_values(rope_gpu):
+    """Tensors that share their memory until one of them is written: what these operators write is separated first."""
+    D, bs, NB = 64, 4, 6
+    table = torch.cat([torch.ones(8, D // 2), torch.zeros(8, D // 2)], 1).cuda()
+    x = torch.randn(3, D, device="cuda")
+    caches = [torch.zeros(NB, 1, bs, D, dtype=torch.uint8, device="cuda").view(E4M3) for _ in range(2)]
+    caches += [e8m0(torch.zeros(NB, 1, 1)).cuda() for _ in range(2)]
+    refs = torch.zeros(NB, dtype=torch.int32, device="cuda")
+    blocks, lens = torch.full((1, 2), -1, dtype=torch.int64, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    q_out, out = torch.zeros_like(x), torch.zeros_like(x)
+    sources = caches + [refs, blocks, lens, q_out, out]
+    before = [t.view(torch.uint8).clone() for t in sources]
+    c, r, b, n, q, o = [torch._lazy_clone(t) for t in caches], *(torch._lazy_clone(t) for t in (refs, blocks, lens, q_out, out))
+    i = lambda *v: torch.tensor(v, device="cuda")  # noqa: E731
+    pair = [torch.zeros(1, dtype=torch.int64, device="cuda") for _ in range(2)]
+    R.rearrange_sequences(blocks, lens, r, i(0), b, n, r, *pair, i(0, 0), bs, room=i(3))
+    R.append_paged_kv_8bit(i(0, 1, 2), x, x, x, table, i(0, 1, 2), *c, D, query_out=q)
+    R.paged_attention_8bit(q, *c, b, n, i(0, 3), o)
+    R.copy_pages(i(0), i(5), c)
+    assert n.tolist() == [3] and r.tolist() == [1, 0, 0, 0, 0, 0] and int(b[0, 0]) == 0
+    assert torch.equal(q, x) and bool((bytes_of(c[0])[5] == bytes_of(c[0])[0]).all())
+    for t, was in zip(sources, before):
+        assert torch.equal(t.view(torch.uint8), was)

@@ -16,8 +16,9 @@
 // requests' tokens 3.5 us, the kernel for many 4.7; a prompt of 512 9.4, 13.7; 1024 requests 11.5, 12.4; 2048 21.3, 20.7.)
 //
 // Many: what an item costs in instructions counts as much as its bytes.  A warp has the runs that begin in a window of
-// tokens, for a set of heads: a run of one row is one group's, the groups having a head each, up to kRows of them at a
-// time; a longer run is the warp's, head by head, its groups taking the rows in turn.  A thread has slots of its own in
+// tokens, for a set of heads: a run of up to kRows rows is one group's, the groups having a head each, kRows rows at a
+// time (the example below in scale blocks of 2 tokens: 111 us, 218 as longer runs go); a longer one is the warp's, head by
+// head, its groups taking the rows in turn.  A thread has slots of its own in
 // shared memory for its pieces of kRows rows and of their table rows, which it copies with cp.async, all at once: an item
 // is a few round trips to memory.  Up to kRows rows a group are read once, longer runs again (from L2) once their largest
 // value is known.  Queries go by heads of a token.  (16384 tokens 84 us, 67% of the copy rate; without the codes, or
@@ -559,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     int singles = 0;
     while (begins) {
-      // ---- what is done at a time: a run of several rows, head by head; or up to kRows runs of one, their heads side by side
+      // ---- what is done at a time: a run of more than kRows rows, head by head; or up to kRows rows of shorter runs, the heads
+      // side by side
       int i0 = __ffs(begins) - 1;
       int n = 1;
       {
@@ -576,20 +578,28 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (off) break;
         }
       }
-      const bool single = n == 1;
-      uint32_t run_of = 0x01010101u * i0;  // the tokens that begin the runs, relative to t0: 8 bits each
-      int count = 1;
-      begins &= begins - 1;
-      while (single && count < kRows && begins) {
-        const int j = __ffs(begins) - 1;
-        if (on_mask >> (j + 1) & 1) break;  // (j is below 16)
-        run_of = (run_of & ~(0xffu << 8 * count)) | (uint32_t)j << 8 * count;
-        ++count;
+      const bool single = n <= kRows;
+      uint32_t run_of = 0, starts = 0;  // single: the slots' tokens, relative to t0, 8 bits each, and which begin runs
+      int count = 0;
+      if (single) {
+        for (;;) {
+          starts |= 1u << count;
+          run_of |= (0x03020100u + 0x01010101u * i0) << 8 * count;
+          count += n;
+          if (count < 4) run_of &= (1u << 8 * count) - 1u;
+          begins &= begins - 1;
+          if (!begins) break;
+          i0 = __ffs(begins) - 1;  // (below 16)
+          n = __ffs(~(on_mask >> (i0 + 1)));
+          if (count + n > kRows) break;
+        }
+      } else {
         begins &= begins - 1;
       }
       if (single && singles++ % a.subs != sub) continue;  // the warps that share the set take them in turn
       const int head0 = single ? 0 : sub, heads_here = single ? 1 : min(a.per_warp, all - u0);
       const int by = single ? 1 : a.subs;
+      bool turned = false;  // the slots hold the table rows of all the run's rows
       for (int j = head0; j < heads_here; j += by) {
         const int u = u0 + (single ? g : j);
         const bool mine = g < a.per_warp && u < all;
@@ -610,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           at = (is_v ? d.vs : d.ks) + (page * heads + h) * a.S + part;
           rows = (is_v ? d.vc : d.kc) + ((page * heads + h) * a.block_size + (int64_t)part * a.per) * a.D;
         };
-        // Rows under way, in slot e: of the one run the row base + e * step, or of run e its only one; with their table rows.
+        // Rows under way, in slot e: of the one run the row base + e * step, or token e of the short runs'; with their table rows.
         auto token_of = [&](int base, int e) { return single ? (int)(run_of >> 8 * e & 0xffu) : i0 + base + e * step; };
         uint32_t on = 0;  // which of them are written, a bit a slot
         auto read = [&](int base) {
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 cp_async16(&sm.data[e][z][threadIdx.x], p + ca + z * (16 / sizeof(T)), policy, sspan, err);
                 cp_async16(&sm.data[e][kPieces + z][threadIdx.x], p + cb + z * (16 / sizeof(T)), policy, sspan, err);
               }
-              if (!MROPE && !is_v) {
+              if (!MROPE && !is_v && !turned) {
                 const TT* const row = table + where.p[0] * a.R;
                 if constexpr (NEOX) {
                   if (ra)
@@ -647,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           cp_async_commit();
           cp_async_wait<0>();
+          turned = turned || (!single && !is_v && n <= kRows * step);
         };
         // Slot e in binary32: rotated twice, for the largest value and for the codes, rather than held.
         float2 xf[VEC / 2], yf[VEC / 2];
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         uint8_t *at, *rows;
         int f;
-        uint32_t old = 0;  // bytes of the blocks (singles: 8 bits each) that hold rows before
+        uint32_t old = 0;  // bytes of the blocks (short runs: of each slot's, 8 bits each) that hold rows before
         for (int e = single ? count - 1 : 0; e >= 0; --e) {
           block_at(token_of(0, e), at, rows, f);
           old = old << 8 | (mine && f > 0 && access_ok(at, 1, zspan, err) ? (uint32_t)*at : 0u);
@@ -690,31 +701,33 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int passes = single ? 1 : (n + kRows * step - 1) / (kRows * step);
         float most = 0.f;
         bool any = false;     // some token of the run is written
-        uint32_t bytes = 0;   // of the blocks now, singles: 8 bits each
+        uint32_t bytes = 0;   // of the blocks now, short runs: 8 bits a slot
         for (int pass = 0; pass < passes; ++pass) {
           const int base = pass * kRows * step + g0;
           read(base);
+          int e0 = 0;  // (short runs: the first slot of this one)
 #pragma unroll 1
           for (int e = 0; e < kRows; ++e) {
-            float m = 0.f;
             if (on >> e & 1) {
               values(base, e);
-              m = L::largest(xf, yf);
+              most = fmaxf(most, L::largest(xf, yf));
             }
             if (!single) {
-              most = fmaxf(most, m);
               any = any || on != 0;
               continue;
             }
             if (e >= count) break;
-            m = me.over_group(m, C);
-            block_at(token_of(0, e), at, rows, f);
-            if (on >> e & 1) {
-              const int was = (int)(old >> 8 * e & 0xffu), byte = L::byte_of(m, f, was);
+            if (e + 1 < count && !(starts >> (e + 1) & 1)) continue;
+            most = me.over_group(most, C);
+            block_at(token_of(0, e0), at, rows, f);
+            if (on >> e0 & ((2u << (e - e0)) - 1u)) {
+              const int was = (int)(old >> 8 * e0 & 0xffu), byte = L::byte_of(most, f, was);
               me.again(rows, 0, 1, f, was, byte, cspan, err, a);
-              bytes |= (uint32_t)byte << 8 * e;
+              bytes |= (0x01010101u >> 8 * (3 - (e - e0))) * (uint32_t)byte << 8 * e0;
               if (me.c == 0 && access_ok(at, 1, zspan, err)) *at = (uint8_t)byte;
             }
+            most = 0.f;
+            e0 = e + 1;
             __syncwarp();
           }
         }
@@ -808,9 +821,11 @@ cudaError_t launch_as(const AppendProblem& p, cudaStream_t stream) {
   constexpr int kQueryHeads = query_heads<T, MROPE>();
   a.q_sets = (a.hq + kQueryHeads * a.per_warp - 1) / (kQueryHeads * a.per_warp);
   // One token to a window, so that all SMs are busy, up to 16 where there are many.  Two warps share a set's heads (16384
-  // tokens, 32 q, 8 k and 8 v heads of 128: 83 us; one 87, four 89).
+  // tokens, 32 q, 8 k and 8 v heads of 128: 83 us; one 87, four 89), four where a block's rows do not fit their slots (scale
+  // blocks of 64: 120 us, 136 by two).
+  constexpr int kRows = Staged<T, TT>::kRows;
   a.window = 1;
-  a.subs = std::min(a.per_warp, 2);
+  a.subs = std::min(a.per_warp, a.per > kRows * a.per_warp ? 4 : 2);
   const int64_t enough = (int64_t)sm_count() * 16;
   while (a.window < 16 && p.T / (2 * a.window) * a.kv_sets * a.subs >= enough) a.window *= 2;
   a.q_items = p.T * a.q_sets;
