@@ -155,18 +155,21 @@ struct CodesRing {
     unsigned char* const to = ring + slot * S::kStage;
     const uint32_t which = __ballot_sync(0xffffffffu, row >= 0);
     const unsigned dst = smem_u32(to);
-    if (which == (uint32_t)((1ull << S::KW) - 1) && a.D == DP) {  // whole rows of all keys
+    // (heads that do not fill their columns in the loop that is unrolled, too: 96, 107 -> 90 us for 64 requests of up to 8192;
+    // wider ones, with more pieces a row, lose by it: 192, 160 -> 175; by three in the other loop 160 takes 187, by one 215)
+    constexpr bool kWhole = DP > 128;
+    if (which == (uint32_t)((1ull << S::KW) - 1) && (!kWhole || a.D == DP)) {  // rows of all keys
 #pragma unroll
       for (int i = 0; i < S::KW * CH / 32; ++i) {
         const int idx = lane + 32 * i;
         const int key = idx / CH, ch = idx - key * CH;
         const int r = __shfl_sync(0xffffffffu, row, key);
-        const Code* p = src + ch * 16 + (uint64_t)(uint32_t)r * (uint32_t)DP;
-        if (access_ok(p, 16, span, g.err))
-          cp_async16_or_zero(dst + piece_at<DP, IS_V>(key, ch), p, true);
+        const bool inside = kWhole || ch * 16 < a.D;
+        const Code* p = src + (inside ? ch * 16 : 0) + (uint64_t)(uint32_t)r * (uint32_t)(kWhole ? DP : a.D);
+        cp_async16_or_zero(dst + piece_at<DP, IS_V>(key, ch), p, inside && access_ok(p, 16, span, g.err));
       }
     } else if (which) {
-#pragma unroll 1
+#pragma unroll 3
       for (int i = 0; i < S::KW * CH / 32; ++i) {
         const int idx = lane + 32 * i;
         const int key = idx / CH, ch = idx - key * CH;
