@@ -1,0 +1,53 @@
+"""Attention over a paged cache of 8-bit codes whose scales lie far apart, against a float64 reference (tests/scales_ref.py),
+in every kernel that the lengths choose between: units of 8, of 16 and of 128 or 256 rows, and a warp a row."""
+import pytest
+import torch
+
+from codes_ref import bytes_of, coded_case
+from scales_ref import check, put
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+# (new, own, query heads a key head, key heads, wide table): what the kernels are chosen by.  Small units of two tiles of keys
+# are not split; of many heads' most come to several tiles a CTA.
+UNITS = {"8": ([1, 1], [240, 133], 2, 1, False), "16": ([7], [240], 2, 1, False),
+         "8 many": ([1] * 4, [400, 398, 390, 260], 2, 64, False), "16 many": ([3] * 4, [400, 395, 390, 260], 4, 64, False),
+         "tall one tile": ([100], [400], 1, 1, True), "tall two tiles": ([150, 70], [400, 70], 3, 1, True)}
+ALL = list(UNITS)
+
+
+def case(units, seed, dtype, D, P=0, **kw):
+    new, own, G, hk, wide = UNITS[units]
+    c = coded_case(seed, dtype, new, own, hq=G * hk, hk=hk, D=D, P=P, S=16, **kw)
+    c["wide"] = wide
+    return c
+
+
+def led_by_key_4(units, dtype, D):
+    """Key 4 is 400 ahead of all others, whose weights are e^-400 of its own; V of about 64 in units of 1."""
+    c = case(units, 21, dtype, D)
+    c["q"][:] = 50 / D ** 0.5
+    bytes_of(c["k_codes"])[:] = 0
+    for name in ("k_scale", "v_scale"):
+        bytes_of(c[name])[:] = 127
+    put(c, "k", 4, code=0x50)  # 8
+    return c
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", ALL)
+@pytest.mark.parametrize("D", [16, 32, 48, 64, 128, 160, 256])
+@pytest.mark.parametrize("step", [89, 90, 91, 95])
+def test_v_in_units_beyond_2_to_the_90_of_the_one_that_counts(rope_gpu, dtype, units, D, step):
+    """A later V in units that many times as large, with no weight to speak of."""
+    if dtype != torch.float32 and D in (16, 48):
+        pytest.skip("16-bit heads are multiples of 32")
+    c = led_by_key_4(units, dtype, D)
+    put(c, "v", 130, byte=127 + step)
+    check(c, "jump")
+    c = led_by_key_4(units, dtype, D)  # and one that the last token alone sees
+    for b, n in enumerate(c["lens"].tolist()):
+        put(c, "v", n - 1, byte=127 + step, b=b)
+    check(c, "last")

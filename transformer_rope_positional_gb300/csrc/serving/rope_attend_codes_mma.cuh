@@ -7,7 +7,9 @@
 //  * The codes become binary16, exactly, on the way from shared memory to the operands of mma.sync m16n8k16, two an
 //    instruction; no product sees a scale.  A score is multiplied by its key's, a power of two, in binary32.  V's
 //    scale goes into the weight: with V_j = c_j 2^(b_j), O holds sum p_j 2^(b_j - B) c_j for the largest b_j so far, B
-//    (one a warp), and is multiplied by 2^(B_old - B) where that grows; l is the sum of p_j.
+//    (one a warp), and is multiplied by 2^(B_old - B) where that grows; l is the sum of p_j.  Where that would take what O
+//    holds out of binary32 it becomes NaN, for mend_rows to find, and what is 0 stays 0: each lane looks at its elements
+//    of O, which are sums over all keys, not at its l, which is a sum over some.
 //  * Which column of q and K a product's place along k stands for is free, as long as both agree, and so is which key
 //    and which column of V an operand's row stands for.  A lane's places are chosen so that it reads 16 bytes of a key
 //    (8 of a value) at once and has the operands of four products (of two keys and 8 columns) in its registers: no
@@ -440,12 +442,10 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
         l1 *= f1;
         m0 = t0;
         m1 = t1;
-        if (bigger) {
-          const int less = unit - (int)about.y;
-          const float down = less >= -90 ? power(less) : l0 + l1 > 0.f ? NAN : 0.f;
-          f0 *= down;
-          f1 *= down;
-          unit = (int)about.y;
+        const int less = unit - (int)about.y;
+        if (bigger && less >= -90) {
+          f0 *= power(less);
+          f1 *= power(less);
         }
 #pragma unroll
         for (int n = 0; n < NO; ++n) {
@@ -454,6 +454,12 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
           o[n][2] *= kEight ? f0 : f1;
           o[n][3] *= f1;
         }
+        if (bigger && less < -90)
+#pragma unroll
+          for (int n = 0; n < NO; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = o[n][e] == 0.f ? 0.f : NAN;
+        if (bigger) unit = (int)about.y;
       }
       // ---- weights: the operands of the product with V
       const float to_unit = power(142 - unit);
