@@ -51,3 +51,21 @@ def test_v_in_units_beyond_2_to_the_90_of_the_one_that_counts(rope_gpu, dtype, u
     for b, n in enumerate(c["lens"].tolist()):
         put(c, "v", n - 1, byte=127 + step, b=b)
     check(c, "last")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", ALL)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("P", [0, 96])
+def test_zeros_in_front(rope_gpu, dtype, units, D, P):
+    """V's first blocks are zeros with the byte 0: as with any other byte for them, bit for bit, so that no row is
+    computed again key by key for it."""
+    c = case(units, 22, dtype, D, P=P)
+    for j in range(192):
+        put(c, "v", j, byte=100, code=0)
+    a = check(c, "zeros in units of 2^-27")
+    for j in range(192):
+        put(c, "v", j, byte=0)
+    b = check(c, "zeros")
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)

@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
       uint32_t there[2 * S::kParts];  // which keys of the job are there
       uint32_t units[kCodes ? 2 * S::kParts : 1];  // codes: the units of their 32 keys each
       float row_scale = a.scale_log2;
-      float o_unit = 1.f;  // codes: O is in units of 2^(o_unit - 127)
+      float o_unit = 0.f;  // codes: O is in units of 2^(o_unit - 127); 0 while all of V was zeros, and O with it
       // The second group has no part of a unit of one row tile and one key tile, waits for nothing there
       // and may come out many tiles ahead of the copies.  The barriers of `seen` come round every 16
       // tiles, so that a parity tells the wanted tile from those 16 before and after it only while the
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
           l *= f;
           m = up;
-          if constexpr (kCodes) f *= o_unit - next_unit >= -90.f ? power((int)(o_unit - next_unit)) : l > 0.f ? NAN : 0.f;
+          if constexpr (kCodes)
+            if (o_unit > 0.f) f *= o_unit - next_unit >= -90.f ? power((int)(o_unit - next_unit)) : l > 0.f ? NAN : 0.f;
 #pragma unroll 1
           for (int ch = 0; ch < DP / 16; ++ch) {  // rare: few registers rather than few waits
             uint32_t x[16];
