@@ -55,6 +55,20 @@ def test_v_in_units_beyond_2_to_the_90_of_the_one_that_counts(rope_gpu, dtype, u
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("units", ALL)
+@pytest.mark.parametrize("D", [32, 64, 128, 256])
+def test_v_in_units_that_grow_again_and_again(rope_gpu, dtype, units, D):
+    """V's units grow by 2^88 twice, each time by less than what a row is computed again for."""
+    c = led_by_key_4(units, dtype, D)
+    for j in range(400):
+        put(c, "v", j, byte=70 if j < 128 else 158 if j < 256 else 246)
+    check(c, "stairs")
+    for j in range(400):  # in steps that grow by 2^9 a tile of 32 keys
+        put(c, "v", j, byte=70 + j // 32 * 14)
+    check(c, "slope")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", ALL)
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("P", [0, 96])
 def test_zeros_in_front(rope_gpu, dtype, units, D, P):

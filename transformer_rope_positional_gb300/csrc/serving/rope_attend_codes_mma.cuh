@@ -8,7 +8,7 @@
 //    instruction; no product sees a scale.  A score is multiplied by its key's, a power of two, in binary32.  V's
 //    scale goes into the weight: with V_j = c_j 2^(b_j), O holds sum p_j 2^(b_j - B) c_j for the largest b_j so far, B
 //    (one a warp), and is multiplied by 2^(B_old - B) where that grows; l is the sum of p_j.  Where that would take what O
-//    holds out of binary32 it becomes NaN, for mend_rows to find, and what is 0 stays 0: each lane looks at its elements
+//    holds out of binary32 (beyond 2^90 of the unit it began in) it becomes NaN, for mend_rows to find, and what is 0 stays 0: each lane looks at its elements
 //    of O, which are sums over all keys, not at its l, which is a sum over some.
 //  * Which column of q and K a product's place along k stands for is free, as long as both agree, and so is which key
 //    and which column of V an operand's row stands for.  A lane's places are chosen so that it reads 16 bytes of a key
@@ -61,6 +61,7 @@ struct CodesShared {
   uint2 there[4][S::kRecent];        // which keys are there, and the largest of V's bytes
   float ml[4][MR][2];
   int power[MR];                     // rows are times 2^power
+  int first[4];                      // a warp's unit in which O was first not 0 (after NaN, again)
   int bad;                           // some finished row is not finite
   int64_t tmp[kCodesThreads / 32 + 2];
 };
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
     for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     int unit = 15;  // O is in units of 2^(unit - 142): V's largest byte so far, at least 15
+    sm.first[warp] = 15;
 
     for (int k = w.k0; k < k1; ++k) {
       cp_async_wait<S - 2>();
@@ -442,10 +444,22 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
         l1 *= f1;
         m0 = t0;
         m1 = t1;
-        const int less = unit - (int)about.y;
-        if (bigger && less >= -90) {
-          f0 *= power(less);
-          f1 *= power(less);
+        bool far = false;
+        if (bigger) {
+          bool some = false;
+#pragma unroll
+          for (int n = 0; n < NO; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) some = some || o[n][e] != 0.f;
+          some = __any_sync(0xffffffffu, some);
+          far = some && (int)about.y - sm.first[warp] > 90;
+          __syncwarp();
+          if (!some || far) sm.first[warp] = (int)about.y;
+          if (some && !far) {
+            f0 *= power(unit - (int)about.y);
+            f1 *= power(unit - (int)about.y);
+          }
+          unit = (int)about.y;
         }
 #pragma unroll
         for (int n = 0; n < NO; ++n) {
@@ -454,12 +468,11 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
           o[n][2] *= kEight ? f0 : f1;
           o[n][3] *= f1;
         }
-        if (bigger && less < -90)
+        if (far)
 #pragma unroll
           for (int n = 0; n < NO; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] = o[n][e] == 0.f ? 0.f : NAN;
-        if (bigger) unit = (int)about.y;
       }
       // ---- weights: the operands of the product with V
       const float to_unit = power(142 - unit);

@@ -79,6 +79,8 @@ struct TcMore<DP, true> {
   uint32_t units[16][4];
   signed char power[2][256];
   float second;
+  float first[8];  // of a softmax warp: the unit in which its O was first not zeros (after NaN, again): beyond 2^90 of it O
+                   // may leave binary32
 };
 
 template <int DP, bool CODED>
@@ -736,6 +738,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         }
         if (!any) {
           m = mt;
+          if constexpr (kCodes) sm.first[warp] = next_unit;
         } else if (__any_sync(0xffffffffu, mt > m + (float)kLag || next_unit > o_unit)) {
           // the last product into O is done before O is changed
           ok = product_done();
@@ -745,8 +748,13 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           float f = fast_exp2(m - (up == -INFINITY ? 0.f : up));
           l *= f;
           m = up;
-          if constexpr (kCodes)
-            if (o_unit > 0.f) f *= o_unit - next_unit >= -90.f ? power((int)(o_unit - next_unit)) : l > 0.f ? NAN : 0.f;
+          if constexpr (kCodes) {
+            const bool far = next_unit - sm.first[warp] > 90.f;
+            __syncwarp();
+            if (o_unit > 0.f) f = !far ? f * power((int)(o_unit - next_unit)) : l > 0.f ? NAN : 0.f;
+            if (o_unit == 0.f || far) sm.first[warp] = next_unit;
+            __syncwarp();
+          }
 #pragma unroll 1
           for (int ch = 0; ch < DP / 16; ++ch) {  // rare: few registers rather than few waits
             uint32_t x[16];
