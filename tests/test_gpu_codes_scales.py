@@ -9,6 +9,7 @@ from scales_ref import check, put
 pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+HALVES = [torch.float16, torch.bfloat16]
 
 # (new, own, query heads a key head, key heads, wide table): what the kernels are chosen by.  Small units of two tiles of keys
 # are not split; of many heads' most come to several tiles a CTA.
@@ -16,6 +17,7 @@ UNITS = {"8": ([1, 1], [240, 133], 2, 1, False), "16": ([7], [240], 2, 1, False)
          "8 many": ([1] * 4, [400, 398, 390, 260], 2, 64, False), "16 many": ([3] * 4, [400, 395, 390, 260], 4, 64, False),
          "tall one tile": ([100], [400], 1, 1, True), "tall two tiles": ([150, 70], [400, 70], 3, 1, True)}
 ALL = list(UNITS)
+FEW = [u for u in ALL if "many" not in u]
 
 
 def case(units, seed, dtype, D, P=0, **kw):
@@ -83,3 +85,44 @@ def test_zeros_in_front(rope_gpu, dtype, units, D, P):
     b = check(c, "zeros")
     for x, y in zip(a, b):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", FEW)
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 192, 256])
+@pytest.mark.parametrize("name", ["k", "v"])
+@pytest.mark.parametrize("far", [9, 11, 14, 15, 16, 40])
+def test_scales_apart(rope_gpu, dtype, units, D, name, far):
+    """Scales up to 2^far apart: from key to key, growing and shrinking along the keys and from one 32 keys to the next,
+    with blocks of zeros among them."""
+    if far == 40 and D not in (64, 256):
+        pytest.skip("as for the others")
+    c = case(units, 23, dtype, D, q_scale=2.0)
+    g = torch.Generator().manual_seed(far)
+    n = 400
+    for kind, bytes_ in (("any", torch.randint(122 - far, 123, (n,), generator=g)),
+                         ("up", 122 - far + torch.arange(n) * far // (n - 1)),
+                         ("down", 122 - torch.arange(n) * far // (n - 1)),
+                         ("by 32", 122 - far * (torch.arange(n) // 32 % 2)),
+                         ("last of 32", 122 - far * (torch.arange(n) % 32 == 31).long())):
+        for j, byte in enumerate(bytes_.tolist()):
+            put(c, name, j, byte=byte if j % 50 != 7 else 0)
+        check(c, kind)
+
+
+@pytest.mark.parametrize("dtype", HALVES, ids=str)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_a_far_scale_that_few_rows_see(rope_gpu, dtype, D, name):
+    """A key in units of 2^-30 of the others': rows that see none of the 32 keys around it are as without it."""
+    new = [250] if D <= 128 else [125]
+    c = coded_case(26, dtype, new, new, hq=1, hk=1, D=D, S=16)
+    c["wide"] = True
+    n = new[0]
+    for j in range(n):
+        put(c, name, j, byte=120 if j % 3 else 119)
+    clean, clean_lse = check(c, "clean")
+    put(c, name, n - 1, byte=90)
+    out, lse = check(c, "far")
+    first = (n - 1) // 32 * 32
+    assert torch.equal(out[:first], clean[:first]) and torch.equal(lse[:first], clean_lse[:first])

@@ -69,8 +69,9 @@ struct TcShape {
 };
 
 // What the units over a cache of codes keep besides: of the last 16 K tiles, 32 keys at a time, the scales that their
-// codes are in units of (K's as a factor, NaN where some key's scale is too far below, with V's byte in its low bits); of the rows of this unit and
-// the next, the power of two that they are times; the unit of the second group's O.
+// codes are in units of (K's as a factor, with V's byte in its low bits and kFar where some key's scale is too far below);
+// of the rows of this unit and the next, the power of two that they are times; the unit of the second group's O.
+constexpr uint32_t kFar = 256;
 template <int DP, bool CODED>
 struct TcMore {};
 template <int DP>
@@ -152,8 +153,8 @@ __device__ __forceinline__ uint32_t times(uint32_t x, __half2 f) {
 // weights: with B the largest of V's so far, weights are e^(s - m) 2^(V's - B), O is in units of 2^B (and multiplied by
 // 2^(B_old - B) where B grows) and the sum of 32 weights goes into l times 2^(B - V's).  So the softmax costs nothing more
 // per score.  Rows of bfloat16 queries are multiplied by powers of two as in rope_attend_codes_mma.cuh.
-// Where scales are further apart (a key's from its 32 keys', or V's from B by more than kSpread), rows that see such
-// keys are made NaN, for mend_rows to find.
+// Where scales are further apart (a key's from its 32 keys', or V's from B by more than kSpread), rows that see any of such
+// 32 keys are made NaN, for mend_rows to find.
 constexpr int kSpread = 10;
 
 // C: elements of the cache, T or Code.
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
             }
             if (lane == 0) {
               sm.seen[k_count & 15][cw] = there;
-              sm.units[k_count & 15][cw] = __float_as_uint(far ? NAN : power_of(km)) | vm;
+              sm.units[k_count & 15][cw] = __float_as_uint(power_of(km)) | vm | (far ? kFar : 0u);
               tc::bar_arrive(&sm.seen_full[k_count & 15]);
             }
             ++k_count;
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
               top4[(i >> 1) & 3] = max3(top4[(i >> 1) & 3], __uint_as_float(v[ch][i]), __uint_as_float(v[ch][i + 1]));
-            sc[ch] = row_scale * __uint_as_float(units[ch] & 0xffffff00u);
+            sc[ch] = row_scale * __uint_as_float(units[ch] & 0xff800000u);
             top[ch] = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * sc[ch];
           }
           const float vm[2] = {(float)(units[0] & 255u), (float)(units[1] & 255u)};
@@ -721,6 +722,11 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           mt = fmaxf(top[0], top[1]) - kLift;  // -infinity stays (the factors are > 0)
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) less[ch] = vm[ch] == 0.f ? 0.f : vm[ch] - next_unit;  // (a V of zeros: in any units)
+          if ((units[0] | units[1]) & kFar) {
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch)
+              if ((units[ch] & kFar) && top[ch] > -INFINITY) l = NAN;
+          }
           if (fminf(less[0], less[1]) < (float)-kSpread) {  // (of weights of less than 2^-30 nothing is asked)
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch)
