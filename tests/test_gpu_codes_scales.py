@@ -126,3 +126,16 @@ def test_a_far_scale_that_few_rows_see(rope_gpu, dtype, D, name):
     out, lse = check(c, "far")
     first = (n - 1) // 32 * 32
     assert torch.equal(out[:first], clean[:first]) and torch.equal(lse[:first], clean_lse[:first])
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", ALL)
+@pytest.mark.parametrize("D", [64, 256])
+def test_a_scale_that_is_nan_without_weight(rope_gpu, dtype, units, D):
+    """V's scale is NaN and its codes are not, of a key of hardly any weight: NaN for the rows that see it, no others."""
+    c = led_by_key_4(units, dtype, D)
+    b = 0
+    n, new = int(c["lens"][b]), int(c["starts"][b + 1])
+    put(c, "v", n - 1, byte=255, b=b)
+    out, _ = check(c, "nan")
+    assert torch.isnan(out[new - 1]).all() and not torch.isnan(out[:new - 1]).any() and not torch.isnan(out[new:]).any()

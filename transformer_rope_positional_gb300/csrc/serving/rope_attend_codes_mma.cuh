@@ -127,7 +127,8 @@ struct CodesRing {
         const int at = (made - 1) & (S::kRecent - 1);
         const uint32_t which = __ballot_sync(0xffffffffu, row >= 0);
         const uint32_t most = __reduce_max_sync(0xffffffffu, vb != 255 ? vb : 0);
-        scales[at][lane] = make_float2(power_of(kb), power_of(vb));
+        // (a V that is NaN makes its key's scores NaN, so that it counts where its weight would not)
+        scales[at][lane] = make_float2(power_of(vb != 255 ? kb : 255), power_of(vb));
         if (lane == 0) there[at] = make_uint2(which, most);
       }
       ++made;
@@ -476,7 +477,7 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
       }
       // ---- weights: the operands of the product with V
       const float to_unit = power(142 - unit);
-      bool lost = false;  // V's scale is NaN, or too small for the weight's exponents
+      bool lost = false;  // V's scale is too small for the weight's exponents (or NaN, as the weight then is)
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
