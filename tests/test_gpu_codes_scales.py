@@ -139,3 +139,19 @@ def test_a_scale_that_is_nan_without_weight(rope_gpu, dtype, units, D):
     put(c, "v", n - 1, byte=255, b=b)
     out, _ = check(c, "nan")
     assert torch.isnan(out[new - 1]).all() and not torch.isnan(out[:new - 1]).any() and not torch.isnan(out[new:]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("units", FEW)
+@pytest.mark.parametrize("D", [64, 256, 288])
+def test_values_beyond_binary32(rope_gpu, dtype, units, D):
+    """Code times scale beyond binary32's range: of V without weight, of K where the query is 0."""
+    c = led_by_key_4(units, dtype, D)
+    put(c, "v", 130, byte=254, code=0x7e)
+    check(c, "v")
+    c = case(units, 27, dtype, D)
+    bytes_of(c["k_codes"])[:] = 0
+    bytes_of(c["k_codes"])[..., 0] = 0x7e
+    bytes_of(c["k_scale"])[:] = 254
+    c["q"].view(c["q"].shape[0], -1, D)[..., 0] = 0
+    check(c, "k")

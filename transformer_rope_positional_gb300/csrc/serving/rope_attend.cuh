@@ -50,6 +50,13 @@ constexpr bool kCoded = std::is_same<C, Code>::value;
 // The scale that byte b stands for: 2^(b - 127), 0 for b = 0 (a block of zeros), NaN for 255.
 __device__ __forceinline__ float power_of(uint32_t b) { return __uint_as_float(b == 255 ? 0x7fc00000u : b << 23); }
 
+// The same as two factors: of the first, up to 2^119, every code is within binary32; the second is 1, or up to 2^8.
+__device__ __forceinline__ void split_power(uint32_t b, float& s, float& x) {
+  const bool large = b > 246 && b < 255;
+  s = power_of(large ? 246u : b);
+  x = large ? __uint_as_float((127 + b - 246) << 23) : 1.f;
+}
+
 __device__ __forceinline__ float widen(Code c) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(c.bits, __NV_E4M3);
   return __half2float(__half(h));
@@ -499,11 +506,12 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
   float m = -INFINITY, l = 0.f;
   for (int j0 = 0; j0 < seen; j0 += KU) {
     int64_t at[KU];
-    float s[KU], ks[KU], vs[KU];
+    float s[KU], ks[KU], vs[KU];  // (codes: values are code * ks, and kx where one factor would take them out of binary32)
+    float kx[KU], vx[KU];
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
       s[u] = 0.f;
-      ks[u] = vs[u] = 1.f;
+      ks[u] = vs[u] = kx[u] = vx[u] = 1.f;
       if constexpr (kCoded<C>) {
         const PageRow r = j0 + u < seen ? page_row(j0 + u, table, g, a) : PageRow{-1, 0};
         const bool there = r.page >= 0 && r.page < a.num_blocks;
@@ -512,8 +520,8 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
         at[u] = there ? row * a.D : -1;
         if (there) {
           const int64_t i = row / a.per;
-          ks[u] = power_of(ldg(g.k_scale + i, a.ks_span, g.err));
-          vs[u] = power_of(ldg(g.v_scale + i, a.vs_span, g.err));
+          split_power(ldg(g.k_scale + i, a.ks_span, g.err), ks[u], kx[u]);
+          split_power(ldg(g.v_scale + i, a.vs_span, g.err), vs[u], vx[u]);
         }
       } else {
         const int64_t r = j0 + u < seen ? key_row(j0 + u, table, g, a) : -1;
@@ -537,6 +545,7 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
     float top = m;
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
+      if constexpr (kCoded<C>) s[u] *= kx[u];
       if (at[u] < 0) s[u] = -INFINITY;
       top = s[u] != s[u] ? s[u] : fmaxf(top, s[u]);
     }
@@ -548,12 +557,12 @@ __device__ __forceinline__ void attend_row(int64_t t, int h, const T* __restrict
 #pragma unroll
     for (int u = 0; u < KU; ++u) {
       if (at[u] < 0) continue;
-      const float w = exp2f(s[u] - base);
+      const float w = exp2f(s[u] - base), wx = kCoded<C> ? w * vx[u] : w;
       l += w;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const int d = lane + 32 * e;
-        if (d < a.D) o[e] = fmaf(w, element(vc + at[u] + d, a.v_span, g.err) * vs[u], o[e]);
+        if (d < a.D) o[e] = fmaf(wx, element(vc + at[u] + d, a.v_span, g.err) * vs[u], o[e]);
       }
     }
     m = top;
