@@ -553,7 +553,7 @@ int rope_paged_attention_8bit_workspace(int64_t num_tokens, int64_t num_q_heads,
  *
  *   block_table I64 [B, W], new_block_table I64 [rows, new W]; seq_lens I64 [B]; parents, room (or NULL), new_seq_lens,
  *   copy_src, copy_dst I64 [rows], rows at most 8192; ref_counts, new_ref_counts I32 [NB], which may be one tensor;
- *   counts I64 [2].  W * BS, rows * new W and NB at most 2^30.  B and rows may be 0.
+ *   counts I64 [2].  W * BS, new W * BS, rows * new W, B and NB at most 2^30, W and new W below it.  B and rows may be 0.
  * What is written shares no memory with any other tensor of the call, new_ref_counts in the place of ref_counts apart.
  * Whole numbers: results are the same whatever the order in which threads run.
  */

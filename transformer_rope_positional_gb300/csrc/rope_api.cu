@@ -797,6 +797,7 @@ int rearrange_call(const rope_tensor_t* table, const rope_tensor_t* lens, const 
   if (B > kMostPages || rows > rope::kMostRearranged || W > kMostPages / bs || new_W > kMostPages / bs ||
       rows * new_W > kMostPages)
     return ROPE_ERR_PARAM_INVALID;
+  if (W == kMostPages || new_W == kMostPages) return ROPE_ERR_PARAM_INVALID;  // (a row's pages and a flag are 31 bits)
   const rope_tensor_t* const refs_read = in_place(refs, new_refs) ? nullptr : refs;
   if (any_meet({new_table, new_lens, new_refs, src, dst, counts}, {table, lens, refs_read, parents, room}))
     return ROPE_ERR_PARAM_INVALID;

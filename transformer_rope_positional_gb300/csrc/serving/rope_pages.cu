@@ -29,7 +29,7 @@ constexpr int kCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClaim = 1 << 30;
-constexpr int kKeeps = 1 << 30;  // a row keeps the page that it writes on
+constexpr int kKeeps = 1 << 30;  // a row keeps the page that it writes on (rows have fewer pages)
 constexpr int64_t kSmallPages = 24576;
 constexpr int64_t kSmallEntries = 16384;
 
