@@ -44,7 +44,8 @@ const at::Tensor& tensor(PyObject* o) {
   return THPVariable_Unpack(o);
 }
 
-int32_t type_of(const at::Tensor& t) {
+// `more`: with the types of the operators on codes and on pages, which the others do not take.
+int32_t type_of(const at::Tensor& t, bool more) {
   switch (t.scalar_type()) {
     case at::kFloat:
       return ROPE_F32;
@@ -55,14 +56,18 @@ int32_t type_of(const at::Tensor& t) {
     case at::kLong:
       return ROPE_I64;
     case at::kFloat8_e4m3fn:
-      return ROPE_F8E4M3;
+      if (more) return ROPE_F8E4M3;
+      break;
     case at::kFloat8_e8m0fnu:
-      return ROPE_E8M0;
+      if (more) return ROPE_E8M0;
+      break;
     case at::kInt:
-      return ROPE_I32;
+      if (more) return ROPE_I32;
+      break;
     default:
-      fail(PyExc_ValueError, "unsupported dtype");
+      break;
   }
+  fail(PyExc_ValueError, "unsupported dtype");
 }
 
 // Descriptors of one call; all tensors on the device of the first.  What the call writes says so
@@ -71,6 +76,8 @@ enum Use { kReads, kWrites };
 
 class Call {
  public:
+  explicit Call(bool more = false) : more_(more) {}
+
   const rope_tensor_t* whole(PyObject* o, Use use = kReads) {  // NULL for None
     if (o == Py_None) return nullptr;
     const at::Tensor& t = tensor(o);
@@ -117,12 +124,13 @@ class Call {
     if (t.dim() < 1 || t.dim() > 4) fail(PyExc_ValueError, "expected 1 to 4 dimensions");
     rope_tensor_t& d = descs_[n_++];
     d.data = use == kWrites ? t.mutable_data_ptr() : const_cast<void*>(t.const_data_ptr());
-    d.dtype = type_of(t);
+    d.dtype = type_of(t, more_);
     d.ndim = (int32_t)t.dim();
     for (int i = 0; i < d.ndim; ++i) d.shape[i] = t.size(i);
     return &d;
   }
 
+  const bool more_;
   rope_tensor_t descs_[14];
   int n_ = 0;
   int64_t device_ = -1;
@@ -256,7 +264,7 @@ PyObject* scaled_cos_sin(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // The arguments of an append: a[0 .. caches) tensors up to the caches (and scales), then
 // (head_size, rotary_dim or None, is_neox, mrope_section or None, cache_mode, stream).
 PyObject* append(PyObject* const* a, bool coded) {
-  Call c;
+  Call c(coded);
   int64_t ks, qs, vs;
   // (written ones first: a query that is its own output, or the fused buffer of an in-place query's key, has
   // the address that it is written at)
@@ -311,7 +319,7 @@ int64_t workspace_bytes(const at::Tensor& q, const at::Tensor& k, int64_t prefix
   if (q.dim() != 2 || k.dim() != 4 || k.size(3) < 1) return -1;
   const bool coded = k.scalar_type() == at::kFloat8_e4m3fn;
   const int st = (coded ? g_workspace_8bit : g_workspace)(q.size(0), q.size(1) / k.size(3), k.size(1), k.size(3),
-                                                          type_of(q), prefix_len, &bytes);
+                                                          type_of(q, coded), prefix_len, &bytes);
   return st == ROPE_OK ? bytes : -1;
 }
 
@@ -326,7 +334,7 @@ PyObject* attention_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //  prefix_len, scale, out, lse or None, workspace or None, stream) -> status.  Without a workspace one is taken from
 // the allocator for the current stream, which then has to be the stream of the call.
 PyObject* attention(PyObject* const* a, bool coded) {
-  Call c;
+  Call c(coded);
   int64_t qs;
   PyObject* const* b = a + (coded ? 5 : 3);  // from block_table on
   const rope_tensor_t *query = c.rows(a[0], &qs), *kc = c.whole(a[1]), *vc = c.whole(a[2]);
@@ -368,7 +376,7 @@ PyObject* paged_attention_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //  copy_dst, counts, block_size, prefix_len, stream) -> status
 PyObject* rearrange_sequences(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 14, [&]() -> PyObject* {
-    Call c;
+    Call c(true);
     const rope_tensor_t* t[11];
     for (int i = 10; i >= 0; --i) t[i] = c.whole(a[i], i >= 5 ? kWrites : kReads);  // (written ones first, as above)
     const int64_t block = integer(a[11]), prefix = integer(a[12]), stream = integer(a[13]);
@@ -383,7 +391,7 @@ PyObject* rearrange_sequences(PyObject*, PyObject* const* a, Py_ssize_t n) {
 //  None, copy_src, copy_dst, counts, block_size, prefix_len, stream) -> status
 PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 13, [&]() -> PyObject* {
-    Call c;
+    Call c(true);
     const rope_tensor_t* t[10];
     for (int i = 9; i >= 0; --i) t[i] = c.whole(a[i], i >= 4 ? kWrites : kReads);
     const int64_t block = integer(a[10]), prefix = integer(a[11]), stream = integer(a[12]);
@@ -396,7 +404,7 @@ PyObject* compact_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (src, dst, count or None, a tuple or list of tensors, stream) -> status
 PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
-    Call c;
+    Call c(true);
     if (!PyList_Check(a[3]) && !PyTuple_Check(a[3])) fail(PyExc_TypeError, "expected a list or tuple of tensors");
     const Py_ssize_t count = PySequence_Fast_GET_SIZE(a[3]);
     std::vector<rope_tensor_t> list;
