@@ -543,8 +543,10 @@ int rope_paged_attention_8bit_workspace(int64_t num_tokens, int64_t num_q_heads,
  *   gets a fresh page, and (that page, the fresh one) is a pair of pages to be copied before the cache is written;
  *   fresh pages follow until the row has room: free pages are given out lowest first, rows in order.
  * copy_src and copy_dst receive the pairs in the order of rows, then -1.  counts[0] is their number, counts[1] how many
- * pages are free then.  new_seq_lens[i] = seq_lens[p] + room[i].  Entries of the new table behind a row's pages are left
- * as they were.  With rope_copy_pages over every layer's caches the new batch is ready to be written and read.
+ * pages are free then.  new_seq_lens[i] = seq_lens[p] + room[i], also where sequence p ends within the prefix or is
+ * empty (a row of a padded batch): room is first what is left of the prefix then.  Entries of the new table behind a
+ * row's pages are left as they were.  With rope_copy_pages over every layer's caches the new batch is ready to be
+ * written and read.
  * Where pages run out, the entries are -1 from there on, a pair's copy_dst too, and ROPE_DEVICE_PAGES_EXHAUSTED is
  * recorded.  A page number outside [0, NB), more tokens than a row's pages hold, and p >= B record
  * ROPE_DEVICE_SLOT_OUT_OF_RANGE; such pages are passed over, tokens past the table dropped, such a p is none.

@@ -171,7 +171,7 @@ __device__ __forceinline__ Taken taken_of(int i, const RearrangeArgs& a, unsigne
     t.parent = -1;
     return t;
   }
-  t.len = ldg(p.lens + t.parent, a.lens_span, err);
+  t.len = max(ldg(p.lens + t.parent, a.lens_span, err), (int64_t)0);
   int64_t own = max(t.len - p.prefix_len, (int64_t)0);
   const int64_t most = min(p.W, p.new_W) * p.block_size;
   if (own > most) {
@@ -261,12 +261,13 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
       copy = t.rest > 0 && !keeps;
       has = t.full + keeps;
       keeps_last = keeps;
-      const int64_t own = max(t.len - p.prefix_len, (int64_t)0);
       const int64_t room = p.room ? max(ldg(p.room + i, a.room_span, err), (int64_t)0) : 0;
-      const int64_t most = p.new_W * bs, grown = room > most - own ? most : own + room;
-      if (own + room != grown && rank == 0) atomicOr(err, kSlotOutOfRange);
-      mine = make_int2((int)((grown + bs - 1) / bs) - has, copy);
-      if (rank == 0 && access_ok(p.new_lens + i, 8, a.new_lens_span, err)) p.new_lens[i] = p.prefix_len + grown;
+      // (a sequence that ends within the prefix has room there first)
+      const int64_t most = p.prefix_len + p.new_W * bs, len = t.len + min(room, most - t.len);
+      if (room > most - t.len && rank == 0) atomicOr(err, kSlotOutOfRange);
+      const int64_t own = max(len - p.prefix_len, (int64_t)0);
+      mine = make_int2((int)((own + bs - 1) / bs) - has, copy);
+      if (rank == 0 && access_ok(p.new_lens + i, 8, a.new_lens_span, err)) p.new_lens[i] = len;
     }
     int2 upto = mine;
 #pragma unroll
