@@ -4,7 +4,7 @@ import torch
 
 import transformer_rope_positional_gb300 as R
 from codes_ref import pages_case
-from test_gpu_pages import run_rearrange
+from test_gpu_pages import run_compact, run_rearrange
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,49 @@ def test_sequences_that_end_within_the_prefix(rope_gpu, spare_columns, room):
     want[torch.tensor(mine + c["prefix"].tolist())] = 1
     assert torch.equal(got["new_refs"], want)
     assert got["counts"].tolist() == [0, int((want == 0).sum())]
+
+
+@pytest.mark.parametrize("spare_columns", [0, 6000])  # one CTA, a cluster
+@pytest.mark.parametrize("bs", [1, 16])
+@pytest.mark.parametrize("P", [0, 40])
+@pytest.mark.parametrize("length", [1 << 31, (1 << 62) + 5, (1 << 63) - 1])
+def test_lengths_beyond_every_table(rope_gpu, spare_columns, bs, P, length):
+    """All of the row's pages are the sequence's then, and the device error says so."""
+    c = pages_case(52, [20, 33, 5], bs, P=P, spare=9, share=False, spare_columns=spare_columns)
+    held = -(-33 // bs)
+    for j in range(held, c["table"].shape[1]):
+        c["table"][1, j] = c["table"][1, 0]
+        c["refs"][c["table"][1, 0]] += 1
+    c["lens"][1] = length
+    got = run_rearrange(c, [0, 2], error=R.ROPE_DEVICE_SLOT_OUT_OF_RANGE)
+    want = c["refs"].clone()
+    want[c["table"][1, :held]] = 0
+    assert torch.equal(got["new_refs"], want)
+    assert got["new_lens"].tolist() == [P + 20, P + 5]
+    got = run_rearrange(c, [1], error=R.ROPE_DEVICE_SLOT_OUT_OF_RANGE)
+    assert got["new_lens"].tolist() == [P + c["table"].shape[1] * bs]
+    assert torch.equal(got["new_table"], c["table"][1:2])
+    got = run_compact(c, error=R.ROPE_DEVICE_SLOT_OUT_OF_RANGE)
+    assert bool((got["new_table"][1] >= 0).all()) and bool((got["new_table"][1] < int(got["counts"][1])).all())
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 63)])
+def test_negative_lengths(rope_gpu, length):
+    """As of an empty sequence."""
+    c = pages_case(53, [20, 0, 5], 16, spare=9, share=False)
+    want = run_rearrange(c, [0, 1, 2])
+    c["lens"][1] = length
+    got = run_rearrange(c, [0, 1, 2])
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
+
+
+@pytest.mark.parametrize("P", [0, 40])
+@pytest.mark.parametrize("room", [1 << 40, (1 << 63) - 1])
+def test_room_beyond_the_table(rope_gpu, P, room):
+    """As much as the row's columns hold."""
+    c = pages_case(54, [20, 3], 16, P=P, spare=40, share=False)
+    got = run_rearrange(c, [0, 1, -1], [room, 5, room], error=R.ROPE_DEVICE_SLOT_OUT_OF_RANGE)
+    W = c["table"].shape[1]
+    assert got["new_lens"].tolist() == [P + 16 * W, P + 8, P + 16 * W]
+    assert bool((got["new_table"][[0, 2]] >= 0).all())

@@ -116,6 +116,14 @@ __device__ __forceinline__ void for_entries(int warp, int64_t rows, const Span& 
   }
 }
 
+// The pages of a sequence of this length: at most those of its row, whatever the length is.
+template <typename P>
+__device__ __forceinline__ int pages_of_length(int64_t len, const P& p, unsigned* err) {
+  const int64_t own = max(len, p.prefix_len) - p.prefix_len, most = p.W * p.block_size;
+  if (own > most) atomicOr(err, kSlotOutOfRange);
+  return (int)((min(own, most) + p.block_size - 1) / p.block_size);
+}
+
 // Counts in shared memory (one CTA) or in global memory.
 template <int CL>
 __device__ __forceinline__ void add_to(int32_t* p, int32_t v) {
@@ -218,12 +226,8 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
     All::sync();
   }
   // ---- old rows let go
-  // (a sequence's pages, at most those of its row)
   auto pages_of_row = [&](int64_t b) -> Entries {
-    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
-    const int64_t pages = (own + bs - 1) / bs;
-    if (pages > p.W) atomicOr(err, kSlotOutOfRange);
-    return {p.table + b * p.W, (int)min(pages, p.W)};
+    return {p.table + b * p.W, pages_of_length(ldg(p.lens + b, a.lens_span, err), p, err)};
   };
   for_entries<All::kAllWarps>(warp, p.B, a.table_span, err, pages_of_row, [&](int64_t, int, int64_t page) {
     if (page < 0 || page >= p.NB) atomicOr(err, kSlotOutOfRange);
@@ -462,10 +466,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(CompactArgs a, unsign
     return now(p.dst + lo);
   };
   auto pages_of_row = [&](int64_t b) -> Entries {
-    const int64_t own = max(ldg(p.lens + b, a.lens_span, err) - p.prefix_len, (int64_t)0);
-    const int64_t pages = (own + p.block_size - 1) / p.block_size;
-    if (pages > p.W) atomicOr(err, kSlotOutOfRange);
-    return {p.table + b * p.W, (int)min(pages, p.W)};
+    return {p.table + b * p.W, pages_of_length(ldg(p.lens + b, a.lens_span, err), p, err)};
   };
   for_entries<All::kAllWarps>(warp, p.B, a.table_span, err, pages_of_row, [&](int64_t b, int c, int64_t page) {
     int64_t* const to = p.new_table + b * p.W + c;
