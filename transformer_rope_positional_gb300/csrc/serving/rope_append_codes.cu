@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_few_kernel(Data<T, TT> d, 
         values();
         most = fmaxf(most, L::largest(xf, yf));
       }
-      // (the byte is read by all before it is written)
+      __syncwarp();  // (the byte is read by all before it is written)
       if (single) {
         most = me.over_group(most, a.group);
       } else {
