@@ -32,23 +32,33 @@ def put(c, name, j, byte=None, code=None, b=None):
                 bytes_of(c[name + "_codes"])[page, :, row] = code
 
 
+def put_bytes(c, name, bytes_):
+    """The scale byte of key j of every sequence (that has it): bytes_[j]."""
+    for b, n in enumerate(c["lens"].tolist()):
+        n = min(n, len(bytes_))
+        page, row = torch.tensor([place(c, b, j) for j in range(n)]).unbind(1)
+        bytes_of(c[name + "_scale"])[page, :, row] = torch.as_tensor(bytes_[:n]).to(torch.uint8)[:, None]
+
+
 def reference(c):
     hq, hk, D = c["hq"], c["hk"], c["D"]
     G, rows, dtype = hq // hk, c["q"].shape[0], c["q"].dtype
-    K, V = values_of(c["k_codes"], c["k_scale"]), values_of(c["v_codes"], c["v_scale"])
-    out = torch.zeros(rows, hq, D, dtype=torch.float64)
-    lse = torch.full((rows, hq), -math.inf, dtype=torch.float64)
+    where = "cuda" if torch.cuda.is_available() else "cpu"  # (plain operations in 64 bits: quicker there)
+    K, V = (values_of(c[n + "_codes"], c[n + "_scale"]).to(where) for n in ("k", "v"))
+    out = torch.zeros(rows, hq, D, dtype=torch.float64, device=where)
+    lse = torch.full((rows, hq), -math.inf, dtype=torch.float64, device=where)
     tol, ltol = torch.zeros_like(out), torch.zeros_like(lse)
     uw = 0.0 if dtype == torch.float32 else half_step(dtype)
     for b in range(len(c["lens"])):
         t0, t1, n = int(c["starts"][b]), int(c["starts"][b + 1]), int(c["lens"][b])
-        at = [place(c, b, j) for j in range(n)]
-        k = torch.stack([K[p, :, r] for p, r in at]).transpose(0, 1)  # [hk, n, D]
-        v = torch.stack([V[p, :, r] for p, r in at]).transpose(0, 1)
-        q = c["q"][t0:t1, :c["width"]].double().reshape(t1 - t0, hk, G, D)
+        if t1 == t0 or n <= 0:
+            continue
+        page, row = torch.tensor([place(c, b, j) for j in range(n)], device=where).unbind(1)
+        k, v = (x[page, :, row].transpose(0, 1) for x in (K, V))  # [hk, n, D]
+        q = c["q"][t0:t1, :c["width"]].to(where).double().reshape(t1 - t0, hk, G, D)
         s = torch.einsum("tkgd,knd->tkgn", q, k) * c["scale"]
         big = torch.einsum("tkgd,knd->tkgn", q.abs(), k.abs()) * c["scale"]
-        seen = torch.arange(n)[None] < (n - (t1 - torch.arange(t0, t1)) + 1)[:, None]  # [t, n]
+        seen = (torch.arange(n)[None] < (n - (t1 - torch.arange(t0, t1)) + 1)[:, None]).to(where)  # [t, n]
         s = s.masked_fill(~seen[:, None, None], -math.inf)
         big = big.masked_fill(~seen[:, None, None], 0.0).amax(-1)
         w = torch.softmax(s, -1).masked_fill(~seen[:, None, None], 0.0)
@@ -65,7 +75,7 @@ def reference(c):
         tol[t0:t1] = (half_step(dtype) * o.abs() + (uw + 2 * d[..., None] + (4 * n + 64) * E32) * A + low
                       + TINY[dtype]).reshape(-1, hq, D)
         ltol[t0:t1] = (d + (n + 64) * E32 + 4 * E32 * ls.abs()).reshape(-1, hq)
-    return out.reshape(rows, -1), lse, tol.reshape(rows, -1), ltol
+    return tuple(x.cpu() for x in (out.reshape(rows, -1), lse, tol.reshape(rows, -1), ltol))
 
 
 def run(c):

@@ -1,10 +1,12 @@
 """Attention over a paged cache of 8-bit codes whose scales lie far apart, against a float64 reference (tests/scales_ref.py),
 in every kernel that the lengths choose between: units of 8, of 16 and of 128 or 256 rows, and a warp a row."""
+import functools
+
 import pytest
 import torch
 
 from codes_ref import bytes_of, coded_case
-from scales_ref import check, put
+from scales_ref import check, put, put_bytes
 
 pytestmark = pytest.mark.gpu
 
@@ -20,11 +22,17 @@ ALL = list(UNITS)
 FEW = [u for u in ALL if "many" not in u]
 
 
-def case(units, seed, dtype, D, P=0, **kw):
+@functools.lru_cache(maxsize=1)
+def made(units, seed, dtype, D, P, q_scale):
     new, own, G, hk, wide = UNITS[units]
-    c = coded_case(seed, dtype, new, own, hq=G * hk, hk=hk, D=D, P=P, S=16, **kw)
+    c = coded_case(seed, dtype, new, own, hq=G * hk, hk=hk, D=D, P=P, S=16, q_scale=q_scale)
+    del c["k"], c["v"]  # (what the codes stand for changes)
     c["wide"] = wide
     return c
+
+
+def case(units, seed, dtype, D, P=0, q_scale=1.0):
+    return {n: x.clone() if torch.is_tensor(x) else x for n, x in made(units, seed, dtype, D, P, q_scale).items()}
 
 
 def led_by_key_4(units, dtype, D):
@@ -38,10 +46,10 @@ def led_by_key_4(units, dtype, D):
     return c
 
 
+@pytest.mark.parametrize("step", [90, 91, 95])
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("units", ALL)
 @pytest.mark.parametrize("D", [16, 32, 48, 64, 128, 160, 256])
-@pytest.mark.parametrize("step", [89, 90, 91, 95])
 def test_v_in_units_beyond_2_to_the_90_of_the_one_that_counts(rope_gpu, dtype, units, D, step):
     """A later V in units that many times as large, with no weight to speak of."""
     if dtype != torch.float32 and D in (16, 48):
@@ -59,13 +67,12 @@ def test_v_in_units_beyond_2_to_the_90_of_the_one_that_counts(rope_gpu, dtype, u
 @pytest.mark.parametrize("units", ALL)
 @pytest.mark.parametrize("D", [32, 64, 128, 256])
 def test_v_in_units_that_grow_again_and_again(rope_gpu, dtype, units, D):
-    """V's units grow by 2^88 twice, each time by less than what a row is computed again for."""
+    """V's units grow by 2^88 twice, each time by less than what a row is computed again for, or by 2^14 each 32 keys."""
     c = led_by_key_4(units, dtype, D)
-    for j in range(400):
-        put(c, "v", j, byte=70 if j < 128 else 158 if j < 256 else 246)
+    j = torch.arange(400)
+    put_bytes(c, "v", 70 + 88 * (j // 128).clamp(max=2))
     check(c, "stairs")
-    for j in range(400):  # in steps that grow by 2^9 a tile of 32 keys
-        put(c, "v", j, byte=70 + j // 32 * 14)
+    put_bytes(c, "v", 70 + j // 32 * 14)
     check(c, "slope")
 
 
@@ -80,18 +87,17 @@ def test_zeros_in_front(rope_gpu, dtype, units, D, P):
     for j in range(192):
         put(c, "v", j, byte=100, code=0)
     a = check(c, "zeros in units of 2^-27")
-    for j in range(192):
-        put(c, "v", j, byte=0)
+    put_bytes(c, "v", torch.zeros(192))
     b = check(c, "zeros")
     for x, y in zip(a, b):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("far", [9, 11, 15, 16, 40])
+@pytest.mark.parametrize("name", ["k", "v"])
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("units", FEW)
 @pytest.mark.parametrize("D", [32, 64, 96, 128, 192, 256])
-@pytest.mark.parametrize("name", ["k", "v"])
-@pytest.mark.parametrize("far", [9, 11, 14, 15, 16, 40])
 def test_scales_apart(rope_gpu, dtype, units, D, name, far):
     """Scales up to 2^far apart: from key to key, growing and shrinking along the keys and from one 32 keys to the next,
     with blocks of zeros among them."""
@@ -105,9 +111,36 @@ def test_scales_apart(rope_gpu, dtype, units, D, name, far):
                          ("down", 122 - torch.arange(n) * far // (n - 1)),
                          ("by 32", 122 - far * (torch.arange(n) // 32 % 2)),
                          ("last of 32", 122 - far * (torch.arange(n) % 32 == 31).long())):
-        for j, byte in enumerate(bytes_.tolist()):
-            put(c, name, j, byte=byte if j % 50 != 7 else 0)
+        put_bytes(c, name, torch.where(torch.arange(n) % 50 == 7, 0, bytes_))
         check(c, kind)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", FEW)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("down", [9, 14])
+def test_large_values_without_weight(rope_gpu, dtype, units, D, down):
+    """The keys in the largest units have almost no weight, and the others are 2^-9 or 2^-14 of those units."""
+    c = case(units, 24, dtype, D)
+    large = torch.arange(400) % 40 == 3
+    put_bytes(c, "v", torch.where(large, 122, 122 - down))
+    put_bytes(c, "k", torch.where(large, 118, 113))
+    for j in range(3, 400, 40):
+        put(c, "k", j, code=0xd8)  # -16 / 512: 14 behind the others, whose scores are about 0
+    c["q"][:] = c["q"].abs() + 56 * 8 / D ** 0.5
+    check(c, "no weight")
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("units", FEW)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_scores_and_ends(rope_gpu, dtype, units, D):
+    """Scores thousands apart; zeros with the bytes 0 and 254."""
+    c = case(units, 25, dtype, D, q_scale=60.0)
+    for j in (3, 40, 100, 300):
+        for name in ("k", "v"):
+            put(c, name, j, byte=0 if j % 2 else 254, code=0)
+    check(c, "large")
 
 
 @pytest.mark.parametrize("dtype", HALVES, ids=str)
@@ -119,8 +152,7 @@ def test_a_far_scale_that_few_rows_see(rope_gpu, dtype, D, name):
     c = coded_case(26, dtype, new, new, hq=1, hk=1, D=D, S=16)
     c["wide"] = True
     n = new[0]
-    for j in range(n):
-        put(c, name, j, byte=120 if j % 3 else 119)
+    put_bytes(c, name, 119 + (torch.arange(n) % 3 > 0).long())
     clean, clean_lse = check(c, "clean")
     put(c, name, n - 1, byte=90)
     out, lse = check(c, "far")
