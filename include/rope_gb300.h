@@ -510,15 +510,23 @@ int rope_append_paged_kv_8bit(const rope_tensor_t* positions, const rope_tensor_
  *   workspace_bytes   at least what rope_paged_attention_8bit_workspace says.
  *
  * Arithmetic: as rope_paged_attention's, scores, statistics and sums in binary32.  The products run on the tensor cores
- * with binary16 operands, which hold codes exactly; scales come in as powers of two.  BF16 and F32 queries are taken times
- * a power of two that brings a row's largest element to about 2^8: BF16 exact down to 2^-22 of it, off by 2^-33 of it
- * below; F32 as a sum of two binary16 values, off by 2^-23 of an element or 2^-33 of the largest.  Softmax weights are
- * rounded to binary16 (half a step, those below 2^-25 of a row's largest by 2^-36 of it), with F32 queries to the sum of two.
+ * with binary16 operands, which hold codes exactly; scales come in as powers of two.  BF16 and F32 queries are taken
+ * times a power of two that brings a row's largest element (where that is not below 2^-102) to about 2^8: BF16 exact
+ * down to 2^-22 of it, off by 2^-33 of it below; F32 as a sum of two binary16 values, off by 2^-23 of an element or
+ * 2^-33 of the largest.  Softmax weights are rounded to binary16, with F32 queries to the sum of two, together with V's
+ * scale: with weights relative to the row's largest, and of a key whose V has 2^-n of the largest scale of V that the
+ * row's part of the keys has had so far (a key that the row does not see among them), off by half a step, below
+ * 2^(n - 29) by 2^(n - 40) at most, and never by more than the weight.  In calls with more than 16 rows a sequence and
+ * key head the limits are 2^(n - 25) and 2^(n - 36), n being that of the largest of 32 keys that follow each other.
  * Scales that lie far apart leave binary16: rows that see such keys are computed again one key at a time, as rows are
- * whose result is not finite (about 1 us a key).  A row meets that where a scale of V is below 2^-15 of the largest
- * of V that it has seen of its part of the keys; in calls with more than 16 rows a sequence and key head where,
- * among 32 keys that follow each other, one's scale of K or V is below 2^-15 of the largest (0 apart), or where the
- * largest of V of 32 keys is below 2^-10 of the largest before.
+ * whose result is not finite (about 1 us a key).  A row meets that where n is more than 15 for a key of more than 2^-30
+ * of the largest weight (of less: weight 0); in calls with more than 16 rows a sequence and key head where it is more
+ * than 10 for the largest scale of V of 32 keys that follow each other, and where among 32 such keys, some of which
+ * the row sees, one's scale of K or V is below 2^-15 of the largest.  Blocks of zeros with the byte 0 count nowhere.
+ * It meets it, too, where the scale of V grows beyond 2^90 of the first that the row's part of the keys had.
+ * Speed: made for decoding, where the cache's bytes bound the call.  With more than 16 rows a sequence and key head the
+ * codes are widened on the way, which costs more than their bytes save: 4 chunks of 1984 tokens behind 4096 take 800 us,
+ * rope_paged_attention over BF16 500.
  */
 int rope_paged_attention_8bit(const rope_tensor_t* query, int64_t query_row_stride, const rope_tensor_t* k_cache,
                               const rope_tensor_t* v_cache, const rope_tensor_t* k_scale,

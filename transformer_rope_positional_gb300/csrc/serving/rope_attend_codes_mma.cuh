@@ -18,7 +18,8 @@
 //  * Queries are binary16 too.  bfloat16 and binary32 rows are multiplied by the power of two that brings their largest
 //    element to [2^8, 2^9): bfloat16 stays exact down to 2^-22 of it and is off by 2^-33 of it below.  binary32 is taken as
 //    the sum of two binary16 parts (off by 2^-23 of an element, or 2^-33 of the largest), with two products each.
-//  * Weights are rounded to binary16 times 2^15 (see weight_lift): half a step relative from 2^-29 of the largest on.
+//  * Weights are rounded to binary16 times 2^15 (see weight_lift), V's scale among them: with 2^-n of the largest scale,
+//    half a step relative from 2^(n - 29) of the largest weight on, and 2^(n - 40) of it below; n is 15 at most (kNoWeight).
 //    With binary32 they are two parts as well.
 #pragma once
 
