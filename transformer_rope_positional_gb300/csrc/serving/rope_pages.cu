@@ -3,10 +3,13 @@
 //
 // The first two work on tables of page numbers and on how many times each page is held (ref_counts).  They are
 // bound by latency: a handful of steps, each of which has to see all of the one before.  Each is one launch: of one CTA
-// that keeps the counts in shared memory where there are up to kSmallPages pages and kSmallEntries table entries, so that
-// a step is a few hundred nanoseconds, else of one cluster of 8 CTAs with the counts in global memory (16 rows of up to
-// 300 tokens reordered: 12 us in the cluster, 7 in one CTA).  Free pages are given out lowest first, rows in order, so results do not
-// depend on the order in which threads run.
+// that keeps the counts in shared memory, so that a step is a few hundred nanoseconds, where they fit (kSmallPages) and
+// there are few rows (kSmallRows, kSmallTable); else of one cluster of 8 CTAs with the counts in global memory.  Rows
+// reordered, us, one CTA and cluster: 16 rows of 32 columns 7.1, 14.9; 64 of 256 13.7, 22.5; 256 of 64 16.7, 20.0; 256 of
+// 256 19.4, 21.6; 384 of 64 21.4, 22.5; 512 of 64 26.7, 23.6; 1024 of 8 33.6, 23.5; 4096 of 4 145, 47.  Compacted: 16 of 32
+// 4.8, 11.4; 64 of 256 17.5, 65; 256 of 256 23, 28; 1024 of 64 35, 43; 2048 of 8 55, 79; 4096 of 4 95, 101, of 1 92, 63;
+// 8000 of 1 170, 105.  Caches that only the cluster takes: 256 rows of 512 in 200000 pages 35 and 158.  Free pages are
+// given out lowest first, rows in order, so results do not depend on the order in which threads run.
 //
 // rearrange_sequences: every old row lets go of its pages; new row i takes the whole pages of its parent once
 // more.  The page that is written on (the last, partly filled one) stays with the first of the new rows that
@@ -30,8 +33,9 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kClaim = 1 << 30;
 constexpr int kKeeps = 1 << 30;  // a row keeps the page that it writes on (rows have fewer pages)
-constexpr int64_t kSmallPages = 24576;
-constexpr int64_t kSmallEntries = 16384;
+constexpr int64_t kSmallPages = 24576;  // 8 bytes each
+constexpr int64_t kSmallRows = 384;     // reordered, old and new
+constexpr int64_t kSmallTable = 2048;   // compacted
 
 // The CTAs of a call: CL is 1 or kCluster.
 template <int CL>
@@ -615,7 +619,7 @@ cudaError_t launch_rearrange(const RearrangeProblem& p, cudaStream_t stream) {
   a.dst_span = make_span(p.dst, p.rows * 8);
   a.counts_span = make_span(p.counts, 16);
   const size_t smem = sizeof(RearrangeShared) + (3 * p.rows + 1) * 4;
-  if (p.NB <= kSmallPages && p.B * p.W <= kSmallEntries && p.rows * p.new_W <= kSmallEntries)
+  if (p.NB <= kSmallPages && p.B <= kSmallRows && p.rows <= kSmallRows)
     return launch_team<1>(rearrange_kernel<1>, smem + p.NB * 4, a, stream);
   return launch_team<kCluster>(rearrange_kernel<kCluster>, smem, a, stream);
 }
@@ -634,7 +638,7 @@ cudaError_t launch_compact(const CompactProblem& p, cudaStream_t stream) {
   a.src_span = make_span(p.src, p.pairs * 8);
   a.dst_span = make_span(p.dst, p.pairs * 8);
   a.counts_span = make_span(p.counts, 16);
-  if (p.NB <= kSmallPages && p.B * p.W <= kSmallEntries)
+  if (p.NB <= kSmallPages && p.B <= kSmallTable)
     return launch_team<1>(compact_kernel<1>, p.NB * (4 + 2 + 2), a, stream);
   return launch_team<kCluster>(compact_kernel<kCluster>, 0, a, stream);
 }
