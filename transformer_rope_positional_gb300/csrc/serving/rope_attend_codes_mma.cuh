@@ -448,18 +448,19 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
         m1 = t1;
         bool far = false;
         if (bigger) {
-          bool some = false;
-#pragma unroll
-          for (int n = 0; n < NO; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) some = some || o[n][e] != 0.f;
-          some = __any_sync(0xffffffffu, some);
-          far = some && (int)about.y - sm.first[warp] > 90;
-          __syncwarp();
-          if (!some || far) sm.first[warp] = (int)about.y;
-          if (some && !far) {
+          if (k == w.k0) {  // O is 0
+            sm.first[warp] = (int)about.y;
+          } else if ((int)about.y - sm.first[warp] <= 90) {
             f0 *= power(unit - (int)about.y);
             f1 *= power(unit - (int)about.y);
+          } else {
+            bool some = false;
+#pragma unroll
+            for (int n = 0; n < NO; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) some = some || o[n][e] != 0.f;
+            far = __any_sync(0xffffffffu, some);
+            sm.first[warp] = (int)about.y;  // (the vote: all have read it)
           }
           unit = (int)about.y;
         }
