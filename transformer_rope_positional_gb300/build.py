@@ -42,8 +42,9 @@ SOURCES = ["rope_api.cu", "rope_launch.cu", "rope_inplace_fwd.cu", "rope_inplace
            "serving/rope_append_codes.cu", "serving/rope_attend_codes.cu", "serving/rope_attend_codes_tall.cu",
            "serving/rope_pages.cu"]
 HEADERS = ["rope_device.cuh", "rope_launch.h", "rope_inplace.cuh", "serving/serving.h",
-           "serving/rope_attend.cuh", "serving/rope_attend_ring.cuh", "serving/rope_attend_mma.cuh", "serving/rope_attend_tc.cuh", "serving/rope_attend_f32.cuh",
-           "serving/rope_attend_join.cuh", "serving/rope_attend_codes_mma.cuh", "serving/tcgen05.cuh", "serving/wait_clock.h"]
+           "serving/rope_attend.cuh", "serving/rope_attend_ring.cuh", "serving/rope_attend_mma.cuh",
+           "serving/rope_attend_tc.cuh", "serving/rope_attend_f32.cuh", "serving/rope_attend_join.cuh",
+           "serving/rope_attend_codes_mma.cuh", "serving/tcgen05.cuh", "serving/wait_clock.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

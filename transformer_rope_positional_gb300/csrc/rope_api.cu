@@ -497,8 +497,9 @@ bool scales_ok(const rope_tensor_t* cache, const rope_tensor_t* scale) {
 int append_call(const rope_tensor_t* positions, const rope_tensor_t* query, const rope_tensor_t* key,
                 const rope_tensor_t* value, const rope_tensor_t* table, const rope_tensor_t* slots,
                 const rope_tensor_t* query_out, const rope_tensor_t* k_cache, const rope_tensor_t* v_cache, bool coded,
-                const rope_tensor_t* k_scale, const rope_tensor_t* v_scale, int64_t D, int64_t R, int32_t is_neox, const int64_t* section, int64_t section_len, int32_t cache_mode,
-                int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride, void* stream) {
+                const rope_tensor_t* k_scale, const rope_tensor_t* v_scale, int64_t D, int64_t R, int32_t is_neox,
+                const int64_t* section, int64_t section_len, int32_t cache_mode, int64_t q_row_stride,
+                int64_t k_row_stride, int64_t v_row_stride, void* stream) {
   for (const rope_tensor_t* t : {positions, key, value, table, slots, k_cache, v_cache})
     if (!t) return ROPE_ERR_PARAM_NULLPTR;
   if ((query_out && !query) || (coded && !(k_scale && v_scale))) return ROPE_ERR_PARAM_NULLPTR;
@@ -979,8 +980,8 @@ int rope_append_paged_kv(const rope_tensor_t* positions, const rope_tensor_t* qu
                          int64_t mrope_section_len, int32_t cache_mode, int64_t query_row_stride,
                          int64_t key_row_stride, int64_t value_row_stride, void* stream) {
   return append_call(positions, query, key, value, cos_sin_cache, slot_mapping, query_out, k_cache, v_cache, false,
-                     nullptr, nullptr, head_size, rotary_dim, is_neox, mrope_section, mrope_section_len, cache_mode, query_row_stride,
-                     key_row_stride, value_row_stride, stream);
+                     nullptr, nullptr, head_size, rotary_dim, is_neox, mrope_section, mrope_section_len, cache_mode,
+                     query_row_stride, key_row_stride, value_row_stride, stream);
 }
 
 int rope_paged_attention(const rope_tensor_t* query, int64_t query_row_stride, const rope_tensor_t* k_cache,
@@ -989,8 +990,8 @@ int rope_paged_attention(const rope_tensor_t* query, int64_t query_row_stride, c
                          const rope_tensor_t* prefix_blocks, int64_t prefix_len, float scale,
                          const rope_tensor_t* out, const rope_tensor_t* lse, void* workspace,
                          int64_t workspace_bytes, void* stream) {
-  return attend_call(query, query_row_stride, k_cache, v_cache, false, nullptr, nullptr, block_table, seq_lens, query_start_loc, prefix_blocks,
-                     prefix_len, scale, out, lse, workspace, workspace_bytes, stream);
+  return attend_call(query, query_row_stride, k_cache, v_cache, false, nullptr, nullptr, block_table, seq_lens,
+                     query_start_loc, prefix_blocks, prefix_len, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 int rope_paged_attention_workspace(int64_t num_tokens, int64_t num_q_heads, int64_t num_k_heads, int64_t head_size,

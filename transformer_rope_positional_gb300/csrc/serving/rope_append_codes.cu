@@ -15,14 +15,15 @@
 // share its heads instead, the groups of a warp taking a head's rows in turn.  (32 q, 8 k and 8 v heads of 128, bf16: 64
 // requests' tokens 3.5 us, the kernel for many 4.7; a prompt of 512 9.4, 13.7; 1024 requests 11.5, 12.4; 2048 21.3, 20.7.)
 //
-// Many: what an item costs in instructions counts as much as its bytes.  A warp has the runs that begin in a window of
+// Many: what an item costs in round trips and instructions counts as much as its bytes.  A warp has the runs that begin in a window of
 // tokens, for a set of heads: a run of up to kRows rows is one group's, the groups having a head each, kRows rows at a
 // time (the example below in scale blocks of 2 tokens: 111 us, 218 as longer runs go); a longer one is the warp's, head by
 // head, its groups taking the rows in turn.  A thread has slots of its own in
 // shared memory for its pieces of kRows rows and of their table rows, which it copies with cp.async, all at once: an item
 // is a few round trips to memory.  Up to kRows rows a group are read once, longer runs again (from L2) once their largest
 // value is known.  Queries go by heads of a token.  (16384 tokens 84 us, 67% of the copy rate; without the codes, or
-// without the queries, 40 and 53: the codes' part is bound by instructions, two rotations and a conversion an element.)
+// without the queries, 40 and 53.  Nothing is full: DRAM 47 %, issue slots 52 %, and 22 % of the warps; an item's copies are
+// waited for before its arithmetic, two rotations and a conversion an element, so it is latency that bounds it.)
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -74,8 +75,8 @@ __device__ __forceinline__ float rotate_one(float a, float b, float c, float d) 
   return diff_of_products(a, b, c, d);
 }
 
-// 2^(e - 127), e from 0 to 254.
-__device__ __forceinline__ float power_of(int e) { return __uint_as_float(e == 0 ? 0x00400000u : (uint32_t)e << 23); }
+// 2^(e - 127), e from 0 to 254 (of 0, too, unlike the scale that the byte 0 stands for).
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(e == 0 ? 0x00400000u : (uint32_t)e << 23); }
 
 // The byte of the least power of two e with most <= 448 * 2^e (448 = 1.75 * 2^8), at least 1; 0 for 0.
 __device__ __forceinline__ int byte_for(float most) {
@@ -264,7 +265,7 @@ struct Lane {
   // The codes of a row at p, in units of 2^(byte - 127).
   __device__ __forceinline__ void write(uint8_t* p, int byte, const float2 (&xf)[VEC / 2], const float2 (&yf)[VEC / 2],
                                         const Span& span, unsigned* err) const {
-    const float f1 = byte == 255 ? NAN : power_of(254 - byte);
+    const float f1 = byte == 255 ? NAN : two_to(254 - byte);
     const float2 f = make_float2(f1, f1);
     float m = 0.f;
 #pragma unroll
@@ -290,10 +291,10 @@ struct Lane {
   }
 
   // The first `before` rows of a block, each `step`-th from i0 on, in units of its new byte.
-  __device__ __forceinline__ void again(uint8_t* rows, int i0, int step, int before, int old, int byte, const Span& span, unsigned* err,
-                                        const CodesArgs& a) const {
+  __device__ __forceinline__ void again(uint8_t* rows, int i0, int step, int before, int old, int byte,
+                                        const Span& span, unsigned* err, const CodesArgs& a) const {
     if (before == 0 || old == byte) return;
-    const float s = old == 0 ? 0.f : power_of(max(127 + old - byte, 0));
+    const float s = old == 0 ? 0.f : two_to(max(127 + old - byte, 0));
     const float2 scale = make_float2(s, s);
 #pragma unroll 1
     for (int i = i0; i < before; i += step)
@@ -305,7 +306,8 @@ struct Lane {
         uint32_t now[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((e < 2 ? was.x : was.y) >> (e & 1) * 16 & 0xffffu, __NV_E4M3);
+          const uint32_t two = (e < 2 ? was.x : was.y) >> (e & 1) * 16 & 0xffffu;
+          const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3);
           now[e] = codes_of<false>(__half22float2(__half2(r)), scale);
         }
         *reinterpret_cast<uint2*>(p) = make_uint2(now[0] | now[1] << 16, now[2] | now[3] << 16);
@@ -325,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_few_kernel(Data<T, TT> d, 
   unsigned* const err = d.err;
   const int sets = a.kv_sets + a.q_sets;
   wait_for_prior_grid();
-  for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < a.items; item += (int64_t)gridDim.x * kWarps) {
+  for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < a.items;
+       item += (int64_t)gridDim.x * kWarps) {
     const int64_t t = div_index(item, sets, a.items32);
     const int set = (int)(item - t * sets);
     const bool is_query = set >= a.kv_sets;
@@ -358,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_few_kernel(Data<T, TT> d, 
     const int P = a.per_warp, all = a.hk + a.hv;
     auto read = [&](int u, int64_t row) {
       const bool is_v = u >= a.hk;
-      const T* const src = is_v ? d.v + row * a.v_stride + (int64_t)(u - a.hk) * a.D : d.k + row * a.k_stride + (int64_t)u * a.D;
+      const T* const src = is_v ? d.v + row * a.v_stride + (int64_t)(u - a.hk) * a.D
+                                : d.k + row * a.k_stride + (int64_t)u * a.D;
       where = L::place_of(row, d, a);
       load_vec<false>(x, src + me.ca, is_v ? a.v_span : a.k_span, err);
       load_vec<false>(y, src + me.cb, is_v ? a.v_span : a.k_span, err);
@@ -369,7 +373,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_few_kernel(Data<T, TT> d, 
     const int64_t block = div_index(slot, a.per, a.items32);
     const int first = (int)(slot - block * a.per);
     // the run's tokens before this one and from it on
-    const bool joins = lane < first && t - 1 - lane >= 0 && ldg(d.slots + t - 1 - lane, a.slot_span, err) == slot - 1 - lane;
+    const bool joins =
+        lane < first && t - 1 - lane >= 0 && ldg(d.slots + t - 1 - lane, a.slot_span, err) == slot - 1 - lane;
     int n = 1;
     for (;;) {
       const int i = n + lane;
@@ -455,14 +460,17 @@ __device__ __forceinline__ void copy16(void* smem, const void* p, const Span& s,
 
 // Four cos and four sin of a chunk: binary32 to two slots, 16 bits to the halves of one.
 template <typename TT>
-__device__ __forceinline__ void copy_turns(uint4* a, uint4* b, const TT* cos, const TT* sin, const Span& s, unsigned* err) {
+__device__ __forceinline__ void copy_turns(uint4* a, uint4* b, const TT* cos, const TT* sin, const Span& s,
+                                           unsigned* err) {
   if constexpr (sizeof(TT) == 4) {
     copy16(a, cos, s, err);
     copy16(b, sin, s, err);
   } else {
     const unsigned to = (unsigned)__cvta_generic_to_shared(a);
-    if (access_ok(cos, 8, s, err)) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(cos) : "memory");
-    if (access_ok(sin, 8, s, err)) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + 8), "l"(sin) : "memory");
+    if (access_ok(cos, 8, s, err))
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(cos) : "memory");
+    if (access_ok(sin, 8, s, err))
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + 8), "l"(sin) : "memory");
   }
 }
 
@@ -560,8 +568,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     int singles = 0;
     while (begins) {
-      // ---- what is done at a time: a run of more than kRows rows, head by head; or up to kRows rows of shorter runs, the heads
-      // side by side
+      // ---- what is done at a time: a run of more than kRows rows, head by head; or up to kRows rows of shorter runs,
+      // the heads side by side
       int i0 = __ffs(begins) - 1;
       int n = 1;
       {
@@ -620,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           at = (is_v ? d.vs : d.ks) + (page * heads + h) * a.S + part;
           rows = (is_v ? d.vc : d.kc) + ((page * heads + h) * a.block_size + (int64_t)part * a.per) * a.D;
         };
-        // Rows under way, in slot e: of the one run the row base + e * step, or token e of the short runs'; with their table rows.
+        // Rows under way, in slot e: of the one run the row base + e * step, or token e of the short runs'; with their
+        // table rows.
         auto token_of = [&](int base, int e) { return single ? (int)(run_of >> 8 * e & 0xffu) : i0 + base + e * step; };
         uint32_t on = 0;  // which of them are written, a bit a slot
         auto read = [&](int base) {
@@ -645,11 +654,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int z = 0; z < kTurns / 2; ++z) {
                       copy16(&sm.turns[e][z][threadIdx.x], row + ia + z * (16 / sizeof(TT)), a.tab_span, err);
-                      copy16(&sm.turns[e][kTurns / 2 + z][threadIdx.x], row + half + ia + z * (16 / sizeof(TT)), a.tab_span, err);
+                      copy16(&sm.turns[e][kTurns / 2 + z][threadIdx.x], row + half + ia + z * (16 / sizeof(TT)),
+                             a.tab_span, err);
                     }
                 } else {
-                  if (ra) copy_turns<TT>(&sm.turns[e][0][threadIdx.x], &sm.turns[e][kTurns / 4][threadIdx.x], row + ia, row + half + ia, a.tab_span, err);
-                  if (rb) copy_turns<TT>(&sm.turns[e][kTurns / 2][threadIdx.x], &sm.turns[e][kTurns * 3 / 4][threadIdx.x], row + ib, row + half + ib, a.tab_span, err);
+                  auto turn_at = [&](int i) { return &sm.turns[e][i][threadIdx.x]; };
+                  if (ra) copy_turns<TT>(turn_at(0), turn_at(kTurns / 4), row + ia, row + half + ia, a.tab_span, err);
+                  if (rb)
+                    copy_turns<TT>(turn_at(kTurns / 2), turn_at(kTurns * 3 / 4), row + ib, row + half + ib, a.tab_span, err);
                 }
               }
             }

@@ -7,9 +7,9 @@
 //  * The codes become binary16, exactly, on the way from shared memory to the operands of mma.sync m16n8k16, two an
 //    instruction; no product sees a scale.  A score is multiplied by its key's, a power of two, in binary32.  V's
 //    scale goes into the weight: with V_j = c_j 2^(b_j), O holds sum p_j 2^(b_j - B) c_j for the largest b_j so far, B
-//    (one a warp), and is multiplied by 2^(B_old - B) where that grows; l is the sum of p_j.  Where that would take what O
-//    holds out of binary32 (beyond 2^90 of the unit it began in) it becomes NaN, for mend_rows to find, and what is 0 stays 0: each lane looks at its elements
-//    of O, which are sums over all keys, not at its l, which is a sum over some.
+//    (one a warp), and is multiplied by 2^(B_old - B) where that grows; l is the sum of p_j.  Where that would take what
+//    O holds out of binary32 (beyond 2^90 of the unit it began in) it becomes NaN, for mend_rows to find, and what is 0
+//    stays 0: each lane looks at its elements of O, which are sums over all keys, not at its l, which is one over some.
 //  * Which column of q and K a product's place along k stands for is free, as long as both agree, and so is which key
 //    and which column of V an operand's row stands for.  A lane's places are chosen so that it reads 16 bytes of a key
 //    (8 of a value) at once and has the operands of four products (of two keys and 8 columns) in its registers: no
@@ -40,7 +40,11 @@ struct CodesShape {
   static constexpr int KW = DP <= 128 ? 32 : 16;
   static constexpr int KT = 4 * KW;
   static constexpr int kCtas = MR == 8 && DP <= 128 && sizeof(T) == 2 ? 3 : 2;
-  static constexpr int kStages = kCtas == 3 ? (DP <= 64 ? 7 : 4) : DP <= 64 ? 10 : DP <= 128 ? 5 : DP <= 192 ? 6 : sizeof(T) == 4 ? 4 : 5;
+  static constexpr int kStages = kCtas == 3  ? (DP <= 64 ? 7 : 4)
+                                 : DP <= 64  ? 10
+                                 : DP <= 128 ? 5
+                                 : DP <= 192 ? 6
+                                             : (sizeof(T) == 4 ? 4 : 5);
   static constexpr int kStage = KW * DP;  // bytes
   static constexpr int kJoin = DP <= 128 && kCtas == 2 ? 4 : 2;
   static constexpr int kRecent = kStages <= 5 ? 4 : 8;  // tiles whose keys' scales are kept
@@ -304,7 +308,8 @@ __global__ void __launch_bounds__(kCodesThreads, CodesShape<T, DP, MR>::kCtas)
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = widen(qs[r * DP + d + e]);
         if constexpr (!std::is_same<T, __half>::value) {
-          const float up = power(sm.power[r]);  // (exact: an element that leaves binary32 downwards is below 2^-33 of the largest)
+          // (exact: an element that leaves binary32 downwards is below 2^-33 of the largest)
+          const float up = power(sm.power[r]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[e] *= up;
         }

@@ -80,8 +80,8 @@ struct TcMore<DP, true> {
   uint32_t units[16][4];
   signed char power[2][256];
   float second;
-  float first[8];  // of a softmax warp: the unit in which its O was first not zeros (after NaN, again): beyond 2^90 of it O
-                   // may leave binary32
+  float first[8];  // of a softmax warp: the unit in which its O was first not zeros (after NaN, again): beyond 2^90 of it
+                   // O may leave binary32
 };
 
 template <int DP, bool CODED>
@@ -256,7 +256,6 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         int head = at.h - w.h * a.G;
         const T* p = q + at.t * a.q_stride + (int64_t)at.h * a.D + ch * 8;
         const int64_t next_token = a.q_stride - (int64_t)a.G * a.D;
-        unsigned dst = tc::smem_at(sm.q[0]) + (ch >> 3) * (128 * 128);
         if constexpr (kCodes && !std::is_same<T, __half>::value) {
           // through registers: rows are brought to binary16's range
           constexpr int U = 4;
@@ -300,8 +299,8 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           }
           __syncwarp();  // (the powers are there for who sees this warp's next arrivals)
         } else {
-        unsigned dst = tc::smem_at(sm.q[0]) + (ch >> 3) * (128 * 128);
-  #pragma unroll 4
+          const unsigned dst = tc::smem_at(sm.q[0]) + (ch >> 3) * (128 * 128);
+#pragma unroll 4
           for (int r = ct / CH; r < 128 * nt; r += kStep) {
             const bool there = r < u.rows && ch * 8 < a.D;
             const int rr = r & 127;
@@ -353,7 +352,8 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
         constexpr int CC = DP / 16;  // 16-byte pieces of a row of codes
         // This lane's piece of row `key` + i * 128 / DP * 4: eight lanes have four pieces of two rows each, so that what
         // they store meets every bank once.
-        const int ch = (lane & 3) | ((lane >> 3) << 2 & (CC - 1)), first_key = (lane >> 2 & 1) | (lane >> (CC == 4 ? 3 : CC == 8 ? 4 : 5)) << 1;
+        const int ch = (lane & 3) | ((lane >> 3) << 2 & (CC - 1));
+        const int first_key = (lane >> 2 & 1) | (lane >> (CC == 4 ? 3 : CC == 8 ? 4 : 5)) << 1;
         constexpr int kKeys = 32 / CC;  // rows of an access
         bool is_there[S::kRaw], is_v[S::kRaw];  // this lane's key of the items under way, and whose they are
         uint32_t kb[S::kRaw], vb[S::kRaw];      // its scales
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(TcShape<DP, kCoded<C>>::kThreads, 1)
           next_unit = max3(o_unit, vm[0], vm[1]);
           mt = fmaxf(top[0], top[1]) - kLift;  // -infinity stays (the factors are > 0)
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) less[ch] = vm[ch] == 0.f ? 0.f : vm[ch] - next_unit;  // (a V of zeros: in any units)
+          for (int ch = 0; ch < 2; ++ch) less[ch] = vm[ch] == 0.f ? 0.f : vm[ch] - next_unit;  // (zeros: in any units)
           if ((units[0] | units[1]) & kFar) {
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch)

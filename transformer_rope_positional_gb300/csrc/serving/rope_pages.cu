@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(kThreads) rearrange_kernel(RearrangeArgs a, un
       const int x = __shfl_up_sync(0xffffffffu, sum.x, d), y = __shfl_up_sync(0xffffffffu, sum.y, d);
       if (lane >= d) sum.x += x, sum.y += y;
     }
-    const int before_x = __shfl_sync(0xffffffffu, sum.x - own_sum.x, cw), before_y = __shfl_sync(0xffffffffu, sum.y - own_sum.y, cw);
+    const int before_x = __shfl_sync(0xffffffffu, sum.x - own_sum.x, cw);
+    const int before_y = __shfl_sync(0xffffffffu, sum.y - own_sum.y, cw);
     if (i < rows) {
       start[i] = run.x + before_x + upto.x - mine.x;
       have[i] = has | (keeps_last ? kKeeps : 0);
