@@ -22,7 +22,7 @@
 // shared memory for its pieces of kRows rows and of their table rows, which it copies with cp.async, all at once: an item
 // is a few round trips to memory.  Up to kRows rows a group are read once, longer runs again (from L2) once their largest
 // value is known.  Queries go by heads of a token.  (16384 tokens 84 us, 67% of the copy rate; without the codes, or
-// without the queries, 40 and 53.  Nothing is full: DRAM 47 %, issue slots 52 %, and 22 % of the warps; an item's copies are
+// without the queries, 40 and 53.  Nothing is full: DRAM 44 %, issue slots 52 %, and 22 % of the warps; an item's copies are
 // waited for before its arithmetic, two rotations and a conversion an element, so it is latency that bounds it.)
 #include <cuda_fp8.h>
 
